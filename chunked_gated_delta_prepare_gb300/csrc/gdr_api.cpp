@@ -11,6 +11,7 @@
 
 #include "gdr.h"
 #include "gdr_internal.h"
+#include "layer_internal.h"
 
 namespace {
 
@@ -523,6 +524,8 @@ gdr_status run_backward(const gdr::Dims& d, BwdPath path, int S, char* base, con
 }
 
 }  // namespace
+
+void gdr::set_last_variant(const char* name) { t_last_variant = name; }
 
 extern "C" {
 

@@ -1,0 +1,163 @@
+// Device helpers shared by the layer operators (norm, convolution, selective scan, single-token delta step).
+//
+// They work on vectors of 8 (or 4) neighbouring channels of one token.  A row may start at any element: where its
+// address is not a multiple of 16 bytes, or the vector passes the row's end, the elements move one by one.  Whether a tensor's rows are all aligned is decided on the host (RowTensor::vec).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdr {
+namespace layer {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename IO> __device__ __forceinline__ IO from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+
+// N neighbouring elements as they lie in memory.
+template <typename IO, int N> struct alignas(sizeof(IO) * N < 16 ? sizeof(IO) * N : 16) RawN {
+    IO e[N];
+};
+template <typename IO> using Raw8 = RawN<IO, 8>;
+
+// Elements [0, N) of p; only the first `left` exist (left <= 0: none), the rest read as zero.
+template <int N, typename IO> __device__ __forceinline__ RawN<IO, N> load_n(const IO* p, int64_t left, bool vec) {
+    RawN<IO, N> r;
+    if (vec && left >= N) {
+        if constexpr (sizeof(r) == 8) {
+            *reinterpret_cast<uint2*>(&r) = __ldg(reinterpret_cast<const uint2*>(p));
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(r) / 16; ++i)
+                reinterpret_cast<uint4*>(&r)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.e[i] = i < left ? p[i] : from_f<IO>(0.f);
+    }
+    return r;
+}
+template <typename IO> __device__ __forceinline__ Raw8<IO> load8(const IO* p, int64_t left, bool vec) {
+    return load_n<8>(p, left, vec);
+}
+
+template <typename IO, int N> __device__ __forceinline__ void widen(const RawN<IO, N>& r, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f(r.e[i]);
+}
+
+template <typename IO, int N>
+__device__ __forceinline__ void store_raw(IO* p, const RawN<IO, N>& r, int64_t left, bool vec) {
+    if (vec && left >= N) {
+        if constexpr (sizeof(r) == 8) {
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(&r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(r) / 16; ++i)
+                reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&r)[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) p[i] = r.e[i];
+    }
+}
+
+template <typename IO, int N>
+__device__ __forceinline__ void store_n(IO* p, const float (&x)[N], int64_t left, bool vec) {
+    RawN<IO, N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.e[i] = from_f<IO>(x[i]);
+    store_raw(p, r, left, vec);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-x): 0 and 1 at the ends of the range, NaN for NaN.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + ex2(-x * kLog2e)); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN where either is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// The packed sequences of a token axis, or a batch of equal ones (cu == nullptr: n rows of T tokens).
+struct Seqs {
+    const int* cu;    // device int32 [n + 1], or nullptr
+    int64_t total;    // tokens on the axis
+    int64_t T;        // tokens of each sequence of a batch
+    int n;
+};
+
+// Sequence s as [start, start + len); whatever cu holds, the range lies in [0, total].
+__device__ __forceinline__ void seq_range(const Seqs& q, int s, int64_t* start, int64_t* len) {
+    if (!q.cu) {
+        *start = (int64_t)s * q.T;
+        *len = q.T;
+        return;
+    }
+    int64_t a = q.cu[s], b = q.cu[s + 1];
+    a = a < 0 ? 0 : (a > q.total ? q.total : a);
+    b = b < a ? a : (b > q.total ? q.total : b);
+    *start = a;
+    *len = b - a;
+}
+
+// Tiles of `tile` tokens, numbered over all sequences.  Sequence s of a packed axis owns the numbers from
+// cu[s] / tile + s up to cu[s + 1] / tile + s + 1 (its tiles and at most one more, which is empty), so the number of
+// blocks, total / tile + n, needs no look at the lengths on the host.  A batch has ceil(T / tile) a sequence.
+struct TileAt {
+    int seq;          // -1: no such tile
+    int64_t tile;     // within the sequence
+    int64_t start, len;
+};
+
+__host__ __device__ __forceinline__ int64_t tile_count(const Seqs& q, int tile) {
+    return q.cu ? q.total / tile + q.n : q.n * ((q.T + tile - 1) / tile);
+}
+
+__device__ __forceinline__ int64_t first_tile(const Seqs& q, int s, int tile) {
+    if (!q.cu) return s * ((q.T + tile - 1) / tile);
+    int64_t a = q.cu[s];
+    a = a < 0 ? 0 : (a > q.total ? q.total : a);
+    return a / tile + s;
+}
+
+__device__ __forceinline__ TileAt find_tile(const Seqs& q, int64_t number, int tile) {
+    TileAt t;
+    if (!q.cu) {
+        const int64_t per = (q.T + tile - 1) / tile;
+        t.seq = (int)(number / per);
+        t.tile = number - t.seq * per;
+        t.start = t.seq * q.T;
+        t.len = q.T;
+        return t;
+    }
+    int lo = 0, hi = q.n - 1;             // the last sequence whose first number is at most this one
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_tile(q, mid, tile) <= number) lo = mid;
+        else hi = mid - 1;
+    }
+    t.seq = lo;
+    t.tile = number - first_tile(q, lo, tile);
+    seq_range(q, lo, &t.start, &t.len);
+    if (t.tile < 0 || (t.tile > 0 && t.tile * tile >= t.len)) t.seq = -1;
+    return t;
+}
+
+}  // namespace layer
+}  // namespace gdr

@@ -1,0 +1,209 @@
+// What the forward, the backward and the single-token form of the selective scan share.
+//
+//   h_t[d][n] = exp(Delta_t[d] A[d][n]) h_{t-1}[d][n] + Delta_t[d] x_t[d] B_t[g][n],   Delta = softplus(dt + bias)
+//   y_t[d]    = (sum_n C_t[g][n] h_t[d][n] + Dk[d] x_t[d]) silu(z_t[d])
+//
+// A channel's states lie on LN neighbouring lanes, 4 on each (N <= 4 LN, the rest zero), a lane takes DC neighbouring
+// channels.  Products go two channels at a time through the packed fp32 instructions: two independent fp32 operations
+// each, rounded as alone.
+#pragma once
+
+#include "layer_common.cuh"
+#include "layer_internal.h"
+
+namespace gdr {
+namespace layer {
+
+constexpr int kSsmThreads = 128;
+
+using F2 = unsigned long long;   // two fp32, the lower channel in the low half
+
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 2^v.  ex2.approx's error is below 2^-22 of the result, and its mean below 1e-8 near 1, where slow decays live.
+__device__ __forceinline__ F2 exp2_2(F2 v) {
+    const float2 f = unpack2(v);
+    return pack2(ex2(f.x), ex2(f.y));
+}
+
+__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(__expf(x)); }
+
+// The operator as the kernels take it.
+struct Ssm {
+    Seqs q;
+    int D, N, G, per;        // per = D / G channels share the B and C of a group
+    int seg;                 // tokens of a segment
+    RowTensor x, dt, z, B, C;
+    const float *A, *bias, *Dk, *h0;
+    bool softplus;
+    bool vec;                // rows of D elements on 16-byte boundaries in the contiguous tensors of tokens
+};
+
+// The channels of a block: [c0, end) of one group.
+struct Channels {
+    int group, c0, end;
+};
+__device__ __forceinline__ Channels block_channels(const Ssm& a, int width) {
+    const int blocks = (a.per + width - 1) / width;
+    Channels c;
+    c.group = blockIdx.y / blocks;
+    c.c0 = c.group * a.per + (blockIdx.y - c.group * blocks) * width;
+    c.end = (c.group + 1) * a.per;
+    return c;
+}
+
+// 8 channels from c of a token's row; `left` of them exist.
+template <typename IO> __device__ __forceinline__ Raw8<IO> load_row8(const RowTensor& t, int64_t row, int c, int left) {
+    return load8(reinterpret_cast<const IO*>(t.p) + row * t.ld + c, left, t.vec && (c & 7) == 0);
+}
+
+__device__ __forceinline__ float step_size(const Ssm& a, float raw, int c) {
+    if (a.bias) raw += a.bias[c];
+    return a.softplus ? softplus(raw) : raw;
+}
+
+// log2(e) A of channels c .. c + DC and states n .. n + 4, channel pairs packed; zero outside.
+template <int DC>
+__device__ __forceinline__ void load_decay(const Ssm& a, int c, int end, int n, F2 (&A2)[4][DC / 2]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < DC / 2; ++i) {
+            float v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int d = c + 2 * i + k;
+                v[k] = d < end && n + j < a.N ? a.A[(int64_t)d * a.N + n + j] * kLog2e : 0.f;
+            }
+            A2[j][i] = pack2(v[0], v[1]);
+        }
+}
+
+// States [d][n] of channels c .. c + DC and states n .. n + 4, to and from memory [D][N].
+template <int DC>
+__device__ __forceinline__ void load_states(const float* p, const Ssm& a, int c, int end, int n, F2 (&h)[4][DC / 2]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < DC / 2; ++i) {
+            float v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int d = c + 2 * i + k;
+                v[k] = p && d < end && n + j < a.N ? p[(int64_t)d * a.N + n + j] : 0.f;
+            }
+            h[j][i] = pack2(v[0], v[1]);
+        }
+}
+template <int DC>
+__device__ __forceinline__ void store_states(float* p, const Ssm& a, int c, int end, int n, const F2 (&h)[4][DC / 2]) {
+#pragma unroll
+    for (int i = 0; i < DC; ++i) {
+        if (c + i >= end) continue;
+        float* q = p + (int64_t)(c + i) * a.N + n;
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = i & 1 ? unpack2(h[j][i / 2]).y : unpack2(h[j][i / 2]).x;
+        if (n + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+            *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < a.N) q[j] = v[j];
+        }
+    }
+}
+
+// B and C of `tokens` tokens from `row`, each value twice (for both halves of a packed product): [t][4 LN][2].
+// Tokens from `live` on read as zero.
+template <typename IO, int LN>
+__device__ __forceinline__ void load_bc(const Ssm& a, const RowTensor& t, int group, int64_t row, int live, int tokens,
+                                        float2* out) {
+    for (int i = threadIdx.x; i < tokens * 4 * LN; i += kSsmThreads) {
+        const int k = i / (4 * LN), n = i % (4 * LN);
+        const float v =
+            k < live && n < a.N ? to_f(reinterpret_cast<const IO*>(t.p)[(row + k) * t.ld + group * a.N + n]) : 0.f;
+        out[i] = make_float2(v, v);
+    }
+}
+
+// Sums over a channel's LN lanes of v[0 .. 4): lane q (of LN) is left with the sum of v[keep4(q)] in v[0] (LN = 2: of
+// v[2 q] and v[2 q + 1] in v[0], v[1]).
+__device__ __forceinline__ int keep4(int q) { return (q & 1) * 2 + (q >> 1 & 1); }
+template <int LN> __device__ __forceinline__ void lanes_sum4(float (&v)[4], int q) {
+    const bool up = q & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float give = up ? v[i] : v[i + 2], keep = up ? v[i + 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+    }
+    if (LN == 2) return;
+    {
+        const bool up2 = q & 2;
+        const float give = up2 ? v[0] : v[1], keep = up2 ? v[1] : v[0];
+        v[0] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+    }
+#pragma unroll
+    for (int o = 4; o < LN; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+}
+
+// Calls f with a value of the io type and the lanes of a channel.
+template <typename F> cudaError_t ssm_types(int io, int N, F f) {
+    const auto lanes = [&](auto v) {
+        if (N <= 8) return f(v, std::integral_constant<int, 2>());
+        if (N <= 16) return f(v, std::integral_constant<int, 4>());
+        if (N <= 32) return f(v, std::integral_constant<int, 8>());
+        return f(v, std::integral_constant<int, 16>());
+    };
+    if (io == GDR_F32) return lanes(float());
+    if (io == GDR_BF16) return lanes(__nv_bfloat16());
+    return lanes(__half());
+}
+
+inline int ssm_lanes(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+inline Ssm ssm_of(const SsmArgs& a, const SsmTensors& t) {
+    Ssm k{};
+    k.q = Seqs{a.cu, a.total, a.T, (int)a.n};
+    k.D = a.D;
+    k.N = a.N;
+    k.G = a.G;
+    k.per = a.D / a.G;
+    k.x = t.x;
+    k.dt = t.dt;
+    k.z = t.z;
+    k.B = t.B;
+    k.C = t.C;
+    k.A = t.A;
+    k.bias = t.bias;
+    k.Dk = t.Dk;
+    k.h0 = t.h0;
+    k.softplus = a.softplus;
+    return k;
+}
+
+}  // namespace layer
+}  // namespace gdr

@@ -13,6 +13,7 @@ The functions mirror the C ABI names:
     gdr_varlen_backward_workspace_bytes,
     gdr_status_string, gdr_get_device_status, gdr_selftest_bounded_wait,
     gdr_last_variant, gdr_version
+(the operators of the layer around the recurrence are bound in layer.py)
 and `forward(...)` / `backward(...)` are the convenience calls that allocate outputs and
 the workspace (and, given CPU tensors, copy them to the GPU and the results back);
 `forward_varlen(...)` / `backward_varlen(...)` the same for packed variable-length sequences.
@@ -44,6 +45,10 @@ EXPORTS = ["gdr_prepare_wy", "gdr_scan_h", "gdr_chunk_output", "gdr_forward", "g
            "gdr_scan_combine", "gdr_scan_combine_reverse", "gdr_forward_segments",
            "gdr_varlen_forward", "gdr_varlen_forward_workspace_bytes", "gdr_varlen_backward",
            "gdr_varlen_backward_workspace_bytes",
+           "gdr_norm_forward", "gdr_norm_backward", "gdr_norm_backward_workspace_bytes",
+           "gdr_conv_forward", "gdr_conv_backward", "gdr_conv_backward_workspace_bytes", "gdr_conv_step",
+           "gdr_delta_step", "gdr_ssm_forward", "gdr_ssm_forward_workspace_bytes", "gdr_ssm_step",
+           "gdr_ssm_backward", "gdr_ssm_backward_workspace_bytes",
            "gdr_status_string", "gdr_get_device_status", "gdr_selftest_bounded_wait", "gdr_last_variant",
            "gdr_version"]
 
@@ -59,6 +64,30 @@ class gdr_problem(ctypes.Structure):
                 ("V", ctypes.c_int64), ("chunk", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
                 ("gate", ctypes.c_int32), ("scale", ctypes.c_float), ("variant", ctypes.c_int32),
                 ("HV", ctypes.c_int64), ("segments", ctypes.c_int32)]
+
+
+class gdr_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("x_ld", ctypes.c_int64), ("res_ld", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("group", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class gdr_conv_problem(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("T", ctypes.c_int64), ("total", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("x_ld", ctypes.c_int64), ("pool", ctypes.c_int64), ("W", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("silu", ctypes.c_int32)]
+
+
+class gdr_step_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("HV", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("V", ctypes.c_int64), ("pool", ctypes.c_int64), ("q_ld", ctypes.c_int64), ("k_ld", ctypes.c_int64),
+                ("v_ld", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class gdr_ssm_problem(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in ("n", "T", "total", "D", "N", "G", "x_ld", "dt_ld", "z_ld", "b_ld",
+                                                    "c_ld", "pool")] + [("io_dtype", ctypes.c_int32),
+                                                                        ("softplus", ctypes.c_int32)]
 
 
 _lib = None
@@ -109,6 +138,19 @@ def load(path: str | None = None):
             "gdr_varlen_forward_workspace_bytes": [P],
             "gdr_varlen_backward": [P, vp, vp, ctypes.c_int64] + [vp] * 14 + [vp, ctypes.c_size_t, vp],
             "gdr_varlen_backward_workspace_bytes": [P],
+            "gdr_norm_forward": [ctypes.POINTER(gdr_norm_problem)] + [vp] * 8,
+            "gdr_norm_backward": [ctypes.POINTER(gdr_norm_problem)] + [vp] * 7 + [ctypes.c_size_t, vp],
+            "gdr_norm_backward_workspace_bytes": [ctypes.POINTER(gdr_norm_problem)],
+            "gdr_conv_forward": [ctypes.POINTER(gdr_conv_problem)] + [vp] * 8,
+            "gdr_conv_backward": [ctypes.POINTER(gdr_conv_problem)] + [vp] * 12 + [ctypes.c_size_t, vp],
+            "gdr_conv_backward_workspace_bytes": [ctypes.POINTER(gdr_conv_problem), ctypes.c_int32],
+            "gdr_conv_step": [ctypes.POINTER(gdr_conv_problem)] + [vp] * 7,
+            "gdr_delta_step": [ctypes.POINTER(gdr_step_problem)] + [vp] * 9,
+            "gdr_ssm_forward": [ctypes.POINTER(gdr_ssm_problem)] + [vp] * 13 + [ctypes.c_size_t, vp],
+            "gdr_ssm_forward_workspace_bytes": [ctypes.POINTER(gdr_ssm_problem), ctypes.c_int32],
+            "gdr_ssm_backward": [ctypes.POINTER(gdr_ssm_problem)] + [vp] * 22 + [ctypes.c_size_t, vp],
+            "gdr_ssm_backward_workspace_bytes": [ctypes.POINTER(gdr_ssm_problem), ctypes.c_int32],
+            "gdr_ssm_step": [ctypes.POINTER(gdr_ssm_problem)] + [vp] * 12,
             "gdr_status_string": [ctypes.c_int],
             "gdr_get_device_status": [vp],
             "gdr_selftest_bounded_wait": [ctypes.c_int32, ctypes.c_int32, vp],
@@ -118,12 +160,7 @@ def load(path: str | None = None):
         for name, args in sig.items():
             f = getattr(lib, name)
             f.argtypes = args
-            f.restype = ctypes.c_int
-        lib.gdr_forward_workspace_bytes.restype = ctypes.c_size_t
-        lib.gdr_forward_host_scratch_bytes.restype = ctypes.c_size_t
-        lib.gdr_backward_workspace_bytes.restype = ctypes.c_size_t
-        lib.gdr_varlen_forward_workspace_bytes.restype = ctypes.c_size_t
-        lib.gdr_varlen_backward_workspace_bytes.restype = ctypes.c_size_t
+            f.restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
         lib.gdr_status_string.restype = ctypes.c_char_p
         lib.gdr_last_variant.restype = ctypes.c_char_p
         if path is None:

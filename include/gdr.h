@@ -557,6 +557,141 @@ GDR_API gdr_status gdr_varlen_backward(const gdr_problem* p, const int32_t* cu_s
                                        const void* d_o, const float* dh_final, void* dq, void* dk, void* dv, float* dg,
                                        void* dbeta, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------- the layer around the recurrence
+ * What a recurrent layer runs before and beside the delta rule: the norm of its
+ * input, the short convolution, a second kind of recurrence (the selective state
+ * space scan), and the single-token forms that decoding needs.  The method pages
+ * have no counterpart to these calls.
+ *
+ * Conventions, beside those at the top of this file:
+ * - A tensor of tokens is [tokens, columns] with the columns contiguous.  Inputs
+ *   that are usually slices of a wider projection have a row stride in elements
+ *   (`*_ld`; 0 means contiguous).  Outputs are contiguous.  These pointers need
+ *   only their element's alignment (GDR_ERR_ALIGN otherwise): rows on 16-byte
+ *   boundaries move in 16-byte pieces, others element by element.  Workspaces are
+ *   256-byte aligned.
+ * - Weights of the norm and the convolution have the io dtype; their gradients
+ *   are fp32, summed in a fixed order: the same call gives the same bits.
+ * - Sequences: a batch of n sequences of T tokens each (cu_seqlens NULL, tokens
+ *   n * T), or n packed ones on a token axis of `total` tokens, sequence s
+ *   holding the tokens cu_seqlens[s] .. cu_seqlens[s+1]-1.  cu_seqlens is DEVICE
+ *   int32 [n + 1], cu[0] = 0, non-decreasing, cu[n] = total; no call reads it on
+ *   the host.  Other values give undefined results, but no access outside the
+ *   tensors.  Empty sequences are allowed; their final state is the initial one.
+ * - Pools: a single-token call takes its states from a pool of `pool` states,
+ *   row i using the state slots[i] (DEVICE int32), in place.  slots NULL means
+ *   state i (rows <= pool).  A slot outside [0, pool) marks a padding row: its
+ *   output is zero, its inputs do not matter and no state changes.  No two rows
+ *   may name the same slot.
+ */
+
+/* The root-mean-square norm: s = x + residual (x where residual is NULL),
+ *     y = s * w / sqrt(mean(s^2) + eps)   over the D columns of each row.
+ * s is kept in fp32 and rounded once into each output:
+ *     r [rows,D] io = s, y [rows,D] io,
+ *     y8 [rows,D] e4m3 = y * (1 / scale), scales fp32 [rows] (group = 0) or [rows, ceil(D/group)],
+ *     scale = max(amax / 448, 2^-126), amax the largest |y| of the row or of its group of columns.
+ * Any of y, r, (y8, scales) may be NULL (not written); not all of them. */
+typedef struct gdr_norm_problem {
+    int64_t rows, D;         /* rows >= 0; 1 <= D <= 32768 */
+    int64_t x_ld, res_ld;
+    int32_t io_dtype;        /* gdr_dtype */
+    int32_t group;           /* columns of a scale: 0 (the row), 32, 64 or 128 */
+    float eps;               /* >= 0, finite */
+} gdr_norm_problem;
+GDR_API gdr_status gdr_norm_forward(const gdr_norm_problem* p, const void* x, const void* residual, const void* w,
+                                    void* y, void* r, void* y8, float* scales, void* stream);
+/* The gradient, from the r that the forward wrote (x without a residual): with rstd = 1/sqrt(mean r^2 + eps), xh = r rstd,
+ *     dx = rstd (w dy - xh mean(w dy xh)) + dr   (io; the gradient of x and of the residual alike)
+ *     dw = sum over rows of dy xh                (fp32 [D])
+ * dr, the gradient that reached r by other ways, may be NULL.  All tensors are contiguous. */
+GDR_API size_t gdr_norm_backward_workspace_bytes(const gdr_norm_problem* p);
+GDR_API gdr_status gdr_norm_backward(const gdr_norm_problem* p, const void* dy, const void* r, const void* w,
+                                     const void* dr, void* dx, float* dw, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* The short causal convolution of each channel, taps w [D,W] io, bias b [D] io or NULL, over the tokens of its sequence:
+ *     y_t = act(b + sum_{j < W} w_j x_{t-W+1+j}),   act = silu or the identity.
+ * Inputs before a sequence's first token are the rows of its state [n,W-1,D] io (oldest first), or zero where
+ * state is NULL.  state_out [n,W-1,D] io or NULL: the last W-1 inputs, from which the sequence goes on.  It may not
+ * overlap state. */
+typedef struct gdr_conv_problem {
+    int64_t n, T, total;     /* n >= 1 sequences (rows of gdr_conv_step); of T >= 1 tokens, or packed on total >= 0 */
+    int64_t D;
+    int64_t x_ld;
+    int64_t pool;            /* gdr_conv_step: states in the pool */
+    int32_t W;               /* taps: 2, 3 or 4 */
+    int32_t io_dtype;
+    int32_t silu;            /* 1: silu, 0: the identity */
+} gdr_conv_problem;
+GDR_API gdr_status gdr_conv_forward(const gdr_conv_problem* p, const int32_t* cu_seqlens, const void* x, const void* w,
+                                    const void* b, const void* state, void* y, void* state_out, void* stream);
+/* The gradient: dy and dx like y; d_state_out [n,W-1,D] io or NULL the gradient of state_out, d_state [n,W-1,D] io
+ * or NULL (not written) that of state; dw [D,W] and db [D] fp32 (both written, also without a bias).  Partial sums of
+ * dw and db lie in the workspace.  packed: whether cu_seqlens will be given. */
+GDR_API size_t gdr_conv_backward_workspace_bytes(const gdr_conv_problem* p, int32_t packed);
+GDR_API gdr_status gdr_conv_backward(const gdr_conv_problem* p, const int32_t* cu_seqlens, const void* x, const void* w,
+                                     const void* b, const void* state, const void* dy, const void* d_state_out,
+                                     void* dx, float* dw, float* db, void* d_state, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+/* One token of n rows: x, y [n,D]; state [pool,W-1,D] io, shifted by the token in place. */
+GDR_API gdr_status gdr_conv_step(const gdr_conv_problem* p, const int32_t* slots, const void* x, const void* w,
+                                 const void* b, void* state, void* y, void* stream);
+
+/* The gated delta rule for one token of each of B rows (the recurrence at the top of this file, T = 1), the states
+ * h [pool,HV,K,V] fp32 changed in place: with D = exp(g) (per head, or per key dimension),
+ *     S~ = D S,  delta = beta (v - S~^T k),  S = S~ + k delta^T,  o = scale S^T q.
+ * q, k [B,H,K], v [B,HV,V], beta [B,HV] io; g [B,HV] or [B,HV,K] fp32; o [B,HV,V] io.  Value head hv reads the q and
+ * k of head hv / (HV / H).  h lies on a 16-byte boundary.  fp32 arithmetic for every io type. */
+typedef struct gdr_step_problem {
+    int64_t B, H, HV, K, V;  /* HV: a multiple of H, 0 means H; K, V in {64, 128} */
+    int64_t pool;
+    int64_t q_ld, k_ld, v_ld;/* between the rows of the batch */
+    int32_t io_dtype;        /* gdr_dtype */
+    int32_t gate;            /* gdr_gate */
+    float scale;             /* <= 0 selects 1/sqrt(K) */
+} gdr_step_problem;
+GDR_API gdr_status gdr_delta_step(const gdr_step_problem* p, const int32_t* slots, const void* q, const void* k,
+                                  const void* v, const float* g, const void* beta, float* h, void* o, void* stream);
+
+/* The selective state space scan, per channel d of group g = d / (D / G) with N states:
+ *     Delta_t = softplus(dt_t + dt_bias)   (dt_t + dt_bias with softplus = 0),
+ *     h_t[n]  = exp(Delta_t A[n]) h_{t-1}[n] + Delta_t x_t B_t[g][n],   h_0 from h0 [n,D,N] fp32 (NULL: zero),
+ *     y_t     = (sum_n C_t[g][n] h_t[n] + Dk x_t) * silu(z_t)           (without Dk, without z: that part left out).
+ * x, dt, z, y: tokens of D channels, io; B, C: tokens of [G,N], io; A [D,N], dt_bias [D], Dk [D] fp32.  A is <= 0 for a
+ * decaying state.  h_final [n,D,N] fp32 or NULL: the state after each sequence's last token.  fp32 arithmetic for every
+ * io type.  A long sequence is scanned in segments at once where that fills the GPU; each segment's state then comes
+ * from its predecessors' in a fixed order, so the result of a call does not change from run to run. */
+typedef struct gdr_ssm_problem {
+    int64_t n, T, total;     /* n >= 1 sequences (rows of gdr_ssm_step); of T >= 1 tokens, or packed on total >= 0 */
+    int64_t D, N, G;         /* channels, states a channel (1 .. 64), groups (D a multiple of G) */
+    int64_t x_ld, dt_ld, z_ld, b_ld, c_ld;
+    int64_t pool;            /* gdr_ssm_step: states in the pool */
+    int32_t io_dtype;        /* gdr_dtype */
+    int32_t softplus;        /* 1 or 0 */
+} gdr_ssm_problem;
+GDR_API size_t gdr_ssm_forward_workspace_bytes(const gdr_ssm_problem* p, int32_t packed);
+GDR_API gdr_status gdr_ssm_forward(const gdr_ssm_problem* p, const int32_t* cu_seqlens, const void* x, const void* dt,
+                                   const float* A, const void* B, const void* C, const float* Dk, const void* z,
+                                   const float* dt_bias, const float* h0, void* y, float* h_final, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+/* The gradient of gdr_ssm_forward's (y, h_final), from its inputs alone: dy like y; dh_final [n,D,N] fp32 or NULL.
+ * dx, ddt (of the raw dt), dB, dC and dz (with z only) like their inputs, contiguous, io; dA [D,N] fp32; dDk, ddt_bias
+ * [D] and dh0 [n,D,N] fp32, each may be NULL (not written).  dB and dC sum over the channels of their group, dA, dDk
+ * and ddt_bias over all tokens, in a fixed order. */
+GDR_API size_t gdr_ssm_backward_workspace_bytes(const gdr_ssm_problem* p, int32_t packed);
+GDR_API gdr_status gdr_ssm_backward(const gdr_ssm_problem* p, const int32_t* cu_seqlens, const void* x, const void* dt,
+                                    const float* A, const void* B, const void* C, const float* Dk, const void* z,
+                                    const float* dt_bias, const float* h0, const void* dy, const float* dh_final,
+                                    void* dx, void* ddt, float* dA, void* dB, void* dC, float* dDk, void* dz,
+                                    float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+/* One token of n rows: x, dt, z, y [n,D], B, C [n,G,N]; h [pool,D,N] fp32, changed in place. */
+GDR_API gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const int32_t* slots, const void* x, const void* dt,
+                                const float* A, const void* B, const void* C, const float* Dk, const void* z,
+                                const float* dt_bias, float* h, void* y, void* stream);
+
 /* Static, human-readable text for a status code. */
 GDR_API const char* gdr_status_string(gdr_status s);
 
