@@ -43,13 +43,48 @@ template <int N, typename IO> __device__ __forceinline__ RawN<IO, N> load_n(cons
     }
     return r;
 }
+// The same for memory that the kernel also writes (not by way of the read-only cache).
+template <int N, typename IO> __device__ __forceinline__ RawN<IO, N> load_own(const IO* p, int64_t left, bool vec) {
+    RawN<IO, N> r;
+    if (vec && left >= N) {
+        if constexpr (sizeof(r) == 8) {
+            *reinterpret_cast<uint2*>(&r) = *reinterpret_cast<const uint2*>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(r) / 16; ++i)
+                reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p)[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.e[i] = i < left ? p[i] : from_f<IO>(0.f);
+    }
+    return r;
+}
 template <typename IO> __device__ __forceinline__ Raw8<IO> load8(const IO* p, int64_t left, bool vec) {
     return load_n<8>(p, left, vec);
 }
 
+// Two neighbours at a time: half the instructions of one by one.
+__device__ __forceinline__ float2 to_f2(const float* p) { return make_float2(p[0], p[1]); }
+__device__ __forceinline__ float2 to_f2(const __nv_bfloat16* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 to_f2(const __half* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
+__device__ __forceinline__ void from_f2(float* p, float a, float b) { p[0] = a, p[1] = b; }
+__device__ __forceinline__ void from_f2(__nv_bfloat16* p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void from_f2(__half* p, float a, float b) {
+    *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
+}
+
 template <typename IO, int N> __device__ __forceinline__ void widen(const RawN<IO, N>& r, float (&x)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f(r.e[i]);
+    for (int i = 0; i < N; i += 2) {
+        const float2 f = to_f2(r.e + i);
+        x[i] = f.x, x[i + 1] = f.y;
+    }
 }
 
 template <typename IO, int N>
@@ -73,7 +108,7 @@ template <typename IO, int N>
 __device__ __forceinline__ void store_n(IO* p, const float (&x)[N], int64_t left, bool vec) {
     RawN<IO, N> r;
 #pragma unroll
-    for (int i = 0; i < N; ++i) r.e[i] = from_f<IO>(x[i]);
+    for (int i = 0; i < N; i += 2) from_f2(r.e + i, x[i], x[i + 1]);
     store_raw(p, r, left, vec);
 }
 
@@ -85,8 +120,43 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 1 / (1 + e^-x): 0 and 1 at the ends of the range, NaN for NaN.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
+
+// Packed fp32: two independent operations an instruction, each rounded as alone.
+using F2 = unsigned long long;   // the lower channel in the low half
+
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN where either is
     float y;

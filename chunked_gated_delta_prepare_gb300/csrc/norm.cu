@@ -4,7 +4,8 @@
 //   y8 = e4m3(y / scale),  scale = max(amax / 448, 2^-126) over the row or over groups of its columns
 //
 // Bound: memory.  A row is read once and stays in registers (up to 4 vectors of 8 columns a thread) between the sum of
-// squares and the output; w stays in registers over all the rows of a block.  A row is held by 32 threads up to 1024
+// squares and the output; w stays in registers over all the rows of a block, and a block's next row is in flight while
+// it works on this one.  A row is held by 32 threads up to 1024
 // columns (four rows a block, sums by shuffles alone), by a block above that.  With fewer rows than the GPU has room
 // for blocks, a row is spread over more threads, one vector each, since then only the latency of one row counts.
 //
@@ -69,8 +70,14 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&y)[8], floa
     }
 }
 
+// Blocks an SM that the register budget of a kernel leaves room for: 1024 threads at two vectors a thread, 512 at four.
+template <int TPR, int VPT> constexpr int blocks_per_sm() {
+    constexpr int threads = VPT > 2 ? 512 : 1024, nt = TPR < 128 ? 128 : TPR;
+    return threads > nt ? threads / nt : 1;
+}
+
 template <typename IO, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, blocks_per_sm<TPR, VPT>())
 norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict__ w, IO* __restrict__ y,
                     IO* __restrict__ r, uint8_t* __restrict__ y8, float* __restrict__ scales, bool vec_w, bool vec_y,
                     bool vec_r, bool vec_8) {
@@ -78,36 +85,43 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
     __shared__ float red[2 * 32], redm[2 * 32];
     const int tid = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const int D = a.D;
-    Raw8<IO> wr[VPT];
+    Raw8<IO> wr[VPT], xr[VPT], sr[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (tid + i * TPR) * 8;
         wr[i] = load8(w + c, D - c, vec_w);
     }
+    const bool two = res.p != nullptr;
+    const auto fetch = [&](int64_t row) {     // a block's last rows may not exist: zeros
+        const IO* xp = reinterpret_cast<const IO*>(x.p) + row * x.ld;
+        const IO* sp = reinterpret_cast<const IO*>(res.p) + row * res.ld;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (tid + i * TPR) * 8, left = row < a.rows ? D - c : 0;
+            xr[i] = load8(xp + c, left, x.vec);
+            if (two) sr[i] = load8(sp + c, left, res.vec);
+        }
+    };
+    fetch((int64_t)blockIdx.x * RPB + slot);
     int turn = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, ++turn) {
         const int64_t row = row0 + slot;
-        const bool live = row < a.rows;       // a block's last rows may not exist; its threads stay for the shuffles
-        const IO* xp = reinterpret_cast<const IO*>(x.p) + row * x.ld;
-        const IO* sp = res.p ? reinterpret_cast<const IO*>(res.p) + row * res.ld : nullptr;
+        const bool live = row < a.rows;       // threads of a row that does not exist stay for the shuffles
         float v[VPT][8], sum[1] = {0.f};
-        Raw8<IO> xr[VPT], sr[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8;
-            xr[i] = load8(xp + c, live ? D - c : 0, x.vec);
-            if (sp) sr[i] = load8(sp + c, live ? D - c : 0, res.vec);
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8;
             widen(xr[i], v[i]);
-            if (sp) {
+            if (two) {
                 float t[8];
                 widen(sr[i], t);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] += t[j];
             }
+        }
+        fetch(row + (int64_t)gridDim.x * RPB);          // in flight while this row is worked on
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (tid + i * TPR) * 8;
             if (r) store_n(r + row * D + c, v[i], live ? D - c : 0, vec_r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
@@ -118,24 +132,24 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * TPR) * 8;
-            float wf[8];
+            float wf[8], m = 0.f;
             widen(wr[i], wf);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] = v[i][j] * rstd * wf[j];
-                if (y8) top[0] = max_nan(top[0], c + j < D ? fabsf(v[i][j]) : 0.f);
+                if (y8) m = max_nan(m, fabsf(v[i][j]));  // zero past the row's end, or NaN in a row of nothing else
             }
             if (y) store_n(y + row * D + c, v[i], live ? D - c : 0, vec_y);
             if (y8 && a.group) {             // a group's columns lie in group / 8 neighbouring threads
-                float m = top[0];
-                top[0] = 0.f;
                 for (int o = a.group / 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float scale = max_nan(m * (1.f / 448.f), 1.17549435e-38f);
                 if (live && c < D) {
                     store_e4m3(y8 + row * D + c, v[i], 1.f / scale, D - c, vec_8);
-                    if (c % a.group == 0) scales[row * ((D + a.group - 1) / a.group) + c / a.group] = scale;
+                    if ((c & (a.group - 1)) == 0)
+                        scales[row * ((D + a.group - 1) / a.group) + c / a.group] = scale;
                 }
             }
+            top[0] = max_nan(top[0], m);
         }
         if (y8 && !a.group) {
             row_reduce<TPR, 1, true>(top, redm, turn);
@@ -153,14 +167,14 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
 }
 
 template <typename IO, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, blocks_per_sm<TPR, VPT>() > 1 ? blocks_per_sm<TPR, VPT>() / 2 : 1)
 norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict__ r, const IO* __restrict__ w,
                      const IO* __restrict__ dr, IO* __restrict__ dx, float* __restrict__ partial, bool vec) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
     __shared__ float red[2 * 2 * 32];
     const int tid = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const int D = a.D;
-    Raw8<IO> wr[VPT];
+    Raw8<IO> wr[VPT], yr[VPT], rr[VPT], er[VPT];
     float dw[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -169,39 +183,48 @@ norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
-    int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, ++turn) {
-        const int64_t row = row0 + slot;
-        const bool live = row < a.rows;
-        Raw8<IO> yr[VPT], rr[VPT], er[VPT];
-        float sum[2] = {0.f, 0.f};            // of s^2 and of w dy s
+    const auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8, left = live ? D - c : 0;
+            const int c = (tid + i * TPR) * 8, left = row < a.rows ? D - c : 0;
             yr[i] = load8(dy + row * D + c, left, vec);
             rr[i] = load8(r + row * D + c, left, vec);
             if (dr) er[i] = load8(dr + row * D + c, left, vec);
         }
+    };
+    fetch((int64_t)blockIdx.x * RPB + slot);
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, ++turn) {
+        const int64_t row = row0 + slot;
+        const bool live = row < a.rows;
+        Raw8<IO> yc[VPT], rc[VPT], ec[VPT];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < VPT; ++i) yc[i] = yr[i], rc[i] = rr[i], ec[i] = er[i];
+        fetch(row + (int64_t)gridDim.x * RPB);          // in flight while this row is worked on
+        float sum[2] = {0.f, 0.f};            // of s^2 and of w dy s
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float s[8], g[8], wf[8];
+            widen(rc[i], s), widen(yc[i], g), widen(wr[i], wf);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float s = to_f(rr[i].e[j]);
-                sum[0] = fmaf(s, s, sum[0]);
-                sum[1] = fmaf(to_f(wr[i].e[j]) * to_f(yr[i].e[j]), s, sum[1]);
+                sum[0] = fmaf(s[j], s[j], sum[0]);
+                sum[1] = fmaf(wf[j] * g[j], s[j], sum[1]);
             }
+        }
         row_reduce<TPR, 2, false>(sum, red, turn);
         const float rstd = rsqrtf(sum[0] / (float)D + a.eps);
         const float back = sum[1] / (float)D * rstd * rstd;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * TPR) * 8;
-            float o[8];
+            float s[8], g[8], wf[8], o[8];
+            widen(rc[i], s), widen(yc[i], g), widen(wr[i], wf);
+            if (dr) widen(ec[i], o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float s = to_f(rr[i].e[j]), g = to_f(yr[i].e[j]);
-                o[j] = rstd * fmaf(-s, back, to_f(wr[i].e[j]) * g) + (dr ? to_f(er[i].e[j]) : 0.f);
-                if (live) dw[i][j] = fmaf(g, s * rstd, dw[i][j]);
+                o[j] = fmaf(rstd, fmaf(-s[j], back, wf[j] * g[j]), dr ? o[j] : 0.f);
+                if (live) dw[i][j] = fmaf(g[j], s[j] * rstd, dw[i][j]);
             }
             if (live) store_n(dx + row * D + c, o, D - c, vec);
         }
@@ -210,9 +233,7 @@ norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (tid + i * TPR) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < D) mine[c + j] = dw[i][j];
+        store_n(mine + c, dw[i], D - c, (D & 3) == 0);
     }
 }
 
@@ -224,7 +245,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
     if (c < cols + cols2) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t i = threadIdx.y; i < rows; i += 32) s += in[i * ld + c];
     }
     part[threadIdx.y][threadIdx.x] = s;
@@ -262,7 +283,7 @@ cudaError_t launch_forward(const NormArgs& a, RowTensor x, RowTensor res, const 
                            float* scales, cudaStream_t s) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1, NT = TPR < 128 ? 128 : TPR;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
-    const int grid = (int)std::min<int64_t>(blocks, (int64_t)kSms * (2048 / NT));
+    const int grid = (int)std::min<int64_t>(blocks, (int64_t)kSms * blocks_per_sm<TPR, VPT>());
     const auto al = [&](const void* p, int unit) {
         return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ((int64_t)a.D * unit) % 16 == 0;
     };
@@ -272,9 +293,10 @@ cudaError_t launch_forward(const NormArgs& a, RowTensor x, RowTensor res, const 
     return cudaGetLastError();
 }
 
+// One wave of the backward's blocks: half the forward's threads an SM, for the sums of dw in registers.
 int64_t backward_grid(const NormArgs& a, Shape h) {
     const int rpb = h.tpr < 128 ? 128 / h.tpr : 1, nt = h.tpr < 128 ? 128 : h.tpr;
-    return std::min<int64_t>((a.rows + rpb - 1) / rpb, (int64_t)kSms * (nt > 512 ? 1 : 512 / nt));
+    return std::min<int64_t>((a.rows + rpb - 1) / rpb, (int64_t)kSms * std::max(1, (h.vpt > 2 ? 256 : 512) / nt));
 }
 
 template <typename IO, int TPR, int VPT>
