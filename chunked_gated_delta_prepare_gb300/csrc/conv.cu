@@ -44,14 +44,6 @@ struct Conv {
     bool vec_w;      // w and b on 16-byte boundaries
 };
 
-template <typename IO> __device__ __forceinline__ void pairs(const RawN<IO, N>& r, F2 (&v)[P]) {
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-        const float2 f = to_f2(r.e + 2 * k);
-        v[k] = pack2(f.x, f.y);
-    }
-}
-
 // Input u of a sequence: a token (u >= 0), a row of its state, or zero.
 template <typename IO>
 __device__ __forceinline__ RawN<IO, N> input_at(const Conv& a, int seq, int64_t start, int64_t u, int64_t c, int back) {

@@ -158,6 +158,25 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
+template <typename IO, int N> __device__ __forceinline__ void pairs(const RawN<IO, N>& r, F2 (&v)[N / 2]) {
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        const float2 f = to_f2(r.e + 2 * k);
+        v[k] = pack2(f.x, f.y);
+    }
+}
+
+__device__ __forceinline__ F2 both(float x) { return pack2(x, x); }
+__device__ __forceinline__ F2 ex2_2(F2 v) {
+    const float2 f = unpack2(v);
+    return pack2(ex2(f.x), ex2(f.y));
+}
+__device__ __forceinline__ F2 rcp_2(F2 v) {
+    const float2 f = unpack2(v);
+    return pack2(rcp(f.x), rcp(f.y));
+}
+__device__ __forceinline__ F2 sigmoid2(F2 x) { return rcp_2(add2(both(1.f), ex2_2(mul2(x, both(-kLog2e))))); }
+
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN where either is
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));

@@ -1,15 +1,18 @@
 // The selective state space scan over prompts and for single tokens (ssm.cuh has the formulas).
 //
 // Bound: an exponential for every token, channel and state, 32 a clock on an SM, and 4 fp32 operations beside it (the
-// exponent's and the input's products, the recurrence, the output's sum), which at 128 a clock cost the same.  A thread
-// keeps 4 channels x 4 states in registers: 16 independent recurrences hide each other's latency, and only 3 shuffles a
-// token join a channel's output.  The inputs of 16 tokens come through shared memory in fp32: softplus, its product
-// with x, and the widening happen once a value and not once a state.
+// exponent's and the input's products, the recurrence, the output's sum), which at 128 a clock cost the same; next come
+// issue slots and the bytes that shared memory returns to registers.  A thread keeps 4 channels x 8 states: 32
+// independent recurrences hide each other's latency, what it reads of a token (Delta and Delta x of its channels, B and C
+// of its states, 96 bytes) serves all of them, and 2 shuffles join its channels' outputs.  (4 x 4 took 96 bytes for half
+// as many and measured 1.3 times the time.)  Products go two states at a time.  The inputs of 8 tokens come through
+// shared memory in fp32: softplus, its product with x, and the widening happen once a value and not once a state.  The
+// next tile's loads are in flight meanwhile.
 //
 // Few sequences and channels leave most of the GPU idle, so a long sequence is cut into segments: a first kernel scans
 // every segment but the last from a zero state and keeps what it leaves and the sum of its Delta (its decay is
-// exp(A sum Delta)); the second starts each segment from its predecessors' states, joined in order, and does the rest.
-// That is twice the work, so a batch that fills the GPU without it is scanned whole.
+// exp(A sum Delta)); a small one joins these in order to the state before each segment; the third scans all segments
+// from there.  That is twice the work, so a batch that fills the GPU without it is scanned whole.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -18,140 +21,303 @@ namespace gdr {
 namespace layer {
 namespace {
 
-constexpr int kTile = 16;          // tokens staged in shared memory
-constexpr int kDC = 4;             // channels of a thread
+constexpr int kThreads = 128;
+constexpr int kTile = 8;           // tokens staged in shared memory
 constexpr int kMinSegment = 64;
+constexpr int kBlocksPerSm = 3;
 
-template <int LN> constexpr int width_of() { return kSsmThreads / LN * kDC; }
+// Channels of a thread (with a lane a channel 4 would make the tiles of a block too wide) and of a block.
+template <int LN> constexpr int channels_of() { return LN == 1 ? 2 : 4; }
+template <int LN> constexpr int width_of() { return kThreads / LN * channels_of<LN>(); }
+
+// Sums over a channel's LN lanes of v[0 .. DC), one for each of DC channels.  Partners halve the channels between them
+// while there is more than one: lane q is left with those from kept(q) on in v[0 .. kKept).
+template <int LN, int DC> struct ChannelSum {
+    static constexpr int kKept = LN >= DC ? 1 : DC / LN;
+    static __device__ __forceinline__ int kept(int q) {
+        int at = 0;
+#pragma unroll
+        for (int m = 1, size = DC / 2; m < LN && size > 0; m *= 2, size /= 2) at += q & m ? size : 0;
+        return at;
+    }
+    static __device__ __forceinline__ void sum(float (&v)[DC], int q) {
+#pragma unroll
+        for (int m = 1, size = DC / 2; m < LN; m *= 2, size /= 2) {
+            if (size == 0) {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+            } else {
+                const bool up = q & m;
+#pragma unroll
+                for (int i = 0; i < DC / 2; ++i) {
+                    if (i >= size) break;
+                    const float give = up ? v[i] : v[i + size], keep = up ? v[i + size] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                }
+            }
+        }
+    }
+};
+
+// 8 states from n of channels c .. c + DC, to and from memory [D][N], neighbours packed; zero outside.
+template <int DC>
+__device__ __forceinline__ void load_states(const float* p, const Ssm& a, int c, int end, int n, F2 (&h)[DC][4]) {
+#pragma unroll
+    for (int i = 0; i < DC; ++i) {
+        const float* q = p + (int64_t)(c + i) * a.N + n;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            if (p && c + i < end && n + j + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+                const float4 f = *reinterpret_cast<const float4*>(q + j);
+                v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+            } else {
+#pragma unroll
+                for (int k = j; k < j + 4; ++k) v[k] = p && c + i < end && n + k < a.N ? q[k] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = pack2(v[2 * j], v[2 * j + 1]);
+    }
+}
+template <int DC>
+__device__ __forceinline__ void store_states(float* p, const Ssm& a, int c, int end, int n, const F2 (&h)[DC][4]) {
+#pragma unroll
+    for (int i = 0; i < DC; ++i) {
+        if (c + i >= end) continue;
+        float* q = p + (int64_t)(c + i) * a.N + n;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            const float2 lo = unpack2(h[i][j / 2]), hi = unpack2(h[i][j / 2 + 1]);
+            if (n + j + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+                *reinterpret_cast<float4*>(q + j) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (n + j + k < a.N) q[j + k] = v[k];
+            }
+        }
+    }
+}
 
 // LOCAL: what each segment with a successor leaves from a zero state, into ends [segment][D][N], and its sum of Delta,
 // into sums [segment][D].  Else: the scan.
 template <typename IO, int LN, bool LOCAL>
-__global__ void __launch_bounds__(kSsmThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* __restrict__ y,
                 float* __restrict__ h_final) {
-    constexpr int W = width_of<LN>(), P = kDC / 2;
-    __shared__ float4 s_delta[kTile * W / 4], s_u[kTile * W / 4];      // Delta (then y), Delta x
-    __shared__ float2 s_b[kTile * 4 * LN], s_c[LOCAL ? 1 : kTile * 4 * LN];
+    constexpr int DC = channels_of<LN>(), W = width_of<LN>(), V8 = W / 8, NP = 8 * LN;
+    constexpr int U = kTile * V8 <= kThreads ? 1 : kTile * V8 / kThreads;     // 8-channel units of a thread
+    constexpr int M = (kTile * NP + kThreads - 1) / kThreads;                 // values of B (and of C) of a thread
+    using Sum = ChannelSum<LN, DC>;
+    __shared__ float4 s_delta[kTile * W / 4], s_u[kTile * W / 4];             // Delta (then y), Delta x
+    __shared__ float4 s_b[kTile * NP / 4], s_c[LOCAL ? 1 : kTile * NP / 4];
+    __shared__ float4 s_bias[W / 4], s_D[W / 4];
     const TileAt at = find_tile(a.q, blockIdx.x, a.seg);
     if (at.seq < 0) return;
     const bool last = (at.tile + 1) * a.seg >= at.len;
     if (LOCAL && last) return;
     const Channels ch = block_channels(a, W);
-    const int q = threadIdx.x % LN, n = 4 * q, own = threadIdx.x / LN * kDC, c = ch.c0 + own;
+    const int q = threadIdx.x % LN, n = 8 * q, own = threadIdx.x / LN * DC, c = ch.c0 + own;
     const int64_t state = (int64_t)a.D * a.N;
+    const int64_t t0 = at.tile * a.seg, t1 = min(t0 + a.seg, at.len);
 
-    F2 A2[4][P], h[4][P], sum[P];
-    load_decay<kDC>(a, c, ch.end, n, A2);
-    load_states<kDC>(LOCAL || !a.h0 ? nullptr : a.h0 + at.seq * state, a, c, ch.end, n, h);
-    if (!LOCAL)
-        for (int64_t s = (int64_t)blockIdx.x - at.tile; s < (int64_t)blockIdx.x; ++s) {
-            F2 e[4][P];
-            load_states<kDC>(ends + s * state, a, c, ch.end, n, e);
+    // Loads of a tile run one tile ahead, those of z from the tile's start.  Unit i of a thread: 8 channels of a token.
+    const int col = threadIdx.x % V8 * 8, cc = ch.c0 + col, tok = threadIdx.x / V8;
+    const bool vec8 = (cc & 7) == 0;
+    Raw8<IO> dt_r[U], x_r[U], x_now[U], z_r[U];
+    IO b_r[M], c_r[M];
+    const auto fetch = [&](int64_t t) {
+        const int64_t row = at.start + t;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float* p = sums + s * a.D + c + 2 * i;
-                const F2 t = pack2(c + 2 * i < ch.end ? p[0] : 0.f, c + 2 * i + 1 < ch.end ? p[1] : 0.f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h[j][i] = fma2(exp2_2(mul2(A2[j][i], t)), h[j][i], e[j][i]);
-            }
+        for (int i = 0; i < U; ++i) {
+            const int k = tok + i * (kThreads / V8), left = t + k < t1 && k < kTile ? ch.end - cc : 0;
+            dt_r[i] = load8(reinterpret_cast<const IO*>(a.dt.p) + (row + k) * a.dt.ld + cc, left, a.dt.vec && vec8);
+            x_r[i] = load8(reinterpret_cast<const IO*>(a.x.p) + (row + k) * a.x.ld + cc, left, a.x.vec && vec8);
         }
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum[i] = 0;
+        for (int i = 0; i < M; ++i) {
+            const int k = (threadIdx.x + i * kThreads) / NP, m = (threadIdx.x + i * kThreads) % NP;
+            const bool in = k < kTile && t + k < t1 && m < a.N;
+            const int at_n = ch.group * a.N + m;
+            b_r[i] = in ? reinterpret_cast<const IO*>(a.B.p)[(row + k) * a.B.ld + at_n] : from_f<IO>(0.f);
+            if (!LOCAL) c_r[i] = in ? reinterpret_cast<const IO*>(a.C.p)[(row + k) * a.C.ld + at_n] : from_f<IO>(0.f);
+        }
+    };
+    fetch(t0);
+    for (int i = threadIdx.x; i < W; i += kThreads) {
+        const bool in = ch.c0 + i < ch.end;
+        reinterpret_cast<float*>(s_bias)[i] = in && a.bias ? a.bias[ch.c0 + i] : 0.f;
+        reinterpret_cast<float*>(s_D)[i] = in && a.Dk ? a.Dk[ch.c0 + i] : 0.f;
+    }
+    F2 A2[DC][4], h[DC][4];
+    float sum[DC];
+    load_states<DC>(a.A, a, c, ch.end, n, A2);
+#pragma unroll
+    for (int i = 0; i < DC; ++i) {
+        sum[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) A2[i][j] = mul2(A2[i][j], pack2(kLog2e, kLog2e));
+    }
+    const float* from = a.h0 ? a.h0 + at.seq * state : nullptr;
+    if (LOCAL) from = nullptr;
+    else if (at.tile > 0) from = ends + blockIdx.x * state;        // ssm_join_kernel has put it there
+    load_states<DC>(from, a, c, ch.end, n, h);
+    __syncthreads();
 
-    const int64_t t0 = at.tile * a.seg, t1 = min(t0 + a.seg, at.len);
     for (int64_t t = t0; t < t1; t += kTile) {
         const int live = (int)min((int64_t)kTile, t1 - t);
         const int64_t row = at.start + t;
-        for (int i = threadIdx.x; i < kTile * W / 8; i += kSsmThreads) {
-            const int k = i / (W / 8), col = i % (W / 8) * 8, cc = ch.c0 + col;
-            const int left = k < live ? ch.end - cc : 0;
-            float d[8], u[8];
-            widen(load_row8<IO>(a.dt, row + k, cc, left), d);
-            widen(load_row8<IO>(a.x, row + k, cc, left), u);
+        {
+            F2 d[U][4], u[U][4];               // all units side by side: their chains hide each other's latency
+            const F2* bias = reinterpret_cast<const F2*>(s_bias) + col / 2;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] = j < left ? step_size(a, d[j], cc + j) : 0.f;      // Delta = 0: the state stays as it is
-                u[j] = j < left ? u[j] * d[j] : 0.f;
+            for (int i = 0; i < U; ++i) {
+                x_now[i] = x_r[i];
+                pairs(dt_r[i], d[i]);
+                pairs(x_r[i], u[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[i][j] = add2(d[i][j], bias[j]);
             }
-            float4* pd = s_delta + (k * W + col) / 4;
-            float4* pu = s_u + (k * W + col) / 4;
-            pd[0] = make_float4(d[0], d[1], d[2], d[3]), pd[1] = make_float4(d[4], d[5], d[6], d[7]);
-            pu[0] = make_float4(u[0], u[1], u[2], u[3]), pu[1] = make_float4(u[4], u[5], u[6], u[7]);
-        }
-        load_bc<IO, LN>(a, a.B, ch.group, row, live, kTile, s_b);
-        if (!LOCAL) load_bc<IO, LN>(a, a.C, ch.group, row, live, kTile, s_c);
-        __syncthreads();
-#pragma unroll 2
-        for (int k = 0; k < live; ++k) {
-            F2 d[P], u[P], b[4], o[P];
-            const F2* pd = reinterpret_cast<const F2*>(s_delta) + (k * W + own) / 2;
-            const F2* pu = reinterpret_cast<const F2*>(s_u) + (k * W + own) / 2;
-            const F2* pb = reinterpret_cast<const F2*>(s_b) + k * 4 * LN + n;
+            if (a.softplus)
 #pragma unroll
-            for (int i = 0; i < P; ++i) d[i] = pd[i], u[i] = pu[i];
+                for (int i = 0; i < U; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[i][j] = softplus2(d[i][j]);
+            if (tok < kTile)
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int at_k = ((tok + i * (kThreads / V8)) * W + col) / 2;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        reinterpret_cast<F2*>(s_delta)[at_k + j] = d[i][j];
+                        reinterpret_cast<F2*>(s_u)[at_k + j] = mul2(u[i][j], d[i][j]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int at_n = threadIdx.x + i * kThreads;
+            if (kTile * NP % kThreads != 0 && at_n >= kTile * NP) break;
+            reinterpret_cast<float*>(s_b)[at_n] = to_f(b_r[i]);
+            if (!LOCAL) reinterpret_cast<float*>(s_c)[at_n] = to_f(c_r[i]);
+        }
+        __syncthreads();
+        if (t + kTile < t1) fetch(t + kTile);
+        if (!LOCAL && a.z.p)
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int k = tok + i * (kThreads / V8);
+                z_r[i] = load8(reinterpret_cast<const IO*>(a.z.p) + (row + k) * a.z.ld + cc, k < live ? ch.end - cc : 0,
+                               a.z.vec && vec8);
+            }
+#pragma unroll 1
+        for (int k = 0; k < live; ++k) {
+            float d[DC], u[DC], v[DC];
+            F2 b[4];
+            const float* pd = reinterpret_cast<const float*>(s_delta) + k * W + own;
+            const float* pu = reinterpret_cast<const float*>(s_u) + k * W + own;
+            const F2* pb = reinterpret_cast<const F2*>(s_b) + (k * NP + n) / 2;
+#pragma unroll
+            for (int i = 0; i < DC; ++i) d[i] = pd[i], u[i] = pu[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) b[j] = pb[j];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int i = 0; i < DC; ++i) {
+                const F2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]);
 #pragma unroll
-                for (int i = 0; i < P; ++i) h[j][i] = fma2(exp2_2(mul2(A2[j][i], d[i])), h[j][i], mul2(u[i], b[j]));
-            if (LOCAL) {
+                for (int j = 0; j < 4; ++j) h[i][j] = fma2(ex2_2(mul2(A2[i][j], dd)), h[i][j], mul2(uu, b[j]));
+                if (LOCAL) sum[i] += d[i];
+            }
+            if (!LOCAL) {
+                const F2* pc = reinterpret_cast<const F2*>(s_c) + (k * NP + n) / 2;
 #pragma unroll
-                for (int i = 0; i < P; ++i) sum[i] = add2(sum[i], d[i]);
-            } else {
-                const F2* pc = reinterpret_cast<const F2*>(s_c) + k * 4 * LN + n;
+                for (int j = 0; j < 4; ++j) b[j] = pc[j];
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    o[i] = mul2(h[0][i], pc[0]);
+                for (int i = 0; i < DC; ++i) {
+                    F2 o = mul2(h[i][0], b[0]);
 #pragma unroll
-                    for (int j = 1; j < 4; ++j) o[i] = fma2(h[j][i], pc[j], o[i]);
+                    for (int j = 1; j < 4; ++j) o = fma2(h[i][j], b[j], o);
+                    const float2 f = unpack2(o);
+                    v[i] = f.x + f.y;
                 }
-                const float2 lo = unpack2(o[0]), hi = unpack2(o[1]);
-                float v[4] = {lo.x, lo.y, hi.x, hi.y};
-                lanes_sum4<LN>(v, q);          // every lane of the channel has read its Delta by now
-                float* out = reinterpret_cast<float*>(s_delta) + k * W + own;
-                if (LN == 2) *reinterpret_cast<float2*>(out + 2 * q) = make_float2(v[0], v[1]);
-                else if (q < 4) out[keep4(q)] = v[0];
+                Sum::sum(v, q);                // every lane of the channel has read its Delta by now
+                if (q < DC)
+#pragma unroll
+                    for (int i = 0; i < Sum::kKept; ++i)
+                        reinterpret_cast<float*>(s_delta)[k * W + own + Sum::kept(q) + i] = v[i];
             }
         }
         __syncthreads();
-        if (!LOCAL) {
-            for (int i = threadIdx.x; i < live * W / 8; i += kSsmThreads) {
-                const int k = i / (W / 8), col = i % (W / 8) * 8, cc = ch.c0 + col, left = ch.end - cc;
-                if (left <= 0) continue;
-                const float4* py = s_delta + (k * W + col) / 4;
-                const float4 y0 = py[0], y1 = py[1];
-                float o[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w}, v[8];
-                if (a.Dk) {
-                    widen(load_row8<IO>(a.x, row + k, cc, left), v);
+        if (!LOCAL && tok < kTile) {           // a thread reads the units that it alone writes next
+            F2 v[U][4], x[4];
+            const F2* D = reinterpret_cast<const F2*>(s_D) + col / 2;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < left) o[j] = fmaf(a.Dk[cc + j], v[j], o[j]);
-                }
-                if (a.z.p) {
-                    widen(load_row8<IO>(a.z, row + k, cc, left), v);
+            for (int i = 0; i < U; ++i) {
+                pairs(x_now[i], x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] *= v[j] * sigmoid(v[j]);
-                }
-                store_n(y + (row + k) * a.D + cc, o, left, a.vec && (cc & 7) == 0);
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = reinterpret_cast<const F2*>(s_delta)[((tok + i * (kThreads / V8)) * W + col) / 2 + j];
+                if (a.Dk)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][j] = fma2(D[j], x[j], v[i][j]);
             }
-            __syncthreads();
+            if (a.z.p)
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    pairs(z_r[i], x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], mul2(x[j], sigmoid2(x[j])));
+                }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int k = tok + i * (kThreads / V8);
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[2 * j] = unpack2(v[i][j]).x, o[2 * j + 1] = unpack2(v[i][j]).y;
+                store_n(y + (row + k) * a.D + cc, o, k < live ? ch.end - cc : 0, a.vec && vec8);
+            }
         }
     }
     if (LOCAL) {
-        store_states<kDC>(ends + blockIdx.x * state, a, c, ch.end, n, h);
+        store_states<DC>(ends + blockIdx.x * state, a, c, ch.end, n, h);
         if (q == 0)
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 f = unpack2(sum[i]);
-                float* p = sums + (int64_t)blockIdx.x * a.D + c + 2 * i;
-                if (c + 2 * i < ch.end) p[0] = f.x;
-                if (c + 2 * i + 1 < ch.end) p[1] = f.y;
-            }
+            for (int i = 0; i < DC; ++i)
+                if (c + i < ch.end) sums[(int64_t)blockIdx.x * a.D + c + i] = sum[i];
     } else if (last && h_final) {
-        store_states<kDC>(h_final + at.seq * state, a, c, ch.end, n, h);
+        store_states<DC>(h_final + at.seq * state, a, c, ch.end, n, h);
     }
+}
+
+// The state before each segment but the first of a sequence, from what the segments leave, in place: ends[s] becomes the
+// state before segment s.  One thread a channel and state, the segments in order, 8 loads in flight.
+__global__ void __launch_bounds__(128) ssm_join_kernel(Ssm a, float* __restrict__ ends, const float* __restrict__ sums) {
+    constexpr int B = 8;
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, state = (int64_t)a.D * a.N;
+    if (i >= state) return;
+    const int d = (int)(i / a.N);
+    int64_t start, len;
+    seq_range(a.q, blockIdx.y, &start, &len);
+    const int64_t first = first_tile(a.q, blockIdx.y, a.seg), count = (len + a.seg - 1) / a.seg;
+    const float A2 = a.A[i] * kLog2e;
+    float h = a.h0 ? a.h0[blockIdx.y * state + i] : 0.f;
+    for (int64_t s0 = 0; s0 + 1 < count; s0 += B) {
+        float e[B], t[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const bool in = s0 + k + 1 < count;
+            e[k] = in ? ends[(first + s0 + k) * state + i] : 0.f;
+            t[k] = in ? sums[(first + s0 + k) * a.D + d] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (s0 + k + 1 >= count) break;
+            if (s0 + k > 0) ends[(first + s0 + k) * state + i] = h;
+            h = fmaf(ex2(A2 * t[k]), h, e[k]);
+        }
+    }
+    if (count > 1) ends[(first + count - 1) * state + i] = h;
 }
 
 // One token of a row: LN lanes a channel, 4 states each, the state read and written once.
@@ -209,16 +375,34 @@ ssm_step_kernel(Ssm a, int64_t pool, const int* __restrict__ slots, float* __res
     }
 }
 
-int blocks_of_channels(const SsmArgs& a, int width) { return a.G * ((a.D / a.G + width - 1) / width); }
+// Calls f with a value of the io type and the lanes of a channel in the scan (8 states each).
+template <typename F> cudaError_t scan_types(int io, int N, F f) {
+    const auto lanes = [&](auto v) {
+        if (N <= 8) return f(v, std::integral_constant<int, 1>());
+        if (N <= 16) return f(v, std::integral_constant<int, 2>());
+        if (N <= 32) return f(v, std::integral_constant<int, 4>());
+        return f(v, std::integral_constant<int, 8>());
+    };
+    if (io == GDR_F32) return lanes(float());
+    if (io == GDR_BF16) return lanes(__nv_bfloat16());
+    return lanes(__half());
+}
 
-// Tokens of a segment.  A batch whose blocks fill the GPU (4 an SM) is scanned whole; anything else is cut into as many
-// segments as give kSms * 8 blocks.
+int blocks_of_channels(const SsmArgs& a) {
+    const int width = a.N <= 8 ? width_of<1>() : a.N <= 16 ? width_of<2>() : a.N <= 32 ? width_of<4>() : width_of<8>();
+    return a.G * ((a.D / a.G + width - 1) / width);
+}
+
+// Tokens of a segment.  A batch whose blocks fill half the GPU is scanned whole; anything else is cut into segments that
+// make one wave of blocks (a few blocks more would take a second wave's time).  Packed sequences have up to n segments
+// beside those of their tokens; the tokens get at least half the wave.
 int segment_of(const SsmArgs& a) {
-    const int64_t width = kSsmThreads / ssm_lanes(a.N) * kDC, blocks = blocks_of_channels(a, (int)width);
-    const int64_t longest = a.cu ? a.total : a.T;
-    int64_t seg = longest;
-    if (a.cu || a.n * blocks < kSms * 4) seg = std::min(longest, a.total * blocks / (kSms * 8) + 1);
-    seg = std::max<int64_t>(seg, kMinSegment);
+    const int64_t blocks = blocks_of_channels(a), wave = kSms * kBlocksPerSm;
+    if (!a.cu && a.n * blocks >= wave / 2) return (int)((a.T + kTile - 1) / kTile * kTile);
+    const int64_t all = std::max<int64_t>(wave / blocks, 1);
+    const int64_t cuts = a.cu ? std::max<int64_t>(all - a.n, (all + 1) / 2) : std::max<int64_t>(all / a.n, 1);
+    const int64_t tokens = a.cu ? a.total : a.T;
+    const int64_t seg = std::max<int64_t>((tokens + cuts - 1) / cuts, kMinSegment);
     return (int)((seg + kTile - 1) / kTile * kTile);
 }
 
@@ -239,15 +423,18 @@ cudaError_t ssm_forward(const SsmArgs& a, const SsmTensors& t, void* y, float* h
     const int64_t segments = tile_count(k.q, k.seg);
     const bool split = ssm_forward_workspace(a) > 0;
     float *ends = workspace, *sums = split ? workspace + segments * a.D * a.N : nullptr;
-    return ssm_types(a.io, a.N, [&](auto io, auto lanes) {
+    return scan_types(a.io, a.N, [&](auto io, auto lanes) {
         using IO = decltype(io);
         constexpr int LN = decltype(lanes)::value;
-        const dim3 grid((unsigned)segments, (unsigned)blocks_of_channels(a, width_of<LN>()));
+        const dim3 grid((unsigned)segments, (unsigned)blocks_of_channels(a));
         if (split) {
-            ssm_scan_kernel<IO, LN, true><<<grid, kSsmThreads, 0, s>>>(k, ends, sums, nullptr, nullptr);
+            ssm_scan_kernel<IO, LN, true><<<grid, kThreads, 0, s>>>(k, ends, sums, nullptr, nullptr);
+            if (cudaError_t e = cudaGetLastError()) return e;
+            const dim3 states((unsigned)(((int64_t)a.D * a.N + 127) / 128), (unsigned)a.n);
+            ssm_join_kernel<<<states, 128, 0, s>>>(k, ends, sums);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
-        ssm_scan_kernel<IO, LN, false><<<grid, kSsmThreads, 0, s>>>(k, ends, sums, (IO*)y, h_final);
+        ssm_scan_kernel<IO, LN, false><<<grid, kThreads, 0, s>>>(k, ends, sums, (IO*)y, h_final);
         return cudaGetLastError();
     });
 }

@@ -16,25 +16,25 @@ namespace layer {
 
 constexpr int kSsmThreads = 128;
 
-// 2^v.  ex2.approx's error is below 2^-22 of the result, and its mean below 1e-8 near 1, where slow decays live.
-__device__ __forceinline__ F2 exp2_2(F2 v) {
-    const float2 f = unpack2(v);
-    return pack2(ex2(f.x), ex2(f.y));
-}
+// exp(Delta A) is ex2 of a product: ex2.approx's error is below 2^-22 of the result, and its mean below 1e-8 near 1, where
+// slow decays live.
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3, by its
 // series to r^13 (what follows is below 2^-23 of the sum): relative accuracy also where e is small, as steps of 0.001
 // need it, at half the instructions of log1pf.
-__device__ __forceinline__ float softplus(float x) {
-    const float e = ex2(-fabsf(x) * kLog2e), r = e * rcp(2.f + e), t = r * r;
-    float s = fmaf(t, 1.f / 13, 1.f / 11);
-    s = fmaf(s, t, 1.f / 9);
-    s = fmaf(s, t, 1.f / 7);
-    s = fmaf(s, t, 1.f / 5);
-    s = fmaf(s, t, 1.f / 3);
-    s = fmaf(s, t, 1.f);
-    return fmaf(2.f * r, s, fmaxf(x, 0.f));      // a NaN comes through r
+__device__ __forceinline__ F2 softplus2(F2 x) {
+    const float2 f = unpack2(x);
+    const F2 e = ex2_2(mul2(pack2(fminf(f.x, -f.x), fminf(f.y, -f.y)), both(kLog2e)));
+    const F2 r = mul2(e, rcp_2(add2(both(2.f), e))), t = mul2(r, r);
+    F2 s = fma2(t, both(1.f / 13), both(1.f / 11));
+    s = fma2(s, t, both(1.f / 9));
+    s = fma2(s, t, both(1.f / 7));
+    s = fma2(s, t, both(1.f / 5));
+    s = fma2(s, t, both(1.f / 3));
+    s = fma2(s, t, both(1.f));
+    return fma2(add2(r, r), s, pack2(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));      // a NaN comes through r
 }
+__device__ __forceinline__ float softplus(float x) { return unpack2(softplus2(both(x))).x; }
 
 // The operator as the kernels take it.
 struct Ssm {
@@ -135,24 +135,25 @@ __device__ __forceinline__ void load_bc(const Ssm& a, const RowTensor& t, int gr
     }
 }
 
-// Sums over a channel's LN lanes of v[0 .. 4): lane q (of LN) is left with the sum of v[keep4(q)] in v[0] (LN = 2: of
-// v[2 q] and v[2 q + 1] in v[0], v[1]).
-__device__ __forceinline__ int keep4(int q) { return (q & 1) * 2 + (q >> 1 & 1); }
-template <int LN> __device__ __forceinline__ void lanes_sum4(float (&v)[4], int q) {
-    const bool up = q & 1;
+// Sums over a channel's LN lanes of v[0 .. DC), one for each of DC channels: lane q < DC is left with the sum of channel
+// kept<DC>(q) in v[0].  Partners halve the channels between them while there is more than one.
+template <int DC> __device__ __forceinline__ int kept(int q) { return DC == 2 ? q & 1 : (q & 1) * 2 + (q >> 1 & 1); }
+template <int LN, int DC> __device__ __forceinline__ void lanes_sum(float (&v)[DC], int q) {
+    static_assert(LN >= DC, "a lane for each channel");
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float give = up ? v[i] : v[i + 2], keep = up ? v[i + 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-    }
-    if (LN == 2) return;
-    {
-        const bool up2 = q & 2;
-        const float give = up2 ? v[0] : v[1], keep = up2 ? v[1] : v[0];
-        v[0] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-    }
+    for (int size = DC / 2, m = 1; m < LN; size /= 2, m *= 2) {
+        if (size == 0) {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+        } else {
+            const bool up = q & m;
 #pragma unroll
-    for (int o = 4; o < LN; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            for (int i = 0; i < DC / 2; ++i) {
+                if (i >= size) break;
+                const float give = up ? v[i] : v[i + size], keep = up ? v[i + size] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+            }
+        }
+    }
 }
 
 // Calls f with a value of the io type and the lanes of a channel.

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_backward_local_kernel(Ssm a, 
                 sum[i] = add2(sum[i], pd[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const F2 e = exp2_2(mul2(A2[j][i], pd[i]));
+                    const F2 e = ex2_2(mul2(A2[j][i], pd[i]));
                     h[j][i] = fma2(e, h[j][i], mul2(pu[i], pb[j]));
                     if (back) {
                         grown[j][i] = mul2(grown[j][i], e);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) ssm_backward_kernel(Ssm a, Gra
             F2 e[4][1];
             load_states<kDC>(add + s * state, a, c, ch.end, n, e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j][0] = fma2(exp2_2(mul2(A2[j][0], t)), v[j][0], e[j][0]);
+            for (int j = 0; j < 4; ++j) v[j][0] = fma2(ex2_2(mul2(A2[j][0], t)), v[j][0], e[j][0]);
         };
         for (int64_t s = first + segments - 1; s > (int64_t)blockIdx.x; --s) through(s, dh, w.dends);
         F2 start[4][1];                                // the state before a later segment, over its local checkpoints
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) ssm_backward_kernel(Ssm a, Gra
                 const float* p = w.csum + ck * a.D + c;
                 const F2 s = pack2(c < ch.end ? p[0] : 0.f, c + 1 < ch.end ? p[1] : 0.f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h0[j][0] = fma2(exp2_2(mul2(A2[j][0], s)), start[j][0], h0[j][0]);
+                for (int j = 0; j < 4; ++j) h0[j][0] = fma2(ex2_2(mul2(A2[j][0], s)), start[j][0], h0[j][0]);
             }
             load_chunk<IO, W>(a, o.dy, ch, row, live, s_delta, s_u, s_g);
             load_bc<IO, LN>(a, a.B, ch.group, row, live, kChunk, s_b);
@@ -253,14 +253,14 @@ __global__ void __launch_bounds__(kSsmThreads, 3) ssm_backward_kernel(Ssm a, Gra
                     for (int k = 0; k < kHalf; ++k)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            hs[0][j] = fma2(exp2_2(mul2(A2[j][0], pd[k * W / 2])), hs[0][j],
+                            hs[0][j] = fma2(ex2_2(mul2(A2[j][0], pd[k * W / 2])), hs[0][j],
                                             mul2(pu[k * W / 2], pb[k * 4 * LN + j]));
                 const int base = half * kHalf;
 #pragma unroll
                 for (int k = 0; k < kHalf; ++k)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        hs[k + 1][j] = fma2(exp2_2(mul2(A2[j][0], pd[(base + k) * W / 2])), hs[k][j],
+                        hs[k + 1][j] = fma2(ex2_2(mul2(A2[j][0], pd[(base + k) * W / 2])), hs[k][j],
                                             mul2(pu[(base + k) * W / 2], pb[(base + k) * 4 * LN + j]));
 #pragma unroll
                 for (int k = kHalf - 1; k >= 0; --k) {
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) ssm_backward_kernel(Ssm a, Gra
                     float v[8];                        // sums over d: dB, dC
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const F2 e = exp2_2(mul2(A2[j][0], d)), b = pb[bc_k + j], cc = pc[bc_k + j];
+                        const F2 e = ex2_2(mul2(A2[j][0], d)), b = pb[bc_k + j], cc = pc[bc_k + j];
                         dh[j][0] = fma2(g, cc, dh[j][0]);
                         y = fma2(hs[k + 1][j], cc, y);
                         r = fma2(dh[j][0], b, r);
