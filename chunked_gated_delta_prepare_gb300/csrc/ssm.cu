@@ -58,48 +58,6 @@ template <int LN, int DC> struct ChannelSum {
     }
 };
 
-// 8 states from n of channels c .. c + DC, to and from memory [D][N], neighbours packed; zero outside.
-template <int DC>
-__device__ __forceinline__ void load_states(const float* p, const Ssm& a, int c, int end, int n, F2 (&h)[DC][4]) {
-#pragma unroll
-    for (int i = 0; i < DC; ++i) {
-        const float* q = p + (int64_t)(c + i) * a.N + n;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            if (p && c + i < end && n + j + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-                const float4 f = *reinterpret_cast<const float4*>(q + j);
-                v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
-            } else {
-#pragma unroll
-                for (int k = j; k < j + 4; ++k) v[k] = p && c + i < end && n + k < a.N ? q[k] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[i][j] = pack2(v[2 * j], v[2 * j + 1]);
-    }
-}
-template <int DC>
-__device__ __forceinline__ void store_states(float* p, const Ssm& a, int c, int end, int n, const F2 (&h)[DC][4]) {
-#pragma unroll
-    for (int i = 0; i < DC; ++i) {
-        if (c + i >= end) continue;
-        float* q = p + (int64_t)(c + i) * a.N + n;
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            const float2 lo = unpack2(h[i][j / 2]), hi = unpack2(h[i][j / 2 + 1]);
-            if (n + j + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-                *reinterpret_cast<float4*>(q + j) = make_float4(lo.x, lo.y, hi.x, hi.y);
-            } else {
-                const float v[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (n + j + k < a.N) q[j + k] = v[k];
-            }
-        }
-    }
-}
-
 // LOCAL: what each segment with a successor leaves from a zero state, into ends [segment][D][N], and its sum of Delta,
 // into sums [segment][D].  Else: the scan.
 template <typename IO, int LN, bool LOCAL>
@@ -152,17 +110,13 @@ ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* _
     }
     F2 A2[DC][4], h[DC][4];
     float sum[DC];
-    load_states<DC>(a.A, a, c, ch.end, n, A2);
+    load_decay<DC, 8>(a, c, ch.end, n, A2);
 #pragma unroll
-    for (int i = 0; i < DC; ++i) {
-        sum[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) A2[i][j] = mul2(A2[i][j], pack2(kLog2e, kLog2e));
-    }
+    for (int i = 0; i < DC; ++i) sum[i] = 0.f;
     const float* from = a.h0 ? a.h0 + at.seq * state : nullptr;
     if (LOCAL) from = nullptr;
     else if (at.tile > 0) from = ends + blockIdx.x * state;        // ssm_join_kernel has put it there
-    load_states<DC>(from, a, c, ch.end, n, h);
+    load_states<DC, 8>(from, a, c, ch.end, n, h);
     __syncthreads();
 
     for (int64_t t = t0; t < t1; t += kTile) {
@@ -280,44 +234,53 @@ ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* _
         }
     }
     if (LOCAL) {
-        store_states<DC>(ends + blockIdx.x * state, a, c, ch.end, n, h);
+        store_states<DC, 8>(ends + blockIdx.x * state, a, c, ch.end, n, h);
         if (q == 0)
 #pragma unroll
             for (int i = 0; i < DC; ++i)
                 if (c + i < ch.end) sums[(int64_t)blockIdx.x * a.D + c + i] = sum[i];
     } else if (last && h_final) {
-        store_states<DC>(h_final + at.seq * state, a, c, ch.end, n, h);
+        store_states<DC, 8>(h_final + at.seq * state, a, c, ch.end, n, h);
     }
 }
 
-// The state before each segment but the first of a sequence, from what the segments leave, in place: ends[s] becomes the
-// state before segment s.  One thread a channel and state, the segments in order, 8 loads in flight.
-__global__ void __launch_bounds__(128) ssm_join_kernel(Ssm a, float* __restrict__ ends, const float* __restrict__ sums) {
+// One thread a channel and state, the segments of blockIdx.y's sequence in order, 8 loads in flight.  blockIdx.z = 0:
+// ends, forward; 1: dends, backward (see ssm_join).
+__global__ void __launch_bounds__(128)
+ssm_join_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ dends, const float* __restrict__ sums,
+                const float* __restrict__ dh_final, bool first_whole) {
     constexpr int B = 8;
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, state = (int64_t)a.D * a.N;
     if (i >= state) return;
     const int d = (int)(i / a.N);
+    const int seq = a.first_seq + blockIdx.y;
     int64_t start, len;
-    seq_range(a.q, blockIdx.y, &start, &len);
-    const int64_t first = first_tile(a.q, blockIdx.y, a.seg), count = (len + a.seg - 1) / a.seg;
+    seq_range(a.q, seq, &start, &len);
+    const int64_t first = first_tile(a.q, seq, a.seg), count = (len + a.seg - 1) / a.seg;
+    if (count < 2) return;
+    const bool back = blockIdx.z == 1;
     const float A2 = a.A[i] * kLog2e;
-    float h = a.h0 ? a.h0[blockIdx.y * state + i] : 0.f;
+    float* v = back ? dends : ends;
+    const float* from = back ? dh_final : a.h0;
+    float h = from ? from[seq * state + i] : 0.f;
+    // step s: the value at segment `at(s)` becomes h, then h goes through that segment; the last needs no step
+    const auto at = [&](int64_t s) { return first + (back ? count - 1 - s : s); };
     for (int64_t s0 = 0; s0 + 1 < count; s0 += B) {
         float e[B], t[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
             const bool in = s0 + k + 1 < count;
-            e[k] = in ? ends[(first + s0 + k) * state + i] : 0.f;
-            t[k] = in ? sums[(first + s0 + k) * a.D + d] : 0.f;
+            e[k] = in ? v[at(s0 + k) * state + i] : 0.f;
+            t[k] = in ? sums[at(s0 + k) * a.D + d] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < B; ++k) {
             if (s0 + k + 1 >= count) break;
-            if (s0 + k > 0) ends[(first + s0 + k) * state + i] = h;
-            h = fmaf(ex2(A2 * t[k]), h, e[k]);
+            v[at(s0 + k) * state + i] = h;
+            h = first_whole && !back && s0 + k == 0 ? e[k] : fmaf(ex2(A2 * t[k]), h, e[k]);
         }
     }
-    if (count > 1) ends[(first + count - 1) * state + i] = h;
+    v[at(count - 1) * state + i] = h;
 }
 
 // One token of a row: LN lanes a channel, 4 states each, the state read and written once.
@@ -375,29 +338,20 @@ ssm_step_kernel(Ssm a, int64_t pool, const int* __restrict__ slots, float* __res
     }
 }
 
-// Calls f with a value of the io type and the lanes of a channel in the scan (8 states each).
-template <typename F> cudaError_t scan_types(int io, int N, F f) {
-    const auto lanes = [&](auto v) {
-        if (N <= 8) return f(v, std::integral_constant<int, 1>());
-        if (N <= 16) return f(v, std::integral_constant<int, 2>());
-        if (N <= 32) return f(v, std::integral_constant<int, 4>());
-        return f(v, std::integral_constant<int, 8>());
-    };
-    if (io == GDR_F32) return lanes(float());
-    if (io == GDR_BF16) return lanes(__nv_bfloat16());
-    return lanes(__half());
-}
-
-int blocks_of_channels(const SsmArgs& a) {
-    const int width = a.N <= 8 ? width_of<1>() : a.N <= 16 ? width_of<2>() : a.N <= 32 ? width_of<4>() : width_of<8>();
-    return a.G * ((a.D / a.G + width - 1) / width);
+int width_at(int N) {
+    switch (ssm_lanes(N, 8)) {
+        case 1: return width_of<1>();
+        case 2: return width_of<2>();
+        case 4: return width_of<4>();
+        default: return width_of<8>();
+    }
 }
 
 // Tokens of a segment.  A batch whose blocks fill half the GPU is scanned whole; anything else is cut into segments that
 // make one wave of blocks (a few blocks more would take a second wave's time).  Packed sequences have up to n segments
 // beside those of their tokens; the tokens get at least half the wave.
 int segment_of(const SsmArgs& a) {
-    const int64_t blocks = blocks_of_channels(a), wave = kSms * kBlocksPerSm;
+    const int64_t blocks = ssm_blocks(a, width_at(a.N)), wave = kSms * kBlocksPerSm;
     if (!a.cu && a.n * blocks >= wave / 2) return (int)((a.T + kTile - 1) / kTile * kTile);
     const int64_t all = std::max<int64_t>(wave / blocks, 1);
     const int64_t cuts = a.cu ? std::max<int64_t>(all - a.n, (all + 1) / 2) : std::max<int64_t>(all / a.n, 1);
@@ -407,6 +361,20 @@ int segment_of(const SsmArgs& a) {
 }
 
 }  // namespace
+
+cudaError_t ssm_join(const Ssm& a, float* ends, float* dends, const float* sums, const float* dh_final, bool first_whole,
+                     cudaStream_t s) {
+    const int64_t states = (int64_t)a.D * a.N;
+    // sequences are one extent of a grid of at most 65535: more go in several launches
+    for (int n0 = 0; n0 < a.q.n; n0 += 65535) {
+        Ssm k = a;
+        k.first_seq = n0;
+        const dim3 grid((unsigned)((states + 127) / 128), (unsigned)std::min(a.q.n - n0, 65535), dends ? 2 : 1);
+        ssm_join_kernel<<<grid, 128, 0, s>>>(k, ends, dends, sums, dh_final, first_whole);
+        if (cudaError_t e = cudaGetLastError()) return e;
+    }
+    return cudaSuccess;
+}
 
 size_t ssm_forward_workspace(const SsmArgs& a) {
     const int seg = segment_of(a);
@@ -423,16 +391,14 @@ cudaError_t ssm_forward(const SsmArgs& a, const SsmTensors& t, void* y, float* h
     const int64_t segments = tile_count(k.q, k.seg);
     const bool split = ssm_forward_workspace(a) > 0;
     float *ends = workspace, *sums = split ? workspace + segments * a.D * a.N : nullptr;
-    return scan_types(a.io, a.N, [&](auto io, auto lanes) {
+    return ssm_types<8>(a.io, a.N, [&](auto io, auto lanes) {
         using IO = decltype(io);
         constexpr int LN = decltype(lanes)::value;
-        const dim3 grid((unsigned)segments, (unsigned)blocks_of_channels(a));
+        const dim3 grid((unsigned)segments, (unsigned)ssm_blocks(a, width_at(a.N)));
         if (split) {
             ssm_scan_kernel<IO, LN, true><<<grid, kThreads, 0, s>>>(k, ends, sums, nullptr, nullptr);
             if (cudaError_t e = cudaGetLastError()) return e;
-            const dim3 states((unsigned)(((int64_t)a.D * a.N + 127) / 128), (unsigned)a.n);
-            ssm_join_kernel<<<states, 128, 0, s>>>(k, ends, sums);
-            if (cudaError_t e = cudaGetLastError()) return e;
+            if (cudaError_t e = ssm_join(k, ends, nullptr, sums, nullptr, false, s)) return e;
         }
         ssm_scan_kernel<IO, LN, false><<<grid, kThreads, 0, s>>>(k, ends, sums, (IO*)y, h_final);
         return cudaGetLastError();
@@ -442,7 +408,7 @@ cudaError_t ssm_forward(const SsmArgs& a, const SsmTensors& t, void* y, float* h
 cudaError_t ssm_step(const SsmArgs& a, const SsmTensors& t, int64_t pool, const int* slots, float* h, void* y,
                      cudaStream_t s) {
     const Ssm k = ssm_of(a, t);
-    return ssm_types(a.io, a.N, [&](auto io, auto lanes) {
+    return ssm_types<4>(a.io, a.N, [&](auto io, auto lanes) {
         using IO = decltype(io);
         constexpr int LN = decltype(lanes)::value, per = 256 / LN;
         ssm_step_kernel<IO, LN><<<dim3((unsigned)a.n, (unsigned)((a.D + per - 1) / per)), 256, 0, s>>>(k, pool, slots, h,

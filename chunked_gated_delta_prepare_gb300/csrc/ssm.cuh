@@ -3,8 +3,8 @@
 //   h_t[d][n] = exp(Delta_t[d] A[d][n]) h_{t-1}[d][n] + Delta_t[d] x_t[d] B_t[g][n],   Delta = softplus(dt + bias)
 //   y_t[d]    = (sum_n C_t[g][n] h_t[d][n] + Dk[d] x_t[d]) silu(z_t[d])
 //
-// A channel's states lie on LN neighbouring lanes, 4 on each (N <= 4 LN, the rest zero), a lane takes DC neighbouring
-// channels.  Products go two channels at a time through the packed fp32 instructions: two independent fp32 operations
+// A channel's states lie on LN neighbouring lanes, NS (4 or 8) on each, the rest zero; a lane takes DC neighbouring
+// channels.  Products go two states at a time through the packed fp32 instructions: two independent fp32 operations
 // each, rounded as alone.
 #pragma once
 
@@ -13,8 +13,6 @@
 
 namespace gdr {
 namespace layer {
-
-constexpr int kSsmThreads = 128;
 
 // exp(Delta A) is ex2 of a product: ex2.approx's error is below 2^-22 of the result, and its mean below 1e-8 near 1, where
 // slow decays live.
@@ -41,6 +39,7 @@ struct Ssm {
     Seqs q;
     int D, N, G, per;        // per = D / G channels share the B and C of a group
     int seg;                 // tokens of a segment
+    int first_seq;           // ssm_join: sequence of the grid's first row
     RowTensor x, dt, z, B, C;
     const float *A, *bias, *Dk, *h0;
     bool softplus;
@@ -49,20 +48,16 @@ struct Ssm {
 
 // The channels of a block: [c0, end) of one group.
 struct Channels {
-    int group, c0, end;
+    int group, block, c0, end;
 };
 __device__ __forceinline__ Channels block_channels(const Ssm& a, int width) {
     const int blocks = (a.per + width - 1) / width;
     Channels c;
     c.group = blockIdx.y / blocks;
-    c.c0 = c.group * a.per + (blockIdx.y - c.group * blocks) * width;
+    c.block = blockIdx.y - c.group * blocks;
+    c.c0 = c.group * a.per + c.block * width;
     c.end = (c.group + 1) * a.per;
     return c;
-}
-
-// 8 channels from c of a token's row; `left` of them exist.
-template <typename IO> __device__ __forceinline__ Raw8<IO> load_row8(const RowTensor& t, int64_t row, int c, int left) {
-    return load8(reinterpret_cast<const IO*>(t.p) + row * t.ld + c, left, t.vec && (c & 7) == 0);
 }
 
 __device__ __forceinline__ float step_size(const Ssm& a, float raw, int c) {
@@ -70,106 +65,82 @@ __device__ __forceinline__ float step_size(const Ssm& a, float raw, int c) {
     return a.softplus ? softplus(raw) : raw;
 }
 
-// log2(e) A of channels c .. c + DC and states n .. n + 4, channel pairs packed; zero outside.
-template <int DC>
-__device__ __forceinline__ void load_decay(const Ssm& a, int c, int end, int n, F2 (&A2)[4][DC / 2]) {
+// NS states from n of channels c .. c + DC, to and from memory [D][N], neighbours packed; zero outside.
+template <int DC, int NS>
+__device__ __forceinline__ void load_states(const float* p, const Ssm& a, int c, int end, int n, F2 (&h)[DC][NS / 2]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < DC; ++i) {
+        const float* q = p + (int64_t)(c + i) * a.N + n;
+        float v[NS];
 #pragma unroll
-        for (int i = 0; i < DC / 2; ++i) {
-            float v[2];
+        for (int j = 0; j < NS; j += 4) {
+            if (p && c + i < end && n + j + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+                const float4 f = *reinterpret_cast<const float4*>(q + j);
+                v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+            } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int d = c + 2 * i + k;
-                v[k] = d < end && n + j < a.N ? a.A[(int64_t)d * a.N + n + j] * kLog2e : 0.f;
+                for (int k = j; k < j + 4; ++k) v[k] = p && c + i < end && n + k < a.N ? q[k] : 0.f;
             }
-            A2[j][i] = pack2(v[0], v[1]);
         }
+#pragma unroll
+        for (int j = 0; j < NS / 2; ++j) h[i][j] = pack2(v[2 * j], v[2 * j + 1]);
+    }
 }
-
-// States [d][n] of channels c .. c + DC and states n .. n + 4, to and from memory [D][N].
-template <int DC>
-__device__ __forceinline__ void load_states(const float* p, const Ssm& a, int c, int end, int n, F2 (&h)[4][DC / 2]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < DC / 2; ++i) {
-            float v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int d = c + 2 * i + k;
-                v[k] = p && d < end && n + j < a.N ? p[(int64_t)d * a.N + n + j] : 0.f;
-            }
-            h[j][i] = pack2(v[0], v[1]);
-        }
-}
-template <int DC>
-__device__ __forceinline__ void store_states(float* p, const Ssm& a, int c, int end, int n, const F2 (&h)[4][DC / 2]) {
+template <int DC, int NS>
+__device__ __forceinline__ void store_states(float* p, const Ssm& a, int c, int end, int n, const F2 (&h)[DC][NS / 2]) {
 #pragma unroll
     for (int i = 0; i < DC; ++i) {
         if (c + i >= end) continue;
         float* q = p + (int64_t)(c + i) * a.N + n;
-        float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = i & 1 ? unpack2(h[j][i / 2]).y : unpack2(h[j][i / 2]).x;
-        if (n + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-            *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
+        for (int j = 0; j < NS; j += 4) {
+            const float2 lo = unpack2(h[i][j / 2]), hi = unpack2(h[i][j / 2 + 1]);
+            if (n + j + 4 <= a.N && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+                *reinterpret_cast<float4*>(q + j) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                const float v[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j < a.N) q[j] = v[j];
-        }
-    }
-}
-
-// B and C of `tokens` tokens from `row`, each value twice (for both halves of a packed product): [t][4 LN][2].
-// Tokens from `live` on read as zero.
-template <typename IO, int LN>
-__device__ __forceinline__ void load_bc(const Ssm& a, const RowTensor& t, int group, int64_t row, int live, int tokens,
-                                        float2* out) {
-    for (int i = threadIdx.x; i < tokens * 4 * LN; i += kSsmThreads) {
-        const int k = i / (4 * LN), n = i % (4 * LN);
-        const float v =
-            k < live && n < a.N ? to_f(reinterpret_cast<const IO*>(t.p)[(row + k) * t.ld + group * a.N + n]) : 0.f;
-        out[i] = make_float2(v, v);
-    }
-}
-
-// Sums over a channel's LN lanes of v[0 .. DC), one for each of DC channels: lane q < DC is left with the sum of channel
-// kept<DC>(q) in v[0].  Partners halve the channels between them while there is more than one.
-template <int DC> __device__ __forceinline__ int kept(int q) { return DC == 2 ? q & 1 : (q & 1) * 2 + (q >> 1 & 1); }
-template <int LN, int DC> __device__ __forceinline__ void lanes_sum(float (&v)[DC], int q) {
-    static_assert(LN >= DC, "a lane for each channel");
-#pragma unroll
-    for (int size = DC / 2, m = 1; m < LN; size /= 2, m *= 2) {
-        if (size == 0) {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-        } else {
-            const bool up = q & m;
-#pragma unroll
-            for (int i = 0; i < DC / 2; ++i) {
-                if (i >= size) break;
-                const float give = up ? v[i] : v[i + size], keep = up ? v[i + size] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                for (int k = 0; k < 4; ++k)
+                    if (n + j + k < a.N) q[j + k] = v[k];
             }
         }
     }
 }
 
-// Calls f with a value of the io type and the lanes of a channel.
-template <typename F> cudaError_t ssm_types(int io, int N, F f) {
+// log2(e) A of the same channels and states.
+template <int DC, int NS>
+__device__ __forceinline__ void load_decay(const Ssm& a, int c, int end, int n, F2 (&A2)[DC][NS / 2]) {
+    load_states<DC, NS>(a.A, a, c, end, n, A2);
+#pragma unroll
+    for (int i = 0; i < DC; ++i)
+#pragma unroll
+        for (int j = 0; j < NS / 2; ++j) A2[i][j] = mul2(A2[i][j], both(kLog2e));
+}
+
+// Joins the segments of each sequence, in place.  ends: what a segment leaves from a zero state (first_whole: the first
+// one from h0) becomes the state before it, h0 before the first.  dends (may be nullptr): the gradient that a segment's
+// tokens send to the state before it becomes the gradient of the state after it, dh_final after the last.  sums: a
+// segment's sums of Delta.  Sequences of one segment are left alone.
+cudaError_t ssm_join(const Ssm& a, float* ends, float* dends, const float* sums, const float* dh_final, bool first_whole,
+                     cudaStream_t s);
+
+// Calls f with a value of the io type and the lanes of a channel, NS states on each.
+template <int NS, typename F> cudaError_t ssm_types(int io, int N, F f) {
     const auto lanes = [&](auto v) {
-        if (N <= 8) return f(v, std::integral_constant<int, 2>());
-        if (N <= 16) return f(v, std::integral_constant<int, 4>());
-        if (N <= 32) return f(v, std::integral_constant<int, 8>());
-        return f(v, std::integral_constant<int, 16>());
+        if (N <= 8) return f(v, std::integral_constant<int, 8 / NS>());
+        if (N <= 16) return f(v, std::integral_constant<int, 16 / NS>());
+        if (N <= 32) return f(v, std::integral_constant<int, 32 / NS>());
+        return f(v, std::integral_constant<int, 64 / NS>());
     };
     if (io == GDR_F32) return lanes(float());
     if (io == GDR_BF16) return lanes(__nv_bfloat16());
     return lanes(__half());
 }
 
-inline int ssm_lanes(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+inline int ssm_lanes(int64_t N, int NS) { return (N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64) / NS; }
+
+// Blocks of `width` channels in all groups.
+inline int64_t ssm_blocks(const SsmArgs& a, int width) { return a.G * ((int64_t)(a.D / a.G + width - 1) / width); }
 
 inline Ssm ssm_of(const SsmArgs& a, const SsmTensors& t) {
     Ssm k{};

@@ -1,7 +1,6 @@
 // The gradient of the selective state space scan (ssm.cuh has the forward's formulas), from its inputs alone.
 //
-// With g_t = dy_t silu(z_t), a_t = exp(Delta_t A) and dh_t the gradient of h_t (sums over channels d of a group and
-// states n written out):
+// With g_t = dy_t silu(z_t), a_t = exp(Delta_t A) and dh_t the gradient of h_t:
 //   dh_t = g_t C_t + a_{t+1} dh_{t+1}
 //   dC_t[n] = sum_d g_t h_t          dB_t[n] = sum_d dh_t Delta_t x_t
 //   r_t = sum_n dh_t B_t             w_t = dh_t a_t h_{t-1}           (the gradient of log a_t)
@@ -11,15 +10,15 @@
 // The reverse walk needs every h_t.  A first kernel scans forward and keeps the state before each chunk of 16 tokens (a
 // quarter of a byte a token for every byte of state).  The main kernel takes the chunks of a segment from the last to
 // the first; it forms the 8 states of half a chunk again, in registers, and walks back over them: 2.5 exponentials an
-// element beside the first kernel's one, no state through shared memory.  Segments as in the forward: the first kernel
-// scans each from a zero state and in the same walk sums what the gradient at the segment's start gets from its own
-// tokens (the decays multiplied up so far are all that takes); the main kernel joins both over the other segments.
+// element beside the first kernel's one, and no state passes through shared memory.  Segments as in the forward: the
+// first kernel scans each from a zero state and in the same walk sums what its tokens send to the state before it (the
+// decays multiplied up so far are all that takes); ssm_join joins both.
 //
-// Bound: fp32 operations (about 15 an element), then exponentials and shuffles.  A thread has 2 channels x 4 states:
-// sums over n cross the channel's lanes, sums over d first the 2 channels, then the lanes that hold the same n, each
-// value halved between the partners of a shuffle (12 shuffles a token for 8 elements).  dB and dC leave each block of
-// channels as partial sums that a last kernel adds in order; dA, dDk and the bias likewise over the segments.  No
-// atomics: the same bits in every run.
+// Bound: issue slots, then fp32 operations, exponentials and shared memory, within a factor of two of each other.  A
+// thread has 2 channels x 4 states.  Sums over n and over d cross threads: each thread leaves its terms of half a chunk
+// in shared memory, in order of its number, and after the walk the block adds them, 16 bytes at a time; crossing lanes by
+// shuffles token by token took twice the instructions.  dB and dC leave each block of channels as partial sums that a
+// last kernel adds in order; dA, dDk and the bias likewise over the segments.  No atomics: the same bits in every run.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -28,13 +27,12 @@ namespace gdr {
 namespace layer {
 namespace {
 
+constexpr int kThreads = 128;
 constexpr int kChunk = 16, kHalf = 8;
-constexpr int kDC = 2;                        // channels of a thread in the main kernel
+constexpr int kDC = 2;                        // channels of a thread
 constexpr int kMinSegment = 64;
-constexpr int kWarps = kSsmThreads / 32;
+constexpr int kBlocksPerSm = 3;
 constexpr float kLn2 = 0.6931471805599453f;
-
-template <int LN> constexpr int local_channels() { return LN == 2 ? 2 : 4; }   // 4 would not fit 48 KB of tiles there
 
 // Everything the kernels pass on: see plan().
 struct Scratch {
@@ -47,132 +45,197 @@ struct Scratch {
 // Index of the checkpoint of the chunk that starts at token `row` of the axis, in segment `number`.
 __device__ __forceinline__ int64_t ckpt_at(int64_t row, int64_t number) { return row / kChunk + number; }
 
-// Delta, Delta x and g of a chunk's tokens into shared memory, [kChunk][W]; zero past `live` and past the channels.
-template <typename IO, int W>
-__device__ __forceinline__ void load_chunk(const Ssm& a, const IO* dy, const Channels& ch, int64_t row, int live,
-                                           float4* s_delta, float4* s_u, float4* s_g) {
-    for (int i = threadIdx.x; i < kChunk * W / 8; i += kSsmThreads) {
-        const int k = i / (W / 8), col = i % (W / 8) * 8, cc = ch.c0 + col;
-        const int left = k < live ? ch.end - cc : 0;
-        float d[8], u[8], g[8], z[8];
-        widen(load_row8<IO>(a.dt, row + k, cc, left), d);
-        widen(load_row8<IO>(a.x, row + k, cc, left), u);
-        if (dy) {
-            widen(load8(dy + (row + k) * a.D + cc, left, a.vec && (cc & 7) == 0), g);
-            if (a.z.p) widen(load_row8<IO>(a.z, row + k, cc, left), z);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            d[j] = j < left ? step_size(a, d[j], cc + j) : 0.f;
-            u[j] = j < left ? u[j] * d[j] : 0.f;
-            if (dy && a.z.p) g[j] = j < left ? g[j] * z[j] * sigmoid(z[j]) : 0.f;
-        }
-        const int at = (k * W + col) / 4;
-        s_delta[at] = make_float4(d[0], d[1], d[2], d[3]), s_delta[at + 1] = make_float4(d[4], d[5], d[6], d[7]);
-        s_u[at] = make_float4(u[0], u[1], u[2], u[3]), s_u[at + 1] = make_float4(u[4], u[5], u[6], u[7]);
-        if (dy) s_g[at] = make_float4(g[0], g[1], g[2], g[3]), s_g[at + 1] = make_float4(g[4], g[5], g[6], g[7]);
-    }
-}
+// A block's tiles of T tokens x W channels in units of 8 channels, U of them a thread; the loads of a tile run ahead of
+// its use.
+template <typename IO, int T, int W> struct Units {
+    static constexpr int V8 = W / 8, U = T * V8 <= kThreads ? 1 : T * V8 / kThreads, kStep = kThreads / V8;
+    Raw8<IO> dt[U], x[U], dy[U], z[U];
+    int col, tok;
 
-template <int P>
-__device__ __forceinline__ void store_pairs(float* p, int c, int end, const F2 (&v)[P]) {
+    __device__ __forceinline__ Units() : col(threadIdx.x % V8 * 8), tok(threadIdx.x / V8) {}
+
+    __device__ __forceinline__ void fetch(const Ssm& a, const IO* dyp, const Channels& ch, int64_t row, int live) {
+        const int cc = ch.c0 + col;
+        const bool vec8 = (cc & 7) == 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const float2 f = unpack2(v[i]);
-        if (c + 2 * i < end) p[2 * i] = f.x;
-        if (c + 2 * i + 1 < end) p[2 * i + 1] = f.y;
+        for (int i = 0; i < U; ++i) {
+            const int k = tok + i * kStep, left = k < live ? ch.end - cc : 0;
+            dt[i] = load8(reinterpret_cast<const IO*>(a.dt.p) + (row + k) * a.dt.ld + cc, left, a.dt.vec && vec8);
+            x[i] = load8(reinterpret_cast<const IO*>(a.x.p) + (row + k) * a.x.ld + cc, left, a.x.vec && vec8);
+            if (dyp) {
+                dy[i] = load8(dyp + (row + k) * a.D + cc, left, a.vec && vec8);
+                if (a.z.p) z[i] = load8(reinterpret_cast<const IO*>(a.z.p) + (row + k) * a.z.ld + cc, left,
+                                        a.z.vec && vec8);
+            }
+        }
     }
+    // Delta, Delta x and g (with_g) into shared memory [T][W]; zero past `live`, where nothing must happen.
+    __device__ __forceinline__ void put(const Ssm& a, const float* bias, int live, bool with_g, float* s_delta,
+                                        float* s_u, float* s_g) const {
+        F2 d[U][4], u[U][4], g[U][4];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            pairs(dt[i], d[i]);
+            pairs(x[i], u[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[i][j] = add2(d[i][j], reinterpret_cast<const F2*>(bias + col)[j]);
+        }
+        if (a.softplus)
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[i][j] = softplus2(d[i][j]);
+        if (with_g) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) pairs(dy[i], g[i]);
+            if (a.z.p)
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    F2 v[4];
+                    pairs(z[i], v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) g[i][j] = mul2(g[i][j], mul2(v[j], sigmoid2(v[j])));
+                }
+        }
+        if (T * V8 < kThreads && tok >= T) return;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int k = tok + i * kStep, at = (k * W + col) / 2;
+            const bool in = k < live;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                reinterpret_cast<F2*>(s_delta)[at + j] = in ? d[i][j] : 0;
+                reinterpret_cast<F2*>(s_u)[at + j] = in ? mul2(u[i][j], d[i][j]) : 0;
+                if (with_g) reinterpret_cast<F2*>(s_g)[at + j] = in ? g[i][j] : 0;
+            }
+        }
+    }
+};
+
+// B (or C) of T tokens, NP states (zero past N and past `live`), likewise ahead of their use.
+template <typename IO, int T, int NP> struct Values {
+    static constexpr int M = (T * NP + kThreads - 1) / kThreads;
+    IO v[M];
+
+    __device__ __forceinline__ void fetch(const Ssm& a, const RowTensor& t, int group, int64_t row, int live) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int k = (threadIdx.x + i * kThreads) / NP, m = (threadIdx.x + i * kThreads) % NP;
+            v[i] = k < T && k < live && m < a.N
+                       ? reinterpret_cast<const IO*>(t.p)[(row + k) * t.ld + group * a.N + m]
+                       : from_f<IO>(0.f);
+        }
+    }
+    __device__ __forceinline__ void put(float* s) const {
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            if (T * NP % kThreads == 0 || at < T * NP) s[at] = to_f(v[i]);
+        }
+    }
+};
+
+__device__ __forceinline__ void load_channels(const float* p, const Channels& ch, int width, float* s) {
+    for (int i = threadIdx.x; i < width; i += kThreads) s[i] = p && ch.c0 + i < ch.end ? p[ch.c0 + i] : 0.f;
 }
 
 // Checkpoints of each segment from a zero state (the first segment of a sequence: from h0, so exact), what it leaves,
-// its sum of Delta, and the gradient its own tokens send to the state before it.
+// its sum of Delta, and the gradient its own tokens send to the state before it.  2 channels x 8 states a thread.
 template <typename IO, int LN>
-__global__ void __launch_bounds__(kSsmThreads) ssm_backward_local_kernel(Ssm a, const IO* __restrict__ dy, Scratch w) {
-    constexpr int DC = local_channels<LN>(), W = kSsmThreads / LN * DC, P = DC / 2;
-    __shared__ float4 s_delta[kChunk * W / 4], s_u[kChunk * W / 4], s_g[kChunk * W / 4];
-    __shared__ float2 s_b[kChunk * 4 * LN], s_c[kChunk * 4 * LN];
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+ssm_backward_local_kernel(Ssm a, const IO* __restrict__ dy, Scratch w) {
+    constexpr int T = 8, W = kThreads / LN * kDC, NP = 8 * LN;
+    __shared__ float4 s_delta[T * W / 4], s_u[T * W / 4], s_g[T * W / 4], s_b[T * NP / 4], s_c[T * NP / 4], s_bias[W / 4];
     const TileAt at = find_tile(a.q, blockIdx.x, a.seg);
     if (at.seq < 0) return;
-    const bool last = (at.tile + 1) * a.seg >= at.len, back = at.tile > 0, split = back || !last;
+    const bool last = (at.tile + 1) * a.seg >= at.len, back = at.tile > 0;
     const Channels ch = block_channels(a, W);
-    const int q = threadIdx.x % LN, n = 4 * q, own = threadIdx.x / LN * DC, c = ch.c0 + own;
+    const int q = threadIdx.x % LN, n = 8 * q, own = threadIdx.x / LN * kDC, c = ch.c0 + own;
     const int64_t state = (int64_t)a.D * a.N;
-
-    F2 A2[4][P], h[4][P], grown[4][P], dh[4][P], sum[P];
-    load_decay<DC>(a, c, ch.end, n, A2);
-    load_states<DC>(back || !a.h0 ? nullptr : a.h0 + at.seq * state, a, c, ch.end, n, h);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        sum[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) grown[j][i] = pack2(1.f, 1.f), dh[j][i] = 0;
-    }
     const int64_t t0 = at.tile * a.seg, t1 = min(t0 + a.seg, at.len);
-    for (int64_t t = t0; t < t1; t += kChunk) {
-        const int live = (int)min((int64_t)kChunk, t1 - t);
-        const int64_t row = at.start + t, ck = ckpt_at(row, blockIdx.x);
-        store_states<DC>(w.ckpt + ck * state, a, c, ch.end, n, h);
-        if (back && q == 0) store_pairs<P>(w.csum + ck * a.D + c, c, ch.end, sum);
-        if (last && !back && t + kChunk >= t1) break;            // nobody asks for what the last chunk leaves
-        load_chunk<IO, W>(a, back ? dy : nullptr, ch, row, live, s_delta, s_u, s_g);
-        load_bc<IO, LN>(a, a.B, ch.group, row, live, kChunk, s_b);
-        if (back) load_bc<IO, LN>(a, a.C, ch.group, row, live, kChunk, s_c);
+
+    Units<IO, T, W> in;
+    Values<IO, T, NP> vb, vc;
+    const auto fetch = [&](int64_t t) {
+        const int live = (int)min((int64_t)T, t1 - t);
+        in.fetch(a, back ? dy : nullptr, ch, at.start + t, live);
+        vb.fetch(a, a.B, ch.group, at.start + t, live);
+        if (back) vc.fetch(a, a.C, ch.group, at.start + t, live);
+    };
+    fetch(t0);
+    load_channels(a.bias, ch, W, reinterpret_cast<float*>(s_bias));
+    F2 A2[kDC][4], h[kDC][4], grown[kDC][4], dh[kDC][4];
+    float sum[kDC];
+    load_decay<kDC, 8>(a, c, ch.end, n, A2);
+    load_states<kDC, 8>(back || !a.h0 ? nullptr : a.h0 + at.seq * state, a, c, ch.end, n, h);
+#pragma unroll
+    for (int i = 0; i < kDC; ++i) {
+        sum[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) grown[i][j] = both(1.f), dh[i][j] = 0;
+    }
+    __syncthreads();
+    for (int64_t t = t0; t < t1; t += T) {
+        const int live = (int)min((int64_t)T, t1 - t);
+        if ((t - t0) % kChunk == 0) {
+            const int64_t ck = ckpt_at(at.start + t, blockIdx.x);
+            store_states<kDC, 8>(w.ckpt + ck * state, a, c, ch.end, n, h);
+            if (back && q == 0)
+#pragma unroll
+                for (int i = 0; i < kDC; ++i)
+                    if (c + i < ch.end) w.csum[ck * a.D + c + i] = sum[i];
+            if (last && !back && t + kChunk >= t1) break;        // nobody asks for what the last chunk leaves
+        }
+        in.put(a, reinterpret_cast<const float*>(s_bias), live, back, reinterpret_cast<float*>(s_delta),
+               reinterpret_cast<float*>(s_u), reinterpret_cast<float*>(s_g));
+        vb.put(reinterpret_cast<float*>(s_b));
+        if (back) vc.put(reinterpret_cast<float*>(s_c));
         __syncthreads();
-#pragma unroll 2
+        if (t + T < t1) fetch(t + T);
+#pragma unroll 1
         for (int k = 0; k < live; ++k) {
-            const F2* pd = reinterpret_cast<const F2*>(s_delta) + (k * W + own) / 2;
-            const F2* pu = reinterpret_cast<const F2*>(s_u) + (k * W + own) / 2;
-            const F2* pg = reinterpret_cast<const F2*>(s_g) + (k * W + own) / 2;
-            const F2* pb = reinterpret_cast<const F2*>(s_b) + k * 4 * LN + n;
-            const F2* pc = reinterpret_cast<const F2*>(s_c) + k * 4 * LN + n;
+            const float2 d = reinterpret_cast<const float2*>(s_delta)[(k * W + own) / 2];
+            const float2 u = reinterpret_cast<const float2*>(s_u)[(k * W + own) / 2];
+            const F2* pb = reinterpret_cast<const F2*>(s_b) + (k * NP + n) / 2;
+            F2 b[4], cg[4];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                sum[i] = add2(sum[i], pd[i]);
+            for (int j = 0; j < 4; ++j) b[j] = pb[j];
+            if (back) {
+                const float2 g = reinterpret_cast<const float2*>(s_g)[(k * W + own) / 2];
+                const F2* pc = reinterpret_cast<const F2*>(s_c) + (k * NP + n) / 2;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const F2 e = ex2_2(mul2(A2[j][i], pd[i]));
-                    h[j][i] = fma2(e, h[j][i], mul2(pu[i], pb[j]));
-                    if (back) {
-                        grown[j][i] = mul2(grown[j][i], e);
-                        dh[j][i] = fma2(grown[j][i], mul2(pg[i], pc[j]), dh[j][i]);
+                for (int j = 0; j < 4; ++j) cg[j] = pc[j];
+#pragma unroll
+                for (int i = 0; i < kDC; ++i) {
+                    const F2 dd = both(i ? d.y : d.x), uu = both(i ? u.y : u.x), gg = both(i ? g.y : g.x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const F2 e = ex2_2(mul2(A2[i][j], dd));
+                        h[i][j] = fma2(e, h[i][j], mul2(uu, b[j]));
+                        grown[i][j] = mul2(grown[i][j], e);
+                        dh[i][j] = fma2(grown[i][j], mul2(gg, cg[j]), dh[i][j]);
                     }
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kDC; ++i) {
+                    const F2 dd = both(i ? d.y : d.x), uu = both(i ? u.y : u.x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[i][j] = fma2(ex2_2(mul2(A2[i][j], dd)), h[i][j], mul2(uu, b[j]));
+                }
             }
+            sum[0] += d.x, sum[1] += d.y;
         }
         __syncthreads();
     }
-    if (!split) return;
-    if (!last) store_states<DC>(w.ends + blockIdx.x * state, a, c, ch.end, n, h);
-    if (back) store_states<DC>(w.dends + blockIdx.x * state, a, c, ch.end, n, dh);
-    if (q == 0) store_pairs<P>(w.sums + (int64_t)blockIdx.x * a.D + c, c, ch.end, sum);
+    if (last && !back) return;                 // a sequence of one segment
+    if (!last) store_states<kDC, 8>(w.ends + blockIdx.x * state, a, c, ch.end, n, h);
+    if (back) store_states<kDC, 8>(w.dends + blockIdx.x * state, a, c, ch.end, n, dh);
+    if (q == 0)
+#pragma unroll
+        for (int i = 0; i < kDC; ++i)
+            if (c + i < ch.end) w.sums[(int64_t)blockIdx.x * a.D + c + i] = sum[i];
 }
-
-// Sums over the lanes that hold the same states (lane / LN differs) of v[0 .. 8), halving the values between partners
-// while there are steps for it.  Lane group l is left with V values, the first of index first_value(l).
-template <int LN> struct GroupSum {
-    static constexpr int kGroups = 32 / LN;
-    static constexpr int V = kGroups >= 8 ? 1 : 8 / kGroups;
-    static __device__ __forceinline__ int first_value(int l) {
-        int at = 0;
-#pragma unroll
-        for (int size = 4, bit = 1; size >= V; size /= 2, bit *= 2) at += l & bit ? size : 0;
-        return at;
-    }
-    static __device__ __forceinline__ void sum(float (&v)[8], int l) {
-        int mask = LN;
-#pragma unroll
-        for (int size = 4; size >= V; size /= 2, mask *= 2) {
-            const bool up = l & (mask / LN);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i >= size) break;
-                const float give = up ? v[i] : v[i + size], keep = up ? v[i + size] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, mask);
-            }
-        }
-        if (kGroups == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-    }
-};
 
 template <typename IO> struct Grads {
     const IO* dy;
@@ -181,214 +244,274 @@ template <typename IO> struct Grads {
     float* dh0;
 };
 
+// Shared memory of the main kernel, in floats.  terms_bc: dB and dC terms [token of the half][B or C][thread], 4 states
+// each; terms_n: r, y and sum A w, [token of the half][which][channel of the thread][thread].
+template <int LN> struct MainTiles {
+    static constexpr int W = kThreads / LN * kDC, NP = 4 * LN;
+    static constexpr int delta = 0, u = delta + kChunk * W, g = u + kChunk * W, b = g + kChunk * W, c = b + kChunk * NP,
+                         bias = c + kChunk * NP, D = bias + W, terms_bc = D + W,
+                         terms_n = terms_bc + kHalf * 2 * kThreads * 4, total = terms_n + kHalf * 3 * kDC * kThreads;
+    static_assert(terms_bc % 4 == 0 && terms_n % 4 == 0, "16-byte pieces");
+};
+
 template <typename IO, int LN>
-__global__ void __launch_bounds__(kSsmThreads, 3) ssm_backward_kernel(Ssm a, Grads<IO> o, Scratch w) {
-    constexpr int W = kSsmThreads / LN * kDC, V8 = W / 8;
-    using Sum = GroupSum<LN>;
-    __shared__ float4 s_delta[kChunk * W / 4], s_u[kChunk * W / 4], s_g[kChunk * W / 4];
-    __shared__ float2 s_b[kChunk * 4 * LN], s_c[kChunk * 4 * LN];
-    __shared__ float s_bc[kWarps][kHalf][8][LN];       // dB (values 0 .. 3 of each lane), dC (4 .. 7) of half a chunk
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ssm a, Grads<IO> o, Scratch w) {
+    using S = MainTiles<LN>;
+    constexpr int W = S::W, NP = S::NP, W4 = W / 4;
+    constexpr int U4 = kHalf * W4 <= kThreads ? 1 : kHalf * W4 / kThreads;     // 4-channel units of a thread in half a chunk
+    extern __shared__ float4 smem4[];
+    float* sm = reinterpret_cast<float*>(smem4);
     const TileAt at = find_tile(a.q, blockIdx.x, a.seg);
     const Channels ch = block_channels(a, W);
     const int q = threadIdx.x % LN, n = 4 * q, own = threadIdx.x / LN * kDC, c = ch.c0 + own;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, group = lane / LN;
     const int64_t state = (int64_t)a.D * a.N;
-    const int col8 = threadIdx.x % V8 * 8;             // the channels this thread moves to and from memory
+    const int col4 = threadIdx.x % W4 * 4, cc = ch.c0 + col4, tok4 = threadIdx.x / W4;
+    const bool vec4 = (cc & 7) == 0 || (cc & 7) == 4;
+    const int left = ch.end - cc;
 
-    F2 A2[4][1], dh[4][1], dA[4][1];
-    float dD[8], dbias[8];
+    F2 dA[kDC][2];
+    float dD[4], dbias[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dA[j][0] = 0;
+    for (int j = 0; j < 2; ++j) dA[0][j] = dA[1][j] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dD[j] = 0.f, dbias[j] = 0.f;
+    for (int j = 0; j < 4; ++j) dD[j] = dbias[j] = 0.f;
 
     if (at.seq >= 0) {
-        load_decay<kDC>(a, c, ch.end, n, A2);
-        load_states<kDC>(o.dh_final ? o.dh_final + at.seq * state : nullptr, a, c, ch.end, n, dh);
         const int64_t t0 = at.tile * a.seg, t1 = min(t0 + a.seg, at.len);
-        const int64_t first = (int64_t)blockIdx.x - at.tile, segments = (at.len + a.seg - 1) / a.seg;
-        // the decay of a whole segment on a state
-        const auto through = [&](int64_t s, F2 (&v)[4][1], const float* add) {
-            const float* p = w.sums + s * a.D + c;
-            const F2 t = pack2(c < ch.end ? p[0] : 0.f, c + 1 < ch.end ? p[1] : 0.f);
-            F2 e[4][1];
-            load_states<kDC>(add + s * state, a, c, ch.end, n, e);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j][0] = fma2(ex2_2(mul2(A2[j][0], t)), v[j][0], e[j][0]);
+        int64_t t = t1 > t0 ? t0 + (t1 - t0 - 1) / kChunk * kChunk : t0 - 1;
+        Units<IO, kChunk, W> in;
+        Values<IO, kChunk, NP> vb, vc;
+        const auto fetch = [&](int64_t from) {
+            const int live = (int)min((int64_t)kChunk, t1 - from);
+            in.fetch(a, o.dy, ch, at.start + from, live);
+            vb.fetch(a, a.B, ch.group, at.start + from, live);
+            vc.fetch(a, a.C, ch.group, at.start + from, live);
         };
-        for (int64_t s = first + segments - 1; s > (int64_t)blockIdx.x; --s) through(s, dh, w.dends);
-        F2 start[4][1];                                // the state before a later segment, over its local checkpoints
-        if (at.tile > 0) {
-            load_states<kDC>(w.ends + first * state, a, c, ch.end, n, start);
-            for (int64_t s = first + 1; s < (int64_t)blockIdx.x; ++s) through(s, start, w.ends);
-        }
+        if (t >= t0) fetch(t);
+        load_channels(a.bias, ch, W, sm + S::bias);
+        load_channels(a.Dk, ch, W, sm + S::D);
+        F2 A2[kDC][2], dh[kDC][2];
+        load_decay<kDC, 4>(a, c, ch.end, n, A2);
+        const bool one = at.len <= a.seg;              // a sequence of one segment; else ssm_join has joined them
+        const float* after = one ? (o.dh_final ? o.dh_final + at.seq * state : nullptr) : w.dends + blockIdx.x * state;
+        load_states<kDC, 4>(after, a, c, ch.end, n, dh);
+        __syncthreads();
 
-        for (int64_t t = t1 > t0 ? t0 + (t1 - t0 - 1) / kChunk * kChunk : t0 - 1; t >= t0; t -= kChunk) {
+        for (; t >= t0; t -= kChunk) {
             const int live = (int)min((int64_t)kChunk, t1 - t);
             const int64_t row = at.start + t, ck = ckpt_at(row, blockIdx.x);
-            F2 h0[4][1];
-            load_states<kDC>(w.ckpt + ck * state, a, c, ch.end, n, h0);
-            if (at.tile > 0) {
-                const float* p = w.csum + ck * a.D + c;
-                const F2 s = pack2(c < ch.end ? p[0] : 0.f, c + 1 < ch.end ? p[1] : 0.f);
+            F2 h0[kDC][2];
+            load_states<kDC, 4>(w.ckpt + ck * state, a, c, ch.end, n, h0);
+            if (at.tile > 0) {                         // over the local checkpoint, the state before the segment
+                F2 start[kDC][2];
+                load_states<kDC, 4>(w.ends + blockIdx.x * state, a, c, ch.end, n, start);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h0[j][0] = fma2(ex2_2(mul2(A2[j][0], s)), start[j][0], h0[j][0]);
+                for (int i = 0; i < kDC; ++i) {
+                    const F2 s = both(c + i < ch.end ? w.csum[ck * a.D + c + i] : 0.f);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) h0[i][j] = fma2(ex2_2(mul2(A2[i][j], s)), start[i][j], h0[i][j]);
+                }
             }
-            load_chunk<IO, W>(a, o.dy, ch, row, live, s_delta, s_u, s_g);
-            load_bc<IO, LN>(a, a.B, ch.group, row, live, kChunk, s_b);
-            load_bc<IO, LN>(a, a.C, ch.group, row, live, kChunk, s_c);
+            in.put(a, sm + S::bias, live, true, sm + S::delta, sm + S::u, sm + S::g);
+            vb.put(sm + S::b);
+            vc.put(sm + S::c);
             __syncthreads();
-            const F2* pd = reinterpret_cast<const F2*>(s_delta) + own / 2;
-            const F2* pu = reinterpret_cast<const F2*>(s_u) + own / 2;
-            const F2* pg = reinterpret_cast<const F2*>(s_g) + own / 2;
-            const F2* pb = reinterpret_cast<const F2*>(s_b) + n;
-            const F2* pc = reinterpret_cast<const F2*>(s_c) + n;
+            if (t > t0) fetch(t - kChunk);
+            const float2* pd = reinterpret_cast<const float2*>(sm + S::delta + own);
+            const float2* pu = reinterpret_cast<const float2*>(sm + S::u + own);
+            const float2* pg = reinterpret_cast<const float2*>(sm + S::g + own);
+            const F2* pb = reinterpret_cast<const F2*>(sm + S::b + n);
+            const F2* pc = reinterpret_cast<const F2*>(sm + S::c + n);
 #pragma unroll 1
             for (int half = live > kHalf ? 1 : 0; half >= 0; --half) {
-                F2 hs[kHalf + 1][4];                   // the states before each token of the half, and after the last
+                const int base = half * kHalf, tokens = min(kHalf, live - base);
+                // what the elementwise end needs of the half's tokens, on its way meanwhile
+                RawN<IO, 4> x_r[U4], dt_r[U4], dy_r[U4], z_r[U4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) hs[0][j] = h0[j][0];
+                for (int i = 0; i < U4; ++i) {
+                    const int k = tok4 + i * (kThreads / W4), l = k < tokens ? left : 0;
+                    const int64_t r = row + base + k;
+                    x_r[i] = load_n<4>(reinterpret_cast<const IO*>(a.x.p) + r * a.x.ld + cc, l, a.x.vec && vec4);
+                    dt_r[i] = load_n<4>(reinterpret_cast<const IO*>(a.dt.p) + r * a.dt.ld + cc, l, a.dt.vec && vec4);
+                    if (a.z.p) {
+                        dy_r[i] = load_n<4>(o.dy + r * a.D + cc, l, a.vec && vec4);
+                        z_r[i] = load_n<4>(reinterpret_cast<const IO*>(a.z.p) + r * a.z.ld + cc, l, a.z.vec && vec4);
+                    }
+                }
+                F2 hs[kHalf + 1][kDC][2];              // the states before each token of the half, and after the last
+#pragma unroll
+                for (int i = 0; i < kDC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) hs[0][i][j] = h0[i][j];
+                const auto step = [&](int k, const F2 (&from)[kDC][2], F2 (&to)[kDC][2]) {
+                    const float2 d = pd[k * W / 2], u = pu[k * W / 2];
+                    const F2 b[2] = {pb[k * NP / 2], pb[k * NP / 2 + 1]};
+#pragma unroll
+                    for (int i = 0; i < kDC; ++i) {
+                        const F2 dd = both(i ? d.y : d.x), uu = both(i ? u.y : u.x);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            to[i][j] = fma2(ex2_2(mul2(A2[i][j], dd)), from[i][j], mul2(uu, b[j]));
+                    }
+                };
                 if (half)
 #pragma unroll 2
-                    for (int k = 0; k < kHalf; ++k)
+                    for (int k = 0; k < kHalf; ++k) step(k, hs[0], hs[0]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            hs[0][j] = fma2(ex2_2(mul2(A2[j][0], pd[k * W / 2])), hs[0][j],
-                                            mul2(pu[k * W / 2], pb[k * 4 * LN + j]));
-                const int base = half * kHalf;
+                for (int k = 0; k < kHalf; ++k) step(base + k, hs[k], hs[k + 1]);
+                F2 dAh[kDC][2];                        // dA of the half: short sums first keep its rounding small
 #pragma unroll
-                for (int k = 0; k < kHalf; ++k)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        hs[k + 1][j] = fma2(ex2_2(mul2(A2[j][0], pd[(base + k) * W / 2])), hs[k][j],
-                                            mul2(pu[(base + k) * W / 2], pb[(base + k) * 4 * LN + j]));
+                for (int i = 0; i < kDC; ++i) dAh[i][0] = dAh[i][1] = 0;
 #pragma unroll
                 for (int k = kHalf - 1; k >= 0; --k) {
-                    const int at_k = (base + k) * W / 2, bc_k = (base + k) * 4 * LN;
-                    const F2 d = pd[at_k], u = pu[at_k], g = pg[at_k];
-                    F2 y = 0, r = 0, s = 0;            // sums over n: C h, dh B, log2(e) A w
-                    float v[8];                        // sums over d: dB, dC
+                    const int tk = base + k;
+                    const float2 d2 = pd[tk * W / 2], u2 = pu[tk * W / 2], g2 = pg[tk * W / 2];
+                    const F2 b[2] = {pb[tk * NP / 2], pb[tk * NP / 2 + 1]}, cv[2] = {pc[tk * NP / 2], pc[tk * NP / 2 + 1]};
+                    F2 dB[2], dC[2];
+                    float* tn = sm + S::terms_n + k * 3 * kDC * kThreads + threadIdx.x;
+#pragma unroll
+                    for (int i = 0; i < kDC; ++i) {
+                        const F2 d = both(i ? d2.y : d2.x), u = both(i ? u2.y : u2.x), g = both(i ? g2.y : g2.x);
+                        F2 y, r, s;                    // terms of C h, dh B and log2(e) A w
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const F2 e = ex2_2(mul2(A2[i][j], d));
+                            dh[i][j] = fma2(g, cv[j], dh[i][j]);
+                            y = j ? fma2(hs[k + 1][i][j], cv[j], y) : mul2(hs[k + 1][i][j], cv[j]);
+                            r = j ? fma2(dh[i][j], b[j], r) : mul2(dh[i][j], b[j]);
+                            dB[j] = i ? fma2(dh[i][j], u, dB[j]) : mul2(dh[i][j], u);
+                            dC[j] = i ? fma2(hs[k + 1][i][j], g, dC[j]) : mul2(hs[k + 1][i][j], g);
+                            dh[i][j] = mul2(e, dh[i][j]);
+                            const F2 wt = mul2(dh[i][j], hs[k][i][j]);
+                            s = j ? fma2(A2[i][j], wt, s) : mul2(A2[i][j], wt);
+                            dAh[i][j] = fma2(d, wt, dAh[i][j]);
+                        }
+                        const float2 fr = unpack2(r), fy = unpack2(y), fs = unpack2(s);
+                        tn[(0 * kDC + i) * kThreads] = fr.x + fr.y;
+                        tn[(1 * kDC + i) * kThreads] = fy.x + fy.y;
+                        tn[(2 * kDC + i) * kThreads] = fs.x + fs.y;
+                    }
+                    ulonglong2* tb = reinterpret_cast<ulonglong2*>(sm + S::terms_bc) + k * 2 * kThreads + threadIdx.x;
+                    tb[0] = make_ulonglong2(dB[0], dB[1]);
+                    tb[kThreads] = make_ulonglong2(dC[0], dC[1]);
+                }
+#pragma unroll
+                for (int i = 0; i < kDC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) dA[i][j] = add2(dA[i][j], dAh[i][j]);
+                __syncthreads();
+
+                // dB and dC of the half from this block's channels: 4 states of (token, B or C) an output, its terms
+                // shared by `parts` neighbouring threads
+                constexpr int outs = kHalf * 2 * LN, parts = outs < kThreads ? kThreads / outs : 1;
+#pragma unroll
+                for (int i = 0; i < (outs + kThreads - 1) / kThreads; ++i) {
+                    const int out = (threadIdx.x + i * kThreads) / parts, part = threadIdx.x % parts;
+                    const int qq = out % LN, bc = out / LN % 2, k = out / LN / 2;
+                    const float4* p = reinterpret_cast<const float4*>(sm + S::terms_bc) + (k * 2 + bc) * kThreads + qq;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < kThreads / LN / parts; ++j) {
+                        const float4 f = p[(j * parts + part) * LN];
+                        v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+                    }
+#pragma unroll
+                    for (int m = 1; m < parts; m *= 2) {
+                        v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
+                        v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
+                        v.z += __shfl_xor_sync(0xffffffffu, v.z, m);
+                        v.w += __shfl_xor_sync(0xffffffffu, v.w, m);
+                    }
+                    if (part == 0 && k < tokens) {
+                        const int m = 4 * qq;
+                        float* to = w.part_bc +
+                                    ((((int64_t)ch.block * a.q.total + row + base + k) * a.G + ch.group) * 2 + bc) * a.N + m;
+                        if ((a.N & 3) == 0 && m < a.N) {
+                            *reinterpret_cast<float4*>(to) = v;
+                        } else {
+                            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (m + j < a.N) to[j] = f[j];
+                        }
+                    }
+                }
+                // the elementwise end: 4 channels of a token a unit
+#pragma unroll
+                for (int i = 0; i < U4; ++i) {
+                    const int k = tok4 + i * (kThreads / W4);
+                    if (k >= tokens || left <= 0) continue;
+                    float v[3][4];                     // r, y, sum A w: channels 4 .. of 2 of each of two threads' groups
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float* p = sm + S::terms_n + ((k * 3 + j) * kDC + x % 2) * kThreads + (col4 + x) / 2 * LN;
+                            float f[LN];
+                            if constexpr (LN % 4 == 0) {
+#pragma unroll
+                                for (int m = 0; m < LN; m += 4) {
+                                    const float4 f4 = *reinterpret_cast<const float4*>(p + m);
+                                    f[m] = f4.x, f[m + 1] = f4.y, f[m + 2] = f4.z, f[m + 3] = f4.w;
+                                }
+                            } else {
+                                const float2 f2 = *reinterpret_cast<const float2*>(p);
+                                f[0] = f2.x, f[1] = f2.y;
+                            }
+                            v[j][x] = f[0];
+#pragma unroll
+                            for (int m = 1; m < LN; ++m) v[j][x] += f[m];
+                        }
+                    const float4 delta4 = *reinterpret_cast<const float4*>(sm + S::delta + (base + k) * W + col4);
+                    const float4 g4 = *reinterpret_cast<const float4*>(sm + S::g + (base + k) * W + col4);
+                    const float4 D4 = *reinterpret_cast<const float4*>(sm + S::D + col4);
+                    const float4 bias4 = *reinterpret_cast<const float4*>(sm + S::bias + col4);
+                    const float delta[4] = {delta4.x, delta4.y, delta4.z, delta4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
+                    const float D[4] = {D4.x, D4.y, D4.z, D4.w}, bias[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
+                    float x[4], raw[4], dy[4], z[4], out[4];
+                    widen(x_r[i], x);
+                    widen(dt_r[i], raw);
+                    const int64_t to = (row + base + k) * a.D + cc;
+                    if (a.z.p) {
+                        widen(dy_r[i], dy);
+                        widen(z_r[i], z);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float sig = sigmoid(z[j]), pre = a.Dk ? fmaf(D[j], x[j], v[1][j]) : v[1][j];
+                            out[j] = dy[j] * pre * sig * fmaf(z[j], 1.f - sig, 1.f);
+                        }
+                        store_n(o.dz + to, out, left, a.vec && vec4);
+                    }
+                    float ddt[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const F2 e = ex2_2(mul2(A2[j][0], d)), b = pb[bc_k + j], cc = pc[bc_k + j];
-                        dh[j][0] = fma2(g, cc, dh[j][0]);
-                        y = fma2(hs[k + 1][j], cc, y);
-                        r = fma2(dh[j][0], b, r);
-                        const float2 fb = unpack2(mul2(dh[j][0], u)), fc = unpack2(mul2(hs[k + 1][j], g));
-                        v[j] = fb.x + fb.y;
-                        v[4 + j] = fc.x + fc.y;
-                        dh[j][0] = mul2(e, dh[j][0]);
-                        const F2 wt = mul2(dh[j][0], hs[k][j]);
-                        s = fma2(A2[j][0], wt, s);
-                        dA[j][0] = fma2(d, wt, dA[j][0]);
-                    }
-                    // a channel's sums over its lanes: lane bit 0 keeps a channel, bit 1 splits (r, y) from s
-                    const float2 fr = unpack2(r), fy = unpack2(y), fs = unpack2(s);
-                    const bool odd = q & 1, two = q & 2;
-                    float vr = (odd ? fr.y : fr.x) + __shfl_xor_sync(0xffffffffu, odd ? fr.x : fr.y, 1);
-                    float vy = (odd ? fy.y : fy.x) + __shfl_xor_sync(0xffffffffu, odd ? fy.x : fy.y, 1);
-                    float vs = (odd ? fs.y : fs.x) + __shfl_xor_sync(0xffffffffu, odd ? fs.x : fs.y, 1);
-                    const int slot = (base + k) * W + own + odd;
-                    if (LN == 2) {
-                        reinterpret_cast<float*>(s_u)[slot] = vr;
-                        reinterpret_cast<float*>(s_g)[slot] = vy;
-                        reinterpret_cast<float*>(s_delta)[slot] = vs;
-                    } else {
-                        vr = (two ? vs : vr) + __shfl_xor_sync(0xffffffffu, two ? vr : vs, 2);
-                        vy += __shfl_xor_sync(0xffffffffu, vy, 2);
-#pragma unroll
-                        for (int m = 4; m < LN; m *= 2) {
-                            vr += __shfl_xor_sync(0xffffffffu, vr, m);
-                            vy += __shfl_xor_sync(0xffffffffu, vy, m);
-                        }
-                        if (q < 2) {
-                            reinterpret_cast<float*>(s_u)[slot] = vr;
-                            reinterpret_cast<float*>(s_g)[slot] = vy;
-                        } else if (q < 4) {
-                            reinterpret_cast<float*>(s_delta)[slot] = vr;
-                        }
-                    }
-                    Sum::sum(v, group);
-                    if (Sum::kGroups < 16 || group < 8)
-#pragma unroll
-                        for (int i = 0; i < Sum::V; ++i) s_bc[warp][k][Sum::first_value(group) + i][q] = v[i];
-                }
-                __syncthreads();
-                // dB and dC of the half from this block's channels: value (B or C, n) of token base + k
-                const int tokens = min(kHalf, live - base);
-                for (int i = threadIdx.x; i < tokens * 8 * LN; i += kSsmThreads) {
-                    const int k = i / (8 * LN), bc = i / (4 * LN) % 2, m = i % (4 * LN);
-                    if (m >= a.N) continue;
-                    float t4 = 0.f;
-#pragma unroll
-                    for (int x = 0; x < kWarps; ++x) t4 += s_bc[x][k][bc * 4 + m % 4][m / 4];
-                    const int blk = blockIdx.y - ch.group * ((a.per + W - 1) / W);
-                    w.part_bc[((((int64_t)blk * a.q.total + row + base + k) * a.G + ch.group) * 2 + bc) * a.N + m] = t4;
-                }
-                __syncthreads();
-            }
-            for (int i = threadIdx.x; i < live * V8; i += kSsmThreads) {
-                const int k = i / V8, cc = ch.c0 + col8, left = ch.end - cc;
-                if (left <= 0) continue;
-                const bool vec = a.vec && (cc & 7) == 0;
-                const float* r = reinterpret_cast<const float*>(s_u) + k * W + col8;
-                const float* y = reinterpret_cast<const float*>(s_g) + k * W + col8;
-                const float* s = reinterpret_cast<const float*>(s_delta) + k * W + col8;
-                float x[8], raw[8], g[8], z[8], out[8];
-                widen(load_row8<IO>(a.x, row + k, cc, left), x);
-                widen(load_row8<IO>(a.dt, row + k, cc, left), raw);
-                widen(load8(o.dy + (row + k) * a.D + cc, left, vec), g);
-                const int64_t to = (row + k) * a.D + cc;
-                if (a.z.p) {
-                    widen(load_row8<IO>(a.z, row + k, cc, left), z);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float sig = sigmoid(z[j]), Dx = a.Dk && j < left ? a.Dk[cc + j] * x[j] : 0.f;
-                        out[j] = g[j] * (y[j] + Dx) * sig * fmaf(z[j], 1.f - sig, 1.f);
-                        g[j] *= z[j] * sig;
-                    }
-                    store_n(o.dz + to, out, left, vec);
-                }
-                float ddt[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float v = raw[j] + (a.bias && j < left ? a.bias[cc + j] : 0.f);
-                    const float delta = a.softplus ? softplus(v) : v;
-                    out[j] = fmaf(r[j], delta, a.Dk && j < left ? a.Dk[cc + j] * g[j] : 0.f);
-                    ddt[j] = fmaf(r[j], x[j], kLn2 * s[j]);
-                    if (a.softplus) ddt[j] *= sigmoid(v);
-                    if (j < left) {
+                        out[j] = v[0][j] * delta[j];
+                        if (a.Dk) out[j] = fmaf(D[j], g[j], out[j]);
+                        ddt[j] = fmaf(v[0][j], x[j], kLn2 * v[2][j]);
+                        if (a.softplus) ddt[j] *= sigmoid(raw[j] + bias[j]);
                         dD[j] = fmaf(g[j], x[j], dD[j]);
                         dbias[j] += ddt[j];
                     }
+                    store_n(o.dx + to, out, left, a.vec && vec4);
+                    store_n(o.ddt + to, ddt, left, a.vec && vec4);
                 }
-                store_n(o.dx + to, out, left, vec);
-                store_n(o.ddt + to, ddt, left, vec);
+                __syncthreads();
             }
-            __syncthreads();
         }
-        if (at.tile == 0 && o.dh0) store_states<kDC>(o.dh0 + at.seq * state, a, c, ch.end, n, dh);
+        if (at.tile == 0 && o.dh0) store_states<kDC, 4>(o.dh0 + at.seq * state, a, c, ch.end, n, dh);
     }
-    store_states<kDC>(w.part_a + blockIdx.x * state, a, c, ch.end, n, dA);
-    // dDk and the bias: over the threads that moved the same channels, lanes first, then warps
-    float (*sums)[V8][16] = reinterpret_cast<float (*)[V8][16]>(s_delta);
-    static_assert(kWarps * V8 * 16 <= kChunk * W, "the sums fit the tile");
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int m = V8; m < 32; m *= 2) {
-            dD[j] += __shfl_xor_sync(0xffffffffu, dD[j], m);
-            dbias[j] += __shfl_xor_sync(0xffffffffu, dbias[j], m);
-        }
-        if (lane < V8) sums[warp][lane][j] = dD[j], sums[warp][lane][8 + j] = dbias[j];
-    }
+    store_states<kDC, 4>(w.part_a + blockIdx.x * state, a, c, ch.end, n, dA);
+    // dDk and the bias: over the threads that moved the same channels, in order
+    float4* sums = reinterpret_cast<float4*>(sm + S::terms_bc);
+    sums[threadIdx.x] = make_float4(dD[0], dD[1], dD[2], dD[3]);
+    sums[kThreads + threadIdx.x] = make_float4(dbias[0], dbias[1], dbias[2], dbias[3]);
     __syncthreads();
-    for (int i = threadIdx.x; i < V8 * 16; i += kSsmThreads) {
-        const int l = i / 16, j = i % 16, cc = ch.c0 + l * 8 + j % 8;
-        float t = 0.f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) t += sums[x][l][j];
-        if (cc < ch.end) w.part_d[((int64_t)blockIdx.x * 2 + j / 8) * a.D + cc] = t;
+    for (int i = threadIdx.x; i < 2 * W; i += kThreads) {
+        const int which = i / W, x = i % W;
+        float v = 0.f;
+        for (int m = 0; m < kThreads / W4; ++m)
+            v += reinterpret_cast<const float*>(sums)[(which * kThreads + m * W4) * 4 + x];
+        if (ch.c0 + x < ch.end) w.part_d[((int64_t)blockIdx.x * 2 + which) * a.D + ch.c0 + x] = v;
     }
 }
 
@@ -405,26 +528,24 @@ __global__ void __launch_bounds__(256) ssm_backward_bc_kernel(const float* __res
     }
 }
 
-int blocks_of_group(const SsmArgs& a) {
-    const int width = kSsmThreads / ssm_lanes(a.N) * kDC;
-    return (a.D / a.G + width - 1) / width;
-}
+int main_width(const SsmArgs& a) { return kThreads / ssm_lanes(a.N, 4) * kDC; }
 
-// Tokens of a segment: two waves of blocks (3 an SM), or whole sequences where a batch has one wave of them.
+// Tokens of a segment: one wave of the main kernel's blocks, or whole sequences where a batch has half a wave of them.
+// Packed sequences have up to n segments beside those of their tokens; the tokens get at least half the wave.
 int segment_of(const SsmArgs& a) {
-    const int64_t blocks = (int64_t)a.G * blocks_of_group(a), wave = kSms * 3;
-    int64_t seg;
-    if (a.cu) seg = std::min(a.total, a.total * blocks / (2 * wave) + 1);
-    else if (a.n * blocks >= wave) seg = a.T;
-    else seg = (a.T + 2 * wave / (a.n * blocks) - 1) / (2 * wave / (a.n * blocks));
-    seg = std::max<int64_t>(seg, kMinSegment);
+    const int64_t blocks = ssm_blocks(a, main_width(a)), wave = kSms * kBlocksPerSm;
+    if (!a.cu && a.n * blocks >= wave / 2) return (int)((a.T + kChunk - 1) / kChunk * kChunk);
+    const int64_t all = std::max<int64_t>(wave / blocks, 1);
+    const int64_t cuts = a.cu ? std::max<int64_t>(all - a.n, (all + 1) / 2) : std::max<int64_t>(all / a.n, 1);
+    const int64_t tokens = a.cu ? a.total : a.T;
+    const int64_t seg = std::max<int64_t>((tokens + cuts - 1) / cuts, kMinSegment);
     return (int)((seg + kChunk - 1) / kChunk * kChunk);
 }
 
 size_t plan(const SsmArgs& a, float* base, Scratch* w) {
     const Seqs q{a.cu, a.total, a.T, (int)a.n};
     const int64_t segments = tile_count(q, segment_of(a)), ckpts = a.total / kChunk + segments;
-    const int64_t D = a.D, DN = D * a.N;
+    const int64_t D = a.D, DN = D * a.N, group_blocks = ssm_blocks(a, main_width(a)) / a.G;
     const bool split = a.cu || segment_of(a) < a.T;
     size_t at = 0;
     const auto take = [&](int64_t floats) {
@@ -437,7 +558,7 @@ size_t plan(const SsmArgs& a, float* base, Scratch* w) {
     w->ends = take(split ? segments * DN : 0);
     w->dends = take(split ? segments * DN : 0);
     w->sums = take(split ? segments * D : 0);
-    w->part_bc = take((int64_t)blocks_of_group(a) * a.total * a.G * 2 * a.N);
+    w->part_bc = take(group_blocks * a.total * a.G * 2 * a.N);
     w->part_a = take(segments * DN);
     w->part_d = take(segments * 2 * D);
     return at * sizeof(float);
@@ -458,29 +579,39 @@ cudaError_t ssm_backward(const SsmArgs& a, const SsmTensors& t, const SsmGrads& 
     k.vec = (int64_t)a.D * (a.io == GDR_F32 ? 4 : 2) % 16 == 0;
     for (const void* p : {g.dy, (const void*)g.dx, (const void*)g.ddt, (const void*)g.dz})
         k.vec = k.vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    const int64_t segments = tile_count(k.q, k.seg);
-    const cudaError_t e = ssm_types(a.io, a.N, [&](auto io, auto lanes) {
+    const unsigned segments = (unsigned)tile_count(k.q, k.seg);
+    const bool split = a.cu || k.seg < a.T;
+    cudaError_t e = ssm_types<8>(a.io, a.N, [&](auto io, auto lanes) {
         using IO = decltype(io);
-        constexpr int LN = decltype(lanes)::value, local = kSsmThreads / LN * local_channels<LN>();
+        constexpr int LN = decltype(lanes)::value, width = kThreads / LN * kDC;
+        ssm_backward_local_kernel<IO, LN>
+            <<<dim3(segments, (unsigned)ssm_blocks(a, width)), kThreads, 0, s>>>(k, (const IO*)g.dy, w);
+        return cudaGetLastError();
+    });
+    if (e == cudaSuccess && split) e = ssm_join(k, w.ends, w.dends, w.sums, g.dh_final, true, s);
+    if (e != cudaSuccess) return e;
+    e = ssm_types<4>(a.io, a.N, [&](auto io, auto lanes) {
+        using IO = decltype(io);
+        constexpr int LN = decltype(lanes)::value, bytes = MainTiles<LN>::total * 4;
         const Grads<IO> o{(const IO*)g.dy, g.dh_final, (IO*)g.dx, (IO*)g.ddt, (IO*)g.dz, g.dh0};
-        const unsigned locals = (unsigned)(a.G * ((a.D / a.G + local - 1) / local));
-        ssm_backward_local_kernel<IO, LN><<<dim3((unsigned)segments, locals), kSsmThreads, 0, s>>>(k, o.dy, w);
-        if (cudaError_t x = cudaGetLastError()) return x;
+        if (cudaError_t x = cudaFuncSetAttribute(ssm_backward_kernel<IO, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 bytes))
+            return x;
         ssm_backward_kernel<IO, LN>
-            <<<dim3((unsigned)segments, (unsigned)(a.G * blocks_of_group(a))), kSsmThreads, 0, s>>>(k, o, w);
+            <<<dim3(segments, (unsigned)ssm_blocks(a, main_width(a))), kThreads, bytes, s>>>(k, o, w);
         if (cudaError_t x = cudaGetLastError()) return x;
         const int64_t values = a.total * a.G * 2 * a.N;
         if (values)
             ssm_backward_bc_kernel<IO><<<(unsigned)std::min<int64_t>((values + 255) / 256, kSms * 8), 256, 0, s>>>(
-                w.part_bc, blocks_of_group(a), values, a.N, (IO*)g.dB, (IO*)g.dC);
+                w.part_bc, (int)(ssm_blocks(a, main_width(a)) / a.G), values, a.N, (IO*)g.dB, (IO*)g.dC);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
-    if (cudaError_t x = column_sum(w.part_a, segments, (int64_t)a.D * a.N, (int64_t)a.D * a.N, g.dA, 0, nullptr, s))
-        return x;
+    const int64_t D = a.D, DN = D * a.N;
+    if (cudaError_t x = column_sum(w.part_a, segments, DN, DN, g.dA, 0, nullptr, s)) return x;
     if (g.dDk)
-        if (cudaError_t x = column_sum(w.part_d, segments, 2 * (int64_t)a.D, a.D, g.dDk, 0, nullptr, s)) return x;
-    if (g.dbias) return column_sum(w.part_d + a.D, segments, 2 * (int64_t)a.D, a.D, g.dbias, 0, nullptr, s);
+        if (cudaError_t x = column_sum(w.part_d, segments, 2 * D, D, g.dDk, 0, nullptr, s)) return x;
+    if (g.dbias) return column_sum(w.part_d + D, segments, 2 * D, D, g.dbias, 0, nullptr, s);
     return cudaSuccess;
 }
 
