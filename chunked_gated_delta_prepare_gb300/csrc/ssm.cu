@@ -180,7 +180,7 @@ ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* _
             for (int i = 0; i < DC; ++i) {
                 const F2 dd = pack2(d[i], d[i]), uu = pack2(u[i], u[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[i][j] = fma2(ex2_2(mul2(A2[i][j], dd)), h[i][j], mul2(uu, b[j]));
+                for (int j = 0; j < 4; ++j) h[i][j] = fma2(decay2(A2[i][j], dd), h[i][j], mul2(uu, b[j]));
                 if (LOCAL) sum[i] += d[i];
             }
             if (!LOCAL) {
@@ -318,7 +318,7 @@ ssm_step_kernel(Ssm a, int64_t pool, const int* __restrict__ slots, float* __res
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (n + j >= a.N) continue;
-        s[j] = fmaf(ex2(A[j] * d), s[j], x * d * to_f(Bp[j]));
+        s[j] = fmaf(decay(A[j], d), s[j], x * d * to_f(Bp[j]));
         o = fmaf(s[j], to_f(Cp[j]), o);
     }
 #pragma unroll

@@ -39,7 +39,7 @@ struct Scratch {
     float *ckpt, *csum;           // [total / kChunk + segments][D][N], [...][D]
     float *ends, *dends, *sums;   // [segments][D][N] twice, [segments][D]
     float *part_bc;               // [blocks of a group][total][G][2][N]
-    float *part_a, *part_d;       // [segments][D][N], [segments][2][D] (Dk, bias)
+    float *part_a, *part_d;       // [walks][D][N], [walks][2][D] (Dk, bias)
 };
 
 // Index of the checkpoint of the chunk that starts at token `row` of the axis, in segment `number`.
@@ -210,7 +210,7 @@ ssm_backward_local_kernel(Ssm a, const IO* __restrict__ dy, Scratch w) {
                     const F2 dd = both(i ? d.y : d.x), uu = both(i ? u.y : u.x), gg = both(i ? g.y : g.x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const F2 e = ex2_2(mul2(A2[i][j], dd));
+                        const F2 e = decay2(A2[i][j], dd);
                         h[i][j] = fma2(e, h[i][j], mul2(uu, b[j]));
                         grown[i][j] = mul2(grown[i][j], e);
                         dh[i][j] = fma2(grown[i][j], mul2(gg, cg[j]), dh[i][j]);
@@ -221,7 +221,7 @@ ssm_backward_local_kernel(Ssm a, const IO* __restrict__ dy, Scratch w) {
                 for (int i = 0; i < kDC; ++i) {
                     const F2 dd = both(i ? d.y : d.x), uu = both(i ? u.y : u.x);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) h[i][j] = fma2(ex2_2(mul2(A2[i][j], dd)), h[i][j], mul2(uu, b[j]));
+                    for (int j = 0; j < 4; ++j) h[i][j] = fma2(decay2(A2[i][j], dd), h[i][j], mul2(uu, b[j]));
                 }
             }
             sum[0] += d.x, sum[1] += d.y;
@@ -254,14 +254,16 @@ template <int LN> struct MainTiles {
     static_assert(terms_bc % 4 == 0 && terms_n % 4 == 0, "16-byte pieces");
 };
 
+// span: segments (of the local kernel) of a block's walk.
 template <typename IO, int LN>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ssm a, Grads<IO> o, Scratch w) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ssm a, int span, Grads<IO> o, Scratch w) {
     using S = MainTiles<LN>;
     constexpr int W = S::W, NP = S::NP, W4 = W / 4;
     constexpr int U4 = kHalf * W4 <= kThreads ? 1 : kHalf * W4 / kThreads;     // 4-channel units of a thread in half a chunk
     extern __shared__ float4 smem4[];
     float* sm = reinterpret_cast<float*>(smem4);
-    const TileAt at = find_tile(a.q, blockIdx.x, a.seg);
+    const int walk = a.seg * span;
+    const TileAt at = find_tile(a.q, blockIdx.x, walk);
     const Channels ch = block_channels(a, W);
     const int q = threadIdx.x % LN, n = 4 * q, own = threadIdx.x / LN * kDC, c = ch.c0 + own;
     const int64_t state = (int64_t)a.D * a.N;
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
     for (int j = 0; j < 4; ++j) dD[j] = dbias[j] = 0.f;
 
     if (at.seq >= 0) {
-        const int64_t t0 = at.tile * a.seg, t1 = min(t0 + a.seg, at.len);
+        const int64_t t0 = at.tile * walk, t1 = min(t0 + walk, at.len);
+        const int64_t first = first_tile(a.q, at.seq, a.seg);          // the sequence's first segment
         int64_t t = t1 > t0 ? t0 + (t1 - t0 - 1) / kChunk * kChunk : t0 - 1;
         Units<IO, kChunk, W> in;
         Values<IO, kChunk, NP> vb, vc;
@@ -293,29 +296,33 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
         F2 A2[kDC][2], dh[kDC][2];
         load_decay<kDC, 4>(a, c, ch.end, n, A2);
         const bool one = at.len <= a.seg;              // a sequence of one segment; else ssm_join has joined them
-        const float* after = one ? (o.dh_final ? o.dh_final + at.seq * state : nullptr) : w.dends + blockIdx.x * state;
+        const float* after = o.dh_final ? o.dh_final + at.seq * state : nullptr;
+        if (!one) after = w.dends + (first + (t1 - 1) / a.seg) * state;
         load_states<kDC, 4>(after, a, c, ch.end, n, dh);
         __syncthreads();
 
         for (; t >= t0; t -= kChunk) {
             const int live = (int)min((int64_t)kChunk, t1 - t);
-            const int64_t row = at.start + t, ck = ckpt_at(row, blockIdx.x);
-            F2 h0[kDC][2];
+            const int64_t row = at.start + t, number = first + t / a.seg, ck = ckpt_at(row, number);
+            F2 h0[kDC][2], start[kDC][2];
+            float since[kDC];                          // of Delta, from the segment's start
             load_states<kDC, 4>(w.ckpt + ck * state, a, c, ch.end, n, h0);
-            if (at.tile > 0) {                         // over the local checkpoint, the state before the segment
-                F2 start[kDC][2];
-                load_states<kDC, 4>(w.ends + blockIdx.x * state, a, c, ch.end, n, start);
+            const bool later = t >= a.seg;             // its checkpoints are local ones
+            if (later) {
+                load_states<kDC, 4>(w.ends + number * state, a, c, ch.end, n, start);
 #pragma unroll
-                for (int i = 0; i < kDC; ++i) {
-                    const F2 s = both(c + i < ch.end ? w.csum[ck * a.D + c + i] : 0.f);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) h0[i][j] = fma2(ex2_2(mul2(A2[i][j], s)), start[i][j], h0[i][j]);
-                }
+                for (int i = 0; i < kDC; ++i) since[i] = c + i < ch.end ? w.csum[ck * a.D + c + i] : 0.f;
             }
             in.put(a, sm + S::bias, live, true, sm + S::delta, sm + S::u, sm + S::g);
             vb.put(sm + S::b);
             vc.put(sm + S::c);
             __syncthreads();
+            if (later)
+#pragma unroll
+                for (int i = 0; i < kDC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        h0[i][j] = fma2(decay2(A2[i][j], both(since[i])), start[i][j], h0[i][j]);
             if (t > t0) fetch(t - kChunk);
             const float2* pd = reinterpret_cast<const float2*>(sm + S::delta + own);
             const float2* pu = reinterpret_cast<const float2*>(sm + S::u + own);
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
                         const F2 dd = both(i ? d.y : d.x), uu = both(i ? u.y : u.x);
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            to[i][j] = fma2(ex2_2(mul2(A2[i][j], dd)), from[i][j], mul2(uu, b[j]));
+                            to[i][j] = fma2(decay2(A2[i][j], dd), from[i][j], mul2(uu, b[j]));
                     }
                 };
                 if (half)
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
                         F2 y, r, s;                    // terms of C h, dh B and log2(e) A w
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const F2 e = ex2_2(mul2(A2[i][j], d));
+                            const F2 e = decay2(A2[i][j], d);
                             dh[i][j] = fma2(g, cv[j], dh[i][j]);
                             y = j ? fma2(hs[k + 1][i][j], cv[j], y) : mul2(hs[k + 1][i][j], cv[j]);
                             r = j ? fma2(dh[i][j], b[j], r) : mul2(dh[i][j], b[j]);
@@ -530,23 +537,36 @@ __global__ void __launch_bounds__(256) ssm_backward_bc_kernel(const float* __res
 
 int main_width(const SsmArgs& a) { return kThreads / ssm_lanes(a.N, 4) * kDC; }
 
-// Tokens of a segment: one wave of the main kernel's blocks, or whole sequences where a batch has half a wave of them.
-// Packed sequences have up to n segments beside those of their tokens; the tokens get at least half the wave.
-int segment_of(const SsmArgs& a) {
+int local_width(const SsmArgs& a) { return kThreads / ssm_lanes(a.N, 8) * kDC; }
+
+// Tokens of a segment of the local kernel, and segments of a walk of the main one.  Walks: one wave of the main kernel's
+// blocks, or whole sequences where a batch has half a wave of them (packed sequences have up to n walks beside those of
+// their tokens; the tokens get at least half the wave).  The local kernel's blocks are wider, so fewer: its segments are
+// as many to a walk as fill its own wave.
+struct Cuts {
+    int seg, span;
+};
+Cuts cuts_of(const SsmArgs& a) {
     const int64_t blocks = ssm_blocks(a, main_width(a)), wave = kSms * kBlocksPerSm;
-    if (!a.cu && a.n * blocks >= wave / 2) return (int)((a.T + kChunk - 1) / kChunk * kChunk);
-    const int64_t all = std::max<int64_t>(wave / blocks, 1);
-    const int64_t cuts = a.cu ? std::max<int64_t>(all - a.n, (all + 1) / 2) : std::max<int64_t>(all / a.n, 1);
-    const int64_t tokens = a.cu ? a.total : a.T;
-    const int64_t seg = std::max<int64_t>((tokens + cuts - 1) / cuts, kMinSegment);
-    return (int)((seg + kChunk - 1) / kChunk * kChunk);
+    const int64_t tokens = a.cu ? a.total : a.T, n = a.n;
+    int64_t cuts = std::max<int64_t>(wave / blocks, 1);
+    if (a.cu) cuts = std::max(cuts - n, (cuts + 1) / 2);
+    else cuts = n * blocks >= wave / 2 ? 1 : std::max<int64_t>(cuts / n, 1);
+    const int64_t walk = std::max<int64_t>((tokens + cuts - 1) / cuts, kMinSegment);
+    const int64_t walks = (a.cu ? 1 : n) * ((tokens + walk - 1) / walk);
+    const int64_t span = std::max<int64_t>(
+        std::min(wave / std::max<int64_t>(walks * ssm_blocks(a, local_width(a)), 1), walk / kMinSegment), 1);
+    const int64_t seg = ((walk + span - 1) / span + kChunk - 1) / kChunk * kChunk;
+    return {(int)seg, (int)span};
 }
 
 size_t plan(const SsmArgs& a, float* base, Scratch* w) {
     const Seqs q{a.cu, a.total, a.T, (int)a.n};
-    const int64_t segments = tile_count(q, segment_of(a)), ckpts = a.total / kChunk + segments;
+    const Cuts cuts = cuts_of(a);
+    const int64_t segments = tile_count(q, cuts.seg), walks = tile_count(q, cuts.seg * cuts.span);
+    const int64_t ckpts = a.total / kChunk + segments;
     const int64_t D = a.D, DN = D * a.N, group_blocks = ssm_blocks(a, main_width(a)) / a.G;
-    const bool split = a.cu || segment_of(a) < a.T;
+    const bool split = a.cu || cuts.seg < a.T;
     size_t at = 0;
     const auto take = [&](int64_t floats) {
         float* p = base ? base + at : nullptr;
@@ -559,8 +579,8 @@ size_t plan(const SsmArgs& a, float* base, Scratch* w) {
     w->dends = take(split ? segments * DN : 0);
     w->sums = take(split ? segments * D : 0);
     w->part_bc = take(group_blocks * a.total * a.G * 2 * a.N);
-    w->part_a = take(segments * DN);
-    w->part_d = take(segments * 2 * D);
+    w->part_a = take(walks * DN);
+    w->part_d = take(walks * 2 * D);
     return at * sizeof(float);
 }
 
@@ -575,17 +595,18 @@ cudaError_t ssm_backward(const SsmArgs& a, const SsmTensors& t, const SsmGrads& 
     Scratch w;
     plan(a, workspace, &w);
     Ssm k = ssm_of(a, t);
-    k.seg = segment_of(a);
+    const Cuts cuts = cuts_of(a);
+    k.seg = cuts.seg;
     k.vec = (int64_t)a.D * (a.io == GDR_F32 ? 4 : 2) % 16 == 0;
     for (const void* p : {g.dy, (const void*)g.dx, (const void*)g.ddt, (const void*)g.dz})
         k.vec = k.vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    const unsigned segments = (unsigned)tile_count(k.q, k.seg);
+    const unsigned segments = (unsigned)tile_count(k.q, k.seg), walks = (unsigned)tile_count(k.q, k.seg * cuts.span);
     const bool split = a.cu || k.seg < a.T;
     cudaError_t e = ssm_types<8>(a.io, a.N, [&](auto io, auto lanes) {
         using IO = decltype(io);
-        constexpr int LN = decltype(lanes)::value, width = kThreads / LN * kDC;
+        constexpr int LN = decltype(lanes)::value;
         ssm_backward_local_kernel<IO, LN>
-            <<<dim3(segments, (unsigned)ssm_blocks(a, width)), kThreads, 0, s>>>(k, (const IO*)g.dy, w);
+            <<<dim3(segments, (unsigned)ssm_blocks(a, local_width(a))), kThreads, 0, s>>>(k, (const IO*)g.dy, w);
         return cudaGetLastError();
     });
     if (e == cudaSuccess && split) e = ssm_join(k, w.ends, w.dends, w.sums, g.dh_final, true, s);
@@ -598,7 +619,7 @@ cudaError_t ssm_backward(const SsmArgs& a, const SsmTensors& t, const SsmGrads& 
                                                  bytes))
             return x;
         ssm_backward_kernel<IO, LN>
-            <<<dim3(segments, (unsigned)ssm_blocks(a, main_width(a))), kThreads, bytes, s>>>(k, o, w);
+            <<<dim3(walks, (unsigned)ssm_blocks(a, main_width(a))), kThreads, bytes, s>>>(k, cuts.span, o, w);
         if (cudaError_t x = cudaGetLastError()) return x;
         const int64_t values = a.total * a.G * 2 * a.N;
         if (values)
@@ -608,10 +629,10 @@ cudaError_t ssm_backward(const SsmArgs& a, const SsmTensors& t, const SsmGrads& 
     });
     if (e != cudaSuccess) return e;
     const int64_t D = a.D, DN = D * a.N;
-    if (cudaError_t x = column_sum(w.part_a, segments, DN, DN, g.dA, 0, nullptr, s)) return x;
+    if (cudaError_t x = column_sum(w.part_a, walks, DN, DN, g.dA, 0, nullptr, s)) return x;
     if (g.dDk)
-        if (cudaError_t x = column_sum(w.part_d, segments, 2 * D, D, g.dDk, 0, nullptr, s)) return x;
-    if (g.dbias) return column_sum(w.part_d + D, segments, 2 * D, D, g.dbias, 0, nullptr, s);
+        if (cudaError_t x = column_sum(w.part_d, walks, 2 * D, D, g.dDk, 0, nullptr, s)) return x;
+    if (g.dbias) return column_sum(w.part_d + D, walks, 2 * D, D, g.dbias, 0, nullptr, s);
     return cudaSuccess;
 }
 
