@@ -4,6 +4,10 @@ Each translation unit under csrc/ is compiled in parallel into _build/, then
 linked into _build/libgdr.so (CUDA runtime linked statically, so loading the
 library needs no libcudart on the path and no GPU).  A unit is rebuilt only
 when it or a header under csrc/ or include/ is newer than its object file.
+
+binding/layer_binding.cpp, the torch binding of the layer operators, is a host
+file: it becomes _build/_gdr_layer.so with the host compiler against the
+installed torch's headers, beside the units of libgdr, which it links to.
 """
 from __future__ import annotations
 
@@ -11,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdr.so")
+BINDING_SRC = os.path.join(PKG, "binding", "layer_binding.cpp")
+BINDING = os.path.join(BUILD, "_gdr_layer.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -42,6 +49,20 @@ def _headers_mtime() -> float:
     return max((os.path.getmtime(h) for h in hs), default=0.0)
 
 
+def _binding_commands(obj: str, out: str):
+    """The compile and link commands of the layer binding, for the torch and Python that run this."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    cxx = shutil.which("g++") or "g++"
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE,
+             "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+             "-I", sysconfig.get_paths()["include"], "-I", cuda, "-c", BINDING_SRC, "-o", obj],
+            [cxx, "-shared", "-o", out, obj, "-L", BUILD, "-lgdr", "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda",
+             "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(home, "lib")])
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -55,20 +76,31 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr):
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
 
+    binding_obj = os.path.join(BUILD, "layer_binding.o")
+    compile_binding, link_binding = _binding_commands(binding_obj, BINDING + f".tmp{os.getpid()}")
+    new_binding = force or not os.path.exists(BINDING) or \
+        os.path.getmtime(BINDING) < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "gdr.h")))
+    units = len(jobs)
+    if new_binding:
+        jobs.append(compile_binding)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"the compiler failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
-    if jobs or not os.path.exists(LIB) or force:
+    if units or not os.path.exists(LIB) or force:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if new_binding:
+        run(link_binding)
+        os.replace(BINDING + f".tmp{os.getpid()}", BINDING)
     return LIB
 
 
