@@ -4,9 +4,10 @@
 //   its state, or zero.  The state it leaves is the last W - 1 inputs.
 //
 // Bound: memory, x read once and y written once.  A thread takes 4 neighbouring channels down a run of tokens with the
-// window of W inputs in registers, so each input is loaded once and the next 8 loads are in flight while the last ones
-// are used; only the W - 1 inputs before a run are read again.  (8 channels a thread took 168 registers, and a sixth of
-// the SM's warps did not keep enough loads in flight.)  Products go two channels at a time.
+// window of W inputs in registers, so each input is loaded once; only the W - 1 inputs before a run are read again.
+// The next 12 tokens are on their way into the thread's own column of shared memory while these 4 are used: held in
+// registers they cost occupancy (168 registers with 8 channels a thread, 92 with 4) and fewer were in flight.  Products
+// go two channels at a time.
 //
 // Gradient: with dp_t = dy_t act'(p_t), p_t formed again from x,
 //   dx_u = sum_j w_j dp_{u + W - 1 - j},  dw_j = sum_t dp_t x_{t - W + 1 + j},  db = sum_t dp_t.
@@ -75,16 +76,73 @@ __device__ __forceinline__ void load_taps(const Conv& a, int64_t c, F2 (&w)[W][P
     }
 }
 
-// silu(p) and its derivative
-__device__ __forceinline__ float silu(float p) { return p * sigmoid(p); }
-__device__ __forceinline__ float silu_slope(float p) {
-    const float s = sigmoid(p);
-    return s * fmaf(p, 1.f - s, 1.f);
+// silu of two, and its derivative
+__device__ __forceinline__ F2 silu2(F2 p) { return mul2(p, sigmoid2(p)); }
+__device__ __forceinline__ F2 silu_slope2(F2 p) {
+    const F2 s = sigmoid2(p);
+    return mul2(s, fma2(p, add2(both(1.f), mul2(s, both(-1.f))), both(1.f)));
 }
 
-template <typename IO, int W>
+// Groups of kGroup tokens; a run whose tokens are all there and aligned has kRing<IO> of them on their way, each thread's
+// in its own column of shared memory.
+constexpr int kGroup = 4;
+template <typename IO> constexpr int kRing = sizeof(IO) == 2 ? 4 : 2;
+template <typename IO> using Ring = RawN<IO, N>[kRing<IO> * kGroup][kThreads];
+
+template <bool FAST, typename IO>
+__device__ __forceinline__ void store_token(IO* p, const F2 (&v)[P], int64_t left, bool vec) {
+    float f[N];
+#pragma unroll
+    for (int k = 0; k < P; ++k) f[2 * k] = unpack2(v[k]).x, f[2 * k + 1] = unpack2(v[k]).y;
+    store_n(p, f, FAST ? N : left, FAST || vec);
+}
+
+// The run's outputs.  FAST: a whole run of aligned tokens.
+template <typename IO, int W, bool SILU, bool FAST>
+__device__ __forceinline__ void forward_run(const Conv& a, Ring<IO>& ring, const IO* xp, IO* yp, int run, int64_t left,
+                                            F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P]) {
+    constexpr int kBack = W - 1, S = kRing<IO>;
+    const auto ahead = [&](int i0, int slot) {
+        if (i0 < run)
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) copy_ahead(&ring[slot * kGroup + i][threadIdx.x], xp + (i0 + i) * a.x.ld);
+        copy_group();
+    };
+    if (FAST)
+#pragma unroll
+        for (int g = 0; g < S - 1; ++g) ahead(g * kGroup, g);
+    for (int i0 = 0, slot = 0; i0 < run; i0 += kGroup, slot = slot + 1 == S ? 0 : slot + 1) {
+        RawN<IO, N> raw[kGroup];
+        if (FAST) {
+            ahead(i0 + (S - 1) * kGroup, slot == 0 ? S - 1 : slot - 1);
+            copy_wait<S - 1>();
+        }
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            raw[i] = FAST ? ring[slot * kGroup + i][threadIdx.x]
+                          : load_n<N>(xp + (i0 + i) * a.x.ld, i0 + i < run ? left : 0, a.x.vec);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            pairs(raw[i], win[kBack]);
+            F2 o[P];
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                o[k] = b[k];
+#pragma unroll
+                for (int j = 0; j < W; ++j) o[k] = fma2(w[j][k], win[j][k], o[k]);
+#pragma unroll
+                for (int j = 0; j < kBack; ++j) win[j][k] = win[j + 1][k];
+                if (SILU) o[k] = silu2(o[k]);
+            }
+            store_token<FAST>(yp + (i0 + i) * a.D, o, i0 + i < run ? left : 0, a.vec);
+        }
+    }
+}
+
+template <typename IO, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __restrict__ y, IO* __restrict__ state_out) {
-    constexpr int kBack = W - 1, U = 8;
+    constexpr int kBack = W - 1;
+    __shared__ Ring<IO> ring;
     const int lane = threadIdx.x % a.lanes, sub = threadIdx.x / a.lanes;
     const int tile = a.run * (kThreads / a.lanes);
     const int64_t c = ((int64_t)blockIdx.y * a.lanes + lane) * N, left = a.D - c;
@@ -100,28 +158,10 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
     const IO* xp = reinterpret_cast<const IO*>(a.x.p) + (at.start + t0) * a.x.ld + c;
     IO* yp = y + (at.start + t0) * a.D + c;
     const int run = (int)min((int64_t)a.run, at.len - t0);
-    for (int i0 = 0; i0 < run; i0 += U) {
-        RawN<IO, N> raw[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) raw[i] = load_n<N>(xp + (i0 + i) * a.x.ld, i0 + i < run ? left : 0, a.x.vec);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            pairs(raw[i], win[kBack]);
-            float o[N];
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-                F2 p = b[k];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fma2(w[j][k], win[j][k], p);
-#pragma unroll
-                for (int j = 0; j < kBack; ++j) win[j][k] = win[j + 1][k];
-                const float2 f = unpack2(p);
-                o[2 * k] = a.silu ? silu(f.x) : f.x;
-                o[2 * k + 1] = a.silu ? silu(f.y) : f.y;
-            }
-            store_n(yp + (i0 + i) * a.D, o, i0 + i < run ? left : 0, a.vec);
-        }
-    }
+    if (run == a.run && left >= N && a.x.vec && a.vec)
+        forward_run<IO, W, SILU, true>(a, ring, xp, yp, a.run, left, win, w, b);
+    else
+        forward_run<IO, W, SILU, false>(a, ring, xp, yp, run, left, win, w, b);
     if (t0 == 0 && state_out)                 // the first run leaves the state, an empty sequence's too
 #pragma unroll
         for (int j = 0; j < kBack; ++j)
@@ -129,11 +169,105 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
                       input_at<IO>(a, at.seq, at.start, at.len - kBack + j, c, kBack), left, a.vec);
 }
 
-template <typename IO, int W>
+// Where a run's gradients go, counted from its first token: token i gives dp_i and completes dx of i - (W - 1).
+template <typename IO> struct BackwardRun {
+    const IO *x, *dy;
+    IO *dx, *d_state;             // d_state: the sequence's rows, one past the last
+    const IO* d_state_out;        // the sequence's rows, shifted so that [u] is the one of input u
+    int run, seen;                // tokens of the run; of them and the W - 1 after them those that exist
+    int from, kept;               // first input with a gradient to store; first that is in the state the sequence left
+};
+
+// FAST: a whole run of aligned tokens inside a sequence, far from both its ends.
+template <typename IO, int W, bool SILU, bool FAST>
+__device__ __forceinline__ void backward_run(const Conv& a, Ring<IO> (&ring)[2], const BackwardRun<IO>& r, int64_t left,
+                                             F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P], F2 (&dw)[W][P],
+                                             F2 (&db)[P]) {
+    constexpr int kBack = W - 1, S = kRing<IO>;
+    F2 dp[W][P];
+#pragma unroll
+    for (int j = 0; j < kBack; ++j)
+#pragma unroll
+        for (int k = 0; k < P; ++k) dp[j][k] = 0;
+    const auto ahead = [&](int i0, int slot) {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            if (i0 + i < r.seen) {
+                copy_ahead(&ring[0][slot * kGroup + i][threadIdx.x], r.x + (i0 + i) * a.x.ld);
+                copy_ahead(&ring[1][slot * kGroup + i][threadIdx.x], r.dy + (i0 + i) * a.D);
+            }
+        copy_group();
+    };
+    // token t: dp_t, and (OWN: a token of the run) its part of dw and db, then the gradient of input t - kBack
+    const auto token = [&](int t, const RawN<IO, N>& x, const RawN<IO, N>& y, bool own) {
+        const int u = t - kBack;
+        F2 o[P];
+        pairs(x, win[kBack]);
+        pairs(y, dp[kBack]);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            if (SILU) {
+                F2 p = b[k];
+#pragma unroll
+                for (int j = 0; j < W; ++j) p = fma2(w[j][k], win[j][k], p);
+                dp[kBack][k] = mul2(dp[kBack][k], silu_slope2(p));
+            }
+            if (!FAST && t >= r.seen) dp[kBack][k] = 0;    // not zero times an infinite input's slope
+        }
+        if (own)
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                db[k] = add2(db[k], dp[kBack][k]);
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][k] = fma2(dp[kBack][k], win[j][k], dw[j][k]);
+            }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            o[k] = mul2(w[0][k], dp[kBack][k]);
+#pragma unroll
+            for (int j = 1; j < W; ++j) o[k] = fma2(w[j][k], dp[kBack - j][k], o[k]);
+#pragma unroll
+            for (int j = 0; j < kBack; ++j) win[j][k] = win[j + 1][k], dp[j][k] = dp[j + 1][k];
+        }
+        if (u < r.from || (!FAST && u >= r.run)) return;
+        if (!FAST && u >= r.kept) {                        // the gradient that comes through the state it left
+            F2 e[P];
+            pairs(load_n<N>(r.d_state_out + (int64_t)u * a.D, left, a.vec), e);
+#pragma unroll
+            for (int k = 0; k < P; ++k) o[k] = add2(o[k], e[k]);
+        }
+        if (FAST || u >= 0) store_token<FAST>(r.dx + (int64_t)u * a.D, o, left, a.vec);
+        else store_token<FAST>(r.d_state + (int64_t)u * a.D, o, left, a.vec);
+    };
+    if (FAST) {
+#pragma unroll
+        for (int g = 0; g < S - 1; ++g) ahead(g * kGroup, g);
+        int slot = 0;
+        for (int i0 = 0; i0 < r.run; i0 += kGroup, slot = slot + 1 == S ? 0 : slot + 1) {
+            ahead(i0 + (S - 1) * kGroup, slot == 0 ? S - 1 : slot - 1);
+            copy_wait<S - 1>();
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+                token(i0 + i, ring[0][slot * kGroup + i][threadIdx.x], ring[1][slot * kGroup + i][threadIdx.x], true);
+        }
+        copy_wait<0>();
+#pragma unroll
+        for (int i = 0; i < kBack; ++i)
+            token(r.run + i, ring[0][slot * kGroup + i][threadIdx.x], ring[1][slot * kGroup + i][threadIdx.x], false);
+    } else {
+        for (int t = 0; t < r.run + kBack; ++t) {
+            const int64_t l = t < r.seen ? left : 0;
+            token(t, load_n<N>(r.x + t * a.x.ld, l, a.x.vec), load_n<N>(r.dy + t * a.D, l, a.vec), t < r.run);
+        }
+    }
+}
+
+template <typename IO, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads)
 conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d_state_out, IO* __restrict__ dx,
                      IO* __restrict__ d_state, float* __restrict__ partial) {
-    constexpr int kBack = W - 1, U = 4;
+    constexpr int kBack = W - 1;
+    __shared__ Ring<IO> ring[2];
     __shared__ float sums[kThreads][N * (W + 1) + 1];     // + 1: threads on different banks
     const int lane = threadIdx.x % a.lanes, sub = threadIdx.x / a.lanes, subs = kThreads / a.lanes;
     const int tile = a.run * subs;
@@ -149,73 +283,24 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
         for (int j = 0; j < W; ++j) dw[j][k] = 0;
     }
     if (at.seq >= 0 && left > 0 && (t0 < at.len || t0 == 0)) {
-        F2 win[W][P], dp[W][P], w[W][P], b[P];
+        F2 win[W][P], w[W][P], b[P];
         load_taps<W, IO>(a, c, w, b);
 #pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            pairs(input_at<IO>(a, at.seq, at.start, t0 - kBack + j, c, kBack), win[j]);
-#pragma unroll
-            for (int k = 0; k < P; ++k) dp[j][k] = 0;
-        }
-        // Counted from t0: token i gives dp_i and completes dx of i - kBack, for those of the run; the first run has the
-        // state's rows, before 0, too.
-        const int run = (int)min((int64_t)a.run, at.len - t0);
-        const int seen = (int)min((int64_t)run + kBack, at.len - t0);   // tokens of the walk that exist
-        const int from = t0 == 0 && d_state ? -kBack : 0;
-        const int kept = d_state_out ? (int)min(at.len - kBack - t0, (int64_t)run) : run;   // rows from here are in its state
-        const IO* xp = reinterpret_cast<const IO*>(a.x.p) + (at.start + t0) * a.x.ld + c;
-        const IO* yp = dy + (at.start + t0) * a.D + c;
-        IO* op = dx + (at.start + t0) * a.D + c;
-        for (int i0 = 0; i0 < run + kBack; i0 += U) {
-            RawN<IO, N> xr[U], yr[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int64_t l = i0 + i < seen ? left : 0;
-                xr[i] = load_n<N>(xp + (i0 + i) * a.x.ld, l, a.x.vec);
-                yr[i] = load_n<N>(yp + (i0 + i) * a.D, l, a.vec);
-            }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int t = i0 + i, u = t - kBack;
-                F2 o[P];
-                pairs(xr[i], win[kBack]);
-                pairs(yr[i], dp[kBack]);
-#pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    if (a.silu) {
-                        F2 p = b[k];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) p = fma2(w[j][k], win[j][k], p);
-                        const float2 f = unpack2(p);
-                        dp[kBack][k] = mul2(dp[kBack][k], pack2(silu_slope(f.x), silu_slope(f.y)));
-                    }
-                    if (t >= seen) dp[kBack][k] = 0;       // not zero times an infinite input's slope
-                    if (t < run) {
-                        db[k] = add2(db[k], dp[kBack][k]);
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][k] = fma2(dp[kBack][k], win[j][k], dw[j][k]);
-                    }
-                    o[k] = mul2(w[0][k], dp[kBack][k]);
-#pragma unroll
-                    for (int j = 1; j < W; ++j) o[k] = fma2(w[j][k], dp[kBack - j][k], o[k]);
-#pragma unroll
-                    for (int j = 0; j < kBack; ++j) win[j][k] = win[j + 1][k], dp[j][k] = dp[j + 1][k];
-                }
-                if (u < from || u >= run) continue;
-                if (u >= kept) {                           // the gradient that comes through the state it left
-                    F2 e[P];
-                    const int64_t row = t0 + u - (at.len - kBack);
-                    pairs(load_n<N>(d_state_out + ((int64_t)at.seq * kBack + row) * a.D + c, left, a.vec), e);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) o[k] = add2(o[k], e[k]);
-                }
-                float f[N];
-#pragma unroll
-                for (int k = 0; k < P; ++k) f[2 * k] = unpack2(o[k]).x, f[2 * k + 1] = unpack2(o[k]).y;
-                if (u >= 0) store_n(op + (int64_t)u * a.D, f, left, a.vec);
-                else store_n(d_state + ((int64_t)at.seq * kBack + kBack + u) * a.D + c, f, left, a.vec);
-            }
-        }
+        for (int j = 0; j < kBack; ++j) pairs(input_at<IO>(a, at.seq, at.start, t0 - kBack + j, c, kBack), win[j]);
+        const int64_t row = at.start + t0, rows = (int64_t)at.seq * kBack;
+        BackwardRun<IO> r;
+        r.x = reinterpret_cast<const IO*>(a.x.p) + row * a.x.ld + c;
+        r.dy = dy + row * a.D + c;
+        r.dx = dx + row * a.D + c;
+        r.d_state = d_state ? d_state + (rows + kBack) * a.D + c : nullptr;
+        r.d_state_out = d_state_out ? d_state_out + (rows + kBack - (at.len - t0)) * a.D + c : nullptr;
+        r.run = (int)min((int64_t)a.run, at.len - t0);
+        r.seen = (int)min((int64_t)r.run + kBack, at.len - t0);
+        r.from = t0 == 0 && d_state ? -kBack : 0;
+        r.kept = d_state_out ? (int)min(at.len - kBack - t0, (int64_t)r.run) : r.run;
+        const bool inside = r.seen == a.run + kBack && r.from == 0 && r.kept == a.run;
+        if (inside && left >= N && a.x.vec && a.vec) backward_run<IO, W, SILU, true>(a, ring, r, left, win, w, b, dw, db);
+        else backward_run<IO, W, SILU, false>(a, ring, r, left, win, w, b, dw, db);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -231,7 +316,7 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
         const int e = bias ? i - a.lanes * N * W : i, per = bias ? N : N * W;
         const int l = e / per, k = e % per;
         float s = 0.f;
-        for (int r = 0; r < subs; ++r) s += sums[r * a.lanes + l][(bias ? N * W : 0) + k];
+        for (int m = 0; m < subs; ++m) s += sums[m * a.lanes + l][(bias ? N * W : 0) + k];
         const int64_t first = (int64_t)blockIdx.y * a.lanes * per + e;
         if (first < (bias ? a.D : a.D * W)) mine[(bias ? a.D * W : 0) + first] = s;
     }
@@ -265,9 +350,8 @@ conv_step_kernel(Conv a, int64_t pool, const int* __restrict__ slots, IO* __rest
     }
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-        const float2 f = unpack2(b[k]);
-        o[2 * k] = a.silu ? silu(f.x) : f.x;
-        o[2 * k + 1] = a.silu ? silu(f.y) : f.y;
+        const float2 f = unpack2(a.silu ? silu2(b[k]) : b[k]);
+        o[2 * k] = f.x, o[2 * k + 1] = f.y;
     }
     store_n(y + row * a.D + c, o, left, a.vec);
 #pragma unroll
@@ -304,12 +388,13 @@ Conv conv_of(const ConvArgs& a, RowTensor x, const void* w, const void* b, const
     return k;
 }
 
-// Calls f with a value of the io type and the number of taps.
+// Calls f with a value of the io type, the number of taps and whether the output goes through silu.
 template <typename F> cudaError_t with_types(const ConvArgs& a, F f) {
+    const auto act = [&](auto io, auto W) { return a.silu ? f(io, W, std::true_type()) : f(io, W, std::false_type()); };
     const auto taps = [&](auto io) {
-        if (a.W == 2) return f(io, std::integral_constant<int, 2>());
-        if (a.W == 3) return f(io, std::integral_constant<int, 3>());
-        return f(io, std::integral_constant<int, 4>());
+        if (a.W == 2) return act(io, std::integral_constant<int, 2>());
+        if (a.W == 3) return act(io, std::integral_constant<int, 3>());
+        return act(io, std::integral_constant<int, 4>());
     };
     if (a.io == GDR_F32) return taps(float());
     if (a.io == GDR_BF16) return taps(__nv_bfloat16());
@@ -322,9 +407,9 @@ cudaError_t conv_forward(const ConvArgs& a, RowTensor x, const void* w, const vo
                          void* state_out, cudaStream_t s) {
     const Conv k = conv_of(a, x, w, b, state, {y, state_out});
     const int64_t tiles = tile_count(k.q, k.run * (kThreads / k.lanes));
-    return with_types(a, [&](auto io, auto taps) {
+    return with_types(a, [&](auto io, auto taps, auto silu) {
         using IO = decltype(io);
-        conv_forward_kernel<IO, decltype(taps)::value>
+        conv_forward_kernel<IO, decltype(taps)::value, decltype(silu)::value>
             <<<dim3((unsigned)tiles, channel_blocks(a.D, k.lanes)), kThreads, 0, s>>>(k, (IO*)y, (IO*)state_out);
         return cudaGetLastError();
     });
@@ -340,9 +425,9 @@ cudaError_t conv_backward(const ConvArgs& a, RowTensor x, const void* w, const v
                           float* partial, cudaStream_t s) {
     const Conv k = conv_of(a, x, w, b, state, {dy, d_state_out, dx, d_state});
     const int64_t tiles = conv_partial_rows(a);
-    const cudaError_t e = with_types(a, [&](auto io, auto taps) {
+    const cudaError_t e = with_types(a, [&](auto io, auto taps, auto silu) {
         using IO = decltype(io);
-        conv_backward_kernel<IO, decltype(taps)::value>
+        conv_backward_kernel<IO, decltype(taps)::value, decltype(silu)::value>
             <<<dim3((unsigned)tiles, channel_blocks(a.D, k.lanes)), kThreads, 0, s>>>(
                 k, (const IO*)dy, (const IO*)d_state_out, (IO*)dx, (IO*)d_state, partial);
         return cudaGetLastError();
@@ -354,7 +439,7 @@ cudaError_t conv_backward(const ConvArgs& a, RowTensor x, const void* w, const v
 cudaError_t conv_step(const ConvArgs& a, int64_t pool, const int* slots, RowTensor x, const void* w, const void* b,
                       void* state, void* y, cudaStream_t s) {
     const Conv k = conv_of(a, x, w, b, state, {y});
-    return with_types(a, [&](auto io, auto taps) {
+    return with_types(a, [&](auto io, auto taps, auto silu) {
         using IO = decltype(io);
         conv_step_kernel<IO, decltype(taps)::value>
             <<<dim3((unsigned)a.n, channel_blocks(a.D, kThreads)), kThreads, 0, s>>>(k, pool, slots, (IO*)state, (IO*)y);

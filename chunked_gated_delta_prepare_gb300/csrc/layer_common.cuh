@@ -87,6 +87,18 @@ template <typename IO, int N> __device__ __forceinline__ void widen(const RawN<I
     }
 }
 
+// An aligned vector on its way into the thread's own place in shared memory: no register holds it meanwhile.
+template <typename IO, int N> __device__ __forceinline__ void copy_ahead(RawN<IO, N>* to, const IO* from) {
+    static_assert(sizeof(RawN<IO, N>) == 8 || sizeof(RawN<IO, N>) == 16, "one copy");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "n"((int)sizeof(RawN<IO, N>))
+                 : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() {   // until at most LEFT groups are on their way
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 template <typename IO, int N>
 __device__ __forceinline__ void store_raw(IO* p, const RawN<IO, N>& r, int64_t left, bool vec) {
     if (vec && left >= N) {

@@ -283,57 +283,47 @@ ssm_join_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ dends, cons
     v[at(count - 1) * state + i] = h;
 }
 
-// One token of a row: LN lanes a channel, 4 states each, the state read and written once.
+// One token of a row: LN lanes a channel, 8 states each, the state read and written once.  What is left beside the
+// state's bytes (softplus, the gate, addresses) is a channel's, so 8 states a thread halve it against 4.
 template <typename IO, int LN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 ssm_step_kernel(Ssm a, int64_t pool, const int* __restrict__ slots, float* __restrict__ h, IO* __restrict__ y) {
-    const int q = threadIdx.x % LN, n = 4 * q, c = blockIdx.y * (256 / LN) + threadIdx.x / LN;
+    const int q = threadIdx.x % LN, n = 8 * q, c = blockIdx.y * (kThreads / LN) + threadIdx.x / LN;
     const int64_t row = blockIdx.x, slot = slots ? slots[row] : row;
+    const bool in = c < a.D;              // lanes past the last channel stay for the shuffles
     if (slot < 0 || slot >= pool) {
-        if (q == 0 && c < a.D) y[row * a.D + c] = from_f<IO>(0.f);
+        if (q == 0 && in) y[row * a.D + c] = from_f<IO>(0.f);
         return;
     }
-    const bool in = c < a.D;              // lanes past the last channel stay for the shuffles
-    float* hp = h + (slot * a.D + c) * a.N + n;
-    const float* Ap = a.A + (int64_t)c * a.N + n;
-    const bool whole = in && n + 4 <= a.N && (reinterpret_cast<uintptr_t>(hp) & 15) == 0;
-    float s[4], A[4];
-    if (whole) {
-        const float4 v = *reinterpret_cast<const float4*>(hp);
-        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = in && n + j < a.N ? hp[j] : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) A[j] = in && n + j < a.N ? Ap[j] * kLog2e : 0.f;
-    float x = 0.f, d = 0.f, o = 0.f;
+    float* hp = h + slot * a.D * a.N;
+    F2 s[1][4], A2[1][4], b[4], cv[4];
+    load_states<1, 8>(hp, a, c, a.D, n, s);
+    load_decay<1, 8>(a, c, a.D, n, A2);
+    const int g = in ? c / a.per : 0;
+    const bool vec = (a.N & 7) == 0;
+    pairs(load8(reinterpret_cast<const IO*>(a.B.p) + row * a.B.ld + g * a.N + n, a.N - n, vec && a.B.vec), b);
+    pairs(load8(reinterpret_cast<const IO*>(a.C.p) + row * a.C.ld + g * a.N + n, a.N - n, vec && a.C.vec), cv);
+    float x = 0.f, d = 0.f, z = 0.f;
     if (in) {
         x = to_f(reinterpret_cast<const IO*>(a.x.p)[row * a.x.ld + c]);
         d = step_size(a, to_f(reinterpret_cast<const IO*>(a.dt.p)[row * a.dt.ld + c]), c);
+        if (a.z.p) z = to_f(reinterpret_cast<const IO*>(a.z.p)[row * a.z.ld + c]);
     }
-    const int g = in ? c / a.per : 0;
-    const IO* Bp = reinterpret_cast<const IO*>(a.B.p) + row * a.B.ld + g * a.N + n;
-    const IO* Cp = reinterpret_cast<const IO*>(a.C.p) + row * a.C.ld + g * a.N + n;
+    const F2 dd = both(d), uu = both(x * d);
+    F2 sum = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (n + j >= a.N) continue;
-        s[j] = fmaf(decay(A[j], d), s[j], x * d * to_f(Bp[j]));
-        o = fmaf(s[j], to_f(Cp[j]), o);
+        s[0][j] = fma2(decay2(A2[0][j], dd), s[0][j], mul2(uu, b[j]));
+        sum = fma2(s[0][j], cv[j], sum);
     }
+    const float2 f = unpack2(sum);
+    float o = f.x + f.y;
 #pragma unroll
     for (int k = 1; k < LN; k *= 2) o += __shfl_xor_sync(0xffffffffu, o, k);
-    if (whole) *reinterpret_cast<float4*>(hp) = make_float4(s[0], s[1], s[2], s[3]);
-    else
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (in && n + j < a.N) hp[j] = s[j];
+    store_states<1, 8>(hp, a, c, a.D, n, s);
     if (q == 0 && in) {
         if (a.Dk) o = fmaf(a.Dk[c], x, o);
-        if (a.z.p) {
-            const float z = to_f(reinterpret_cast<const IO*>(a.z.p)[row * a.z.ld + c]);
-            o *= z * sigmoid(z);
-        }
+        if (a.z.p) o *= z * sigmoid(z);
         y[row * a.D + c] = from_f<IO>(o);
     }
 }
@@ -408,11 +398,11 @@ cudaError_t ssm_forward(const SsmArgs& a, const SsmTensors& t, void* y, float* h
 cudaError_t ssm_step(const SsmArgs& a, const SsmTensors& t, int64_t pool, const int* slots, float* h, void* y,
                      cudaStream_t s) {
     const Ssm k = ssm_of(a, t);
-    return ssm_types<4>(a.io, a.N, [&](auto io, auto lanes) {
+    return ssm_types<8>(a.io, a.N, [&](auto io, auto lanes) {
         using IO = decltype(io);
-        constexpr int LN = decltype(lanes)::value, per = 256 / LN;
-        ssm_step_kernel<IO, LN><<<dim3((unsigned)a.n, (unsigned)((a.D + per - 1) / per)), 256, 0, s>>>(k, pool, slots, h,
-                                                                                                      (IO*)y);
+        constexpr int LN = decltype(lanes)::value, per = kThreads / LN;
+        ssm_step_kernel<IO, LN>
+            <<<dim3((unsigned)a.n, (unsigned)((a.D + per - 1) / per)), kThreads, 0, s>>>(k, pool, slots, h, (IO*)y);
         return cudaGetLastError();
     });
 }
