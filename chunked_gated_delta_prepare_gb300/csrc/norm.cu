@@ -4,8 +4,8 @@
 //   y8 = e4m3(y / scale),  scale = max(amax / 448, 2^-126) over the row or over groups of its columns
 //
 // Bound: memory.  A row is read once and stays in registers (up to 4 vectors of 8 columns a thread) between the sum of
-// squares and the output; w stays in registers over all the rows of a block, and a block's next row is in flight while
-// it works on this one.  A row is held by 32 threads up to 1024
+// squares and the output; w stays in registers over all the rows of a block, whose next row is in flight while it works
+// on this one.  A row is held by 32 threads up to 1024
 // columns (four rows a block, sums by shuffles alone), by a block above that.  With fewer rows than the GPU has room
 // for blocks, a row is spread over more threads, one vector each, since then only the latency of one row counts.
 //
@@ -69,6 +69,62 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&y)[8], floa
             if (i < left) p[i] = (uint8_t)(q[i >> 1] >> (8 * (i & 1)));
     }
 }
+
+// The backward's rows: dy, r and dr of the next RING - 1 rows of a block are on their way into shared memory, each
+// thread's vectors in its own places, while the block works on one.  (With one row ahead in registers, as the forward
+// has it, the kernel took twice the time; the forward's two tensors are faster that way, 20 against 28 us at 8192 x
+// 2048.)  RING = 1: a row is loaded when it is its turn (few rows, rows not aligned, or rows too wide for the ring).
+constexpr int kRingBytes = 56 * 1024;     // of a block, so that three or more fit an SM
+template <typename IO, int NT, int VPT> constexpr int ring_of() {
+    constexpr int row = NT * VPT * 3 * (int)sizeof(Raw8<IO>);
+    return 4 * row <= kRingBytes ? 4 : 3 * row <= kRingBytes ? 3 : 2 * row <= kRingBytes ? 2 : 1;
+}
+
+template <typename IO, int NT, int VPT, int RING> struct Pipe {
+    const IO* base[3];            // the tensors, or nullptr
+    int64_t rows;
+    int D, tid, tpr;
+    bool vec;
+    uint4* ring;                  // [RING][3][VPT][16-byte pieces of a vector][NT]
+
+    __device__ __forceinline__ uint4* place(int slot, int t, int i, int part) const {
+        constexpr int parts = sizeof(IO) / 2;
+        return ring + ((((slot * 3 + t) * VPT + i) * parts + part) * NT + threadIdx.x);
+    }
+    // Starts row `row` towards its slot; a row that does not exist starts nothing.
+    __device__ __forceinline__ void ahead(int64_t row, int slot) const {
+        if (row < rows)
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                if (base[t])
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i) {
+                        const int c = (tid + i * tpr) * 8;
+                        if (c < D)
+#pragma unroll
+                            for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
+                                copy_ahead(reinterpret_cast<RawN<IO, 16 / sizeof(IO)>*>(place(slot, t, i, part)),
+                                           base[t] + row * D + c + part * (16 / (int)sizeof(IO)));
+                    }
+        copy_group();
+    }
+    // The thread's vectors of tensor t of the row; zeros past the row's end and for a row that does not exist.
+    __device__ __forceinline__ void take(int64_t row, int slot, int t, Raw8<IO> (&v)[VPT]) const {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (tid + i * tpr) * 8, left = row < rows ? D - c : 0;
+            if (RING == 1) {
+                v[i] = load8(base[t] + row * D + c, left, vec);
+            } else if (left > 0) {
+#pragma unroll
+                for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
+                    reinterpret_cast<uint4*>(&v[i])[part] = *place(slot, t, i, part);
+            } else {
+                v[i] = load8((const IO*)nullptr, 0, false);
+            }
+        }
+    }
+};
 
 // Blocks an SM that the register budget of a kernel leaves room for: 1024 threads at two vectors a thread, 512 at four.
 template <int TPR, int VPT> constexpr int blocks_per_sm() {
@@ -166,15 +222,16 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
     }
 }
 
-template <typename IO, int TPR, int VPT>
+template <typename IO, int TPR, int VPT, int RING>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, blocks_per_sm<TPR, VPT>() > 1 ? blocks_per_sm<TPR, VPT>() / 2 : 1)
 norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict__ r, const IO* __restrict__ w,
                      const IO* __restrict__ dr, IO* __restrict__ dx, float* __restrict__ partial, bool vec) {
-    constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
+    constexpr int RPB = TPR < 128 ? 128 / TPR : 1, NT = TPR * RPB;
+    extern __shared__ uint4 smem[];
     __shared__ float red[2 * 2 * 32];
     const int tid = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const int D = a.D;
-    Raw8<IO> wr[VPT], yr[VPT], rr[VPT], er[VPT];
+    Raw8<IO> wr[VPT];
     float dw[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -183,29 +240,25 @@ norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
-    const auto fetch = [&](int64_t row) {
+    const int64_t step = (int64_t)gridDim.x * RPB, first = (int64_t)blockIdx.x * RPB + slot;
+    const Pipe<IO, NT, VPT, RING> in{{dy, r, dr}, a.rows, D, tid, TPR, vec, smem};
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8, left = row < a.rows ? D - c : 0;
-            yr[i] = load8(dy + row * D + c, left, vec);
-            rr[i] = load8(r + row * D + c, left, vec);
-            if (dr) er[i] = load8(dr + row * D + c, left, vec);
-        }
-    };
-    fetch((int64_t)blockIdx.x * RPB + slot);
-    int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, ++turn) {
-        const int64_t row = row0 + slot;
+    for (int k = 0; k < RING - 1; ++k) in.ahead(first + k * step, k);
+    int turn = 0, at = 0;
+    for (int64_t row = first; row - slot < a.rows; row += step, ++turn, at = at + 1 == RING ? 0 : at + 1) {
         const bool live = row < a.rows;
-        Raw8<IO> yc[VPT], rc[VPT], ec[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) yc[i] = yr[i], rc[i] = rr[i], ec[i] = er[i];
-        fetch(row + (int64_t)gridDim.x * RPB);          // in flight while this row is worked on
+        Raw8<IO> yr[VPT], rr[VPT];
+        if (RING > 1) {
+            in.ahead(row + (RING - 1) * step, at == 0 ? RING - 1 : at - 1);
+            copy_wait<RING - 1>();
+        }
+        in.take(row, at, 0, yr);
+        in.take(row, at, 1, rr);
         float sum[2] = {0.f, 0.f};            // of s^2 and of w dy s
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float s[8], g[8], wf[8];
-            widen(rc[i], s), widen(yc[i], g), widen(wr[i], wf);
+            widen(rr[i], s), widen(yr[i], g), widen(wr[i], wf);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 sum[0] = fmaf(s[j], s[j], sum[0]);
@@ -215,12 +268,14 @@ norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict
         row_reduce<TPR, 2, false>(sum, red, turn);
         const float rstd = rsqrtf(sum[0] / (float)D + a.eps);
         const float back = sum[1] / (float)D * rstd * rstd;
+        Raw8<IO> er[VPT];
+        if (dr) in.take(row, at, 2, er);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * TPR) * 8;
             float s[8], g[8], wf[8], o[8];
-            widen(rc[i], s), widen(yc[i], g), widen(wr[i], wf);
-            if (dr) widen(ec[i], o);
+            widen(rr[i], s), widen(yr[i], g), widen(wr[i], wf);
+            if (dr) widen(er[i], o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 o[j] = fmaf(rstd, fmaf(-s[j], back, wf[j] * g[j]), dr ? o[j] : 0.f);
@@ -302,12 +357,21 @@ int64_t backward_grid(const NormArgs& a, Shape h) {
 template <typename IO, int TPR, int VPT>
 cudaError_t launch_backward(const NormArgs& a, const void* dy, const void* r, const void* w, const void* dr, void* dx,
                             float* partial, cudaStream_t s) {
-    constexpr int NT = TPR < 128 ? 128 : TPR;
+    constexpr int RPB = TPR < 128 ? 128 / TPR : 1, NT = TPR < 128 ? 128 : TPR, RING = ring_of<IO, NT, VPT>();
     bool vec = ((int64_t)a.D * sizeof(IO)) % 16 == 0;
     for (const void* p : {dy, r, w, dr, (const void*)dx}) vec = vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    norm_backward_kernel<IO, TPR, VPT><<<(int)backward_grid(a, {TPR, VPT}), NT, 0, s>>>(
-        a, (const IO*)dy, (const IO*)r, (const IO*)w, (const IO*)dr, (IO*)dx, partial, vec);
-    return cudaGetLastError();
+    const int64_t grid = backward_grid(a, {TPR, VPT});
+    const auto go = [&](auto ring) {
+        constexpr int R = decltype(ring)::value, bytes = R > 1 ? R * NT * VPT * 3 * (int)sizeof(Raw8<IO>) : 0;
+        const auto kernel = norm_backward_kernel<IO, TPR, VPT, R>;
+        if (bytes > 40 * 1024)
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+        kernel<<<(unsigned)grid, NT, bytes, s>>>(a, (const IO*)dy, (const IO*)r, (const IO*)w, (const IO*)dr, (IO*)dx,
+                                                 partial, vec);
+        return cudaGetLastError();
+    };
+    if (RING > 1 && a.D % 8 == 0 && vec && grid * RPB < a.rows) return go(std::integral_constant<int, RING>());
+    return go(std::integral_constant<int, 1>());
 }
 
 // Calls f with the shape's constants.

@@ -82,7 +82,7 @@ ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* _
 
     // Loads of a tile run one tile ahead, those of z from the tile's start.  Unit i of a thread: 8 channels of a token.
     const int col = threadIdx.x % V8 * 8, cc = ch.c0 + col, tok = threadIdx.x / V8;
-    const bool vec8 = (cc & 7) == 0;
+    const bool vec8 = cc % (16 / (int)sizeof(IO)) == 0;
     Raw8<IO> dt_r[U], x_r[U], x_now[U], z_r[U];
     IO b_r[M], c_r[M];
     const auto fetch = [&](int64_t t) {

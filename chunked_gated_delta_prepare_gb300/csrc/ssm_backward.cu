@@ -56,7 +56,7 @@ template <typename IO, int T, int W> struct Units {
 
     __device__ __forceinline__ void fetch(const Ssm& a, const IO* dyp, const Channels& ch, int64_t row, int live) {
         const int cc = ch.c0 + col;
-        const bool vec8 = (cc & 7) == 0;
+        const bool vec8 = cc % (16 / (int)sizeof(IO)) == 0;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int k = tok + i * kStep, left = k < live ? ch.end - cc : 0;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
     const int q = threadIdx.x % LN, n = 4 * q, own = threadIdx.x / LN * kDC, c = ch.c0 + own;
     const int64_t state = (int64_t)a.D * a.N;
     const int col4 = threadIdx.x % W4 * 4, cc = ch.c0 + col4, tok4 = threadIdx.x / W4;
-    const bool vec4 = (cc & 7) == 0 || (cc & 7) == 4;
+    const bool vec4 = (cc & 3) == 0;
     const int left = ch.end - cc;
 
     F2 dA[kDC][2];
