@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 8;           // tokens staged in shared memory
-constexpr int kMinSegment = 64;
+constexpr int kMinSegment = 32;
 constexpr int kBlocksPerSm = 3;
 
 // Channels of a thread (with a lane a channel 4 would make the tiles of a block too wide) and of a block.

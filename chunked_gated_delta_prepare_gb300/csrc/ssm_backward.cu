@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kChunk = 16, kHalf = 8;
 constexpr int kDC = 2;                        // channels of a thread
-constexpr int kMinSegment = 64;
+constexpr int kMinSegment = 32;
 constexpr int kBlocksPerSm = 3;
 constexpr float kLn2 = 0.6931471805599453f;
 
