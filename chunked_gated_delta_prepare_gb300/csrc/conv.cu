@@ -76,13 +76,6 @@ __device__ __forceinline__ void load_taps(const Conv& a, int64_t c, F2 (&w)[W][P
     }
 }
 
-// silu of two, and its derivative
-__device__ __forceinline__ F2 silu2(F2 p) { return mul2(p, sigmoid2(p)); }
-__device__ __forceinline__ F2 silu_slope2(F2 p) {
-    const F2 s = sigmoid2(p);
-    return mul2(s, fma2(p, add2(both(1.f), mul2(s, both(-1.f))), both(1.f)));
-}
-
 // Groups of kGroup tokens; a run whose tokens are all there and aligned has kRing<IO> of them on their way, each thread's
 // in its own column of shared memory.
 constexpr int kGroup = 4;

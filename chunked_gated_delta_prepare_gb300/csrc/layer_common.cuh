@@ -189,6 +189,13 @@ __device__ __forceinline__ F2 rcp_2(F2 v) {
 }
 __device__ __forceinline__ F2 sigmoid2(F2 x) { return rcp_2(add2(both(1.f), ex2_2(mul2(x, both(-kLog2e))))); }
 
+// silu of two, and its derivative
+__device__ __forceinline__ F2 silu2(F2 p) { return mul2(p, sigmoid2(p)); }
+__device__ __forceinline__ F2 silu_slope2(F2 p) {
+    const F2 s = sigmoid2(p);
+    return mul2(s, fma2(p, add2(both(1.f), mul2(s, both(-1.f))), both(1.f)));
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN where either is
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));

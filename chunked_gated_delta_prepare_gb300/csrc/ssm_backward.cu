@@ -31,7 +31,7 @@ constexpr int kThreads = 128;
 constexpr int kChunk = 16, kHalf = 8;
 constexpr int kDC = 2;                        // channels of a thread
 constexpr int kMinSegment = 32;
-constexpr int kBlocksPerSm = 3;
+constexpr int kLocalPerSm = 3, kMainPerSm = 2;   // blocks on an SM
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Everything the kernels pass on: see plan().
@@ -142,7 +142,7 @@ __device__ __forceinline__ void load_channels(const float* p, const Channels& ch
 // Checkpoints of each segment from a zero state (the first segment of a sequence: from h0, so exact), what it leaves,
 // its sum of Delta, and the gradient its own tokens send to the state before it.  2 channels x 8 states a thread.
 template <typename IO, int LN>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, kLocalPerSm)
 ssm_backward_local_kernel(Ssm a, const IO* __restrict__ dy, Scratch w) {
     constexpr int T = 8, W = kThreads / LN * kDC, NP = 8 * LN;
     __shared__ float4 s_delta[T * W / 4], s_u[T * W / 4], s_g[T * W / 4], s_b[T * NP / 4], s_c[T * NP / 4], s_bias[W / 4];
@@ -244,22 +244,50 @@ template <typename IO> struct Grads {
     float* dh0;
 };
 
+// The sum of LN neighbouring floats in shared memory.
+template <int LN> __device__ __forceinline__ float lanes_total(const float* p) {
+    if constexpr (LN == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(p);
+        return f.x + f.y;
+    } else {
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < LN; m += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(p + m);
+            s += (f.x + f.y) + (f.z + f.w);
+        }
+        return s;
+    }
+}
+
+template <typename IO> __device__ __forceinline__ void store_pairs(IO* p, const F2 (&v)[4], int left, bool vec) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[2 * j] = unpack2(v[j]).x, f[2 * j + 1] = unpack2(v[j]).y;
+    store_n(p, f, left, vec);
+}
+
 // Shared memory of the main kernel, in floats.  terms_bc: dB and dC terms [token of the half][B or C][thread], 4 states
-// each; terms_n: r, y and sum A w, [token of the half][which][channel of the thread][thread].
+// each; terms_n: r, y and sum A w, [token of the chunk][which][channel of the thread][thread].
+// The terms of one token, value and channel parity: group g = thread / LN (2 channels) at term_at<LN>(g), so that the
+// writers, and the readers of 4 neighbouring groups, both meet all banks.
+constexpr int kTerms = 4 * (32 + 8);
+template <int LN> __device__ __forceinline__ int term_at(int g) { return g % 4 * (32 + 8) + g / 4 * LN; }
+
 template <int LN> struct MainTiles {
     static constexpr int W = kThreads / LN * kDC, NP = 4 * LN;
     static constexpr int delta = 0, u = delta + kChunk * W, g = u + kChunk * W, b = g + kChunk * W, c = b + kChunk * NP,
                          bias = c + kChunk * NP, D = bias + W, terms_bc = D + W,
-                         terms_n = terms_bc + kHalf * 2 * kThreads * 4, total = terms_n + kHalf * 3 * kDC * kThreads;
+                         terms_n = terms_bc + kHalf * 2 * kThreads * 4, total = terms_n + kChunk * 3 * kDC * kTerms;
     static_assert(terms_bc % 4 == 0 && terms_n % 4 == 0, "16-byte pieces");
 };
 
 // span: segments (of the local kernel) of a block's walk.
 template <typename IO, int LN>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ssm a, int span, Grads<IO> o, Scratch w) {
+__global__ void __launch_bounds__(kThreads, kMainPerSm) ssm_backward_kernel(Ssm a, int span, Grads<IO> o, Scratch w) {
     using S = MainTiles<LN>;
-    constexpr int W = S::W, NP = S::NP, W4 = W / 4;
-    constexpr int U4 = kHalf * W4 <= kThreads ? 1 : kHalf * W4 / kThreads;     // 4-channel units of a thread in half a chunk
+    constexpr int W = S::W, NP = S::NP;
+    using In = Units<IO, kChunk, W>;
     extern __shared__ float4 smem4[];
     float* sm = reinterpret_cast<float*>(smem4);
     const int walk = a.seg * span;
@@ -267,28 +295,35 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
     const Channels ch = block_channels(a, W);
     const int q = threadIdx.x % LN, n = 4 * q, own = threadIdx.x / LN * kDC, c = ch.c0 + own;
     const int64_t state = (int64_t)a.D * a.N;
-    const int col4 = threadIdx.x % W4 * 4, cc = ch.c0 + col4, tok4 = threadIdx.x / W4;
-    const bool vec4 = (cc & 3) == 0;
-    const int left = ch.end - cc;
 
-    F2 dA[kDC][2];
-    float dD[4], dbias[4];
+    In in;
+    const int cc = ch.c0 + in.col, left = ch.end - cc;
+    const bool vec8 = cc % (16 / (int)sizeof(IO)) == 0;
+    F2 dA[kDC][2], dD[4], dbias[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) dA[0][j] = dA[1][j] = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dD[j] = dbias[j] = 0.f;
+    for (int j = 0; j < 4; ++j) dD[j] = dbias[j] = 0;
 
     if (at.seq >= 0) {
         const int64_t t0 = at.tile * walk, t1 = min(t0 + walk, at.len);
         const int64_t first = first_tile(a.q, at.seq, a.seg);          // the sequence's first segment
         int64_t t = t1 > t0 ? t0 + (t1 - t0 - 1) / kChunk * kChunk : t0 - 1;
-        Units<IO, kChunk, W> in;
         Values<IO, kChunk, NP> vb, vc;
+        F2 ckpt[kDC][2], start[kDC][2];                // the state before a chunk: its checkpoint, and in a later segment,
+        float since[kDC];                              // whose checkpoints are local, the state before that decayed since
         const auto fetch = [&](int64_t from) {
             const int live = (int)min((int64_t)kChunk, t1 - from);
-            in.fetch(a, o.dy, ch, at.start + from, live);
-            vb.fetch(a, a.B, ch.group, at.start + from, live);
-            vc.fetch(a, a.C, ch.group, at.start + from, live);
+            const int64_t row = at.start + from, number = first + from / a.seg, ck = ckpt_at(row, number);
+            load_states<kDC, 4>(w.ckpt + ck * state, a, c, ch.end, n, ckpt);
+            if (from >= a.seg) {
+                load_states<kDC, 4>(w.ends + number * state, a, c, ch.end, n, start);
+#pragma unroll
+                for (int i = 0; i < kDC; ++i) since[i] = c + i < ch.end ? w.csum[ck * a.D + c + i] : 0.f;
+            }
+            in.fetch(a, o.dy, ch, row, live);
+            vb.fetch(a, a.B, ch.group, row, live);
+            vc.fetch(a, a.C, ch.group, row, live);
         };
         if (t >= t0) fetch(t);
         load_channels(a.bias, ch, W, sm + S::bias);
@@ -303,26 +338,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
 
         for (; t >= t0; t -= kChunk) {
             const int live = (int)min((int64_t)kChunk, t1 - t);
-            const int64_t row = at.start + t, number = first + t / a.seg, ck = ckpt_at(row, number);
-            F2 h0[kDC][2], start[kDC][2];
-            float since[kDC];                          // of Delta, from the segment's start
-            load_states<kDC, 4>(w.ckpt + ck * state, a, c, ch.end, n, h0);
-            const bool later = t >= a.seg;             // its checkpoints are local ones
-            if (later) {
-                load_states<kDC, 4>(w.ends + number * state, a, c, ch.end, n, start);
-#pragma unroll
-                for (int i = 0; i < kDC; ++i) since[i] = c + i < ch.end ? w.csum[ck * a.D + c + i] : 0.f;
-            }
+            const int64_t row = at.start + t;
             in.put(a, sm + S::bias, live, true, sm + S::delta, sm + S::u, sm + S::g);
             vb.put(sm + S::b);
             vc.put(sm + S::c);
+            const In now = in;                         // what the elementwise end needs of this chunk
+            F2 h0[kDC][2];
+#pragma unroll
+            for (int i = 0; i < kDC; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    h0[i][j] = t < a.seg ? ckpt[i][j]
+                                         : fma2(decay2(A2[i][j], both(since[i])), start[i][j], ckpt[i][j]);
             __syncthreads();
-            if (later)
-#pragma unroll
-                for (int i = 0; i < kDC; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        h0[i][j] = fma2(decay2(A2[i][j], both(since[i])), start[i][j], h0[i][j]);
             if (t > t0) fetch(t - kChunk);
             const float2* pd = reinterpret_cast<const float2*>(sm + S::delta + own);
             const float2* pu = reinterpret_cast<const float2*>(sm + S::u + own);
@@ -332,19 +360,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
 #pragma unroll 1
             for (int half = live > kHalf ? 1 : 0; half >= 0; --half) {
                 const int base = half * kHalf, tokens = min(kHalf, live - base);
-                // what the elementwise end needs of the half's tokens, on its way meanwhile
-                RawN<IO, 4> x_r[U4], dt_r[U4], dy_r[U4], z_r[U4];
-#pragma unroll
-                for (int i = 0; i < U4; ++i) {
-                    const int k = tok4 + i * (kThreads / W4), l = k < tokens ? left : 0;
-                    const int64_t r = row + base + k;
-                    x_r[i] = load_n<4>(reinterpret_cast<const IO*>(a.x.p) + r * a.x.ld + cc, l, a.x.vec && vec4);
-                    dt_r[i] = load_n<4>(reinterpret_cast<const IO*>(a.dt.p) + r * a.dt.ld + cc, l, a.dt.vec && vec4);
-                    if (a.z.p) {
-                        dy_r[i] = load_n<4>(o.dy + r * a.D + cc, l, a.vec && vec4);
-                        z_r[i] = load_n<4>(reinterpret_cast<const IO*>(a.z.p) + r * a.z.ld + cc, l, a.z.vec && vec4);
-                    }
-                }
                 F2 hs[kHalf + 1][kDC][2];              // the states before each token of the half, and after the last
 #pragma unroll
                 for (int i = 0; i < kDC; ++i)
@@ -366,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
                     for (int k = 0; k < kHalf; ++k) step(k, hs[0], hs[0]);
 #pragma unroll
                 for (int k = 0; k < kHalf; ++k) step(base + k, hs[k], hs[k + 1]);
+                if (half == 0 && live > kHalf) __syncthreads();        // the later half's dB and dC terms are used up
                 F2 dAh[kDC][2];                        // dA of the half: short sums first keep its rounding small
 #pragma unroll
                 for (int i = 0; i < kDC; ++i) dAh[i][0] = dAh[i][1] = 0;
@@ -375,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
                     const float2 d2 = pd[tk * W / 2], u2 = pu[tk * W / 2], g2 = pg[tk * W / 2];
                     const F2 b[2] = {pb[tk * NP / 2], pb[tk * NP / 2 + 1]}, cv[2] = {pc[tk * NP / 2], pc[tk * NP / 2 + 1]};
                     F2 dB[2], dC[2];
-                    float* tn = sm + S::terms_n + k * 3 * kDC * kThreads + threadIdx.x;
+                    float* tn = sm + S::terms_n + tk * 3 * kDC * kTerms + term_at<LN>(threadIdx.x / LN) + q;
 #pragma unroll
                     for (int i = 0; i < kDC; ++i) {
                         const F2 d = both(i ? d2.y : d2.x), u = both(i ? u2.y : u2.x), g = both(i ? g2.y : g2.x);
@@ -394,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
                             dAh[i][j] = fma2(d, wt, dAh[i][j]);
                         }
                         const float2 fr = unpack2(r), fy = unpack2(y), fs = unpack2(s);
-                        tn[(0 * kDC + i) * kThreads] = fr.x + fr.y;
-                        tn[(1 * kDC + i) * kThreads] = fy.x + fy.y;
-                        tn[(2 * kDC + i) * kThreads] = fs.x + fs.y;
+                        tn[(0 * kDC + i) * kTerms] = fr.x + fr.y;
+                        tn[(1 * kDC + i) * kTerms] = fy.x + fy.y;
+                        tn[(2 * kDC + i) * kTerms] = fs.x + fs.y;
                     }
                     ulonglong2* tb = reinterpret_cast<ulonglong2*>(sm + S::terms_bc) + k * 2 * kThreads + threadIdx.x;
                     tb[0] = make_ulonglong2(dB[0], dB[1]);
@@ -415,109 +431,101 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) ssm_backward_kernel(Ss
                 for (int i = 0; i < (outs + kThreads - 1) / kThreads; ++i) {
                     const int out = (threadIdx.x + i * kThreads) / parts, part = threadIdx.x % parts;
                     const int qq = out % LN, bc = out / LN % 2, k = out / LN / 2;
-                    const float4* p = reinterpret_cast<const float4*>(sm + S::terms_bc) + (k * 2 + bc) * kThreads + qq;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const ulonglong2* p = reinterpret_cast<const ulonglong2*>(sm + S::terms_bc) + (k * 2 + bc) * kThreads + qq;
+                    F2 lo = 0, hi = 0;
 #pragma unroll
                     for (int j = 0; j < kThreads / LN / parts; ++j) {
-                        const float4 f = p[(j * parts + part) * LN];
-                        v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+                        const ulonglong2 f = p[(j * parts + part) * LN];
+                        lo = add2(lo, f.x), hi = add2(hi, f.y);
                     }
+                    const float2 f0 = unpack2(lo), f1 = unpack2(hi);
+                    float v[4] = {f0.x, f0.y, f1.x, f1.y};
 #pragma unroll
-                    for (int m = 1; m < parts; m *= 2) {
-                        v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
-                        v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
-                        v.z += __shfl_xor_sync(0xffffffffu, v.z, m);
-                        v.w += __shfl_xor_sync(0xffffffffu, v.w, m);
-                    }
+                    for (int m = 1; m < parts; m *= 2)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], m);
                     if (part == 0 && k < tokens) {
                         const int m = 4 * qq;
                         float* to = w.part_bc +
                                     ((((int64_t)ch.block * a.q.total + row + base + k) * a.G + ch.group) * 2 + bc) * a.N + m;
                         if ((a.N & 3) == 0 && m < a.N) {
-                            *reinterpret_cast<float4*>(to) = v;
+                            *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
                         } else {
-                            const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                if (m + j < a.N) to[j] = f[j];
+                                if (m + j < a.N) to[j] = v[j];
                         }
                     }
                 }
-                // the elementwise end: 4 channels of a token a unit
+            }
+            // the elementwise end: 8 channels of a token a unit, pairs of channels packed
 #pragma unroll
-                for (int i = 0; i < U4; ++i) {
-                    const int k = tok4 + i * (kThreads / W4);
-                    if (k >= tokens || left <= 0) continue;
-                    float v[3][4];                     // r, y, sum A w: channels 4 .. of 2 of each of two threads' groups
+            for (int i = 0; i < In::U; ++i) {
+                const int k = in.tok + i * In::kStep;
+                if (k >= live || left <= 0) continue;
+                F2 v[3][4];                            // r, y, sum A w
 #pragma unroll
-                    for (int j = 0; j < 3; ++j)
+                for (int j = 0; j < 3; ++j)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float* p = sm + S::terms_n + ((k * 3 + j) * kDC + x % 2) * kThreads + (col4 + x) / 2 * LN;
-                            float f[LN];
-                            if constexpr (LN % 4 == 0) {
+                    for (int x = 0; x < 8; x += 2) {   // channels x and x + 1 are one thread's two
+                        const float* p = sm + S::terms_n + (k * 3 + j) * kDC * kTerms + term_at<LN>((in.col + x) / 2);
+                        float f[2];
 #pragma unroll
-                                for (int m = 0; m < LN; m += 4) {
-                                    const float4 f4 = *reinterpret_cast<const float4*>(p + m);
-                                    f[m] = f4.x, f[m + 1] = f4.y, f[m + 2] = f4.z, f[m + 3] = f4.w;
-                                }
-                            } else {
-                                const float2 f2 = *reinterpret_cast<const float2*>(p);
-                                f[0] = f2.x, f[1] = f2.y;
-                            }
-                            v[j][x] = f[0];
-#pragma unroll
-                            for (int m = 1; m < LN; ++m) v[j][x] += f[m];
-                        }
-                    const float4 delta4 = *reinterpret_cast<const float4*>(sm + S::delta + (base + k) * W + col4);
-                    const float4 g4 = *reinterpret_cast<const float4*>(sm + S::g + (base + k) * W + col4);
-                    const float4 D4 = *reinterpret_cast<const float4*>(sm + S::D + col4);
-                    const float4 bias4 = *reinterpret_cast<const float4*>(sm + S::bias + col4);
-                    const float delta[4] = {delta4.x, delta4.y, delta4.z, delta4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
-                    const float D[4] = {D4.x, D4.y, D4.z, D4.w}, bias[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
-                    float x[4], raw[4], dy[4], z[4], out[4];
-                    widen(x_r[i], x);
-                    widen(dt_r[i], raw);
-                    const int64_t to = (row + base + k) * a.D + cc;
-                    if (a.z.p) {
-                        widen(dy_r[i], dy);
-                        widen(z_r[i], z);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float sig = sigmoid(z[j]), pre = a.Dk ? fmaf(D[j], x[j], v[1][j]) : v[1][j];
-                            out[j] = dy[j] * pre * sig * fmaf(z[j], 1.f - sig, 1.f);
-                        }
-                        store_n(o.dz + to, out, left, a.vec && vec4);
+                        for (int m = 0; m < 2; ++m) f[m] = lanes_total<LN>(p + m * kTerms);
+                        v[j][x / 2] = pack2(f[0], f[1]);
                     }
-                    float ddt[4];
+                const F2* delta = reinterpret_cast<const F2*>(sm + S::delta + k * W + in.col);
+                const F2* g = reinterpret_cast<const F2*>(sm + S::g + k * W + in.col);
+                const F2* D = reinterpret_cast<const F2*>(sm + S::D + in.col);
+                const F2* bias = reinterpret_cast<const F2*>(sm + S::bias + in.col);
+                F2 x[4], raw[4], out[4];
+                pairs(now.x[i], x);
+                pairs(now.dt[i], raw);
+                const int64_t to = (row + k) * a.D + cc;
+                if (a.z.p) {
+                    F2 dy[4], z[4];
+                    pairs(now.dy[i], dy);
+                    pairs(now.z[i], z);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        out[j] = v[0][j] * delta[j];
-                        if (a.Dk) out[j] = fmaf(D[j], g[j], out[j]);
-                        ddt[j] = fmaf(v[0][j], x[j], kLn2 * v[2][j]);
-                        if (a.softplus) ddt[j] *= sigmoid(raw[j] + bias[j]);
-                        dD[j] = fmaf(g[j], x[j], dD[j]);
-                        dbias[j] += ddt[j];
+                        const F2 pre = a.Dk ? fma2(D[j], x[j], v[1][j]) : v[1][j];
+                        out[j] = mul2(mul2(dy[j], pre), silu_slope2(z[j]));
                     }
-                    store_n(o.dx + to, out, left, a.vec && vec4);
-                    store_n(o.ddt + to, ddt, left, a.vec && vec4);
+                    store_pairs(o.dz + to, out, left, a.vec && vec8);
                 }
-                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    out[j] = mul2(v[0][j], delta[j]);
+                    if (a.Dk) out[j] = fma2(D[j], g[j], out[j]);
+                }
+                store_pairs(o.dx + to, out, left, a.vec && vec8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    out[j] = fma2(v[0][j], x[j], mul2(both(kLn2), v[2][j]));
+                    if (a.softplus) out[j] = mul2(out[j], sigmoid2(add2(raw[j], bias[j])));
+                    dD[j] = fma2(g[j], x[j], dD[j]);
+                    dbias[j] = add2(dbias[j], out[j]);
+                }
+                store_pairs(o.ddt + to, out, left, a.vec && vec8);
             }
+            __syncthreads();
         }
         if (at.tile == 0 && o.dh0) store_states<kDC, 4>(o.dh0 + at.seq * state, a, c, ch.end, n, dh);
     }
     store_states<kDC, 4>(w.part_a + blockIdx.x * state, a, c, ch.end, n, dA);
     // dDk and the bias: over the threads that moved the same channels, in order
-    float4* sums = reinterpret_cast<float4*>(sm + S::terms_bc);
-    sums[threadIdx.x] = make_float4(dD[0], dD[1], dD[2], dD[3]);
-    sums[kThreads + threadIdx.x] = make_float4(dbias[0], dbias[1], dbias[2], dbias[3]);
+    ulonglong2* sums = reinterpret_cast<ulonglong2*>(sm + S::terms_bc);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        sums[2 * threadIdx.x + j] = make_ulonglong2(dD[2 * j], dD[2 * j + 1]);
+        sums[2 * (kThreads + threadIdx.x) + j] = make_ulonglong2(dbias[2 * j], dbias[2 * j + 1]);
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * W; i += kThreads) {
         const int which = i / W, x = i % W;
         float v = 0.f;
-        for (int m = 0; m < kThreads / W4; ++m)
-            v += reinterpret_cast<const float*>(sums)[(which * kThreads + m * W4) * 4 + x];
+        for (int m = 0; m < kThreads / In::V8; ++m)
+            v += reinterpret_cast<const float*>(sums)[(which * kThreads + m * In::V8) * 8 + x];
         if (ch.c0 + x < ch.end) w.part_d[((int64_t)blockIdx.x * 2 + which) * a.D + ch.c0 + x] = v;
     }
 }
@@ -539,23 +547,35 @@ int main_width(const SsmArgs& a) { return kThreads / ssm_lanes(a.N, 4) * kDC; }
 
 int local_width(const SsmArgs& a) { return kThreads / ssm_lanes(a.N, 8) * kDC; }
 
-// Tokens of a segment of the local kernel, and segments of a walk of the main one.  Walks: one wave of the main kernel's
-// blocks, or whole sequences where a batch has half a wave of them (packed sequences have up to n walks beside those of
-// their tokens; the tokens get at least half the wave).  The local kernel's blocks are wider, so fewer: its segments are
-// as many to a walk as fill its own wave.
+// Tokens of a segment of the local kernel, and segments of a walk of the main one.
+//
+// Walks: a batch's sequences are cut where the waves of blocks times the tokens of a walk are least (kWalkStart tokens for
+// a walk's start, about what a block takes before its first chunk); 7 walks of 293 tokens of a sequence measured 10 %
+// less time than 2 of 1024 that left a sixth of the GPU idle.  Packed sequences, whose lengths the host does not know,
+// have one wave, at least half of it for their tokens, the rest for the up to n walks that their ends add.  The local
+// kernel's blocks are wider, so fewer: its segments are as many to a walk as fill its own wave.
+constexpr int kWalkStart = 32, kMostCuts = 64;
 struct Cuts {
     int seg, span;
 };
 Cuts cuts_of(const SsmArgs& a) {
-    const int64_t blocks = ssm_blocks(a, main_width(a)), wave = kSms * kBlocksPerSm;
+    const int64_t blocks = ssm_blocks(a, main_width(a)), wave = kSms * kMainPerSm;
     const int64_t tokens = a.cu ? a.total : a.T, n = a.n;
-    int64_t cuts = std::max<int64_t>(wave / blocks, 1);
-    if (a.cu) cuts = std::max(cuts - n, (cuts + 1) / 2);
-    else cuts = n * blocks >= wave / 2 ? 1 : std::max<int64_t>(cuts / n, 1);
+    int64_t cuts = 1;
+    if (a.cu) {
+        const int64_t all = std::max<int64_t>(wave / blocks, 1);
+        cuts = std::max(all - n, (all + 1) / 2);
+    } else {
+        const auto cost = [&](int64_t c) {
+            return (n * c * blocks + wave - 1) / wave * ((tokens + c - 1) / c + kWalkStart);
+        };
+        for (int64_t c = 2; c <= kMostCuts && tokens / c >= kMinSegment; ++c)
+            if (cost(c) < cost(cuts)) cuts = c;
+    }
     const int64_t walk = std::max<int64_t>((tokens + cuts - 1) / cuts, kMinSegment);
     const int64_t walks = (a.cu ? 1 : n) * ((tokens + walk - 1) / walk);
-    const int64_t span = std::max<int64_t>(
-        std::min(wave / std::max<int64_t>(walks * ssm_blocks(a, local_width(a)), 1), walk / kMinSegment), 1);
+    const int64_t wanted = kSms * kLocalPerSm / std::max<int64_t>(walks * ssm_blocks(a, local_width(a)), 1);
+    const int64_t span = std::max<int64_t>(std::min(wanted, walk / kMinSegment), 1);
     const int64_t seg = ((walk + span - 1) / span + kChunk - 1) / kChunk * kChunk;
     return {(int)seg, (int)span};
 }
