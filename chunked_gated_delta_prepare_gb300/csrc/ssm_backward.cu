@@ -650,10 +650,9 @@ cudaError_t ssm_backward(const SsmArgs& a, const SsmTensors& t, const SsmGrads& 
     if (e != cudaSuccess) return e;
     const int64_t D = a.D, DN = D * a.N;
     if (cudaError_t x = column_sum(w.part_a, walks, DN, DN, g.dA, 0, nullptr, s)) return x;
-    if (g.dDk)
-        if (cudaError_t x = column_sum(w.part_d, walks, 2 * D, D, g.dDk, 0, nullptr, s)) return x;
-    if (g.dbias) return column_sum(w.part_d + D, walks, 2 * D, D, g.dbias, 0, nullptr, s);
-    return cudaSuccess;
+    if (!g.dDk && !g.dbias) return cudaSuccess;
+    if (!g.dDk) return column_sum(w.part_d + D, walks, 2 * D, D, g.dbias, 0, nullptr, s);
+    return column_sum(w.part_d, walks, 2 * D, D, g.dDk, g.dbias ? D : 0, g.dbias, s);
 }
 
 }  // namespace layer
