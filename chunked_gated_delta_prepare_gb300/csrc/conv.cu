@@ -49,7 +49,7 @@ struct Conv {
 template <typename IO>
 __device__ __forceinline__ RawN<IO, N> input_at(const Conv& a, int seq, int64_t start, int64_t u, int64_t c, int back) {
     const int64_t left = a.D - c;
-    if (u >= 0) return load_n<N>(reinterpret_cast<const IO*>(a.x.p) + (start + u) * a.x.ld + c, left, a.x.vec);
+    if (u >= 0) return load_n<N>(reinterpret_cast<const IO*>(a.x.p) + (start + u) * a.x.ld + c, left, a.x.vec, c);
     if (a.state)
         return load_n<N>(reinterpret_cast<const IO*>(a.state) + ((int64_t)seq * back + back + u) * a.D + c, left, a.vec);
     return load_n<N>((const IO*)nullptr, 0, false);
@@ -92,8 +92,8 @@ __device__ __forceinline__ void store_token(IO* p, const F2 (&v)[P], int64_t lef
 
 // The run's outputs.  FAST: a whole run of aligned tokens.
 template <typename IO, int W, bool SILU, bool FAST>
-__device__ __forceinline__ void forward_run(const Conv& a, Ring<IO>& ring, const IO* xp, IO* yp, int run, int64_t left,
-                                            F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P]) {
+__device__ __forceinline__ void forward_run(const Conv& a, Ring<IO>& ring, const IO* xp, IO* yp, int run,
+                                            int64_t before, int64_t left, F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P]) {
     constexpr int kBack = W - 1, S = kRing<IO>;
     const auto ahead = [&](int i0, int slot) {
         if (i0 < run)
@@ -113,7 +113,7 @@ __device__ __forceinline__ void forward_run(const Conv& a, Ring<IO>& ring, const
 #pragma unroll
         for (int i = 0; i < kGroup; ++i)
             raw[i] = FAST ? ring[slot * kGroup + i][threadIdx.x]
-                          : load_n<N>(xp + (i0 + i) * a.x.ld, i0 + i < run ? left : 0, a.x.vec);
+                          : load_n<N>(xp + (i0 + i) * a.x.ld, i0 + i < run ? left : 0, a.x.vec, before);
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
             pairs(raw[i], win[kBack]);
@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
     IO* yp = y + (at.start + t0) * a.D + c;
     const int run = (int)min((int64_t)a.run, at.len - t0);
     if (run == a.run && left >= N && a.x.vec && a.vec)
-        forward_run<IO, W, SILU, true>(a, ring, xp, yp, a.run, left, win, w, b);
+        forward_run<IO, W, SILU, true>(a, ring, xp, yp, a.run, c, left, win, w, b);
     else
-        forward_run<IO, W, SILU, false>(a, ring, xp, yp, run, left, win, w, b);
+        forward_run<IO, W, SILU, false>(a, ring, xp, yp, run, c, left, win, w, b);
     if (t0 == 0 && state_out)                 // the first run leaves the state, an empty sequence's too
 #pragma unroll
         for (int j = 0; j < kBack; ++j)
@@ -168,6 +168,7 @@ template <typename IO> struct BackwardRun {
     IO *dx, *d_state;             // d_state: the sequence's rows, one past the last
     const IO* d_state_out;        // the sequence's rows, shifted so that [u] is the one of input u
     int run, seen;                // tokens of the run; of them and the W - 1 after them those that exist
+    int64_t before;               // channels of a row in front of the thread's
     int from, kept;               // first input with a gradient to store; first that is in the state the sequence left
 };
 
@@ -250,7 +251,8 @@ __device__ __forceinline__ void backward_run(const Conv& a, Ring<IO> (&ring)[2],
     } else {
         for (int t = 0; t < r.run + kBack; ++t) {
             const int64_t l = t < r.seen ? left : 0;
-            token(t, load_n<N>(r.x + t * a.x.ld, l, a.x.vec), load_n<N>(r.dy + t * a.D, l, a.vec), t < r.run);
+            token(t, load_n<N>(r.x + t * a.x.ld, l, a.x.vec, r.before), load_n<N>(r.dy + t * a.D, l, a.vec, r.before),
+                  t < r.run);
         }
     }
 }
@@ -287,6 +289,7 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
         r.dx = dx + row * a.D + c;
         r.d_state = d_state ? d_state + (rows + kBack) * a.D + c : nullptr;
         r.d_state_out = d_state_out ? d_state_out + (rows + kBack - (at.len - t0)) * a.D + c : nullptr;
+        r.before = c;
         r.run = (int)min((int64_t)a.run, at.len - t0);
         r.seen = (int)min((int64_t)r.run + kBack, at.len - t0);
         r.from = t0 == 0 && d_state ? -kBack : 0;
@@ -332,7 +335,7 @@ conv_step_kernel(Conv a, int64_t pool, const int* __restrict__ slots, IO* __rest
     RawN<IO, N> in[W];
 #pragma unroll
     for (int j = 0; j < kBack; ++j) in[j] = load_own<N>(state + (slot * kBack + j) * a.D + c, left, a.vec);
-    in[kBack] = load_n<N>(reinterpret_cast<const IO*>(a.x.p) + row * a.x.ld + c, left, a.x.vec);
+    in[kBack] = load_n<N>(reinterpret_cast<const IO*>(a.x.p) + row * a.x.ld + c, left, a.x.vec, c);
     F2 w[W][P], b[P], v[P];
     load_taps<W, IO>(a, c, w, b);
 #pragma unroll

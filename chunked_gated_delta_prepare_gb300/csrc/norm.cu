@@ -114,7 +114,7 @@ template <typename IO, int NT, int VPT, int RING> struct Pipe {
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * tpr) * 8, left = row < rows ? D - c : 0;
             if (RING == 1) {
-                v[i] = load8(base[t] + row * D + c, left, vec);
+                v[i] = load8(base[t] + row * D + c, left, vec, c);
             } else if (left > 0) {
 #pragma unroll
                 for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
@@ -155,8 +155,8 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * TPR) * 8, left = row < a.rows ? D - c : 0;
-            xr[i] = load8(xp + c, left, x.vec);
-            if (two) sr[i] = load8(sp + c, left, res.vec);
+            xr[i] = load8(xp + c, left, x.vec, c);
+            if (two) sr[i] = load8(sp + c, left, res.vec, c);
         }
     };
     fetch((int64_t)blockIdx.x * RPB + slot);

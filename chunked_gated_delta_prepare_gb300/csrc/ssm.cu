@@ -90,8 +90,8 @@ ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* _
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int k = tok + i * (kThreads / V8), left = t + k < t1 && k < kTile ? ch.end - cc : 0;
-            dt_r[i] = load8(reinterpret_cast<const IO*>(a.dt.p) + (row + k) * a.dt.ld + cc, left, a.dt.vec && vec8);
-            x_r[i] = load8(reinterpret_cast<const IO*>(a.x.p) + (row + k) * a.x.ld + cc, left, a.x.vec && vec8);
+            dt_r[i] = load8(reinterpret_cast<const IO*>(a.dt.p) + (row + k) * a.dt.ld + cc, left, a.dt.vec && vec8, cc);
+            x_r[i] = load8(reinterpret_cast<const IO*>(a.x.p) + (row + k) * a.x.ld + cc, left, a.x.vec && vec8, cc);
         }
 #pragma unroll
         for (int i = 0; i < M; ++i) {
@@ -163,7 +163,7 @@ ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* _
             for (int i = 0; i < U; ++i) {
                 const int k = tok + i * (kThreads / V8);
                 z_r[i] = load8(reinterpret_cast<const IO*>(a.z.p) + (row + k) * a.z.ld + cc, k < live ? ch.end - cc : 0,
-                               a.z.vec && vec8);
+                               a.z.vec && vec8, cc);
             }
 #pragma unroll 1
         for (int k = 0; k < live; ++k) {

@@ -60,12 +60,12 @@ template <typename IO, int T, int W> struct Units {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int k = tok + i * kStep, left = k < live ? ch.end - cc : 0;
-            dt[i] = load8(reinterpret_cast<const IO*>(a.dt.p) + (row + k) * a.dt.ld + cc, left, a.dt.vec && vec8);
-            x[i] = load8(reinterpret_cast<const IO*>(a.x.p) + (row + k) * a.x.ld + cc, left, a.x.vec && vec8);
+            dt[i] = load8(reinterpret_cast<const IO*>(a.dt.p) + (row + k) * a.dt.ld + cc, left, a.dt.vec && vec8, cc);
+            x[i] = load8(reinterpret_cast<const IO*>(a.x.p) + (row + k) * a.x.ld + cc, left, a.x.vec && vec8, cc);
             if (dyp) {
-                dy[i] = load8(dyp + (row + k) * a.D + cc, left, a.vec && vec8);
+                dy[i] = load8(dyp + (row + k) * a.D + cc, left, a.vec && vec8, cc);
                 if (a.z.p) z[i] = load8(reinterpret_cast<const IO*>(a.z.p) + (row + k) * a.z.ld + cc, left,
-                                        a.z.vec && vec8);
+                                        a.z.vec && vec8, cc);
             }
         }
     }
