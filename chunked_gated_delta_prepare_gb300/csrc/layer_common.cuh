@@ -27,6 +27,22 @@ template <typename IO, int N> struct alignas(sizeof(IO) * N < 16 ? sizeof(IO) * 
 };
 template <typename IO> using Raw8 = RawN<IO, 8>;
 
+// A vector that starts `off` bytes into aligned blocks, from the blocks' words (the last one is only ever shifted out).
+template <int N, typename IO, int WORDS> __device__ __forceinline__ RawN<IO, N> shift_words(uint32_t (&w)[WORDS], int off) {
+    if (WORDS > N * (int)sizeof(IO) / 4 + 3 && (off & 8))
+#pragma unroll
+        for (int i = 0; i < WORDS - 2; ++i) w[i] = w[i + 2];
+    if (off & 4)
+#pragma unroll
+        for (int i = 0; i < WORDS - 1; ++i) w[i] = w[i + 1];
+    RawN<IO, N> r;
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(IO) / 4; ++i)
+        reinterpret_cast<uint32_t*>(&r)[i] =
+            sizeof(IO) == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+    return r;
+}
+
 // A vector that starts at any element: the aligned blocks around it, shifted together.  Every block read must lie in the
 // row, so a vector of it must come before and another after.
 template <int N, typename IO> __device__ __forceinline__ RawN<IO, N> load_shifted(const IO* p) {
@@ -34,6 +50,7 @@ template <int N, typename IO> __device__ __forceinline__ RawN<IO, N> load_shifte
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     const int off = (int)(at % block);
     uint32_t w[words + 1];
+    w[words] = 0;
     if constexpr (block == 8) {
         const uint2* s = reinterpret_cast<const uint2*>(at - off);
 #pragma unroll
@@ -43,19 +60,7 @@ template <int N, typename IO> __device__ __forceinline__ RawN<IO, N> load_shifte
 #pragma unroll
         for (int i = 0; i < words / 4; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = __ldg(s + i);
     }
-    w[words] = 0;                                       // only ever shifted out
-    if (block == 16 && (off & 8))
-#pragma unroll
-        for (int i = 0; i < words - 2; ++i) w[i] = w[i + 2];
-    if (off & 4)
-#pragma unroll
-        for (int i = 0; i < words - 1; ++i) w[i] = w[i + 1];
-    RawN<IO, N> r;
-#pragma unroll
-    for (int i = 0; i < bytes / 4; ++i)
-        reinterpret_cast<uint32_t*>(&r)[i] =
-            sizeof(IO) == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
-    return r;
+    return shift_words<N, IO>(w, off);
 }
 
 // Elements [0, N) of p; only the first `left` exist (left <= 0: none), the rest read as zero.  vec: the row starts on a
