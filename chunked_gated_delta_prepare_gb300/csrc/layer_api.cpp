@@ -54,7 +54,9 @@ gdr_status done(cudaError_t e, const char* variant) {
     return GDR_OK;
 }
 
-constexpr int64_t kMaxTokens = int64_t{1} << 31;   // rows of any tensor here: 32-bit cu_seqlens, 31-bit grids
+// Rows of any tensor, and sequences: the kernels number up to two tiles a token in 31 bits (one for the tokens, one for a
+// sequence's end), and round the lengths of segments up in them.
+constexpr int64_t kMaxTokens = int64_t{1} << 30;
 
 gdr_status norm_args(const gdr_norm_problem* p, NormArgs* a) {
     if (!p) return GDR_ERR_NULL;
@@ -92,7 +94,7 @@ gdr_status ssm_args(const gdr_ssm_problem* p, const int32_t* cu, bool packed, Ss
     if (!known_dtype(p->io_dtype)) return GDR_ERR_DTYPE;
     const int64_t tokens = token_axis(p->n, p->T, p->total, packed);
     if (tokens < 0 || p->D < 1 || p->D > kMaxChannels || p->N < 1 || p->N > kSsmMaxN) return GDR_ERR_SHAPE;
-    // the blocks of channels of all groups are one extent of a grid
+    // the blocks of channels of all groups, and those of all channels, are one extent of a grid
     if (p->G < 1 || p->D % p->G || p->G * ((p->D / p->G + kSsmMinWidth - 1) / kSsmMinWidth) > 65535)
         return GDR_ERR_SHAPE;
     for (int64_t ld : {p->x_ld, p->dt_ld, p->z_ld})

@@ -2,7 +2,8 @@
 //
 // They work on vectors of 8 (or 4) neighbouring channels of one token.  A row may start at any element: where its
 // address is not a multiple of 16 bytes, a vector comes from the aligned blocks around it (4 times fewer trips through
-// the L1 cache than element by element), and goes out in aligned words; at a row's ends the elements move one by one.  Whether a tensor's rows are all aligned is decided on the host (RowTensor::vec).
+// the L1 cache than element by element), and goes out in aligned words; at a row's ends the elements move one by one.
+// Whether a tensor's rows are all aligned is decided on the host (RowTensor::vec).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -77,7 +77,7 @@ cudaError_t delta_step(const DeltaStepArgs& a, const int* slots, const void* q, 
 
 // ---- ssm.cu
 constexpr int kSsmMaxN = 64;
-constexpr int kSsmMinWidth = 32;   // channels of a block at the most states
+constexpr int kSsmMinWidth = 16;   // channels of the smallest block: of the step's and the gradient's at more than 32 states
 struct SsmArgs {
     int64_t n, T, total;   // cu: total tokens on the packed axis; else n * T
     const int* cu;

@@ -568,9 +568,9 @@ GDR_API gdr_status gdr_varlen_backward(const gdr_problem* p, const int32_t* cu_s
  * - A tensor of tokens is [tokens, columns] with the columns contiguous.  Inputs
  *   that are usually slices of a wider projection have a row stride in elements
  *   (`*_ld`; 0 means contiguous).  Outputs are contiguous.  These pointers need
- *   only their element's alignment (GDR_ERR_ALIGN otherwise): rows on 16-byte
- *   boundaries move in 16-byte pieces, others element by element.  Workspaces are
- *   256-byte aligned.
+ *   only their element's alignment (GDR_ERR_ALIGN otherwise).  Rows on 16-byte
+ *   boundaries move fastest.  Workspaces are 256-byte aligned.
+ * - Tokens, rows and sequences number less than 2^30 each.
  * - Weights of the norm and the convolution have the io dtype; their gradients
  *   are fp32, summed in a fixed order: the same call gives the same bits.
  * - Sequences: a batch of n sequences of T tokens each (cu_seqlens NULL, tokens

@@ -152,3 +152,20 @@ def test_the_binding_is_built_and_refuses_host_tensors(lib):
               lambda: layer.norm_forward(None, w), lambda: layer.norm_forward([1.0], w)):
         with pytest.raises(ValueError):
             f()
+
+
+@pytest.mark.parametrize("name", ["gdr_ssm_forward", "gdr_ssm_backward", "gdr_ssm_step"])
+def test_channels_beyond_the_grid(lib, name):
+    """At more than 32 states a block has as few as 16 channels: 2^20 of them are one block more than a grid takes."""
+    make, ptrs = CALLS[name]
+    assert call(name, make(D=1 << 20, N=64, n=1, T=1), ptrs.values()) == SHAPE
+
+
+@pytest.mark.parametrize("name", ["gdr_conv_forward", "gdr_ssm_forward", "gdr_norm_forward"])
+def test_tokens_beyond_31_bit_tiles(lib, name):
+    make, ptrs = CALLS[name]
+    kw = dict(rows=1 << 30) if make is norm else dict(n=1 << 30, T=1)
+    assert call(name, make(**kw), ptrs.values()) == SHAPE
+    if make is not norm:
+        packed = make(n=1, total=1 << 30)
+        assert call(name, packed, (ptrs | dict(cu=16)).values()) == SHAPE
