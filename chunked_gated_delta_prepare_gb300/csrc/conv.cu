@@ -41,8 +41,8 @@ struct Conv {
     const void *w, *b, *state;
     int lanes, run;  // row_lanes; tokens of a thread
     bool silu;
-    bool vec;        // rows of D elements on 16-byte boundaries in every contiguous tensor
-    bool vec_w;      // w and b on 16-byte boundaries
+    bool vec;        // rows of D elements on vectors' boundaries in every contiguous tensor (x.vec: in x)
+    bool vec_w;      // w and b on 16-byte boundaries, which a thread's taps keep
 };
 
 // Input u of a sequence: a token (u >= 0), a row of its state, or zero.
@@ -76,44 +76,115 @@ __device__ __forceinline__ void load_taps(const Conv& a, int64_t c, F2 (&w)[W][P
     }
 }
 
-// Groups of kGroup tokens; a run whose tokens are all there and aligned has kRing<IO> of them on their way, each thread's
-// in its own column of shared memory.
+// Groups of kGroup tokens are used while kRing groups lie in, or are on their way into, the thread's own column of shared
+// memory.  VEC: rows of aligned vectors, one copy each.  Other rows start anywhere; there a slot of 16 bytes takes the
+// aligned words around a vector, and the neighbours' outputs are joined to aligned vectors.
 constexpr int kGroup = 4;
-template <typename IO> constexpr int kRing = sizeof(IO) == 2 ? 4 : 2;
-template <typename IO> using Ring = RawN<IO, N>[kRing<IO> * kGroup][kThreads];
+template <typename IO, bool VEC> constexpr int kRing = VEC && sizeof(IO) == 2 ? 4 : 2;
+struct alignas(16) Words {
+    uint32_t w[4];
+};
+template <typename IO, bool VEC> using Slot = std::conditional_t<VEC, RawN<IO, N>, Words>;
+template <typename IO, bool VEC> using Ring = Slot<IO, VEC>[kRing<IO, VEC> * kGroup][kThreads];
 
-template <bool FAST, typename IO>
-__device__ __forceinline__ void store_token(IO* p, const F2 (&v)[P], int64_t left, bool vec) {
+// The thread's place in its row.
+struct Place {
+    int64_t c, left;      // first channel; channels from there on
+    int lane, lanes;      // lanes that share a token, neighbours of one warp
+    unsigned mask;        // those of them that have channels
+};
+
+// p's elements [0, min(left, N)) on their way; base: the tensor's first element.
+template <bool VEC, typename IO>
+__device__ __forceinline__ void fetch(Slot<IO, VEC>* to, const IO* p, const Place& at, const IO* base) {
+    if constexpr (VEC) {
+        copy_ahead(to, p);
+    } else if constexpr (sizeof(IO) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < at.left) copy_word(to->w + i, p + i, 4);
+    } else {
+        const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1);      // the first word holds the element before p too
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int64_t have = at.left - (2 * i - odd);
+            if (i == 0 && odd && p == base) reinterpret_cast<IO*>(to)[1] = p[0];    // nothing lies before p
+            else if (have > 0 && (i < 2 || odd)) copy_word(to->w + i, p + (2 * i - odd), have > 1 ? 4 : 2);
+        }
+    }
+}
+template <bool VEC, typename IO>
+__device__ __forceinline__ RawN<IO, N> take(const Slot<IO, VEC>& slot, const IO* p) {
+    if constexpr (VEC) {
+        return slot;
+    } else {
+        const Words s = slot;
+        uint32_t w[5] = {s.w[0], s.w[1], s.w[2], s.w[3], 0};
+        return shift_words<N, IO>(w, sizeof(IO) == 2 ? (int)(reinterpret_cast<uintptr_t>(p) & 2) : 0);
+    }
+}
+
+// The thread's channels of a token to p.  Rows that start anywhere: every lane of a token calls it at the same time; each
+// takes from the one before it what shares the aligned vector in which its own channels begin.
+template <bool VEC, typename IO>
+__device__ __forceinline__ void store_token(IO* p, const F2 (&v)[P], const Place& at) {
     float f[N];
 #pragma unroll
     for (int k = 0; k < P; ++k) f[2 * k] = unpack2(v[k]).x, f[2 * k + 1] = unpack2(v[k]).y;
-    store_n(p, f, FAST ? N : left, FAST || vec);
+    if constexpr (VEC) {
+        store_n(p, f, N, true);
+    } else {
+        constexpr int block = N * (int)sizeof(IO), words = block / 4;
+        RawN<IO, N> own;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) from_f2(own.e + i, f[i], f[i + 1]);
+        const int off = (int)(reinterpret_cast<uintptr_t>(p) % block), gone = off / (int)sizeof(IO);
+        uint32_t w[2 * words + 1];
+        w[2 * words] = 0;
+#pragma unroll
+        for (int i = 0; i < words; ++i) {
+            w[words + i] = reinterpret_cast<const uint32_t*>(&own)[i];
+            w[i] = __shfl_up_sync(at.mask, w[words + i], 1, at.lanes);
+        }
+        // elements [-gone, N - gone) of p
+        const RawN<IO, N> r = off ? shift_words<N, IO>(w, block - off) : own;
+        const bool whole = at.left >= N - gone && (at.lane > 0 || gone == 0);
+        if (whole) store_raw(p - gone, r, N, true);
+        const bool end = at.lane == at.lanes - 1 || at.left <= N;       // no lane after it takes its last elements
+        if (!whole || (end && gone)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (!whole && (i >= gone || at.lane > 0) && i < gone + at.left) p[i - gone] = r.e[i];
+#pragma unroll
+            for (int i = 1; i < N; ++i)
+                if (end && i >= N - gone && i < at.left) p[i] = own.e[i];
+        }
+    }
 }
 
 // The run's outputs.  FAST: a whole run of aligned tokens.
-template <typename IO, int W, bool SILU, bool FAST>
-__device__ __forceinline__ void forward_run(const Conv& a, Ring<IO>& ring, const IO* xp, IO* yp, int run,
-                                            int64_t before, int64_t left, F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P]) {
-    constexpr int kBack = W - 1, S = kRing<IO>;
+template <typename IO, int W, bool SILU, bool VEC, bool FAST>
+__device__ __forceinline__ void forward_run(const Conv& a, Ring<IO, VEC>& ring, const IO* xp, IO* yp, int run,
+                                            const Place& at, F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P]) {
+    constexpr int kBack = W - 1, S = kRing<IO, VEC>;
+    const IO* base = reinterpret_cast<const IO*>(a.x.p);
     const auto ahead = [&](int i0, int slot) {
         if (i0 < run)
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) copy_ahead(&ring[slot * kGroup + i][threadIdx.x], xp + (i0 + i) * a.x.ld);
+            for (int i = 0; i < kGroup; ++i)
+                if (FAST || i0 + i < run)
+                    fetch<VEC>(&ring[slot * kGroup + i][threadIdx.x], xp + (i0 + i) * a.x.ld, at, base);
         copy_group();
     };
-    if (FAST)
 #pragma unroll
-        for (int g = 0; g < S - 1; ++g) ahead(g * kGroup, g);
+    for (int g = 0; g < S - 1; ++g) ahead(g * kGroup, g);
     for (int i0 = 0, slot = 0; i0 < run; i0 += kGroup, slot = slot + 1 == S ? 0 : slot + 1) {
         RawN<IO, N> raw[kGroup];
-        if (FAST) {
-            ahead(i0 + (S - 1) * kGroup, slot == 0 ? S - 1 : slot - 1);
-            copy_wait<S - 1>();
-        }
+        ahead(i0 + (S - 1) * kGroup, slot == 0 ? S - 1 : slot - 1);
+        copy_wait<S - 1>();
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-            raw[i] = FAST ? ring[slot * kGroup + i][threadIdx.x]
-                          : load_n<N>(xp + (i0 + i) * a.x.ld, i0 + i < run ? left : 0, a.x.vec, before);
+        for (int i = 0; i < kGroup; ++i)       // past the run's end: what the slot held
+            raw[i] = take<VEC>(ring[slot * kGroup + i][threadIdx.x], xp + (i0 + i) * a.x.ld);
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
             pairs(raw[i], win[kBack]);
@@ -127,18 +198,30 @@ __device__ __forceinline__ void forward_run(const Conv& a, Ring<IO>& ring, const
                 for (int j = 0; j < kBack; ++j) win[j][k] = win[j + 1][k];
                 if (SILU) o[k] = silu2(o[k]);
             }
-            store_token<FAST>(yp + (i0 + i) * a.D, o, i0 + i < run ? left : 0, a.vec);
+            if (FAST || i0 + i < run) store_token<VEC>(yp + (i0 + i) * a.D, o, at);
         }
     }
 }
 
-template <typename IO, int W, bool SILU>
+__device__ __forceinline__ Place place_of(const Conv& a) {
+    Place p;
+    p.lanes = a.lanes;
+    p.lane = threadIdx.x % a.lanes;
+    const int64_t first = (int64_t)blockIdx.y * a.lanes * N;
+    p.c = first + p.lane * N;
+    p.left = a.D - p.c;
+    const int live = (int)min((int64_t)a.lanes, (a.D - first + N - 1) / N);
+    p.mask = (live == 32 ? ~0u : (1u << live) - 1) << (threadIdx.x % 32 - p.lane);
+    return p;
+}
+
+template <typename IO, int W, bool SILU, bool VEC>
 __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __restrict__ y, IO* __restrict__ state_out) {
     constexpr int kBack = W - 1;
-    __shared__ Ring<IO> ring;
-    const int lane = threadIdx.x % a.lanes, sub = threadIdx.x / a.lanes;
-    const int tile = a.run * (kThreads / a.lanes);
-    const int64_t c = ((int64_t)blockIdx.y * a.lanes + lane) * N, left = a.D - c;
+    __shared__ Ring<IO, VEC> ring;
+    const Place place = place_of(a);
+    const int sub = threadIdx.x / a.lanes, tile = a.run * (kThreads / a.lanes);
+    const int64_t c = place.c, left = place.left;
     const TileAt at = find_tile(a.q, blockIdx.x, tile);
     const int64_t t0 = at.tile * tile + (int64_t)sub * a.run;
     if (at.seq < 0 || left <= 0 || (t0 >= at.len && t0 > 0)) return;
@@ -151,10 +234,8 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
     const IO* xp = reinterpret_cast<const IO*>(a.x.p) + (at.start + t0) * a.x.ld + c;
     IO* yp = y + (at.start + t0) * a.D + c;
     const int run = (int)min((int64_t)a.run, at.len - t0);
-    if (run == a.run && left >= N && a.x.vec && a.vec)
-        forward_run<IO, W, SILU, true>(a, ring, xp, yp, a.run, c, left, win, w, b);
-    else
-        forward_run<IO, W, SILU, false>(a, ring, xp, yp, run, c, left, win, w, b);
+    if (VEC && run == a.run) forward_run<IO, W, SILU, VEC, VEC>(a, ring, xp, yp, a.run, place, win, w, b);
+    else forward_run<IO, W, SILU, VEC, false>(a, ring, xp, yp, run, place, win, w, b);
     if (t0 == 0 && state_out)                 // the first run leaves the state, an empty sequence's too
 #pragma unroll
         for (int j = 0; j < kBack; ++j)
@@ -164,20 +245,20 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
 
 // Where a run's gradients go, counted from its first token: token i gives dp_i and completes dx of i - (W - 1).
 template <typename IO> struct BackwardRun {
-    const IO *x, *dy;
+    const IO *x, *dy, *dy_base;
     IO *dx, *d_state;             // d_state: the sequence's rows, one past the last
     const IO* d_state_out;        // the sequence's rows, shifted so that [u] is the one of input u
     int run, seen;                // tokens of the run; of them and the W - 1 after them those that exist
-    int64_t before;               // channels of a row in front of the thread's
     int from, kept;               // first input with a gradient to store; first that is in the state the sequence left
 };
 
 // FAST: a whole run of aligned tokens inside a sequence, far from both its ends.
-template <typename IO, int W, bool SILU, bool FAST>
-__device__ __forceinline__ void backward_run(const Conv& a, Ring<IO> (&ring)[2], const BackwardRun<IO>& r, int64_t left,
-                                             F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P], F2 (&dw)[W][P],
-                                             F2 (&db)[P]) {
-    constexpr int kBack = W - 1, S = kRing<IO>;
+template <typename IO, int W, bool SILU, bool VEC, bool FAST>
+__device__ __forceinline__ void backward_run(const Conv& a, Ring<IO, VEC> (&ring)[2], const BackwardRun<IO>& r,
+                                             const Place& at, F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P],
+                                             F2 (&dw)[W][P], F2 (&db)[P]) {
+    constexpr int kBack = W - 1, S = kRing<IO, VEC>;
+    const IO* base = reinterpret_cast<const IO*>(a.x.p);
     F2 dp[W][P];
 #pragma unroll
     for (int j = 0; j < kBack; ++j)
@@ -187,8 +268,8 @@ __device__ __forceinline__ void backward_run(const Conv& a, Ring<IO> (&ring)[2],
 #pragma unroll
         for (int i = 0; i < kGroup; ++i)
             if (i0 + i < r.seen) {
-                copy_ahead(&ring[0][slot * kGroup + i][threadIdx.x], r.x + (i0 + i) * a.x.ld);
-                copy_ahead(&ring[1][slot * kGroup + i][threadIdx.x], r.dy + (i0 + i) * a.D);
+                fetch<VEC>(&ring[0][slot * kGroup + i][threadIdx.x], r.x + (i0 + i) * a.x.ld, at, base);
+                fetch<VEC>(&ring[1][slot * kGroup + i][threadIdx.x], r.dy + (i0 + i) * a.D, at, r.dy_base);
             }
         copy_group();
     };
@@ -226,47 +307,45 @@ __device__ __forceinline__ void backward_run(const Conv& a, Ring<IO> (&ring)[2],
         if (u < r.from || (!FAST && u >= r.run)) return;
         if (!FAST && u >= r.kept) {                        // the gradient that comes through the state it left
             F2 e[P];
-            pairs(load_n<N>(r.d_state_out + (int64_t)u * a.D, left, a.vec), e);
+            pairs(load_n<N>(r.d_state_out + (int64_t)u * a.D, at.left, VEC), e);
 #pragma unroll
             for (int k = 0; k < P; ++k) o[k] = add2(o[k], e[k]);
         }
-        if (FAST || u >= 0) store_token<FAST>(r.dx + (int64_t)u * a.D, o, left, a.vec);
-        else store_token<FAST>(r.d_state + (int64_t)u * a.D, o, left, a.vec);
+        store_token<VEC>((FAST || u >= 0 ? r.dx : r.d_state) + (int64_t)u * a.D, o, at);
     };
+    const auto taken = [&](int t, int slot, bool own) {
+        token(t, take<VEC>(ring[0][slot][threadIdx.x], r.x + t * a.x.ld),
+              take<VEC>(ring[1][slot][threadIdx.x], r.dy + t * a.D), own);
+    };
+#pragma unroll
+    for (int g = 0; g < S - 1; ++g) ahead(g * kGroup, g);
+    // past `seen` a slot gives what it held: no sum and no output has a part of it
+    const int tokens = r.run + (FAST ? 0 : kBack);
+    int slot = 0;
+    for (int i0 = 0; i0 < tokens; i0 += kGroup, slot = slot + 1 == S ? 0 : slot + 1) {
+        ahead(i0 + (S - 1) * kGroup, slot == 0 ? S - 1 : slot - 1);
+        copy_wait<S - 1>();
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            if (FAST || i0 + i < tokens) taken(i0 + i, slot * kGroup + i, FAST || i0 + i < r.run);
+    }
     if (FAST) {
-#pragma unroll
-        for (int g = 0; g < S - 1; ++g) ahead(g * kGroup, g);
-        int slot = 0;
-        for (int i0 = 0; i0 < r.run; i0 += kGroup, slot = slot + 1 == S ? 0 : slot + 1) {
-            ahead(i0 + (S - 1) * kGroup, slot == 0 ? S - 1 : slot - 1);
-            copy_wait<S - 1>();
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-                token(i0 + i, ring[0][slot * kGroup + i][threadIdx.x], ring[1][slot * kGroup + i][threadIdx.x], true);
-        }
         copy_wait<0>();
 #pragma unroll
-        for (int i = 0; i < kBack; ++i)
-            token(r.run + i, ring[0][slot * kGroup + i][threadIdx.x], ring[1][slot * kGroup + i][threadIdx.x], false);
-    } else {
-        for (int t = 0; t < r.run + kBack; ++t) {
-            const int64_t l = t < r.seen ? left : 0;
-            token(t, load_n<N>(r.x + t * a.x.ld, l, a.x.vec, r.before), load_n<N>(r.dy + t * a.D, l, a.vec, r.before),
-                  t < r.run);
-        }
+        for (int i = 0; i < kBack; ++i) taken(r.run + i, slot * kGroup + i, false);
     }
 }
 
-template <typename IO, int W, bool SILU>
+template <typename IO, int W, bool SILU, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d_state_out, IO* __restrict__ dx,
                      IO* __restrict__ d_state, float* __restrict__ partial) {
     constexpr int kBack = W - 1;
-    __shared__ Ring<IO> ring[2];
+    __shared__ Ring<IO, VEC> ring[2];
     __shared__ float sums[kThreads][N * (W + 1) + 1];     // + 1: threads on different banks
-    const int lane = threadIdx.x % a.lanes, sub = threadIdx.x / a.lanes, subs = kThreads / a.lanes;
-    const int tile = a.run * subs;
-    const int64_t c = ((int64_t)blockIdx.y * a.lanes + lane) * N, left = a.D - c;
+    const Place place = place_of(a);
+    const int sub = threadIdx.x / a.lanes, subs = kThreads / a.lanes, tile = a.run * subs;
+    const int64_t c = place.c, left = place.left;
     const TileAt at = find_tile(a.q, blockIdx.x, tile);
     const int64_t t0 = at.tile * tile + (int64_t)sub * a.run;
 
@@ -289,14 +368,14 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
         r.dx = dx + row * a.D + c;
         r.d_state = d_state ? d_state + (rows + kBack) * a.D + c : nullptr;
         r.d_state_out = d_state_out ? d_state_out + (rows + kBack - (at.len - t0)) * a.D + c : nullptr;
-        r.before = c;
+        r.dy_base = dy;
         r.run = (int)min((int64_t)a.run, at.len - t0);
         r.seen = (int)min((int64_t)r.run + kBack, at.len - t0);
         r.from = t0 == 0 && d_state ? -kBack : 0;
         r.kept = d_state_out ? (int)min(at.len - kBack - t0, (int64_t)r.run) : r.run;
         const bool inside = r.seen == a.run + kBack && r.from == 0 && r.kept == a.run;
-        if (inside && left >= N && a.x.vec && a.vec) backward_run<IO, W, SILU, true>(a, ring, r, left, win, w, b, dw, db);
-        else backward_run<IO, W, SILU, false>(a, ring, r, left, win, w, b, dw, db);
+        if (VEC && inside) backward_run<IO, W, SILU, VEC, VEC>(a, ring, r, place, win, w, b, dw, db);
+        else backward_run<IO, W, SILU, VEC, false>(a, ring, r, place, win, w, b, dw, db);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -376,8 +455,10 @@ Conv conv_of(const ConvArgs& a, RowTensor x, const void* w, const void* b, const
     k.b = b;
     k.state = state;
     k.silu = a.silu;
-    k.vec = a.D * (a.io == GDR_F32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(state) % 16 == 0;
-    for (const void* p : others) k.vec = k.vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    const uintptr_t size = N * (a.io == GDR_F32 ? 4 : 2);
+    k.vec = a.D % N == 0 && reinterpret_cast<uintptr_t>(state) % size == 0;
+    for (const void* p : others) k.vec = k.vec && reinterpret_cast<uintptr_t>(p) % size == 0;
+    k.x.vec = x.ld % N == 0 && reinterpret_cast<uintptr_t>(x.p) % size == 0;
     k.vec_w = reinterpret_cast<uintptr_t>(w) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0;
     k.lanes = row_lanes(a.D);
     k.run = run_of(a);
@@ -405,8 +486,11 @@ cudaError_t conv_forward(const ConvArgs& a, RowTensor x, const void* w, const vo
     const int64_t tiles = tile_count(k.q, k.run * (kThreads / k.lanes));
     return with_types(a, [&](auto io, auto taps, auto silu) {
         using IO = decltype(io);
-        conv_forward_kernel<IO, decltype(taps)::value, decltype(silu)::value>
-            <<<dim3((unsigned)tiles, channel_blocks(a.D, k.lanes)), kThreads, 0, s>>>(k, (IO*)y, (IO*)state_out);
+        constexpr int W = decltype(taps)::value;
+        constexpr bool kSilu = decltype(silu)::value;
+        const auto kernel =
+            k.vec && k.x.vec ? conv_forward_kernel<IO, W, kSilu, true> : conv_forward_kernel<IO, W, kSilu, false>;
+        kernel<<<dim3((unsigned)tiles, channel_blocks(a.D, k.lanes)), kThreads, 0, s>>>(k, (IO*)y, (IO*)state_out);
         return cudaGetLastError();
     });
 }
@@ -423,9 +507,12 @@ cudaError_t conv_backward(const ConvArgs& a, RowTensor x, const void* w, const v
     const int64_t tiles = conv_partial_rows(a);
     const cudaError_t e = with_types(a, [&](auto io, auto taps, auto silu) {
         using IO = decltype(io);
-        conv_backward_kernel<IO, decltype(taps)::value, decltype(silu)::value>
-            <<<dim3((unsigned)tiles, channel_blocks(a.D, k.lanes)), kThreads, 0, s>>>(
-                k, (const IO*)dy, (const IO*)d_state_out, (IO*)dx, (IO*)d_state, partial);
+        constexpr int W = decltype(taps)::value;
+        constexpr bool kSilu = decltype(silu)::value;
+        const auto kernel =
+            k.vec && k.x.vec ? conv_backward_kernel<IO, W, kSilu, true> : conv_backward_kernel<IO, W, kSilu, false>;
+        kernel<<<dim3((unsigned)tiles, channel_blocks(a.D, k.lanes)), kThreads, 0, s>>>(
+            k, (const IO*)dy, (const IO*)d_state_out, (IO*)dx, (IO*)d_state, partial);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;

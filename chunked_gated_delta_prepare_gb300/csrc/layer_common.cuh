@@ -138,6 +138,12 @@ template <typename IO, int N> __device__ __forceinline__ void copy_ahead(RawN<IO
                  "n"((int)sizeof(RawN<IO, N>))
                  : "memory");
 }
+// A word, of which `bytes` are read and the rest becomes zero.
+__device__ __forceinline__ void copy_word(void* to, const void* from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT> __device__ __forceinline__ void copy_wait() {   // until at most LEFT groups are on their way
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
