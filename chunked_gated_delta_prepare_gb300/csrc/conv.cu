@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_taps(const Conv& a, int64_t c, F2 (&w)[W][P
 // memory.  VEC: rows of aligned vectors, one copy each.  Other rows start anywhere; there a slot of 16 bytes takes the
 // aligned words around a vector, and the neighbours' outputs are joined to aligned vectors.
 constexpr int kGroup = 4;
-template <typename IO, bool VEC> constexpr int kRing = VEC && sizeof(IO) == 2 ? 4 : 2;
+template <typename IO, bool VEC> constexpr int kRing = VEC && sizeof(IO) == 2 ? 4 : VEC ? 2 : 3;
 struct alignas(16) Words {
     uint32_t w[4];
 };
@@ -342,7 +342,8 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
                      IO* __restrict__ d_state, float* __restrict__ partial) {
     constexpr int kBack = W - 1;
     __shared__ Ring<IO, VEC> ring[2];
-    __shared__ float sums[kThreads][N * (W + 1) + 1];     // + 1: threads on different banks
+    auto& sums = *reinterpret_cast<float(*)[kThreads][N * (W + 1) + 1]>(ring);   // after it; + 1: on different banks
+    static_assert(sizeof(sums) <= sizeof(ring), "the sums fit");
     const Place place = place_of(a);
     const int sub = threadIdx.x / a.lanes, subs = kThreads / a.lanes, tile = a.run * subs;
     const int64_t c = place.c, left = place.left;
@@ -377,6 +378,8 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
         if (VEC && inside) backward_run<IO, W, SILU, VEC, VEC>(a, ring, r, place, win, w, b, dw, db);
         else backward_run<IO, W, SILU, VEC, false>(a, ring, r, place, win, w, b, dw, db);
     }
+    copy_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
 #pragma unroll

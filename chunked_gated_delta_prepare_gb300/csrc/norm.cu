@@ -47,6 +47,7 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
                     bool vec_r, bool vec_8) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
     __shared__ float red[2 * 32], redm[2 * 32];
+    extern __shared__ int tops[];             // CUT, groups: [2][RPB][groups], a row's largest |y| of each group
     const int tid = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const int D = a.D;
     const int shift = CUT ? first_shift<IO>((int64_t)blockIdx.x * RPB + slot, D) : 0;
@@ -54,7 +55,7 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (tid + i * TPR) * 8 - shift;
-        wr[i] = CUT ? load_cut(w, c, D, vec_w && shift == 0, false) : load8(w + c, D - c, vec_w);
+        wr[i] = CUT ? load_cut(w, c, D, vec_w && shift == 0) : load8(w + c, D - c, vec_w);
     }
     const bool two = res.p != nullptr;
     const auto fetch = [&](int64_t row) {     // a block's last rows may not exist: zeros
@@ -64,8 +65,8 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * TPR) * 8 - shift, left = row < a.rows ? D - c : 0;
             if (CUT) {
-                xr[i] = load_cut(xp, c, left > 0 ? D : 0, true, row + 1 < a.rows);
-                if (two) sr[i] = load_cut(sp, c, left > 0 ? D : 0, true, row + 1 < a.rows);
+                xr[i] = load_around(reinterpret_cast<const IO*>(x.p), left > 0 ? row * D + c : 0, a.rows * D);
+                if (two) sr[i] = load_around(reinterpret_cast<const IO*>(res.p), left > 0 ? row * D + c : 0, a.rows * D);
             } else {
                 xr[i] = load8(xp + c, left, x.vec);
                 if (two) sr[i] = load8(sp + c, left, res.vec);
@@ -73,6 +74,9 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
         }
     };
     fetch((int64_t)blockIdx.x * RPB + slot);
+    const int groups = y8 && a.group ? (D + a.group - 1) / a.group : 0;
+    if (CUT)
+        for (int g = tid; g < groups; g += TPR) tops[slot * groups + g] = 0;
     int turn = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, ++turn) {
         const int64_t row = row0 + slot;
@@ -81,8 +85,13 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
         if (CUT)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                mask_cut(xr[i], (tid + i * TPR) * 8 - shift, D);
-                if (two) mask_cut(sr[i], (tid + i * TPR) * 8 - shift, D);
+                const int c = (tid + i * TPR) * 8 - shift;
+                mask_cut(xr[i], c, D);
+                if (two) mask_cut(sr[i], c, D);
+                if (row + 1 == a.rows && c < D && c + 8 > D) {
+                    xr[i] = load_cut(reinterpret_cast<const IO*>(x.p) + row * D, c, D, false);
+                    if (two) sr[i] = load_cut(reinterpret_cast<const IO*>(res.p) + row * D, c, D, false);
+                }
             }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -107,6 +116,10 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
         }
         row_reduce<TPR, 1, false>(sum, red, turn);
+        if (CUT) {                               // the row before has been read out
+            if (TPR == 32) __syncwarp();
+            for (int g = tid; g < groups; g += TPR) tops[((turn + 1 & 1) * RPB + slot) * groups + g] = 0;
+        }
         const float rstd = rsqrtf(sum[0] / (float)D + a.eps);
         float top[1] = {0.f};
 #pragma unroll
@@ -124,7 +137,19 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
             } else if (y) {
                 store_n(y + row * D + c, v[i], live ? D - c : 0, vec_y);
             }
-            if (y8 && a.group) {             // a group's columns lie in group / 8 neighbouring threads
+            if (CUT && groups) {             // a vector has columns of at most two groups
+                int* top = tops + ((turn & 1) * RPB + slot) * groups;
+                const int g = max(c, 0) / a.group, next = (g + 1) * a.group - c;
+                float lo = 0.f, hi = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < next) lo = max_nan(lo, fabsf(v[i][j]));
+                    else hi = max_nan(hi, fabsf(v[i][j]));
+                if (c < D) {                 // not negative or NaN: in the order of their bits
+                    atomicMax(top + g, __float_as_int(lo));
+                    if (next < 8 && c + next < D) atomicMax(top + g + 1, __float_as_int(hi));
+                }
+            } else if (y8 && a.group) {      // a group's columns lie in group / 8 neighbouring threads
                 for (int o = a.group / 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float scale = max_nan(m * (1.f / 448.f), 1.17549435e-38f);
                 if (live && c < D) {
@@ -134,6 +159,26 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
                 }
             }
             top[0] = max_nan(top[0], m);
+        }
+        if (CUT && groups) {
+            if (TPR == 32) __syncwarp();
+            else __syncthreads();
+            const int* top = tops + ((turn & 1) * RPB + slot) * groups;
+            const auto scale_of = [&](int g) {
+                return max_nan(__int_as_float(top[g]) * (1.f / 448.f), 1.17549435e-38f);
+            };
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int c = (tid + i * TPR) * 8 - shift, g = max(c, 0) / a.group, next = (g + 1) * a.group - c;
+                    if (c >= D) continue;
+                    const float lo = 1.f / scale_of(g), hi = next < 8 && c + next < D ? 1.f / scale_of(g + 1) : lo;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] *= j < next ? lo : hi;
+                    store_e4m3<CUT>(y8 + row * D, v[i], 1.f, c, D, vec_8);
+                }
+                for (int g = tid; g < groups; g += TPR) scales[row * groups + g] = scale_of(g);
+            }
         }
         if (y8 && !a.group) {
             row_reduce<TPR, 1, true>(top, redm, turn);
@@ -162,9 +207,10 @@ Shape shape_of(const NormArgs& a) {
         for (int tpr = 128; tpr <= 1024; tpr *= 2)
             if (v <= tpr) return {tpr, 1};
     if (v <= 256) return {128, 2};
-    if (v <= 384) return {128, 3};
+    if (v <= 320) return {160, 2};
+    if (v <= 384) return {192, 2};
     if (v <= 512) return {256, 2};
-    if (v <= 768) return {256, 3};
+    if (v <= 768) return {384, 2};
     return {v <= 1024 ? 256 : v <= 2048 ? 512 : 1024, 4};
 }
 
@@ -176,16 +222,17 @@ cudaError_t launch_forward(const NormArgs& a, RowTensor x, RowTensor res, const 
     // a wave is a multiple of 8 blocks: of every period of a row's shift
     static_assert(kSms % 8 == 0, "a multiple of the shifts' period");
     const int grid = (int)std::min<int64_t>(blocks, (int64_t)kSms * blocks_per_sm<TPR, VPT>());
-    // Cut at the boundaries: rows not aligned, every tensor contiguous from a boundary on.  Scales of column groups need
-    // the cuts at column 0.
-    bool cut = (int64_t)a.D * sizeof(IO) % 16 != 0 && x.ld == a.D && (!res.p || res.ld == a.D) && !(y8 && a.group);
+    // Cut at the boundaries: rows not aligned, every tensor contiguous from a boundary on.
+    bool cut = (int64_t)a.D * sizeof(IO) % 16 != 0 && a.rows * a.D >= 8 && x.ld == a.D && (!res.p || res.ld == a.D);
     for (const void* p : {x.p, res.p, (const void*)y, (const void*)r, (const void*)y8})
         cut = cut && reinterpret_cast<uintptr_t>(p) % 16 == 0;
     const auto al = [&](const void* p, int unit) {
         return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && ((int64_t)a.D * unit) % 16 == 0;
     };
     const auto go = [&](auto in_cuts) {
-        norm_forward_kernel<IO, TPR, VPT, decltype(in_cuts)::value><<<grid, NT, 0, s>>>(
+        constexpr bool kCut = decltype(in_cuts)::value;
+        const int bytes = kCut && y8 && a.group ? 2 * RPB * ((a.D + a.group - 1) / a.group) * 4 : 0;
+        norm_forward_kernel<IO, TPR, VPT, kCut><<<grid, NT, bytes, s>>>(
             a, x, res, (const IO*)w, (IO*)y, (IO*)r, (uint8_t*)y8, scales, reinterpret_cast<uintptr_t>(w) % 16 == 0,
             cut || al(y, sizeof(IO)), cut || al(r, sizeof(IO)),
             reinterpret_cast<uintptr_t>(y8) % 8 == 0 && (cut || a.D % 8 == 0));
@@ -206,7 +253,7 @@ template <typename F> cudaError_t with_shape(Shape h, F f) {
     if (h.tpr == T && h.vpt == V) return f(std::integral_constant<int, T>(), std::integral_constant<int, V>());
     GDR_SHAPE(32, 1) GDR_SHAPE(32, 2) GDR_SHAPE(32, 4)
     GDR_SHAPE(128, 1) GDR_SHAPE(256, 1) GDR_SHAPE(512, 1) GDR_SHAPE(1024, 1)
-    GDR_SHAPE(128, 2) GDR_SHAPE(256, 2) GDR_SHAPE(128, 3) GDR_SHAPE(256, 3)
+    GDR_SHAPE(128, 2) GDR_SHAPE(160, 2) GDR_SHAPE(192, 2) GDR_SHAPE(256, 2) GDR_SHAPE(384, 2)
     GDR_SHAPE(256, 4) GDR_SHAPE(512, 4) GDR_SHAPE(1024, 4)
 #undef GDR_SHAPE
     return cudaErrorInvalidValue;

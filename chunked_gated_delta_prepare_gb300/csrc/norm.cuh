@@ -53,16 +53,35 @@ template <typename IO> __device__ __forceinline__ int first_shift(int64_t row, i
 // first and last vector go element by element.  The shift returns after `period` rows, so with a multiple of that many
 // rows from one turn to the next it is a block's own, and w and the sums of dw stay in registers as for aligned rows.
 // (16384 rows of 4089 instead of 4096 columns: fp32 434 us before, 141 now, 137 aligned; bf16 214, 167 and 75.)
-// Elements [c, c + 8) of a row, which may begin before its first or end past its last element: those read as zero, or, in
-// a vector that lies in the tensor all the same (`more`: rows follow this one), as what is there, for mask_cut to take
-// out when it is used.  (Taken out on arrival, they would keep their warp, and at its barrier the block, waiting for
-// memory in every row.)
-template <typename IO> __device__ __forceinline__ Raw8<IO> load_cut(const IO* row, int c, int D, bool vec, bool more) {
-    if (vec && c < D && (more || c + 8 <= D)) return load8(row + c, 8, true);   // c < 0: the end of the row before
+// Elements [at, at + 8) of a tensor of `total`, or any vector where they are not all in it.  A row's first and last vector
+// bring the neighbour rows' elements along; mask_cut takes them out when they are used, and the tensor's last vector is
+// loaded then.  Done on arrival, both would read or write the registers that the load fills, and keep the warp, and at
+// its barrier the block, waiting for memory in every row.
+template <typename IO> __device__ __forceinline__ Raw8<IO> load_around(const IO* p, int64_t at, int64_t total) {
+    return load8(p + (at + 8 <= total ? at : 0), 8, true);
+}
+// Elements [c, c + 8) of a row, zeros outside it.
+template <typename IO> __device__ __forceinline__ Raw8<IO> load_cut(const IO* row, int c, int D, bool vec) {
+    if (vec && c >= 0 && c + 8 <= D) return load8(row + c, 8, true);
     Raw8<IO> r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.e[i] = c + i >= 0 && c + i < D ? row[c + i] : from_f<IO>(0.f);
     return r;
+}
+// Elements [lo, hi) of an aligned vector at p, either lo = 0 or hi = 8.
+template <typename IO> __device__ __forceinline__ void store_piece(IO* p, const Raw8<IO>& r, int lo, int hi) {
+    using Four = RawN<IO, 4>;
+    using Two = RawN<IO, 2>;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+        if (i >= lo && i + 4 <= hi) *reinterpret_cast<Four*>(p + i) = *reinterpret_cast<const Four*>(r.e + i);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {           // a half of a quarter that is not whole
+        const bool four = (i & 4) >= lo && (i & 4) + 4 <= hi;
+        if (!four && i >= lo && i + 2 <= hi) *reinterpret_cast<Two*>(p + i) = *reinterpret_cast<const Two*>(r.e + i);
+        if (i + 1 == lo) p[i + 1] = r.e[i + 1];
+        if (i + 1 == hi) p[i] = r.e[i];
+    }
 }
 template <typename IO> __device__ __forceinline__ void mask_cut(Raw8<IO>& r, int c, int D) {
     if (c < 0 || c + 8 > D)
@@ -70,20 +89,26 @@ template <typename IO> __device__ __forceinline__ void mask_cut(Raw8<IO>& r, int
         for (int i = 0; i < 8; ++i)
             if (c + i < 0 || c + i >= D) r.e[i] = from_f<IO>(0.f);
 }
+// vec: column c lies on a 16-byte boundary, so what a row has of its first or last vector goes in pieces of 4, 2 and 1.
 template <typename IO> __device__ __forceinline__ void store_cut(IO* row, const float (&x)[8], int c, int D, bool vec) {
-    if (c >= 0) {
-        store_n(row + c, x, D - c, vec);
+    Raw8<IO> r;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) from_f2(r.e + i, x[i], x[i + 1]);
+    if (c >= 0 && c + 8 <= D) {
+        store_raw(row + c, r, 8, vec);
+    } else if (vec && (c >= 0 || c + 8 <= D)) {
+        store_piece(row + c, r, c < 0 ? -c : 0, c < 0 ? 8 : D - c);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i >= 0 && c + i < D) row[c + i] = from_f<IO>(x[i]);
+            if (c + i >= 0 && c + i < D) row[c + i] = r.e[i];
     }
 }
 
 // Blocks an SM that a kernel's registers leave room for: 1024 threads at one vector a thread, 768 at two (1024 spill and
 // take 179 us instead of 160 for 32768 x 4096 to e4m3, 512 take 188), 512 at four.
 template <int TPR, int VPT> constexpr int blocks_per_sm() {
-    constexpr int threads = VPT > 2 ? 512 : VPT > 1 ? 768 : 1024, nt = TPR < 128 ? 128 : TPR;
+    constexpr int threads = VPT > 2 ? 512 : VPT > 1 ? 800 : 1024, nt = TPR < 128 ? 128 : TPR;
     return threads > nt ? threads / nt : 1;
 }
 

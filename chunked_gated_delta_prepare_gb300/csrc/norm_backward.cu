@@ -14,10 +14,10 @@ namespace {
 // thread's vectors in its own places, while the block works on one.  (With one row ahead in registers, as the forward
 // has it, the kernel took twice the time; the forward's two tensors are faster that way, 20 against 28 us at 8192 x
 // 2048.)  RING = 1: a row is loaded when it is its turn (few rows, rows not aligned, or rows too wide for the ring).
-constexpr int kRingBytes = 56 * 1024;     // of a block, so that three or more fit an SM
+template <int NT> constexpr int kRingBytes = NT < 512 ? 56 * 1024 : 200 * 1024;   // of a block: several fit an SM, or one
 template <typename IO, int NT, int VPT> constexpr int ring_of() {
     constexpr int row = NT * VPT * 3 * (int)sizeof(Raw8<IO>);
-    return 4 * row <= kRingBytes ? 4 : 3 * row <= kRingBytes ? 3 : 2 * row <= kRingBytes ? 2 : 1;
+    return 4 * row <= kRingBytes<NT> ? 4 : 3 * row <= kRingBytes<NT> ? 3 : 2 * row <= kRingBytes<NT> ? 2 : 1;
 }
 
 template <typename IO, int NT, int VPT, int RING, bool CUT> struct Pipe {
@@ -40,13 +40,13 @@ template <typename IO, int NT, int VPT, int RING, bool CUT> struct Pipe {
 #pragma unroll
                     for (int i = 0; i < VPT; ++i) {
                         const int c = (tid + i * tpr) * 8 - shift;
-                        if (c < D && (!CUT || row + 1 < rows || c + 8 <= D)) {      // in the tensor: see load_cut
+                        if (c < D && (!CUT || row + 1 < rows || c + 8 <= D)) {      // in the tensor: see load_around
 #pragma unroll
                             for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
                                 copy_ahead(reinterpret_cast<RawN<IO, 16 / sizeof(IO)>*>(place(slot, t, i, part)),
                                            base[t] + row * D + c + part * (16 / (int)sizeof(IO)));
                         } else if (CUT && c < D) {
-                            const Raw8<IO> v = load_cut(base[t] + row * D, c, D, false, false);
+                            const Raw8<IO> v = load_cut(base[t] + row * D, c, D, false);
 #pragma unroll
                             for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
                                 *place(slot, t, i, part) = reinterpret_cast<const uint4*>(&v)[part];
@@ -60,8 +60,7 @@ template <typename IO, int NT, int VPT, int RING, bool CUT> struct Pipe {
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * tpr) * 8 - shift, left = row < rows ? D - c : 0;
             if (RING == 1) {
-                v[i] = load_cut(base[t] + row * D, c, left > 0 ? D : 0, vec, false);
-                mask_cut(v[i], c, D);
+                v[i] = load_cut(base[t] + row * D, c, left > 0 ? D : 0, vec);
             } else if (left > 0) {
 #pragma unroll
                 for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
@@ -88,7 +87,7 @@ norm_backward_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict
     const int shift = CUT ? first_shift<IO>((int64_t)blockIdx.x * RPB + slot, D) : 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        wr[i] = load_cut(w, (tid + i * TPR) * 8 - shift, D, vec && shift == 0, false);
+        wr[i] = load_cut(w, (tid + i * TPR) * 8 - shift, D, vec && shift == 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
@@ -172,7 +171,7 @@ Shape backward_shape(const NormArgs& a) {
     const int v = vectors_of(a);
     if (v <= 64) return {32, v <= 32 ? 1 : 2};
     if (v <= 256) return {v <= 128 ? 128 : 256, 1};
-    if (v <= 512) return {256, 2};
+    if (v <= 512) return {512, 1};
     return {v <= 1024 ? 256 : v <= 2048 ? 512 : 1024, 4};
 }
 
@@ -210,7 +209,7 @@ cudaError_t launch_backward(const NormArgs& a, const void* dy, const void* r, co
 template <typename F> cudaError_t with_shape(Shape h, F f) {
 #define GDR_SHAPE(T, V) \
     if (h.tpr == T && h.vpt == V) return f(std::integral_constant<int, T>(), std::integral_constant<int, V>());
-    GDR_SHAPE(32, 1) GDR_SHAPE(32, 2) GDR_SHAPE(128, 1) GDR_SHAPE(256, 1) GDR_SHAPE(256, 2)
+    GDR_SHAPE(32, 1) GDR_SHAPE(32, 2) GDR_SHAPE(128, 1) GDR_SHAPE(256, 1) GDR_SHAPE(512, 1)
     GDR_SHAPE(256, 4) GDR_SHAPE(512, 4) GDR_SHAPE(1024, 4)
 #undef GDR_SHAPE
     return cudaErrorInvalidValue;
