@@ -89,12 +89,21 @@ template <typename IO, bool VEC> using Ring = Slot<IO, VEC>[kRing<IO, VEC> * kGr
 
 // The thread's place in its row.
 struct Place {
-    int64_t c, left;      // first channel; channels from there on
+    int64_t c;            // first channel
+    int left;             // channels from there on, 2 N at most
     int lane, lanes;      // lanes that share a token, neighbours of one warp
-    unsigned mask;        // those of them that have channels
+    unsigned mask;        // the lanes of them that have channels
+    int live, last_left;  // their number, and `left` of the last one
+    int before;           // the lane before, of the first one the last
 };
 
-// p's elements [0, min(left, N)) on their way; base: the tensor's first element.
+// The tensor's first element where its address is an odd one's (fetch's base), else nullptr.
+template <typename IO> __device__ __forceinline__ const IO* odd_start(const IO* p) {
+    return sizeof(IO) == 2 && (reinterpret_cast<uintptr_t>(p) & 2) ? p : nullptr;
+}
+
+// p's elements [0, min(left, N)) on their way.  Without VEC by words: with a 16-bit type and an odd element first, the word
+// around it brings the element before, which a tensor's first element does not have (base, where it is an odd one).
 template <bool VEC, typename IO>
 __device__ __forceinline__ void fetch(Slot<IO, VEC>* to, const IO* p, const Place& at, const IO* base) {
     if constexpr (VEC) {
@@ -104,13 +113,12 @@ __device__ __forceinline__ void fetch(Slot<IO, VEC>* to, const IO* p, const Plac
         for (int i = 0; i < N; ++i)
             if (i < at.left) copy_word(to->w + i, p + i, 4);
     } else {
-        const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1);      // the first word holds the element before p too
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int64_t have = at.left - (2 * i - odd);
-            if (i == 0 && odd && p == base) reinterpret_cast<IO*>(to)[1] = p[0];    // nothing lies before p
-            else if (have > 0 && (i < 2 || odd)) copy_word(to->w + i, p + (2 * i - odd), have > 1 ? 4 : 2);
-        }
+        const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1), have = 2 * (at.left + odd);
+        const IO* q = p - odd;
+        if (odd && base && p == base) reinterpret_cast<IO*>(to)[1] = p[0];
+        else copy_word(to->w, q, min(have, 4));
+        if (have > 4) copy_word(to->w + 1, q + 2, min(have - 4, 4));
+        if (odd && have > 8) copy_word(to->w + 2, q + 4, min(have - 8, 4));
     }
 }
 template <bool VEC, typename IO>
@@ -124,8 +132,9 @@ __device__ __forceinline__ RawN<IO, N> take(const Slot<IO, VEC>& slot, const IO*
     }
 }
 
-// The thread's channels of a token to p.  Rows that start anywhere: every lane of a token calls it at the same time; each
-// takes from the one before it what shares the aligned vector in which its own channels begin.
+// The thread's channels of a token to p.  Without VEC every lane of a token calls it at the same time, and takes from the
+// lane before it what shares the aligned vector in which its own channels begin; the first lane stores the row's (or the
+// block's) two ends.
 template <bool VEC, typename IO>
 __device__ __forceinline__ void store_token(IO* p, const F2 (&v)[P], const Place& at) {
     float f[N];
@@ -144,20 +153,20 @@ __device__ __forceinline__ void store_token(IO* p, const F2 (&v)[P], const Place
 #pragma unroll
         for (int i = 0; i < words; ++i) {
             w[words + i] = reinterpret_cast<const uint32_t*>(&own)[i];
-            w[i] = __shfl_up_sync(at.mask, w[words + i], 1, at.lanes);
+            w[i] = __shfl_sync(at.mask, w[words + i], at.before, at.lanes);
         }
-        // elements [-gone, N - gone) of p
+        // elements [-gone, N - gone) of p; the first lane's first ones are the last lane's last
         const RawN<IO, N> r = off ? shift_words<N, IO>(w, block - off) : own;
-        const bool whole = at.left >= N - gone && (at.lane > 0 || gone == 0);
-        if (whole) store_raw(p - gone, r, N, true);
-        const bool end = at.lane == at.lanes - 1 || at.left <= N;       // no lane after it takes its last elements
-        if (!whole || (end && gone)) {
+        IO* q = p - gone;
+        const bool ends = gone > 0 && at.lane == 0;
+        if (!ends && at.left >= N - gone) {
+            store_raw(q, r, N, true);
+        } else {
+            const int tail = ends ? gone : 0, have = at.left + gone, end_have = at.last_left + gone - N;
+            IO* e = q + at.live * N;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (!whole && (i >= gone || at.lane > 0) && i < gone + at.left) p[i - gone] = r.e[i];
-#pragma unroll
-            for (int i = 1; i < N; ++i)
-                if (end && i >= N - gone && i < at.left) p[i] = own.e[i];
+                if (i < (i < tail ? end_have : have)) (i < tail ? e : q)[i] = r.e[i];
         }
     }
 }
@@ -167,7 +176,7 @@ template <typename IO, int W, bool SILU, bool VEC, bool FAST>
 __device__ __forceinline__ void forward_run(const Conv& a, Ring<IO, VEC>& ring, const IO* xp, IO* yp, int run,
                                             const Place& at, F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P]) {
     constexpr int kBack = W - 1, S = kRing<IO, VEC>;
-    const IO* base = reinterpret_cast<const IO*>(a.x.p);
+    const IO* base = odd_start(reinterpret_cast<const IO*>(a.x.p));
     const auto ahead = [&](int i0, int slot) {
         if (i0 < run)
 #pragma unroll
@@ -208,10 +217,13 @@ __device__ __forceinline__ Place place_of(const Conv& a) {
     p.lanes = a.lanes;
     p.lane = threadIdx.x % a.lanes;
     const int64_t first = (int64_t)blockIdx.y * a.lanes * N;
+    const int here = (int)min((int64_t)a.lanes * N, a.D - first);
     p.c = first + p.lane * N;
-    p.left = a.D - p.c;
-    const int live = (int)min((int64_t)a.lanes, (a.D - first + N - 1) / N);
-    p.mask = (live == 32 ? ~0u : (1u << live) - 1) << (threadIdx.x % 32 - p.lane);
+    p.left = (int)max(min(a.D - p.c, (int64_t)2 * N), (int64_t)0);
+    p.live = (here + N - 1) / N;
+    p.last_left = (int)min(a.D - first - (p.live - 1) * N, (int64_t)2 * N);
+    p.mask = (p.live == 32 ? ~0u : (1u << p.live) - 1) << (threadIdx.x % 32 - p.lane);
+    p.before = p.lane == 0 ? p.live - 1 : p.lane - 1;
     return p;
 }
 
@@ -221,7 +233,8 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
     __shared__ Ring<IO, VEC> ring;
     const Place place = place_of(a);
     const int sub = threadIdx.x / a.lanes, tile = a.run * (kThreads / a.lanes);
-    const int64_t c = place.c, left = place.left;
+    const int64_t c = place.c;
+    const int left = place.left;
     const TileAt at = find_tile(a.q, blockIdx.x, tile);
     const int64_t t0 = at.tile * tile + (int64_t)sub * a.run;
     if (at.seq < 0 || left <= 0 || (t0 >= at.len && t0 > 0)) return;
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(Conv a, IO* __re
     const IO* xp = reinterpret_cast<const IO*>(a.x.p) + (at.start + t0) * a.x.ld + c;
     IO* yp = y + (at.start + t0) * a.D + c;
     const int run = (int)min((int64_t)a.run, at.len - t0);
-    if (VEC && run == a.run) forward_run<IO, W, SILU, VEC, VEC>(a, ring, xp, yp, a.run, place, win, w, b);
+    if (run == a.run) forward_run<IO, W, SILU, VEC, true>(a, ring, xp, yp, a.run, place, win, w, b);
     else forward_run<IO, W, SILU, VEC, false>(a, ring, xp, yp, run, place, win, w, b);
     if (t0 == 0 && state_out)                 // the first run leaves the state, an empty sequence's too
 #pragma unroll
@@ -258,7 +271,7 @@ __device__ __forceinline__ void backward_run(const Conv& a, Ring<IO, VEC> (&ring
                                              const Place& at, F2 (&win)[W][P], const F2 (&w)[W][P], const F2 (&b)[P],
                                              F2 (&dw)[W][P], F2 (&db)[P]) {
     constexpr int kBack = W - 1, S = kRing<IO, VEC>;
-    const IO* base = reinterpret_cast<const IO*>(a.x.p);
+    const IO* base = odd_start(reinterpret_cast<const IO*>(a.x.p));
     F2 dp[W][P];
 #pragma unroll
     for (int j = 0; j < kBack; ++j)
@@ -346,7 +359,8 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
     static_assert(sizeof(sums) <= sizeof(ring), "the sums fit");
     const Place place = place_of(a);
     const int sub = threadIdx.x / a.lanes, subs = kThreads / a.lanes, tile = a.run * subs;
-    const int64_t c = place.c, left = place.left;
+    const int64_t c = place.c;
+    const int left = place.left;
     const TileAt at = find_tile(a.q, blockIdx.x, tile);
     const int64_t t0 = at.tile * tile + (int64_t)sub * a.run;
 
@@ -369,13 +383,13 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
         r.dx = dx + row * a.D + c;
         r.d_state = d_state ? d_state + (rows + kBack) * a.D + c : nullptr;
         r.d_state_out = d_state_out ? d_state_out + (rows + kBack - (at.len - t0)) * a.D + c : nullptr;
-        r.dy_base = dy;
+        r.dy_base = odd_start(dy);
         r.run = (int)min((int64_t)a.run, at.len - t0);
         r.seen = (int)min((int64_t)r.run + kBack, at.len - t0);
         r.from = t0 == 0 && d_state ? -kBack : 0;
         r.kept = d_state_out ? (int)min(at.len - kBack - t0, (int64_t)r.run) : r.run;
         const bool inside = r.seen == a.run + kBack && r.from == 0 && r.kept == a.run;
-        if (VEC && inside) backward_run<IO, W, SILU, VEC, VEC>(a, ring, r, place, win, w, b, dw, db);
+        if (inside) backward_run<IO, W, SILU, VEC, true>(a, ring, r, place, win, w, b, dw, db);
         else backward_run<IO, W, SILU, VEC, false>(a, ring, r, place, win, w, b, dw, db);
     }
     copy_wait<0>();
