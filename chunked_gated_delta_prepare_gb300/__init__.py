@@ -1,7 +1,8 @@
 """libgdr: the chunked gated-delta-rule forward on one GB300 (sm_103a).
 
 The compute path is the C-ABI shared library built from csrc/ (see include/gdr.h);
-`gdr` is its thin ctypes binding.  Importing this package loads nothing: the
+`gdr` is its thin ctypes binding.  `layer` has the operators a recurrent layer runs
+beside the delta rule, on torch tensors.  Importing this package loads nothing: the
 library is loaded on the first call, and a missing library raises.
 """
 from .gdr import (GdrError, forward, gdr_chunk_output, gdr_forward, gdr_forward_workspace_bytes,  # noqa: F401

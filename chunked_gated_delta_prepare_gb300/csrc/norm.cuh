@@ -52,7 +52,8 @@ template <typename IO> __device__ __forceinline__ int first_shift(int64_t row, i
 // cut at the boundaries instead of at column 0: vector i of a row covers the columns from 8 i - shift on, and only a row's
 // first and last vector go element by element.  The shift returns after `period` rows, so with a multiple of that many
 // rows from one turn to the next it is a block's own, and w and the sums of dw stay in registers as for aligned rows.
-// (16384 rows of 4089 instead of 4096 columns: fp32 434 us before, 141 now, 137 aligned; bf16 214, 167 and 75.)
+// (16384 rows of 4089 columns to e4m3: fp32 434 us with vectors from column 0 on, 158 cut, 137 with 4096 columns; bf16
+// 214, 85 and 75.)
 // Elements [at, at + 8) of a tensor of `total`, or any vector where they are not all in it.  A row's first and last vector
 // bring the neighbour rows' elements along; mask_cut takes them out when they are used, and the tensor's last vector is
 // loaded then.  Done on arrival, both would read or write the registers that the load fills, and keep the warp, and at
@@ -105,8 +106,8 @@ template <typename IO> __device__ __forceinline__ void store_cut(IO* row, const 
     }
 }
 
-// Blocks an SM that a kernel's registers leave room for: 1024 threads at one vector a thread, 768 at two (1024 spill and
-// take 179 us instead of 160 for 32768 x 4096 to e4m3, 512 take 188), 512 at four.
+// Blocks an SM that a kernel's registers leave room for: 1024 threads at one vector a thread, 800 at two (with 256 a block
+// that is 768: 164 us for 32768 x 4096 to e4m3; 1024 spill and take 179, 512 take 188), 512 at four.
 template <int TPR, int VPT> constexpr int blocks_per_sm() {
     constexpr int threads = VPT > 2 ? 512 : VPT > 1 ? 800 : 1024, nt = TPR < 128 ? 128 : TPR;
     return threads > nt ? threads / nt : 1;

@@ -4,6 +4,8 @@
 //   ds = rstd (w dy - xh mean(w dy xh)) + dr,   dw = sum over rows of dy xh
 // One pass over dy and r: both sums of a row come from registers.  Each block adds its rows' dw in registers and
 // leaves one row of partial sums, which column_sum adds in a fixed order: no atomics, the same bits in every run.
+// Bound: memory.  Measured: 8192 x 2048 bf16 with dr 25 us, 5.4 TB/s (0.80 of a copy's rate), and 3 us for column_sum;
+// 4452 x 4096 fp32 49 us, 6.0 TB/s.
 #include "norm.cuh"
 
 namespace gdr {
@@ -165,8 +167,8 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
     else if (threadIdx.x == 0 && cc < cols + cols2) out2[cc - cols] = t;
 }
 
-// The gradient's: one vector a thread as far as 256 threads reach, since its sums of dw and a row's inputs fill the
-// registers at two (30 us instead of 24 at 8192 x 2048); wider rows take two, or an SM would hold one block of them.
+// The gradient's: one vector a thread as far as 512 threads reach, since its sums of dw and a row's inputs fill the
+// registers at two (30 us instead of 25 at 8192 x 2048 bf16; 77 instead of 49 on 512 threads at 4452 x 4096 fp32).
 Shape backward_shape(const NormArgs& a) {
     const int v = vectors_of(a);
     if (v <= 64) return {32, v <= 32 ? 1 : 2};
