@@ -7,7 +7,7 @@
 // window of W inputs in registers, so each input is loaded once; only the W - 1 inputs before a run are read again.
 // The next 12 tokens are on their way into the thread's own column of shared memory while these 4 are used: held in
 // registers they cost occupancy (168 registers with 8 channels a thread, 92 with 4) and fewer were in flight.  Products
-// go two channels at a time.  Measured: 16384 x 12288 bf16 in 11 packed sequences 144 us, 5.6 TB/s (0.84 of a copy's
+// go two channels at a time.  Measured: 16384 x 12288 bf16 in 11 packed sequences 134 us, 6.0 TB/s (0.90 of a copy's
 // rate).  Rows that start anywhere (see Ring) are bound by instructions, three times as many a token: 326 us with 12287
 // channels, fp32 8220 x 10838 158 us (0.68 of a copy's rate).
 //
@@ -16,7 +16,7 @@
 // The same walk with a second window, of dp: at token t the gradient of x_{t - W + 1} is complete.  A run goes W - 1
 // tokens past its end for the last of its dx.  dw and db are added in registers, then over the block's runs in shared
 // memory, and leave as one row of partial sums a block, which column_sum adds in a fixed order.  Bound: issue slots and
-// latency, 122 registers leaving 16 warps an SM.  Measured: 8192 x 6144 bf16 86 us, 3.5 TB/s, and 8 us for column_sum.
+// latency, 122 registers leaving 16 warps an SM.  Measured: 8192 x 6144 bf16 82 us, 3.7 TB/s, and 7 us for column_sum.
 #include <algorithm>
 
 #include "layer_common.cuh"
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int N = 4, P = N / 2;      // channels of a thread, and pairs of them
-constexpr int kRun = 32;             // tokens of a thread, fewer where there are few
+constexpr int kRun = 64;             // tokens of a thread, fewer where there are few
 
 // Lanes that share a token: the vectors of a row, at most 32 (a block's threads then hold kThreads / lanes runs).
 int row_lanes(int64_t D) {
@@ -457,13 +457,14 @@ conv_step_kernel(Conv a, int64_t pool, const int* __restrict__ slots, IO* __rest
 
 unsigned channel_blocks(int64_t D, int lanes) { return (unsigned)((D + lanes * N - 1) / (lanes * N)); }
 
-// Tokens of a thread: kRun, halved down to 4 while the blocks are fewer than two an SM.  Taps and the window are loaded
-// once a run, so long ones cost less; at few tokens the blocks count for more.
+// Tokens of a thread: kRun, halved down to 4 while the blocks are fewer than four an SM.  Taps and the window are loaded
+// once a run, so long ones cost less (16384 x 12288: 144 us with 32, 134 with 64, 138 with 128; 8192 x 4096 30 and 28); at
+// few tokens the blocks count for more (7252 x 1366: 22 us with 627 blocks of 32, 30 with 319 of 64).
 int run_of(const ConvArgs& a) {
     const int lanes = row_lanes(a.D);
     const int64_t per = kThreads / lanes;
     int run = kRun;
-    while (run > 4 && a.total / (run * per) * channel_blocks(a.D, lanes) < 2 * kSms) run /= 2;
+    while (run > 4 && a.total / (run * per) * channel_blocks(a.D, lanes) < 4 * kSms) run /= 2;
     return run;
 }
 

@@ -245,3 +245,31 @@ def test_refusals():
         with pytest.raises(GdrError) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [2500, 2501, 2502])
+def test_long_runs(D, io):
+    """Enough tokens and channels for the longest runs, whole and cut short by the sequences' ends."""
+    lens = [3000, 129, 0, 2500, 64, 2307]
+    x, state, cu = packed(lens, D, 4, io)
+    w, b = randn(D, 4, io=io, seed=5), randn(D, io=io, seed=6)
+    y, out = layer.conv_forward(x, w, b, state, cu_seqlens=cu)
+    check_sequences(x.split(lens), y.split(lens), out, w, b, state, True, io)
+    dy, d_out = randn(sum(lens), D, io=io, seed=7), randn(len(lens), 3, D, io=io, seed=8)
+    got = layer.conv_backward(x, w, b, dy, state, d_out, cu_seqlens=cu)
+    backward_check(x.split(lens), dy.split(lens), w, b, state, d_out, True, io, got)
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("D", [33, 65, 130])
+def test_a_row_does_not_see_its_neighbours(D, io):
+    """Rows that share an aligned word or vector with their neighbours' ends, which hold NaN and infinity."""
+    lens = [40, 30, 50]
+    x, state, cu = packed(lens, D, 4, io)
+    w, dy = randn(D, 4, io=io, seed=5), randn(120, D, io=io, seed=6)
+    y = layer.conv_forward(x, w, None, state, cu_seqlens=cu)[0]
+    dx = layer.conv_backward(x, w, None, dy, state, cu_seqlens=cu)[0]
+    x[:40], x[70:], dy[:40], dy[70:] = float("nan"), float("inf"), float("inf"), float("nan")
+    assert torch.equal(y[40:70], layer.conv_forward(x, w, None, state, cu_seqlens=cu)[0][40:70])
+    assert torch.equal(dx[40:70], layer.conv_backward(x, w, None, dy, state, cu_seqlens=cu)[0][40:70])

@@ -196,3 +196,23 @@ def test_refusals():
     with pytest.raises(GdrError) as e:
         layer.norm_backward(x, x, w, workspace=torch.empty(1, device="cuda", dtype=torch.uint8))
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,D", [(7, 33), (700, 250), (1300, 887), (1300, 2133), (700, 4089)])
+@pytest.mark.parametrize("quant", [None, "row", 32, 128])
+def test_a_row_does_not_see_its_neighbours(rows, D, quant, io):
+    """Rows that share an aligned vector with their neighbours' ends, which hold NaN and infinity."""
+    gen = torch.Generator().manual_seed(rows)
+    x, res, dy = (torch.randn(rows, D, generator=gen).to(io).cuda() for _ in range(3))
+    w = torch.randn(D, generator=gen).to(io).cuda()
+    clean = layer.norm_forward(x, w, res, eps=EPS, quant=quant)
+    dx = layer.norm_backward(dy, clean[1], w, eps=EPS)[0]
+    bad = torch.arange(rows, device="cuda") % 3 == 1
+    x[bad], dy[bad] = float("nan"), float("inf")
+    got = layer.norm_forward(x, w, res, eps=EPS, quant=quant)
+    for a, b in zip(clean, got):
+        if a is not None:
+            assert torch.equal(a[~bad].view(torch.uint8), b[~bad].view(torch.uint8))
+    assert torch.equal(dx[~bad], layer.norm_backward(dy, got[1], w, eps=EPS)[0][~bad])
+    assert got[1][bad].isnan().all() and (quant is None or got[3][bad].isnan().all())
