@@ -8,8 +8,8 @@
 // The next 12 tokens are on their way into the thread's own column of shared memory while these 4 are used: held in
 // registers they cost occupancy (168 registers with 8 channels a thread, 92 with 4) and fewer were in flight.  Products
 // go two channels at a time.  Measured: 16384 x 12288 bf16 in 11 packed sequences 134 us, 6.0 TB/s (0.90 of a copy's
-// rate).  Rows that start anywhere (see Ring) are bound by instructions, three times as many a token: 326 us with 12287
-// channels, fp32 8220 x 10838 158 us (0.68 of a copy's rate).
+// rate).  Rows that start anywhere (see Ring) are bound by instructions, three times as many a token: 310 us with 12287
+// channels, fp32 8220 x 10838 155 us (0.69 of a copy's rate).
 //
 // Gradient: with dp_t = dy_t act'(p_t), p_t formed again from x,
 //   dx_u = sum_j w_j dp_{u + W - 1 - j},  dw_j = sum_t dp_t x_{t - W + 1 + j},  db = sum_t dp_t.

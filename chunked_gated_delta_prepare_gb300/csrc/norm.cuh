@@ -50,10 +50,11 @@ template <typename IO> __device__ __forceinline__ int first_shift(int64_t row, i
 // Rows that do not start on 16-byte boundaries.  Where all tensors of a call share the place `shift` of a row's first
 // element between two boundaries (contiguous rows of D elements that are no multiple of 16 bytes), a thread's vectors are
 // cut at the boundaries instead of at column 0: vector i of a row covers the columns from 8 i - shift on, and only a row's
-// first and last vector go element by element.  The shift returns after `period` rows, so with a multiple of that many
+// first and last vector are not whole.  The shift returns after `period` rows, so with a multiple of that many
 // rows from one turn to the next it is a block's own, and w and the sums of dw stay in registers as for aligned rows.
 // (16384 rows of 4089 columns to e4m3: fp32 434 us with vectors from column 0 on, 158 cut, 137 with 4096 columns; bf16
 // 214, 85 and 75.)
+
 // Elements [at, at + 8) of a tensor of `total`, or any vector where they are not all in it.  A row's first and last vector
 // bring the neighbour rows' elements along; mask_cut takes them out when they are used, and the tensor's last vector is
 // loaded then.  Done on arrival, both would read or write the registers that the load fills, and keep the warp, and at

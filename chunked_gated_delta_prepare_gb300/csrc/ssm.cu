@@ -5,7 +5,7 @@
 // issue slots and the bytes that shared memory returns to registers.  A thread keeps 4 channels x 8 states: 32
 // independent recurrences hide each other's latency, what it reads of a token (Delta and Delta x of its channels, B and C
 // of its states, 96 bytes) serves all of them, and 2 shuffles join its channels' outputs.  (4 x 4 took 96 bytes for half
-// as many and measured 1.3 times the time.)  Products go two states at a time.  The inputs of 8 tokens come through
+// as many and measured 1.3 times the time.)  Products go two states at a time.  The inputs of a few tokens come through
 // shared memory in fp32: softplus, its product with x, and the widening happen once a value and not once a state.  The
 // next tile's loads are in flight meanwhile.  Measured: 32768 tokens x 4096 channels x 16 states bf16 652 us, 3.3 T
 // exponentials/s of the 9.4 T/s that they reach alone; issue slots 0.6 full with 12 warps an SM.
@@ -24,13 +24,15 @@ namespace layer {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 8;           // tokens staged in shared memory
 constexpr int kMinSegment = 32;
 constexpr int kBlocksPerSm = 3;
 
 // Channels of a thread (with a lane a channel 4 would make the tiles of a block too wide) and of a block.
 template <int LN> constexpr int channels_of() { return LN == 1 ? 2 : 4; }
 template <int LN> constexpr int width_of() { return kThreads / LN * channels_of<LN>(); }
+// Tokens staged in shared memory: 8, and 16 where a block has only 64 channels, so that each thread has a vector of 8
+// channels to stage (8192 x 4096 x 64 bf16: 1108 us for the scan with 8, 919 with 16).
+template <int LN> constexpr int tile_of() { return LN < 8 ? 8 : 16; }
 
 // Sums over a channel's LN lanes of v[0 .. DC), one for each of DC channels.  Partners halve the channels between them
 // while there is more than one: lane q is left with those from kept(q) on in v[0 .. kKept).
@@ -66,7 +68,7 @@ template <typename IO, int LN, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 ssm_scan_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ sums, IO* __restrict__ y,
                 float* __restrict__ h_final) {
-    constexpr int DC = channels_of<LN>(), W = width_of<LN>(), V8 = W / 8, NP = 8 * LN;
+    constexpr int DC = channels_of<LN>(), W = width_of<LN>(), V8 = W / 8, NP = 8 * LN, kTile = tile_of<LN>();
     constexpr int U = kTile * V8 <= kThreads ? 1 : kTile * V8 / kThreads;     // 8-channel units of a thread
     constexpr int M = (kTile * NP + kThreads - 1) / kThreads;                 // values of B (and of C) of a thread
     using Sum = ChannelSum<LN, DC>;
@@ -345,13 +347,14 @@ int width_at(int N) {
 // make one wave of blocks (a few blocks more would take a second wave's time).  Packed sequences have up to n segments
 // beside those of their tokens; the tokens get at least half the wave.
 int segment_of(const SsmArgs& a) {
+    const int tile = ssm_lanes(a.N, 8) < 8 ? tile_of<1>() : tile_of<8>();
     const int64_t blocks = ssm_blocks(a, width_at(a.N)), wave = kSms * kBlocksPerSm;
-    if (!a.cu && a.n * blocks >= wave / 2) return (int)((a.T + kTile - 1) / kTile * kTile);
+    if (!a.cu && a.n * blocks >= wave / 2) return (int)((a.T + tile - 1) / tile * tile);
     const int64_t all = std::max<int64_t>(wave / blocks, 1);
     const int64_t cuts = a.cu ? std::max<int64_t>(all - a.n, (all + 1) / 2) : std::max<int64_t>(all / a.n, 1);
     const int64_t tokens = a.cu ? a.total : a.T;
     const int64_t seg = std::max<int64_t>((tokens + cuts - 1) / cuts, kMinSegment);
-    return (int)((seg + kTile - 1) / kTile * kTile);
+    return (int)((seg + tile - 1) / tile * tile);
 }
 
 }  // namespace

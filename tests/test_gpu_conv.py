@@ -273,3 +273,23 @@ def test_a_row_does_not_see_its_neighbours(D, io):
     x[:40], x[70:], dy[:40], dy[70:] = float("nan"), float("inf"), float("inf"), float("nan")
     assert torch.equal(y[40:70], layer.conv_forward(x, w, None, state, cu_seqlens=cu)[0][40:70])
     assert torch.equal(dx[40:70], layer.conv_backward(x, w, None, dy, state, cu_seqlens=cu)[0][40:70])
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("D", [5, 64, 131])
+def test_tensors_that_start_at_one_element(D, io):
+    """x is a slice from column 1 on, dy and the states start one element into their memory."""
+    B, T = 2, 37
+
+    def shifted(*shape, seed):
+        t = randn(*shape, io=io, seed=seed)
+        out = torch.empty(t.numel() + 1, dtype=io, device="cuda")[1:].view(shape)
+        return out.copy_(t)
+
+    x = randn(B, T, D + 3, io=io)[..., 1:D + 1]
+    w, b = shifted(D, 4, seed=1), shifted(D, seed=2)
+    state, dy = shifted(B, 3, D, seed=3), shifted(B, T, D, seed=4)
+    y, out = layer.conv_forward(x, w, b, state)
+    check_sequences(x, y, out, w, b, state, True, io)
+    got = layer.conv_backward(x, w, b, dy, state)
+    backward_check(x, dy, w, b, state, None, True, io, (got[0].flatten(0, 1), *got[1:]))
