@@ -227,7 +227,8 @@ cudaError_t launch_forward(const NormArgs& a, RowTensor x, RowTensor res, const 
     static_assert(kSms % 8 == 0, "a multiple of the shifts' period");
     const int grid = (int)std::min<int64_t>(blocks, (int64_t)kSms * blocks_per_sm<TPR, VPT>());
     // Cut at the boundaries: rows not aligned, every tensor contiguous from a boundary on.
-    bool cut = (int64_t)a.D * sizeof(IO) % 16 != 0 && a.rows * a.D >= 8 && x.ld == a.D && (!res.p || res.ld == a.D);
+    bool cut = (int64_t)a.D * sizeof(IO) % 16 != 0 && vectors_of(a) <= TPR * VPT && a.rows * a.D >= 8 && x.ld == a.D &&
+               (!res.p || res.ld == a.D);
     for (const void* p : {x.p, res.p, (const void*)y, (const void*)r, (const void*)y8})
         cut = cut && reinterpret_cast<uintptr_t>(p) % 16 == 0;
     const auto al = [&](const void* p, int unit) {

@@ -114,7 +114,8 @@ template <int TPR, int VPT> constexpr int blocks_per_sm() {
     return threads > nt ? threads / nt : 1;
 }
 
-// a.D + 7: cut at the boundaries (see load_cut) a row may touch one vector more.
+// a.D + 7: cut at the boundaries a row may touch one vector more (in the longest rows one more than a block holds; they
+// are not cut).
 inline int vectors_of(const NormArgs& a) {
     return (a.D + (a.D * (a.io == GDR_F32 ? 4 : 2) % 16 ? 14 : 7)) / 8;
 }

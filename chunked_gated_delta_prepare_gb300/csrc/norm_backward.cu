@@ -189,7 +189,9 @@ cudaError_t launch_backward(const NormArgs& a, const void* dy, const void* r, co
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1, NT = TPR < 128 ? 128 : TPR, RING = ring_of<IO, NT, VPT>();
     bool vec = true;
     for (const void* p : {dy, r, w, dr, (const void*)dx}) vec = vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    const bool cut = vec && (int64_t)a.D * sizeof(IO) % 16 != 0;    // rows not aligned: cut at the boundaries
+    const bool odd = (int64_t)a.D * sizeof(IO) % 16 != 0;           // rows not aligned: cut at the boundaries
+    const bool cut = vec && odd && vectors_of(a) <= TPR * VPT;
+    vec = vec && (cut || !odd);
     const int64_t grid = backward_grid(a, {TPR, VPT});
     const auto go = [&](auto ring, auto in_cuts) {
         constexpr int R = decltype(ring)::value, bytes = R > 1 ? R * NT * VPT * 3 * (int)sizeof(Raw8<IO>) : 0;

@@ -216,3 +216,15 @@ def test_a_row_does_not_see_its_neighbours(rows, D, quant, io):
             assert torch.equal(a[~bad].view(torch.uint8), b[~bad].view(torch.uint8))
     assert torch.equal(dx[~bad], layer.norm_backward(dy, got[1], w, eps=EPS)[0][~bad])
     assert got[1][bad].isnan().all() and (quant is None or got[3][bad].isnan().all())
+
+
+LONG_ODD = [(400, 2553), (400, 5001), (310, 8191), (305, 16001), (305, 32761), (3, 32767), (310, 32767)]
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,D", LONG_ODD)
+def test_long_odd_rows(rows, D, io):
+    test_forward(rows, D, io)
+    test_eight_bits(rows, D, io, "row")
+    test_eight_bits(rows, D, io, 64)
+    test_backward(rows, D, io, True)
