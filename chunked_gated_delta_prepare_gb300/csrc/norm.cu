@@ -90,7 +90,7 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
                 const int c = (tid + i * TPR) * 8 - shift;
                 mask_cut(xr[i], c, D);
                 if (two) mask_cut(sr[i], c, D);
-                if (row + 1 == a.rows && c < D && c + 8 > D) {
+                if (live && c < D && ends_past(row, a.rows, c, D)) {
                     xr[i] = load_cut(reinterpret_cast<const IO*>(x.p) + row * D, c, D, false);
                     if (two) sr[i] = load_cut(reinterpret_cast<const IO*>(res.p) + row * D, c, D, false);
                 }

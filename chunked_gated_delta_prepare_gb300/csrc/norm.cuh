@@ -55,10 +55,15 @@ template <typename IO> __device__ __forceinline__ int first_shift(int64_t row, i
 // (16384 rows of 4089 columns to e4m3: fp32 434 us with vectors from column 0 on, 158 cut, 137 with 4096 columns; bf16
 // 214, 85 and 75.)
 
+// Whether the vector that starts at column c < D of a row ends past the tensor of `rows` rows.  In rows narrower than a
+// vector that is so in several of the tensor's last rows (up to 8: a vector has no more columns), not in the very last alone.
+__host__ __device__ __forceinline__ bool ends_past(int64_t row, int64_t rows, int c, int D) {
+    return rows - row <= 8 && c + 8 > (int)(rows - row) * D;
+}
 // Elements [at, at + 8) of a tensor of `total`, or any vector where they are not all in it.  A row's first and last vector
-// bring the neighbour rows' elements along; mask_cut takes them out when they are used, and the tensor's last vector is
-// loaded then.  Done on arrival, both would read or write the registers that the load fills, and keep the warp, and at
-// its barrier the block, waiting for memory in every row.
+// bring the neighbour rows' elements along; mask_cut takes them out when they are used, and a vector that ends past the
+// tensor is loaded then.  Done on arrival, both would read or write the registers that the load fills, and keep the warp,
+// and at its barrier the block, waiting for memory in every row.
 template <typename IO> __device__ __forceinline__ Raw8<IO> load_around(const IO* p, int64_t at, int64_t total) {
     return load8(p + (at + 8 <= total ? at : 0), 8, true);
 }

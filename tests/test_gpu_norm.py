@@ -228,3 +228,16 @@ def test_long_odd_rows(rows, D, io):
     test_eight_bits(rows, D, io, "row")
     test_eight_bits(rows, D, io, 64)
     test_backward(rows, D, io, True)
+
+
+NARROW = [*range(1, 21), 67, 3000]
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", range(1, 10))
+def test_rows_narrower_than_a_vector(D, io):
+    """Rows of 1 to 9 columns: a vector of 8 spans several of them, and those of more than one row end past the tensor."""
+    for rows in NARROW:
+        test_forward(rows, D, io)
+        test_eight_bits(rows, D, io, "row")
+        test_eight_bits(rows, D, io, 32)
