@@ -8,10 +8,12 @@ when it or a header under csrc/ or include/ is newer than its object file.
 binding/layer_binding.cpp, the torch binding of the layer operators, is a host
 file: it becomes _build/_gdr_layer.so with the host compiler against the
 installed torch's headers, beside the units of libgdr, which it links to.
+libgdr itself needs no torch: run as a script, this file builds it without.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -76,12 +78,13 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr):
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
 
-    binding_obj = os.path.join(BUILD, "layer_binding.o")
-    compile_binding, link_binding = _binding_commands(binding_obj, BINDING + f".tmp{os.getpid()}")
-    new_binding = force or not os.path.exists(BINDING) or \
-        os.path.getmtime(BINDING) < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "gdr.h")))
+    # without torch there is nothing to bind to, and libgdr is built alone
+    new_binding = importlib.util.find_spec("torch") is not None and (force or not os.path.exists(BINDING) or os.path.getmtime(
+        BINDING) < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "gdr.h"))))
     units = len(jobs)
     if new_binding:
+        binding_obj = os.path.join(BUILD, "layer_binding.o")
+        compile_binding, link_binding = _binding_commands(binding_obj, BINDING + f".tmp{os.getpid()}")
         jobs.append(compile_binding)
 
     def run(cmd):
