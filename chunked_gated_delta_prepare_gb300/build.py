@@ -8,6 +8,8 @@ when it or a header under csrc/ or include/ is newer than its object file.
 binding/layer_binding.cpp, the torch binding of the layer operators, is a host
 file: it becomes _build/_gdr_layer.so with the host compiler against the
 installed torch's headers, beside the units of libgdr, which it links to.
+_gdr_layer.so.for says which torch and Python it was built for; for another one
+it is built again.
 libgdr itself needs no torch: run as a script, this file builds it without.
 """
 from __future__ import annotations
@@ -17,6 +19,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -51,6 +54,27 @@ def _headers_mtime() -> float:
     return max((os.path.getmtime(h) for h in hs), default=0.0)
 
 
+def _binding_target():
+    """The torch and Python that a binding is for: where torch lies, its version file and Python's ABI, all without importing
+    torch; None without a torch."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return None
+    home = os.path.dirname(torch.origin)
+    with open(os.path.join(home, "version.py")) as f:
+        return "\n".join([sysconfig.get_config_var("SOABI") or sys.version, home, f.read()])
+
+
+def _binding_is_for(target: str) -> bool:
+    """Whether the built binding is newer than its sources and was built for this torch and Python."""
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING + ".for"):
+        return False
+    if os.path.getmtime(BINDING) < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "gdr.h"))):
+        return False
+    with open(BINDING + ".for") as f:
+        return f.read() == target
+
+
 def _binding_commands(obj: str, out: str):
     """The compile and link commands of the layer binding, for the torch and Python that run this."""
     import torch
@@ -78,9 +102,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr):
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
 
+    built_for = _binding_target()
     # without torch there is nothing to bind to, and libgdr is built alone
-    new_binding = importlib.util.find_spec("torch") is not None and (force or not os.path.exists(BINDING) or os.path.getmtime(
-        BINDING) < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "gdr.h"))))
+    new_binding = built_for is not None and (force or not _binding_is_for(built_for))
     units = len(jobs)
     if new_binding:
         binding_obj = os.path.join(BUILD, "layer_binding.o")
@@ -103,10 +127,13 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         os.replace(tmp, LIB)
     if new_binding:
         run(link_binding)
+        with open(BINDING + ".for", "w"):                # says nothing of the new file until that lies in its place
+            pass
         os.replace(BINDING + f".tmp{os.getpid()}", BINDING)
+        with open(BINDING + ".for", "w") as f:
+            f.write(built_for)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(verbose=True, force="--force" in sys.argv))

@@ -2,9 +2,11 @@
 
 The compilers are stand-ins that only leave the file they were asked for; a folder of the test's own takes the results.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 import types
 
 import pytest
@@ -60,3 +62,36 @@ assert build.build() == build.LIB
     ran = subprocess.run([sys.executable, "-I", "-S", "-c", script], capture_output=True, text=True)
     assert ran.returncode == 0, ran.stderr
     assert not os.path.exists(build.BINDING)
+
+
+def test_the_binding_is_compiled_again_for_another_torch(compiled, monkeypatch, tmp_path):
+    build.build()
+    compiled()
+    other = tmp_path / "elsewhere" / "torch"
+    other.mkdir(parents=True)
+    (other / "__init__.py").touch()
+    (other / "version.py").write_text("__version__ = '0.0.1'\n")
+    found = importlib.util.find_spec("torch")
+    spec = types.SimpleNamespace(origin=str(other / "__init__.py"))
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else None)
+    build.build()
+    assert compiled() == ["_gdr_layer.so", "layer_binding.o"]
+    build.build()
+    assert compiled() == []
+    (other / "version.py").write_text("__version__ = '0.0.2'\n")            # the same place, another version
+    build.build()
+    assert compiled() == ["_gdr_layer.so", "layer_binding.o"]
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: found)
+    build.build()
+    assert compiled() == ["_gdr_layer.so", "layer_binding.o"]
+
+
+def test_the_binding_is_compiled_again_for_another_python(compiled, monkeypatch):
+    build.build()
+    compiled()
+    here = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else here(name))
+    build.build()
+    assert compiled() == ["_gdr_layer.so", "layer_binding.o"]
+    build.build()
+    assert compiled() == []
