@@ -42,7 +42,7 @@ template <typename IO, int NT, int VPT, int RING, bool CUT> struct Pipe {
 #pragma unroll
                     for (int i = 0; i < VPT; ++i) {
                         const int c = (tid + i * tpr) * 8 - shift;
-                        if (c < D && (!CUT || row + 1 < rows || c + 8 <= D)) {      // in the tensor: see load_around
+                        if (c < D && !(CUT && ends_past(row, rows, c, D))) {
 #pragma unroll
                             for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
                                 copy_ahead(reinterpret_cast<RawN<IO, 16 / sizeof(IO)>*>(place(slot, t, i, part)),

@@ -241,3 +241,23 @@ def test_rows_narrower_than_a_vector(D, io):
         test_forward(rows, D, io)
         test_eight_bits(rows, D, io, "row")
         test_eight_bits(rows, D, io, 32)
+
+
+@pytest.mark.parametrize("with_dr", [False, True])
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", range(1, 10))
+def test_backward_of_rows_narrower_than_a_vector(D, io, with_dr):
+    """From 2433 rows on a block has a next row on its way; the tensors' last vectors hold the ends of several rows.
+
+    dw of a column: at most 2 rows a thread's sum, 76 partial sums in turn and 5 additions of a tree, each within 2^-24 of
+    the sum of the terms' sizes, and 4 roundings a term: 87 x 2^-24 = 5.2e-6 of it."""
+    for rows in (1, 2, 5, 8, 13, 600, 2432, 2433, 2440, 3001):
+        r, dy, w = make(rows, D, io, seed=rows)
+        dr = make(rows, D, io, seed=rows + 1)[0] if with_dr else None
+        dx, dw = layer.norm_backward(dy, r, w, dr, eps=EPS)
+        want, want_dw = backward_reference(dy, r, w, dr)
+        rstd = 1 / torch.sqrt((r.double() ** 2).mean(-1, keepdim=True) + EPS)
+        top = (rstd * (dy.double() * w.double()).abs()).amax(-1, keepdim=True) + (dr.double().abs() if with_dr else 0)
+        assert bool(((dx.double() - want).abs() <= 1e-5 * top + HALF_ULP[io] * want.abs() + 2.0 ** -24).all())
+        size = (dy.double() * r.double() * rstd).abs().sum(0)
+        assert bool(((dw.double() - want_dw).abs() <= 5.2e-6 * size + 1e-30).all())
