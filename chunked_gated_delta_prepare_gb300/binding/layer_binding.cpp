@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <array>
 #include <sstream>
 
@@ -45,6 +46,9 @@ double real(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return v;
 }
+// A size as the library's 32-bit fields take it.  What does not fit stays too large for the library, which refuses it: cut
+// to its lower 32 bits it could be a valid size that the outputs were not made for.
+int32_t small(int64_t v) { return (int32_t)std::min<int64_t>(v, INT32_MAX); }
 bool truth(PyObject* o) {
     const int v = PyObject_IsTrue(o);
     if (v < 0) throw python_error();
@@ -231,7 +235,7 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const int64_t D = shape.back(), group = integer(a[4]);
     const Rows xr = rows(c, a[0], shape, "x"), res = rows(c, a[2], shape, "residual");
     void* w = c.whole(a[1], c.io, {D}, "weight");
-    const gdr_norm_problem p{D ? x.numel() / D : 0, D, xr.ld, res.ld, c.io_code, (int32_t)(group > 0 ? group : 0),
+    const gdr_norm_problem p{D ? x.numel() / D : 0, D, xr.ld, res.ld, c.io_code, small(std::max<int64_t>(group, 0)),
                              (float)real(a[3])};
     std::array<Tensor, 4> out;
     if (truth(a[5])) out[0] = c.empty(shape, c.io);
@@ -239,7 +243,7 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     if (group >= 0) {
         out[2] = c.empty(shape, at::kFloat8_e4m3fn);
         std::vector<int64_t> s(shape.begin(), shape.end());
-        s.back() = group ? (D + group - 1) / group : 1;
+        s.back() = group ? (D - 1) / group + 1 : 1;
         out[3] = c.empty(s, F32);
     }
     const int st = gdr_norm_forward(&p, xr.p, res.p, w, at_or_null(out[0]), at_or_null(out[1]), at_or_null(out[2]),
@@ -287,7 +291,7 @@ struct Conv {
         const int64_t D = x.sizes().back(), W = wt.size(1);
         w = c.whole(weight, c.io, {D, W}, "weight");
         b = c.whole(bias, c.io, {D}, "bias");
-        p = gdr_conv_problem{q.n, q.T, q.total, D, xr.ld, 0, (int32_t)W, c.io_code, truth(silu)};
+        p = gdr_conv_problem{q.n, q.T, q.total, D, xr.ld, 0, small(W), c.io_code, truth(silu)};
         states = {q.n, W - 1, D};
     }
 };
@@ -339,7 +343,7 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const Call c(x, "x");
     const int64_t n = x.size(0), D = x.size(1), W = wt.size(1), pool = state.size(0);
     const Rows xr = rows(c, a[0], x.sizes(), "x");
-    const gdr_conv_problem p{n, 1, 0, D, xr.ld, pool, (int32_t)W, c.io_code, truth(a[4])};
+    const gdr_conv_problem p{n, 1, 0, D, xr.ld, pool, small(W), c.io_code, truth(a[4])};
     void *w = c.whole(a[1], c.io, {D, W}, "weight"), *b = c.whole(a[2], c.io, {D}, "bias"),
          *h = c.whole(a[3], c.io, {pool, W - 1, D}, "state");
     const int32_t* slots = (const int32_t*)c.whole(a[5], at::kInt, {n}, "slots");

@@ -293,3 +293,13 @@ def test_tensors_that_start_at_one_element(D, io):
     check_sequences(x, y, out, w, b, state, True, io)
     got = layer.conv_backward(x, w, b, dy, state)
     backward_check(x, dy, w, b, state, None, True, io, (got[0].flatten(0, 1), *got[1:]))
+
+
+def test_taps_beyond_32_bits_are_refused():
+    w = torch.empty(1, 2 ** 32 + 4, dtype=torch.bfloat16, device="cuda")       # 8.6 GB that nobody reads
+    x = torch.zeros(1, 8, 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(GdrError) as e:
+        layer.conv_forward(x, w, want_state=False)
+    assert e.value.status == 2
+    del w
+    torch.cuda.empty_cache()

@@ -261,3 +261,11 @@ def test_backward_of_rows_narrower_than_a_vector(D, io, with_dr):
         assert bool(((dx.double() - want).abs() <= 1e-5 * top + HALF_ULP[io] * want.abs() + 2.0 ** -24).all())
         size = (dy.double() * r.double() * rstd).abs().sum(0)
         assert bool(((dw.double() - want_dw).abs() <= 5.2e-6 * size + 1e-30).all())
+
+
+@pytest.mark.parametrize("quant", [2 ** 32 + 32, 2 ** 32, 2 ** 33 + 128, 2 ** 31, 2 ** 63 - 1])
+def test_groups_beyond_32_bits_are_refused(quant):
+    x, res, w = make(4, 256, torch.bfloat16)
+    with pytest.raises(GdrError) as e:
+        layer.norm_forward(x, w, res, quant=quant)
+    assert e.value.status == 9
