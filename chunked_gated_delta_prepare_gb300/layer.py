@@ -7,9 +7,9 @@
 
 The arithmetic runs in libgdr's CUDA kernels; binding/layer_binding.cpp checks the arguments and calls them, and a
 missing library raises.  Each call takes device tensors, allocates its outputs (and a workspace, unless one is given)
-and returns as soon as its kernels are queued on the current stream, or on `stream`, to which the outputs and the
-workspace then belong.  Shapes, types and devices that do not fit raise ValueError; what the library refuses raises
-GdrError.
+and returns as soon as its kernels are queued on the current stream of the tensors' device, or on `stream` (a stream of
+that device, or its handle), to which the outputs and the workspace then belong.  Shapes, types and devices that do not
+fit raise ValueError; what the library refuses raises GdrError.
 
 Inputs of tokens may be slices of a wider projection ([T, D] or [B, T, D] views with contiguous columns and one
 stride for all rows); views with other strides are copied first, and so are gradients that are not contiguous.
@@ -53,12 +53,19 @@ def _native():
 
 
 def _streamed(f):
-    """Adds `stream` to a call: allocations and kernels of the call then belong to that stream."""
+    """Adds `stream` to a call: allocations and kernels of the call then belong to that stream, one of the tensors' device."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        device = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if device is None or device.type != "cuda":
+            return f(*args, **kw)                    # which refuses them
+        if isinstance(stream, int):                  # a handle says nothing of its device, and the current one may be another
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        elif stream.device != device:
+            raise ValueError(f"stream: a stream of {device} is needed, got one of {stream.device}")
+        with torch.cuda.stream(stream):
             return f(*args, **kw)
     return call
 
