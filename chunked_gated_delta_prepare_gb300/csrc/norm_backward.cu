@@ -56,13 +56,19 @@ template <typename IO, int NT, int VPT, int RING, bool CUT> struct Pipe {
                     }
         copy_group();
     }
-    // The thread's vectors of tensor t of the row; zeros past the row's end and for a row that does not exist.
+    // The thread's vectors of tensor t of the row; zeros past the row's end and for a row that does not exist.  Without a ring
+    // nothing but a row's own loads is under way, so none may wait for another: with load_cut, whose element by element branch
+    // fills the registers of 16-bit vectors in halves, each did (4096 x 5120 bf16 131 us, 68 so; 8192 x 4095 291 and 185).
+    // Rows that start anywhere: fp32 vectors come from the blocks around them (4452 x 4096 115 us, 123 by elements), 16-bit
+    // ones by elements (8192 x 2048 66 us, 72 from blocks).
     __device__ __forceinline__ void take(int64_t row, int slot, int t, Raw8<IO> (&v)[VPT]) const {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * tpr) * 8 - shift, left = row < rows ? D - c : 0;
-            if (RING == 1) {
-                v[i] = load_cut(base[t] + row * D, c, left > 0 ? D : 0, vec);
+            if (RING == 1 && CUT) {
+                v[i] = load_around(base[t], left > 0 ? row * D + c : 0, rows * D);
+            } else if (RING == 1) {
+                v[i] = load8(base[t] + row * D + c, left, vec, sizeof(IO) == 4 ? c : 0);
             } else if (left > 0) {
 #pragma unroll
                 for (int part = 0; part < (int)sizeof(IO) / 2; ++part)
@@ -72,6 +78,13 @@ template <typename IO, int NT, int VPT, int RING, bool CUT> struct Pipe {
                 v[i] = load8((const IO*)nullptr, 0, false);
             }
         }
+        if (RING == 1 && CUT)          // when all loads are under way: see load_around
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (tid + i * tpr) * 8 - shift;
+                mask_cut(v[i], c, row < rows ? D : 0);
+                if (row < rows && c < D && ends_past(row, rows, c, D)) v[i] = load_cut(base[t] + row * D, c, D, false);
+            }
     }
 };
 
@@ -190,7 +203,7 @@ cudaError_t launch_backward(const NormArgs& a, const void* dy, const void* r, co
     bool vec = true;
     for (const void* p : {dy, r, w, dr, (const void*)dx}) vec = vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
     const bool odd = (int64_t)a.D * sizeof(IO) % 16 != 0;           // rows not aligned: cut at the boundaries
-    const bool cut = vec && odd && vectors_of(a) <= TPR * VPT;
+    const bool cut = vec && odd && vectors_of(a) <= TPR * VPT && a.rows * a.D >= 8;
     vec = vec && (cut || !odd);
     const int64_t grid = backward_grid(a, {TPR, VPT});
     const auto go = [&](auto ring, auto in_cuts) {

@@ -269,3 +269,21 @@ def test_groups_beyond_32_bits_are_refused(quant):
     with pytest.raises(GdrError) as e:
         layer.norm_forward(x, w, res, quant=quant)
     assert e.value.status == 9
+
+
+def test_backward_of_wide_rows_in_half_the_bytes_takes_no_longer():
+    """Rows of 4097 to 8192 columns, which no ring holds: loads that wait for one another took 16-bit rows past fp32's time."""
+    def fastest(io):
+        r, dy, w = make(4096, 8192, io, seed=9)
+        times = []
+        for _ in range(12):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            layer.norm_backward(dy, r, w, r)
+            end.record()
+            end.synchronize()
+            times.append(start.elapsed_time(end))
+        return min(times)
+
+    whole = fastest(torch.float32)
+    assert fastest(torch.bfloat16) < whole and fastest(torch.float16) < whole
