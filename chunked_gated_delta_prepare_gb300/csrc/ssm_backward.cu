@@ -272,16 +272,20 @@ template <typename IO> __device__ __forceinline__ void store_pairs(IO* p, const 
 // Shared memory of the main kernel, in floats.  terms_bc: dB and dC terms [token of the half][B or C][thread], 4 states
 // each; terms_n: r, y and sum A w, [token of the chunk][which][channel of the thread][thread].
 // The terms of one token, value and channel parity: group g = thread / LN (2 channels) at term_at<LN>(g), so that the
-// writers, and the readers of 4 neighbouring groups, both meet all banks.
-constexpr int kTerms = 4 * (32 + 8);
-template <int LN> __device__ __forceinline__ int term_at(int g) { return g % 4 * (32 + 8) + g / 4 * LN; }
+// writers, and the readers of 4 neighbouring groups, both meet all banks.  With 2 lanes a channel (up to 8 states) the gap
+// is 4 floats, where two writers share a bank: 8 would leave room for one block an SM, not the two that the registers and
+// the walks' lengths count on (4 x 2048 x 2048 x 8 bf16 608 us, 421 so).
+template <int LN> constexpr int kTermPad = LN == 2 ? 4 : 8;
+template <int LN> constexpr int kTerms = 4 * (32 + kTermPad<LN>);
+template <int LN> __device__ __forceinline__ int term_at(int g) { return g % 4 * (32 + kTermPad<LN>) + g / 4 * LN; }
 
 template <int LN> struct MainTiles {
     static constexpr int W = kThreads / LN * kDC, NP = 4 * LN;
     static constexpr int delta = 0, u = delta + kChunk * W, g = u + kChunk * W, b = g + kChunk * W, c = b + kChunk * NP,
                          bias = c + kChunk * NP, D = bias + W, terms_bc = D + W,
-                         terms_n = terms_bc + kHalf * 2 * kThreads * 4, total = terms_n + kChunk * 3 * kDC * kTerms;
+                         terms_n = terms_bc + kHalf * 2 * kThreads * 4, total = terms_n + kChunk * 3 * kDC * kTerms<LN>;
     static_assert(terms_bc % 4 == 0 && terms_n % 4 == 0, "16-byte pieces");
+    static_assert(kMainPerSm * (total * 4 + 1024) <= 228 * 1024, "the blocks fit an SM");
 };
 
 // span: segments (of the local kernel) of a block's walk.
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kMainPerSm) ssm_backward_kernel(Ssm 
                     const float2 d2 = pd[tk * W / 2], u2 = pu[tk * W / 2], g2 = pg[tk * W / 2];
                     const F2 b[2] = {pb[tk * NP / 2], pb[tk * NP / 2 + 1]}, cv[2] = {pc[tk * NP / 2], pc[tk * NP / 2 + 1]};
                     F2 dB[2], dC[2];
-                    float* tn = sm + S::terms_n + tk * 3 * kDC * kTerms + term_at<LN>(threadIdx.x / LN) + q;
+                    float* tn = sm + S::terms_n + tk * 3 * kDC * kTerms<LN> + term_at<LN>(threadIdx.x / LN) + q;
 #pragma unroll
                     for (int i = 0; i < kDC; ++i) {
                         const F2 d = both(i ? d2.y : d2.x), u = both(i ? u2.y : u2.x), g = both(i ? g2.y : g2.x);
@@ -412,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, kMainPerSm) ssm_backward_kernel(Ssm 
                             dAh[i][j] = fma2(d, wt, dAh[i][j]);
                         }
                         const float2 fr = unpack2(r), fy = unpack2(y), fs = unpack2(s);
-                        tn[(0 * kDC + i) * kTerms] = fr.x + fr.y;
-                        tn[(1 * kDC + i) * kTerms] = fy.x + fy.y;
-                        tn[(2 * kDC + i) * kTerms] = fs.x + fs.y;
+                        tn[(0 * kDC + i) * kTerms<LN>] = fr.x + fr.y;
+                        tn[(1 * kDC + i) * kTerms<LN>] = fy.x + fy.y;
+                        tn[(2 * kDC + i) * kTerms<LN>] = fs.x + fs.y;
                     }
                     ulonglong2* tb = reinterpret_cast<ulonglong2*>(sm + S::terms_bc) + k * 2 * kThreads + threadIdx.x;
                     tb[0] = make_ulonglong2(dB[0], dB[1]);
@@ -470,10 +474,10 @@ __global__ void __launch_bounds__(kThreads, kMainPerSm) ssm_backward_kernel(Ssm 
                 for (int j = 0; j < 3; ++j)
 #pragma unroll
                     for (int x = 0; x < 8; x += 2) {   // channels x and x + 1 are one thread's two
-                        const float* p = sm + S::terms_n + (k * 3 + j) * kDC * kTerms + term_at<LN>((in.col + x) / 2);
+                        const float* p = sm + S::terms_n + (k * 3 + j) * kDC * kTerms<LN> + term_at<LN>((in.col + x) / 2);
                         float f[2];
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) f[m] = lanes_total<LN>(p + m * kTerms);
+                        for (int m = 0; m < 2; ++m) f[m] = lanes_total<LN>(p + m * kTerms<LN>);
                         v[j][x / 2] = pack2(f[0], f[1]);
                     }
                 const F2* delta = reinterpret_cast<const F2*>(sm + S::delta + k * W + in.col);
