@@ -1,8 +1,10 @@
 // Device helpers shared by the layer operators (norm, convolution, selective scan, single-token delta step).
 //
 // They work on vectors of 8 (or 4) neighbouring channels of one token.  A row may start at any element: where its
-// address is not a multiple of 16 bytes, a vector comes from the aligned blocks around it (4 times fewer trips through
-// the L1 cache than element by element), and goes out in aligned words; at a row's ends the elements move one by one.
+// address is not a multiple of 16 bytes, the scan and the norm's fp32 gradient take a vector from the aligned blocks around
+// it (4 times fewer trips through the L1 cache than element by element), the convolution by words; the norm cuts contiguous
+// rows at the boundaries and takes slices element by element (see norm.cu).  Vectors go out in aligned words; at a row's
+// ends the elements move one by one.
 // Whether a tensor's rows are all aligned is decided on the host (RowTensor::vec).
 #pragma once
 

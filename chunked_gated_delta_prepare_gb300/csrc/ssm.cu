@@ -8,7 +8,10 @@
 // as many and measured 1.3 times the time.)  Products go two states at a time.  The inputs of a few tokens come through
 // shared memory in fp32: softplus, its product with x, and the widening happen once a value and not once a state.  The
 // next tile's loads are in flight meanwhile.  Measured: 32768 tokens x 4096 channels x 16 states bf16 652 us, 3.3 T
-// exponentials/s of the 9.4 T/s that they reach alone; issue slots 0.6 full with 12 warps an SM.
+// exponentials/s of the 9.4 T/s that they reach alone.  That is neither pipe's limit: a warp's token is 64 packed fp32
+// instructions and 32 exponentials, 128 cycles of each pipe side by side, and takes about 365 to 390 (3449 warp-tokens a
+// scheduler).  Some 210 of these issue, half of them staging, moves, loads and shuffles; the rest is latency that 12 warps
+// an SM do not hide.
 //
 // Few sequences and channels leave most of the GPU idle, so a long sequence is cut into segments: a first kernel scans
 // every segment but the last from a zero state and keeps what it leaves and the sum of its Delta (its decay is
@@ -290,7 +293,8 @@ ssm_join_kernel(Ssm a, float* __restrict__ ends, float* __restrict__ dends, cons
 // One token of a row: LN lanes a channel, 8 states each, the state read and written once.  What is left beside the
 // state's bytes (softplus, the gate, addresses) is a channel's, so 8 states a thread halve it against 4.  Bound: memory's
 // latency, one load of everything a thread: 64 x 4096 x 16 bf16 9.7 us, 3.7 TB/s (10.8 with 4 states a thread; 14.3 with 4
-// rows a thread that share A, which leave a quarter of the threads).
+// rows a thread that share A, which leave a quarter of the threads).  That latency counts three times: 4096 blocks at 56
+// registers are three waves of 9 an SM, and a block has nothing under way beside its one round of loads.
 template <typename IO, int LN>
 __global__ void __launch_bounds__(kThreads)
 ssm_step_kernel(Ssm a, int64_t pool, const int* __restrict__ slots, float* __restrict__ h, IO* __restrict__ y) {

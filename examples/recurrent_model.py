@@ -5,7 +5,8 @@ and training steps.
 
 Each layer is  residual + norm -> input projection -> short convolution -> recurrence -> output projection, the
 recurrence being the gated delta rule or the selective state space scan.  Serving takes the norm's 8-bit output: a
-row's scale commutes with the projection, so it is applied to the product.  Decoding continues from the states the
+row's scale commutes with the projection, so it is applied to the product (in bf16 here: torch's product widens the
+values first, so the 8 bits save no time in this example).  Decoding continues from the states the
 prompt left, and its logits are those of the whole sequence run as a prompt.
 """
 import os
