@@ -478,10 +478,195 @@ PyObject* delta_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
     END_HANDLE_TH_ERRORS
 }
 
+// ---------------------------------------------------------------- gated linear recurrence
+
+struct Lru {
+    Rows x, r, i;
+    const float* lam;
+    gdr_lru_problem p;
+
+    Lru(const Call& c, const Tensor& xt, PyObject* const* a, PyObject* rate, int64_t n, int64_t T, int64_t total, int64_t pool) {
+        const IntArrayRef shape = xt.sizes();
+        const int64_t D = shape.back();
+        x = rows(c, a[0], shape, "x");
+        TORCH_CHECK_VALUE(!is_none(a[1]), "r: a tensor is needed");
+        r = rows(c, a[1], shape, "r");
+        i = rows(c, a[2], shape, "i");
+        lam = (const float*)c.whole(a[3], F32, {D}, "lam");
+        p = gdr_lru_problem{n, T, total, D, x.ld, r.ld, i.ld, pool, c.io_code, (float)real(rate)};
+    }
+    // Rows of the kept states.
+    int64_t kept(const Sequences& q) const {
+        return p.D ? (int64_t)(gdr_lru_kept_bytes(&p, q.cu != nullptr) / 4) / p.D : 0;
+    }
+};
+
+// x, r, i, lam, h0, c, cu_seqlens, want_h_final, want_kept, workspace -> y, h_final, kept
+PyObject* lru_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 10);
+    const Tensor& x = tensor(a[0], "x");
+    const Call c(x, "x");
+    const Sequences q(c, x, a[6]);
+    const Lru s(c, x, a, a[5], q.n, q.T, q.total, 0);
+    const std::array<int64_t, 2> states{q.n, s.p.D};
+    const float* h0 = (const float*)c.whole(a[4], F32, states, "h0");
+    std::array<Tensor, 3> out{c.empty(x.sizes(), c.io), Tensor(), Tensor()};
+    if (truth(a[7])) out[1] = c.empty(states, F32);
+    if (truth(a[8])) out[2] = c.empty({s.kept(q), s.p.D}, F32);
+    const Workspace ws(c, a[9], gdr_lru_forward_workspace_bytes(&s.p, q.cu != nullptr, out[2].defined()));
+    const int st = gdr_lru_forward(&s.p, q.cu, s.x.p, s.r.p, s.i.p, s.lam, h0, out[0].data_ptr(),
+                                   (float*)at_or_null(out[1]), (float*)at_or_null(out[2]), ws.p, ws.bytes, c.stream());
+    return st ? gdr_error(st, "gdr_lru_forward") : results(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// x, r, i, lam, dy, h0, dh_final, kept, c, cu_seqlens, workspace -> dx, dr, di, dlam, dh0
+PyObject* lru_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 11);
+    const Tensor& x = tensor(a[0], "x");
+    const Call c(x, "x");
+    const Sequences q(c, x, a[9]);
+    const Lru s(c, x, a, a[8], q.n, q.T, q.total, 0);
+    const std::array<int64_t, 2> states{q.n, s.p.D};
+    const float* h0 = (const float*)c.whole(a[5], F32, states, "h0");
+    const float* kept = (const float*)c.whole(a[7], F32, {s.kept(q), s.p.D}, "kept");
+    const Tensor dy = gradient(c, a[4], c.io, x.sizes(), "dy"), dh = gradient(c, a[6], F32, states, "dh_final");
+    TORCH_CHECK_VALUE(dy.defined(), "dy: a tensor is needed");
+    std::array<Tensor, 5> out{c.empty(x.sizes(), c.io), c.empty(x.sizes(), c.io)};
+    if (!is_none(a[2])) out[2] = c.empty(x.sizes(), c.io);
+    if (s.lam) out[3] = c.empty({s.p.D}, F32);
+    if (h0) out[4] = c.empty(states, F32);
+    const Workspace ws(c, a[10], gdr_lru_backward_workspace_bytes(&s.p, q.cu != nullptr, kept != nullptr));
+    const int st = gdr_lru_backward(&s.p, q.cu, s.x.p, s.r.p, s.i.p, s.lam, h0, dy.data_ptr(), (const float*)at_or_null(dh),
+                                    kept, out[0].data_ptr(), out[1].data_ptr(), at_or_null(out[2]),
+                                    (float*)at_or_null(out[3]), (float*)at_or_null(out[4]), ws.p, ws.bytes, c.stream());
+    return st ? gdr_error(st, "gdr_lru_backward") : results(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// x, r, i, lam, h, c, slots -> y
+PyObject* lru_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 7);
+    const Tensor &x = tensor(a[0], "x"), &h = tensor(a[4], "h");
+    TORCH_CHECK_VALUE(x.dim() == 2 && h.dim() == 2, "x [n, D] and h [pool, D] are needed");
+    const Call c(x, "x");
+    const int64_t n = x.size(0), pool = h.size(0);
+    const Lru s(c, x, a, a[5], n, 1, 0, pool);
+    float* hp = (float*)c.whole(a[4], F32, {pool, s.p.D}, "h");
+    const int32_t* slots = (const int32_t*)c.whole(a[6], at::kInt, {n}, "slots");
+    const Tensor y = c.empty(x.sizes(), c.io);
+    const int st = gdr_lru_step(&s.p, slots, s.x.p, s.r.p, s.i.p, s.lam, hp, y.data_ptr(), c.stream());
+    return st ? gdr_error(st, "gdr_lru_step") : wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------- layer norm
+
+// x, weight, bias, residual, eps, want_y -> y, r
+PyObject* layernorm_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 6);
+    const Tensor& x = tensor(a[0], "x");
+    const Call c(x, "x");
+    const IntArrayRef shape = x.sizes();
+    TORCH_CHECK_VALUE(x.dim() >= 1, "x: [..., D] is needed");
+    TORCH_CHECK_VALUE(!is_none(a[1]), "weight: a tensor is needed");
+    const int64_t D = shape.back();
+    const Rows xr = rows(c, a[0], shape, "x"), res = rows(c, a[3], shape, "residual");
+    void *w = c.whole(a[1], c.io, {D}, "weight"), *b = c.whole(a[2], c.io, {D}, "bias");
+    const gdr_layernorm_problem p{D ? x.numel() / D : 0, D, xr.ld, res.ld, c.io_code, (float)real(a[4])};
+    std::array<Tensor, 2> out;
+    if (truth(a[5])) out[0] = c.empty(shape, c.io);
+    if (!is_none(a[3])) out[1] = c.empty(shape, c.io);
+    const int st = gdr_layernorm_forward(&p, xr.p, res.p, w, b, at_or_null(out[0]), at_or_null(out[1]), c.stream());
+    return st ? gdr_error(st, "gdr_layernorm_forward") : results(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// dy, r, weight, d_r, eps, workspace -> dx, dweight, dbias
+PyObject* layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 6);
+    const Call c(tensor(a[1], "r"), "r");
+    const IntArrayRef shape = tensor(a[1], "r").sizes();
+    TORCH_CHECK_VALUE(shape.size() >= 1, "r: [..., D] is needed");
+    TORCH_CHECK_VALUE(!is_none(a[2]), "weight: a tensor is needed");
+    const int64_t D = shape.back();
+    const Tensor dy = gradient(c, a[0], c.io, shape, "dy"), r = gradient(c, a[1], c.io, shape, "r"),
+                 dr = gradient(c, a[3], c.io, shape, "d_r");
+    TORCH_CHECK_VALUE(dy.defined(), "dy: a tensor is needed");
+    void* w = c.whole(a[2], c.io, {D}, "weight");
+    const gdr_layernorm_problem p{D ? r.numel() / D : 0, D, 0, 0, c.io_code, (float)real(a[4])};
+    const std::array<Tensor, 3> out{c.empty(shape, c.io), c.empty({D}, F32), c.empty({D}, F32)};
+    const Workspace ws(c, a[5], gdr_layernorm_backward_workspace_bytes(&p));
+    const int st = gdr_layernorm_backward(&p, dy.data_ptr(), r.data_ptr(), w, at_or_null(dr), out[0].data_ptr(),
+                                          (float*)out[1].data_ptr(), (float*)out[2].data_ptr(), ws.p, ws.bytes, c.stream());
+    return st ? gdr_error(st, "gdr_layernorm_backward") : results(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------- gated norm
+
+struct GatedNorm {
+    const Tensor& x;
+    Call c;
+    IntArrayRef shape;
+    Rows xr, zr;
+    const void* w;
+    gdr_gated_norm_problem p;
+
+    GatedNorm(PyObject* x_, PyObject* z, PyObject* weight, PyObject* gate, PyObject* eps)
+        : x(tensor(x_, "x")), c(x, "x"), shape(x.sizes()) {
+        TORCH_CHECK_VALUE(x.dim() >= 2, "x: [..., H, V] is needed, got ", shape);
+        TORCH_CHECK_VALUE(!is_none(z), "z: a tensor is needed");
+        const int64_t H = x.size(-2), V = x.size(-1);
+        xr = rows(c, x_, shape, "x", 2);
+        zr = rows(c, z, shape, "z", 2);
+        const bool per_head = tensor(weight, "weight").dim() == 2;
+        const std::array<int64_t, 2> hv{H, V};
+        w = c.whole(weight, c.io, IntArrayRef(hv.data() + (per_head ? 0 : 1), per_head ? 2 : 1), "weight");
+        p = gdr_gated_norm_problem{H && V ? x.numel() / (H * V) : 0, H, V, xr.ld, zr.ld, c.io_code, small(integer(gate)),
+                                   per_head, (float)real(eps)};
+    }
+};
+
+// x, z, weight, gate, eps -> y
+PyObject* gated_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 5);
+    const GatedNorm v(a[0], a[1], a[2], a[3], a[4]);
+    const Tensor y = v.c.empty(v.shape, v.c.io);
+    const int st = gdr_gated_norm_forward(&v.p, v.xr.p, v.zr.p, v.w, y.data_ptr(), v.c.stream());
+    return st ? gdr_error(st, "gdr_gated_norm_forward") : wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+// dy, x, z, weight, gate, eps, workspace -> dx, dz, dweight
+PyObject* gated_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    expect(count, 7);
+    const GatedNorm v(a[1], a[2], a[3], a[4], a[5]);
+    const Call& c = v.c;
+    const Tensor dy = gradient(c, a[0], c.io, v.shape, "dy");
+    TORCH_CHECK_VALUE(dy.defined(), "dy: a tensor is needed");
+    const std::array<Tensor, 3> out{c.empty(v.shape, c.io), c.empty(v.shape, c.io), c.empty(tensor(a[3], "weight").sizes(), F32)};
+    const Workspace ws(c, a[6], gdr_gated_norm_backward_workspace_bytes(&v.p));
+    const int st = gdr_gated_norm_backward(&v.p, dy.data_ptr(), v.xr.p, v.zr.p, v.w, out[0].data_ptr(), out[1].data_ptr(),
+                                           (float*)out[2].data_ptr(), ws.p, ws.bytes, c.stream());
+    return st ? gdr_error(st, "gdr_gated_norm_backward") : results(out);
+    END_HANDLE_TH_ERRORS
+}
+
 #define GDR_METHOD(name) {#name, (PyCFunction)(void*)name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GDR_METHOD(norm_forward), GDR_METHOD(norm_backward), GDR_METHOD(conv_forward),
                          GDR_METHOD(conv_backward), GDR_METHOD(conv_step), GDR_METHOD(ssm_forward),
-                         GDR_METHOD(ssm_backward), GDR_METHOD(ssm_step), GDR_METHOD(delta_step), {}};
+                         GDR_METHOD(ssm_backward), GDR_METHOD(ssm_step), GDR_METHOD(delta_step), GDR_METHOD(lru_forward),
+                         GDR_METHOD(lru_backward), GDR_METHOD(lru_step), GDR_METHOD(layernorm_forward),
+                         GDR_METHOD(layernorm_backward), GDR_METHOD(gated_norm_forward),
+                         GDR_METHOD(gated_norm_backward), {}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdr_layer", "Argument checks and calls behind layer.py.", -1, methods};
 
 }  // namespace

@@ -112,6 +112,45 @@ SsmTensors ssm_tensors(const gdr_ssm_problem* p, const void* x, const void* dt, 
                       rows_of(B, p->b_ld, bc, e),   rows_of(C, p->c_ld, bc, e),     A, dt_bias, Dk, h0};
 }
 
+gdr_status lru_args(const gdr_lru_problem* p, const int32_t* cu, bool packed, bool rate, LruArgs* a) {
+    if (!p) return GDR_ERR_NULL;
+    if (!known_dtype(p->io_dtype)) return GDR_ERR_DTYPE;
+    const int64_t tokens = token_axis(p->n, p->T, p->total, packed);
+    if (tokens < 0 || p->D < 1 || p->D > kMaxChannels) return GDR_ERR_SHAPE;
+    for (int64_t ld : {p->x_ld, p->r_ld, p->i_ld})
+        if (!good_ld(ld, p->D, tokens)) return GDR_ERR_SHAPE;
+    if (rate && (!(p->c > 0.f) || std::isinf(p->c))) return GDR_ERR_ARG;
+    *a = LruArgs{p->n, p->T, tokens, cu, (int)p->D, p->io_dtype, p->c};
+    // a block for each tile and 64 channels, numbered in 31 bits
+    if (lru_tiles(*a) > ((int64_t{1} << 31) - 1) / ((p->D + 63) / 64)) return GDR_ERR_SHAPE;
+    return GDR_OK;
+}
+
+LruTensors lru_tensors(const gdr_lru_problem* p, const void* x, const void* r, const void* i, const float* lam,
+                       const float* h0) {
+    const int64_t e = element_size(p->io_dtype);
+    return LruTensors{rows_of(x, p->x_ld, p->D, e), rows_of(r, p->r_ld, p->D, e), rows_of(i, p->i_ld, p->D, e), lam, h0};
+}
+
+gdr_status layernorm_args(const gdr_layernorm_problem* p, NormArgs* a) {
+    if (!p) return GDR_ERR_NULL;
+    const gdr_norm_problem n{p->rows, p->D, p->x_ld, p->res_ld, p->io_dtype, 0, p->eps};
+    return norm_args(&n, a);
+}
+
+gdr_status gated_norm_args(const gdr_gated_norm_problem* p, GatedNormArgs* a) {
+    if (!p) return GDR_ERR_NULL;
+    if (!known_dtype(p->io_dtype)) return GDR_ERR_DTYPE;
+    if (p->H < 1 || p->H > kMaxChannels || p->V < 1 || p->V > kGatedNormMaxV || p->tokens < 0 ||
+        p->tokens > (kMaxTokens - 1) / p->H)
+        return GDR_ERR_SHAPE;
+    if (!good_ld(p->x_ld, p->H * p->V, p->tokens) || !good_ld(p->z_ld, p->H * p->V, p->tokens)) return GDR_ERR_SHAPE;
+    if ((p->gate != 0 && p->gate != 1) || (p->per_head != 0 && p->per_head != 1)) return GDR_ERR_ARG;
+    if (!(p->eps >= 0.f) || std::isinf(p->eps)) return GDR_ERR_ARG;
+    *a = GatedNormArgs{p->tokens, (int)p->H, (int)p->V, p->eps, p->io_dtype, p->gate == 0, p->per_head == 1};
+    return GDR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -301,6 +340,152 @@ gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const int32_t* slots, const vo
     return done(ssm_step(a, ssm_tensors(p, x, dt, A, B, C, Dk, z, dt_bias, nullptr), p->pool, slots, h, y,
                          (cudaStream_t)stream),
                 "ssm_step");
+}
+
+size_t gdr_lru_kept_bytes(const gdr_lru_problem* p, int32_t packed) {
+    LruArgs a;
+    const int32_t some = 0;
+    if (lru_args(p, packed ? &some : nullptr, packed != 0, false, &a)) return 0;
+    return (size_t)lru_tiles(a) * (size_t)a.D * 4;
+}
+
+size_t gdr_lru_forward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept) {
+    LruArgs a;
+    const int32_t some = 0;
+    if (lru_args(p, packed ? &some : nullptr, packed != 0, false, &a)) return 0;
+    return lru_forward_workspace(a, kept != 0);
+}
+
+gdr_status gdr_lru_forward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r, const void* i,
+                           const float* lam, const float* h0, void* y, float* h_final, float* kept, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    LruArgs a;
+    if (gdr_status st = lru_args(p, cu_seqlens, cu_seqlens != nullptr, lam != nullptr, &a)) return st;
+    const int64_t e = element_size(p->io_dtype);
+    const bool any = a.total > 0;
+    if (gdr_status st = check({{cu_seqlens, 4, false}, {x, e, any}, {r, e, any}, {i, e, false}, {lam, 4, false},
+                               {h0, 4, false}, {y, e, any}, {h_final, 4, false}, {kept, 4, false}}))
+        return st;
+    if (gdr_status st = check_workspace(workspace, workspace_bytes, lru_forward_workspace(a, kept != nullptr))) return st;
+    return done(lru_forward(a, lru_tensors(p, x, r, i, lam, h0), y, h_final, kept, (float*)workspace,
+                            (cudaStream_t)stream),
+                "lru");
+}
+
+size_t gdr_lru_backward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept) {
+    LruArgs a;
+    const int32_t some = 0;
+    if (lru_args(p, packed ? &some : nullptr, packed != 0, false, &a)) return 0;
+    return lru_backward_workspace(a, kept != 0);
+}
+
+gdr_status gdr_lru_backward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r,
+                            const void* i, const float* lam, const float* h0, const void* dy, const float* dh_final,
+                            const float* kept, void* dx, void* dr, void* di, float* dlam, float* dh0, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    LruArgs a;
+    if (gdr_status st = lru_args(p, cu_seqlens, cu_seqlens != nullptr, lam != nullptr, &a)) return st;
+    const int64_t e = element_size(p->io_dtype);
+    const bool any = a.total > 0;
+    if (gdr_status st = check({{cu_seqlens, 4, false}, {x, e, any}, {r, e, any}, {i, e, false}, {lam, 4, false},
+                               {h0, 4, false}, {dy, e, any}, {dh_final, 4, false}, {kept, 4, false}, {dx, e, any},
+                               {dr, e, any}, {di, e, any && i}, {dlam, 4, lam != nullptr}, {dh0, 4, false}}))
+        return st;
+    if (gdr_status st = check_workspace(workspace, workspace_bytes, lru_backward_workspace(a, kept != nullptr))) return st;
+    const LruGrads g{dy, dh_final, dx, dr, di, dlam, dh0};
+    return done(lru_backward(a, lru_tensors(p, x, r, i, lam, h0), g, kept, (float*)workspace, (cudaStream_t)stream), "lru");
+}
+
+gdr_status gdr_lru_step(const gdr_lru_problem* p, const int32_t* slots, const void* x, const void* r, const void* i,
+                        const float* lam, float* h, void* y, void* stream) {
+    if (!p) return GDR_ERR_NULL;
+    gdr_lru_problem one = *p;
+    one.T = 1;
+    LruArgs a;
+    if (gdr_status st = lru_args(&one, nullptr, false, lam != nullptr, &a)) return st;
+    if (p->pool < 1 || p->pool >= kMaxTokens || (!slots && p->n > p->pool)) return GDR_ERR_SHAPE;
+    const int64_t e = element_size(p->io_dtype);
+    if (gdr_status st = check({{slots, 4, false}, {x, e, true}, {r, e, true}, {i, e, false}, {lam, 4, false}, {h, 4, true},
+                               {y, e, true}}))
+        return st;
+    return done(lru_step(a, lru_tensors(p, x, r, i, lam, nullptr), p->pool, slots, h, y, (cudaStream_t)stream),
+                "lru_step");
+}
+
+gdr_status gdr_layernorm_forward(const gdr_layernorm_problem* p, const void* x, const void* residual, const void* w,
+                                 const void* b, void* y, void* r, void* stream) {
+    NormArgs a;
+    if (gdr_status st = layernorm_args(p, &a)) return st;
+    if (p->rows == 0) return GDR_OK;
+    const int64_t e = element_size(p->io_dtype);
+    if (gdr_status st = check({{x, e, true}, {residual, e, false}, {w, e, true}, {b, e, false}, {y, e, false},
+                               {r, e, false}}))
+        return st;
+    if (!y && !r) return GDR_ERR_NULL;
+    return done(layernorm_forward(a, rows_of(x, p->x_ld, p->D, e), rows_of(residual, p->res_ld, p->D, e), w, b, y, r,
+                                  (cudaStream_t)stream),
+                "layernorm");
+}
+
+size_t gdr_layernorm_backward_workspace_bytes(const gdr_layernorm_problem* p) {
+    NormArgs a;
+    if (layernorm_args(p, &a)) return 0;
+    return (size_t)layernorm_partial_rows(a) * (size_t)p->D * 8;
+}
+
+gdr_status gdr_layernorm_backward(const gdr_layernorm_problem* p, const void* dy, const void* r, const void* w,
+                                  const void* dr, void* dx, float* dw, float* db, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    NormArgs a;
+    if (gdr_status st = layernorm_args(p, &a)) return st;
+    const int64_t e = element_size(p->io_dtype);
+    const bool any = p->rows > 0;
+    if (gdr_status st = check({{dy, e, any}, {r, e, any}, {w, e, true}, {dr, e, false}, {dx, e, any}, {dw, 4, true},
+                               {db, 4, true}}))
+        return st;
+    if (gdr_status st = check_workspace(workspace, workspace_bytes, gdr_layernorm_backward_workspace_bytes(p))) return st;
+    if (!any) {   // the sums of no rows
+        const cudaError_t first = cudaMemsetAsync(dw, 0, (size_t)p->D * 4, (cudaStream_t)stream);
+        return done(first ? first : cudaMemsetAsync(db, 0, (size_t)p->D * 4, (cudaStream_t)stream), "layernorm");
+    }
+    return done(layernorm_backward(a, dy, r, w, dr, dx, dw, db, (float*)workspace, (cudaStream_t)stream), "layernorm");
+}
+
+gdr_status gdr_gated_norm_forward(const gdr_gated_norm_problem* p, const void* x, const void* z, const void* w, void* y,
+                                  void* stream) {
+    GatedNormArgs a;
+    if (gdr_status st = gated_norm_args(p, &a)) return st;
+    if (p->tokens == 0) return GDR_OK;
+    const int64_t e = element_size(p->io_dtype);
+    if (gdr_status st = check({{x, e, true}, {z, e, true}, {w, e, true}, {y, e, true}})) return st;
+    return done(gated_norm_forward(a, rows_of(x, p->x_ld, p->H * p->V, e), rows_of(z, p->z_ld, p->H * p->V, e), w, y,
+                                   (cudaStream_t)stream),
+                "gated_norm");
+}
+
+size_t gdr_gated_norm_backward_workspace_bytes(const gdr_gated_norm_problem* p) {
+    GatedNormArgs a;
+    if (gated_norm_args(p, &a) || p->tokens == 0) return 0;
+    return (size_t)gated_norm_partial_rows(a) * (size_t)p->V * 4;
+}
+
+gdr_status gdr_gated_norm_backward(const gdr_gated_norm_problem* p, const void* dy, const void* x, const void* z,
+                                   const void* w, void* dx, void* dz, float* dw, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    GatedNormArgs a;
+    if (gdr_status st = gated_norm_args(p, &a)) return st;
+    const int64_t e = element_size(p->io_dtype);
+    const bool any = p->tokens > 0;
+    if (gdr_status st = check({{dy, e, any}, {x, e, any}, {z, e, any}, {w, e, true}, {dx, e, any}, {dz, e, any},
+                               {dw, 4, true}}))
+        return st;
+    if (gdr_status st = check_workspace(workspace, workspace_bytes, gdr_gated_norm_backward_workspace_bytes(p))) return st;
+    if (!any)   // the sum of no rows
+        return done(cudaMemsetAsync(dw, 0, (size_t)(p->V * (p->per_head ? p->H : 1)) * 4, (cudaStream_t)stream),
+                    "gated_norm");
+    return done(gated_norm_backward(a, dy, rows_of(x, p->x_ld, p->H * p->V, e), rows_of(z, p->z_ld, p->H * p->V, e), w, dx,
+                                    dz, dw, (float*)workspace, (cudaStream_t)stream),
+                "gated_norm");
 }
 
 }  // extern "C"

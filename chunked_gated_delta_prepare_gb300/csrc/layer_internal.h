@@ -109,5 +109,57 @@ struct SsmGrads {
 size_t ssm_backward_workspace(const SsmArgs& a);
 cudaError_t ssm_backward(const SsmArgs& a, const SsmTensors& t, const SsmGrads& g, float* workspace, cudaStream_t s);
 
+// ---- lru.cu, lru_backward.cu
+constexpr int kLruKept = 128;      // tokens from one kept state to the next
+struct LruArgs {
+    int64_t n, T, total;   // cu: total tokens on the packed axis; else n * T
+    const int* cu;
+    int D;
+    int io;                // gdr_dtype
+    float c;
+};
+struct LruTensors {
+    RowTensor x, r, i;     // i.p nullptr: no input gate
+    const float *lam, *h0; // lam nullptr: no rates
+};
+struct LruGrads {
+    const void* dy;
+    const float* dh_final;
+    void *dx, *dr, *di;
+    float *dlam, *dh0;
+};
+int64_t lru_tiles(const LruArgs& a);      // rows of the kept states
+size_t lru_forward_workspace(const LruArgs& a, bool kept);
+cudaError_t lru_forward(const LruArgs& a, const LruTensors& t, void* y, float* h_final, float* kept, float* workspace,
+                        cudaStream_t s);
+size_t lru_backward_workspace(const LruArgs& a, bool kept);
+cudaError_t lru_backward(const LruArgs& a, const LruTensors& t, const LruGrads& g, const float* kept, float* workspace,
+                         cudaStream_t s);
+cudaError_t lru_step(const LruArgs& a, const LruTensors& t, int64_t pool, const int* slots, float* h, void* y,
+                     cudaStream_t s);
+
+// ---- layer_norm.cu (NormArgs::group is not used)
+cudaError_t layernorm_forward(const NormArgs& a, RowTensor x, RowTensor res, const void* w, const void* b, void* y,
+                              void* r, cudaStream_t s);
+// Rows of partial sums [2 D] of dw and db that layernorm_backward writes and adds up.
+int64_t layernorm_partial_rows(const NormArgs& a);
+cudaError_t layernorm_backward(const NormArgs& a, const void* dy, const void* r, const void* w, const void* dr, void* dx,
+                               float* dw, float* db, float* partial, cudaStream_t s);
+
+// ---- gated_norm.cu
+constexpr int64_t kGatedNormMaxV = 8192;
+struct GatedNormArgs {
+    int64_t tokens;
+    int H, V;
+    float eps;
+    int io;                // gdr_dtype
+    bool silu, per_head;
+};
+cudaError_t gated_norm_forward(const GatedNormArgs& a, RowTensor x, RowTensor z, const void* w, void* y, cudaStream_t s);
+// Rows of partial sums [V] of dw that gated_norm_backward writes and adds up.
+int64_t gated_norm_partial_rows(const GatedNormArgs& a);
+cudaError_t gated_norm_backward(const GatedNormArgs& a, const void* dy, RowTensor x, RowTensor z, const void* w, void* dx,
+                                void* dz, float* dw, float* partial, cudaStream_t s);
+
 }  // namespace layer
 }  // namespace gdr

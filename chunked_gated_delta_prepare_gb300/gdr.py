@@ -49,6 +49,10 @@ EXPORTS = ["gdr_prepare_wy", "gdr_scan_h", "gdr_chunk_output", "gdr_forward", "g
            "gdr_conv_forward", "gdr_conv_backward", "gdr_conv_backward_workspace_bytes", "gdr_conv_step",
            "gdr_delta_step", "gdr_ssm_forward", "gdr_ssm_forward_workspace_bytes", "gdr_ssm_step",
            "gdr_ssm_backward", "gdr_ssm_backward_workspace_bytes",
+           "gdr_lru_kept_bytes", "gdr_lru_forward", "gdr_lru_forward_workspace_bytes", "gdr_lru_backward",
+           "gdr_lru_backward_workspace_bytes", "gdr_lru_step",
+           "gdr_layernorm_forward", "gdr_layernorm_backward", "gdr_layernorm_backward_workspace_bytes",
+           "gdr_gated_norm_forward", "gdr_gated_norm_backward", "gdr_gated_norm_backward_workspace_bytes",
            "gdr_status_string", "gdr_get_device_status", "gdr_selftest_bounded_wait", "gdr_last_variant",
            "gdr_version"]
 
@@ -88,6 +92,21 @@ class gdr_ssm_problem(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int64) for name in ("n", "T", "total", "D", "N", "G", "x_ld", "dt_ld", "z_ld", "b_ld",
                                                     "c_ld", "pool")] + [("io_dtype", ctypes.c_int32),
                                                                         ("softplus", ctypes.c_int32)]
+
+
+class gdr_lru_problem(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in ("n", "T", "total", "D", "x_ld", "r_ld", "i_ld", "pool")] + [
+        ("io_dtype", ctypes.c_int32), ("c", ctypes.c_float)]
+
+
+class gdr_layernorm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("x_ld", ctypes.c_int64), ("res_ld", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class gdr_gated_norm_problem(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in ("tokens", "H", "V", "x_ld", "z_ld")] + [
+        ("io_dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("per_head", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -151,6 +170,18 @@ def load(path: str | None = None):
             "gdr_ssm_backward": [ctypes.POINTER(gdr_ssm_problem)] + [vp] * 22 + [ctypes.c_size_t, vp],
             "gdr_ssm_backward_workspace_bytes": [ctypes.POINTER(gdr_ssm_problem), ctypes.c_int32],
             "gdr_ssm_step": [ctypes.POINTER(gdr_ssm_problem)] + [vp] * 12,
+            "gdr_lru_kept_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32],
+            "gdr_lru_forward_workspace_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32, ctypes.c_int32],
+            "gdr_lru_forward": [ctypes.POINTER(gdr_lru_problem)] + [vp] * 10 + [ctypes.c_size_t, vp],
+            "gdr_lru_backward_workspace_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32, ctypes.c_int32],
+            "gdr_lru_backward": [ctypes.POINTER(gdr_lru_problem)] + [vp] * 15 + [ctypes.c_size_t, vp],
+            "gdr_lru_step": [ctypes.POINTER(gdr_lru_problem)] + [vp] * 8,
+            "gdr_layernorm_forward": [ctypes.POINTER(gdr_layernorm_problem)] + [vp] * 7,
+            "gdr_layernorm_backward_workspace_bytes": [ctypes.POINTER(gdr_layernorm_problem)],
+            "gdr_layernorm_backward": [ctypes.POINTER(gdr_layernorm_problem)] + [vp] * 8 + [ctypes.c_size_t, vp],
+            "gdr_gated_norm_forward": [ctypes.POINTER(gdr_gated_norm_problem)] + [vp] * 5,
+            "gdr_gated_norm_backward_workspace_bytes": [ctypes.POINTER(gdr_gated_norm_problem)],
+            "gdr_gated_norm_backward": [ctypes.POINTER(gdr_gated_norm_problem)] + [vp] * 8 + [ctypes.c_size_t, vp],
             "gdr_status_string": [ctypes.c_int],
             "gdr_get_device_status": [vp],
             "gdr_selftest_bounded_wait": [ctypes.c_int32, ctypes.c_int32, vp],

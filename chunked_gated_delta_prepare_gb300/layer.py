@@ -4,6 +4,9 @@
     conv_forward, conv_backward, conv_step    short causal convolution
     ssm_forward, ssm_backward, ssm_step       selective state space scan
     delta_step                                the gated delta rule for one token
+    lru_forward, lru_backward, lru_step       gated linear recurrence
+    layernorm_forward, layernorm_backward     layer norm, residual
+    gated_norm_forward, gated_norm_backward   norm of a recurrence's output, times a gate
 
 The arithmetic runs in libgdr's CUDA kernels; binding/layer_binding.cpp checks the arguments and calls them, and a
 missing library raises.  Each call takes device tensors, allocates its outputs (and a workspace, unless one is given)
@@ -179,3 +182,86 @@ def delta_step(q, k, v, g, beta, h, *, scale=None, slots=None):
     g [B, HV] or [B, HV, K] fp32.  h [pool, HV, K, V] fp32 is changed in place, row i using state slots[i] (device
     int32; None: state i); a slot outside the pool marks a padding row, whose o is zero."""
     return _native().delta_step(q, k, v, g, beta, h, scale, slots)
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+
+@_streamed
+def lru_forward(x, r, i=None, lam=None, h0=None, *, c=8.0, cu_seqlens=None, want_h_final=True, want_kept=False,
+                workspace=None):
+    """y, h_final, kept = lru_forward(x, r, i, lam, h0): the gated linear recurrence, one state a channel.
+
+    x, r, i [B, T, D], or packed [total, D] with cu_seqlens (device int32 [n + 1]); lam [D] fp32; h0 [n, D] fp32 (None:
+    zero).  With g = sigmoid(i) (1 without i):
+        with lam:     log a = -c softplus(lam) sigmoid(r);  h = a h + sqrt(1 - a^2) g x
+        without lam:  a = sigmoid(r);                       h = a h + (1 - a) g x
+    y is h in the io type, h_final [n, D] fp32 (None with want_h_final=False).  kept: with want_kept=True the states that
+    lru_backward starts its tiles from, fp32, one row for 128 tokens."""
+    return _native().lru_forward(x, r, i, lam, h0, c, cu_seqlens, want_h_final, want_kept, workspace)
+
+
+class LruGrads(NamedTuple):
+    dx: torch.Tensor
+    dr: torch.Tensor
+    di: torch.Tensor | None
+    dlam: torch.Tensor | None
+    dh0: torch.Tensor | None
+
+
+@_streamed
+def lru_backward(x, r, i, lam, dy, h0=None, dh_final=None, kept=None, *, c=8.0, cu_seqlens=None,
+                 workspace=None) -> LruGrads:
+    """The gradient of lru_forward's y and h_final (dh_final None: unused), from the forward's inputs and its kept states
+    (None: they are formed again).  dx, dr, di are in the io type, dlam and dh0 fp32; those of inputs that are None are
+    None."""
+    return LruGrads(*_native().lru_backward(x, r, i, lam, dy, h0, dh_final, kept, c, cu_seqlens, workspace))
+
+
+@_streamed
+def lru_step(x, r, i, lam, h, *, c=8.0, slots=None):
+    """y = lru_step(x, r, i, lam, h): one token of n rows, x, r, i [n, D].  h [pool, D] fp32 is changed in place, row k
+    using state slots[k] (device int32; None: state k); a slot outside the pool marks a padding row, whose y is zero."""
+    return _native().lru_step(x, r, i, lam, h, c, slots)
+
+
+# ---------------------------------------------------------------- layer norm
+
+@_streamed
+def layernorm_forward(x, weight, bias=None, residual=None, *, eps=1e-5, want_y=True):
+    """y, r = layernorm_forward(x, weight, bias, residual): the layer norm of s = x + residual over the last dimension.
+
+    y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias in x's type (None with want_y=False); r = s in x's type, the
+    new residual (x itself without a residual)."""
+    y, r = _native().layernorm_forward(x, weight, bias, residual, eps, want_y)
+    return y, x if r is None else r
+
+
+@_streamed
+def layernorm_backward(dy, r, weight, d_r=None, *, eps=1e-5, workspace=None):
+    """dx, dweight, dbias = layernorm_backward(dy, r, weight, d_r): from the forward's r, the gradient dy of y and the
+    gradient d_r that reaches r by other ways.  dx is the gradient of x and of the residual alike; dweight and dbias are
+    fp32."""
+    return _native().layernorm_backward(dy, r, weight, d_r, eps, workspace)
+
+
+# ---------------------------------------------------------------- gated norm of a recurrence's output
+
+def _gate_code(gate):
+    if gate not in ("silu", "sigmoid"):
+        raise ValueError(f"gate: 'silu' or 'sigmoid' is needed, got {gate!r}")
+    return 0 if gate == "silu" else 1
+
+
+@_streamed
+def gated_norm_forward(x, z, weight, *, gate="silu", eps=1e-6):
+    """y = gated_norm_forward(x, z, weight): x / sqrt(mean(x^2) + eps) * weight * gate(z), the mean over the V columns of
+    each head.  x, z [..., H, V] (slices of a wider token row are used in place); weight [V], or [H, V] for weights of
+    each head; gate: "silu" or "sigmoid"."""
+    return _native().gated_norm_forward(x, z, weight, _gate_code(gate), eps)
+
+
+@_streamed
+def gated_norm_backward(dy, x, z, weight, *, gate="silu", eps=1e-6, workspace=None):
+    """dx, dz, dweight = gated_norm_backward(dy, x, z, weight): the gradient of gated_norm_forward's y, from its inputs.
+    dweight is fp32, like weight."""
+    return _native().gated_norm_backward(dy, x, z, weight, _gate_code(gate), eps, workspace)

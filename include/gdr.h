@@ -559,9 +559,10 @@ GDR_API gdr_status gdr_varlen_backward(const gdr_problem* p, const int32_t* cu_s
 
 /*
  * ---------------------------------------------------------------- the layer around the recurrence
- * What a recurrent layer runs before and beside the delta rule: the norm of its
- * input, the short convolution, a second kind of recurrence (the selective state
- * space scan), and the single-token forms that decoding needs.  The method pages
+ * What a recurrent layer runs before, beside and behind the delta rule: the norm
+ * of its input, the short convolution, other kinds of recurrence (the selective
+ * state space scan, the gated linear recurrence), the gated norm of the output,
+ * and the single-token forms that decoding needs.  The method pages
  * have no counterpart to these calls.
  *
  * Conventions, beside those at the top of this file:
@@ -571,7 +572,7 @@ GDR_API gdr_status gdr_varlen_backward(const gdr_problem* p, const int32_t* cu_s
  *   only their element's alignment (GDR_ERR_ALIGN otherwise).  Rows on 16-byte
  *   boundaries move fastest.  Workspaces are 256-byte aligned.
  * - Tokens, rows and sequences number less than 2^30 each.
- * - Weights of the norm and the convolution have the io dtype; their gradients
+ * - Weights of the norms and the convolution have the io dtype; their gradients
  *   are fp32, summed in a fixed order: the same call gives the same bits.
  * - Sequences: a batch of n sequences of T tokens each (cu_seqlens NULL, tokens
  *   n * T), or n packed ones on a token axis of `total` tokens, sequence s
@@ -691,6 +692,85 @@ GDR_API gdr_status gdr_ssm_backward(const gdr_ssm_problem* p, const int32_t* cu_
 GDR_API gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const int32_t* slots, const void* x, const void* dt,
                                 const float* A, const void* B, const void* C, const float* Dk, const void* z,
                                 const float* dt_bias, float* h, void* y, void* stream);
+
+/* The gated linear recurrence, one state a channel:  h_t = a_t h_{t-1} + u_t, y_t = h_t,  with q = sigmoid(r_t),
+ * g = sigmoid(i_t) (1 where i is NULL) and
+ *     lam given:  log a_t = -c softplus(lam) q,  u_t = sqrt(1 - a_t^2) g x_t     (lam: a rate for each channel)
+ *     lam NULL:   a_t = q,                       u_t = (1 - a_t) g x_t           (c is not used)
+ * x, r, i, y: tokens of D channels, io; lam [D] fp32; h_0 from h0 [n,D] fp32 (NULL: zero); h_final [n,D] fp32 or NULL:
+ * the state after each sequence's last token.  fp32 arithmetic for every io type.
+ * kept [rows,D] fp32 or NULL: the state before every 128th token of each sequence, for the gradient; its bytes come
+ * from gdr_lru_kept_bytes.  A long sequence is scanned in tiles of that many tokens at once; a tile's state follows
+ * from its predecessor's in a fixed order, so the result of a call does not change from run to run. */
+typedef struct gdr_lru_problem {
+    int64_t n, T, total;     /* n >= 1 sequences (rows of gdr_lru_step); of T >= 1 tokens, or packed on total >= 0 */
+    int64_t D;
+    int64_t x_ld, r_ld, i_ld;
+    int64_t pool;            /* gdr_lru_step: states in the pool */
+    int32_t io_dtype;        /* gdr_dtype */
+    float c;                 /* with lam: > 0, finite */
+} gdr_lru_problem;
+GDR_API size_t gdr_lru_kept_bytes(const gdr_lru_problem* p, int32_t packed);
+/* kept: whether the call will be given one. */
+GDR_API size_t gdr_lru_forward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept);
+GDR_API gdr_status gdr_lru_forward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r,
+                                   const void* i, const float* lam, const float* h0, void* y, float* h_final,
+                                   float* kept, void* workspace, size_t workspace_bytes, void* stream);
+/* The gradient of gdr_lru_forward's (y, h_final): dy like y; dh_final [n,D] fp32 or NULL; kept as the forward of the
+ * same inputs wrote it, or NULL (the call then forms it again, reading x, r and i once more).  dx, dr and di (with i
+ * only) are contiguous, io; dlam [D] (with lam only) and dh0 [n,D] (may be NULL: not written) fp32.  dlam sums over
+ * all tokens in a fixed order. */
+GDR_API size_t gdr_lru_backward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept);
+GDR_API gdr_status gdr_lru_backward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r,
+                                    const void* i, const float* lam, const float* h0, const void* dy,
+                                    const float* dh_final, const float* kept, void* dx, void* dr, void* di, float* dlam,
+                                    float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+/* One token of n rows: x, r, i, y [n,D]; h [pool,D] fp32, changed in place. */
+GDR_API gdr_status gdr_lru_step(const gdr_lru_problem* p, const int32_t* slots, const void* x, const void* r,
+                                const void* i, const float* lam, float* h, void* y, void* stream);
+
+/* The layer norm: s = x + residual (x where residual is NULL), m = mean(s),
+ *     y = (s - m) / sqrt(mean((s - m)^2) + eps) * w + b   over the D columns of each row (b NULL: zero).
+ * s is kept in fp32 and rounded once into each output: r [rows,D] io = s, y [rows,D] io.  Either may be NULL (not
+ * written), not both.  w, b [D] io. */
+typedef struct gdr_layernorm_problem {
+    int64_t rows, D;         /* rows >= 0; 1 <= D <= 32768 */
+    int64_t x_ld, res_ld;
+    int32_t io_dtype;        /* gdr_dtype */
+    float eps;               /* >= 0, finite */
+} gdr_layernorm_problem;
+GDR_API gdr_status gdr_layernorm_forward(const gdr_layernorm_problem* p, const void* x, const void* residual,
+                                         const void* w, const void* b, void* y, void* r, void* stream);
+/* The gradient, from the r that the forward wrote (x without a residual): with xh = (r - m) rstd,
+ *     dx = rstd (w dy - mean(w dy) - xh mean(w dy xh)) + dr   (io; the gradient of x and of the residual alike)
+ *     dw = sum over rows of dy xh,  db = sum over rows of dy  (fp32 [D])
+ * dr, the gradient that reached r by other ways, may be NULL.  All tensors are contiguous. */
+GDR_API size_t gdr_layernorm_backward_workspace_bytes(const gdr_layernorm_problem* p);
+GDR_API gdr_status gdr_layernorm_backward(const gdr_layernorm_problem* p, const void* dy, const void* r, const void* w,
+                                          const void* dr, void* dx, float* dw, float* db, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* The gated norm of a recurrence's output, rows of V columns (one head of one token):
+ *     y = x / sqrt(mean(x^2) + eps) * w * f(z),   f = silu or sigmoid.
+ * x, z: `tokens` of [H,V], a token's heads contiguous; y [tokens,H,V] io; w [V] io, or [H,V] with per_head. */
+typedef struct gdr_gated_norm_problem {
+    int64_t tokens, H, V;    /* tokens >= 0; H >= 1; 1 <= V <= 8192; fewer than 2^30 rows tokens * H */
+    int64_t x_ld, z_ld;
+    int32_t io_dtype;        /* gdr_dtype */
+    int32_t gate;            /* 0: silu, 1: sigmoid */
+    int32_t per_head;        /* 1: a weight for each head and column, 0: for each column */
+    float eps;               /* >= 0, finite */
+} gdr_gated_norm_problem;
+GDR_API gdr_status gdr_gated_norm_forward(const gdr_gated_norm_problem* p, const void* x, const void* z, const void* w,
+                                          void* y, void* stream);
+/* The gradient: with n = x rstd and dn = dy w f(z),
+ *     dx = rstd (dn - n mean(dn n)),  dz = dy n w f'(z)   (contiguous, io),
+ *     dw = sum over tokens (and heads, without per_head) of dy n f(z)   (fp32, like w).
+ * dy is contiguous. */
+GDR_API size_t gdr_gated_norm_backward_workspace_bytes(const gdr_gated_norm_problem* p);
+GDR_API gdr_status gdr_gated_norm_backward(const gdr_gated_norm_problem* p, const void* dy, const void* x, const void* z,
+                                           const void* w, void* dx, void* dz, float* dw, void* workspace,
+                                           size_t workspace_bytes, void* stream);
 
 /* Static, human-readable text for a status code. */
 GDR_API const char* gdr_status_string(gdr_status s);
