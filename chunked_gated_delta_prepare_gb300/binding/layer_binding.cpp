@@ -514,7 +514,7 @@ PyObject* lru_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     std::array<Tensor, 3> out{c.empty(x.sizes(), c.io), Tensor(), Tensor()};
     if (truth(a[7])) out[1] = c.empty(states, F32);
     if (truth(a[8])) out[2] = c.empty({s.kept(q), s.p.D}, F32);
-    const Workspace ws(c, a[9], gdr_lru_forward_workspace_bytes(&s.p, q.cu != nullptr, out[2].defined()));
+    const Workspace ws(c, a[9], gdr_lru_forward_workspace_bytes(&s.p, q.cu != nullptr));
     const int st = gdr_lru_forward(&s.p, q.cu, s.x.p, s.r.p, s.i.p, s.lam, h0, out[0].data_ptr(),
                                    (float*)at_or_null(out[1]), (float*)at_or_null(out[2]), ws.p, ws.bytes, c.stream());
     return st ? gdr_error(st, "gdr_lru_forward") : results(out);

@@ -121,8 +121,8 @@ gdr_status lru_args(const gdr_lru_problem* p, const int32_t* cu, bool packed, bo
         if (!good_ld(ld, p->D, tokens)) return GDR_ERR_SHAPE;
     if (rate && (!(p->c > 0.f) || std::isinf(p->c))) return GDR_ERR_ARG;
     *a = LruArgs{p->n, p->T, tokens, cu, (int)p->D, p->io_dtype, p->c};
-    // a block for each tile and 64 channels, numbered in 31 bits
-    if (lru_tiles(*a) > ((int64_t{1} << 31) - 1) / ((p->D + 63) / 64)) return GDR_ERR_SHAPE;
+    // a number for each tile and 32 channels, of 31 bits
+    if (lru_tiles(*a) > ((int64_t{1} << 31) - 1) / ((p->D + 31) / 32)) return GDR_ERR_SHAPE;
     return GDR_OK;
 }
 
@@ -349,11 +349,11 @@ size_t gdr_lru_kept_bytes(const gdr_lru_problem* p, int32_t packed) {
     return (size_t)lru_tiles(a) * (size_t)a.D * 4;
 }
 
-size_t gdr_lru_forward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept) {
+size_t gdr_lru_forward_workspace_bytes(const gdr_lru_problem* p, int32_t packed) {
     LruArgs a;
     const int32_t some = 0;
     if (lru_args(p, packed ? &some : nullptr, packed != 0, false, &a)) return 0;
-    return lru_forward_workspace(a, kept != 0);
+    return lru_forward_workspace(a);
 }
 
 gdr_status gdr_lru_forward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r, const void* i,
@@ -366,8 +366,8 @@ gdr_status gdr_lru_forward(const gdr_lru_problem* p, const int32_t* cu_seqlens, 
     if (gdr_status st = check({{cu_seqlens, 4, false}, {x, e, any}, {r, e, any}, {i, e, false}, {lam, 4, false},
                                {h0, 4, false}, {y, e, any}, {h_final, 4, false}, {kept, 4, false}}))
         return st;
-    if (gdr_status st = check_workspace(workspace, workspace_bytes, lru_forward_workspace(a, kept != nullptr))) return st;
-    return done(lru_forward(a, lru_tensors(p, x, r, i, lam, h0), y, h_final, kept, (float*)workspace,
+    if (gdr_status st = check_workspace(workspace, workspace_bytes, lru_forward_workspace(a))) return st;
+    return done(lru_forward(a, lru_tensors(p, x, r, i, lam, h0), y, h_final, kept, workspace,
                             (cudaStream_t)stream),
                 "lru");
 }
@@ -393,7 +393,7 @@ gdr_status gdr_lru_backward(const gdr_lru_problem* p, const int32_t* cu_seqlens,
         return st;
     if (gdr_status st = check_workspace(workspace, workspace_bytes, lru_backward_workspace(a, kept != nullptr))) return st;
     const LruGrads g{dy, dh_final, dx, dr, di, dlam, dh0};
-    return done(lru_backward(a, lru_tensors(p, x, r, i, lam, h0), g, kept, (float*)workspace, (cudaStream_t)stream), "lru");
+    return done(lru_backward(a, lru_tensors(p, x, r, i, lam, h0), g, kept, workspace, (cudaStream_t)stream), "lru");
 }
 
 gdr_status gdr_lru_step(const gdr_lru_problem* p, const int32_t* slots, const void* x, const void* r, const void* i,

@@ -129,11 +129,12 @@ struct LruGrads {
     float *dlam, *dh0;
 };
 int64_t lru_tiles(const LruArgs& a);      // rows of the kept states
-size_t lru_forward_workspace(const LruArgs& a, bool kept);
-cudaError_t lru_forward(const LruArgs& a, const LruTensors& t, void* y, float* h_final, float* kept, float* workspace,
+// y, h_final and kept may each be nullptr.
+size_t lru_forward_workspace(const LruArgs& a);
+cudaError_t lru_forward(const LruArgs& a, const LruTensors& t, void* y, float* h_final, float* kept, void* workspace,
                         cudaStream_t s);
 size_t lru_backward_workspace(const LruArgs& a, bool kept);
-cudaError_t lru_backward(const LruArgs& a, const LruTensors& t, const LruGrads& g, const float* kept, float* workspace,
+cudaError_t lru_backward(const LruArgs& a, const LruTensors& t, const LruGrads& g, const float* kept, void* workspace,
                          cudaStream_t s);
 cudaError_t lru_step(const LruArgs& a, const LruTensors& t, int64_t pool, const int* slots, float* h, void* y,
                      cudaStream_t s);

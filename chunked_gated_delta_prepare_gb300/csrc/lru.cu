@@ -1,128 +1,136 @@
 // The gated linear recurrence over prompts and batches, and its single-token step (formulas in lru.cuh).
 //
-// Bound: memory.  A tile of 128 tokens by 64 channels is a block's: warp w takes the tokens 8 w .. 8 w + 7, forms their
-// decays a and terms u in registers, and from a zero state the run's last state and product of decays; a thread then
-// folds the runs in front of its own, from the tile's first state, through shared memory and goes over its run again.
-// The states in front of the tiles come from two kernels before: the tiles' own ends, and a serial pass over them.
+// Bound: memory.  One pass: a tile's rows arrive in shared memory while the block works on the tile before, a thread forms
+// the decays a and terms u of its run of 8 tokens in registers, the runs' maps h -> h * decay + own are joined through
+// shared memory, the tile's state comes from the tiles before it (look_back), and the run is gone over again from its state.
 #include "lru.cuh"
 
 namespace gdr {
 namespace layer {
 namespace {
 
-struct alignas(16) End {     // of a run of tokens: what it makes of state h is h * decay + own
+struct alignas(16) Map {     // what a run of tokens makes of state h: h * decay + own
     F2 decay, own;
 };
 
-// The decays and terms of the thread's tokens; a = 1, u = 0 past the tile's end.
+constexpr int kBlocks = 3;   // an SM
+template <typename IO> constexpr int kBuffers = sizeof(IO) == 2 ? 2 : 1;      // of tiles
+
+template <typename IO, bool GATE> constexpr int lru_forward_smem() {
+    return kBuffers<IO> * (GATE ? 3 : 2) * kLruTile * kLruCols * (int)sizeof(IO);
+}
+
+// y, kept and h_final may each be nullptr.
 template <typename IO, bool RATE, bool GATE>
-__device__ __forceinline__ void load_run(const Lru& p, const LruTile& t, int t0, const Rate& k, F2 (&a)[kLruTokens],
-                                         F2 (&u)[kLruTokens]) {
-    RawN<IO, 2> x[kLruTokens], r[kLruTokens], i[kLruTokens];
-    const int64_t row = t.first + t0;
-    const IO* xp = (const IO*)p.x.p + row * p.x.ld + t.ch;
-    const IO* rp = (const IO*)p.r.p + row * p.r.ld + t.ch;
-    const IO* ip = (const IO*)p.i.p + row * p.i.ld + t.ch;
+__global__ void __launch_bounds__(kLruThreads, kBlocks)
+lru_forward_kernel(Lru p, LruChain chain, IO* __restrict__ y, float* __restrict__ kept, float* __restrict__ h_final) {
+    constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 3 : 2;
+    extern __shared__ uint4 smem[];
+    __shared__ Map runs[kLruRuns][kLruPairs];
+    __shared__ F2 carry[kLruPairs];
+    __shared__ LruPlan plans[3];
+    IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, i
+
+    if (threadIdx.x >= kLruWorkers) {                       // the guide
+        lru_plan<false, RATE>(p, chain, 0, plans);
+        lru_plan<false, RATE>(p, chain, 1, plans + 1);
+        __syncthreads();
+        const int pair = threadIdx.x % kLruPairs;
+        for (unsigned turn = 0; plans[turn % 3].live; ++turn) {
+            __syncthreads();                                // the tile is there
+            lru_plan<false, RATE>(p, chain, turn + 2, plans + (turn + 2) % 3);
+            const LruTile t = plans[turn % 3].t;
+            const int ch = t.col * kLruCols + pair * 2, left = p.D - ch;
+            const int64_t at = ((int64_t)t.number * p.cols + t.col) * kLruPairs + pair;
+            const bool first = threadIdx.x < kLruWorkers + kLruPairs;  // the warp's other half does the same again
+            F2 state = t.seq >= 0 ? state2(p.h0, (int64_t)t.seq * p.D + ch, left) : 0;
+            __syncthreads();                                // the runs' maps are there
+            Map all = runs[0][pair];
 #pragma unroll
-    for (int j = 0; j < kLruTokens; ++j) {
-        if (t0 + j >= t.len) continue;
-        r[j] = load2(rp + j * p.r.ld, t.left, p.r.vec);
-        x[j] = load2(xp + j * p.x.ld, t.left, p.x.vec);
-        if (GATE) i[j] = load2(ip + j * p.i.ld, t.left, p.i.vec);
-    }
-#pragma unroll
-    for (int j = 0; j < kLruTokens; ++j) {
-        if (t0 + j >= t.len) {
-            a[j] = both(1.f), u[j] = both(0.f);
-            continue;
+            for (int w = 1; w < kLruRuns; ++w) {
+                const Map n = runs[w][pair];
+                all.own = fma2(n.decay, all.own, n.own);
+                all.decay = mul2(n.decay, all.decay);
+            }
+            if (t.seq >= 0) {
+                if (first && t.to_tail && t.to_head) publish_map(chain.maps + at, all.decay, all.own);
+                if (t.to_head) state = look_back<false>(chain, t, p.cols, pair, t.to_head);
+                const F2 end = fma2(all.decay, state, all.own);
+                if (first) {
+                    if (t.to_tail) publish_state(chain.states + at + (int64_t)p.cols * kLruPairs, end);
+                    carry[pair] = state;
+                    if (kept) put_state2(kept, (int64_t)t.number * p.D + ch, state, left);
+                    if (h_final && !t.to_tail) put_state2(h_final, (int64_t)t.seq * p.D + ch, end, left);
+                }
+            }
+            __syncthreads();                                // the state is there
         }
-        F2 s;
-        decay_and_part<RATE>(wide2(r[j]), k, a[j], s);
-        u[j] = mul2(s, wide2(x[j]));
-        if (GATE) u[j] = mul2(u[j], sigmoid2(wide2(i[j])));
+        return;
     }
-}
 
-__device__ __forceinline__ End end_of(const F2 (&a)[kLruTokens], const F2 (&u)[kLruTokens]) {
-    End e{a[0], u[0]};
-#pragma unroll
-    for (int j = 1; j < kLruTokens; ++j) {
-        e.own = fma2(a[j], e.own, u[j]);
-        e.decay = mul2(a[j], e.decay);
-    }
-    return e;
-}
-
-// The tiles' ends [tiles][D]: decay, own.
-template <typename IO, bool RATE, bool GATE>
-__global__ void __launch_bounds__(kLruWarps * 32) lru_ends_kernel(Lru p, float2* __restrict__ ends) {
-    __shared__ End run[kLruWarps][32];
-    const LruTile t = lru_tile(p, blockIdx.x);
-    if (t.seq < 0 || t.tail) return;                   // nobody goes on from a sequence's last tile
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Rate k{0, 0};
-    if (RATE) k = load_rate(p, t.ch, false);
-    F2 a[kLruTokens], u[kLruTokens];
-    load_run<IO, RATE, GATE>(p, t, warp * kLruTokens, k, a, u);
-    run[warp][lane] = end_of(a, u);
+    const int run = threadIdx.x / kLruPairs, pair = threadIdx.x % kLruPairs, row = run * kLruRun;
+    const auto fetch = [&](unsigned turn) {
+        if (plans[turn % 3].live) {
+            const LruTile t = plans[turn % 3].t;
+            IO* to = in + (turn % B) * IN * N;
+            lru_fetch(p.r, t, p.D, to);
+            lru_fetch(p.x, t, p.D, to + N);
+            if (GATE) lru_fetch(p.i, t, p.D, to + 2 * N);
+        }
+        copy_group();
+    };
     __syncthreads();
-    if (warp) return;
-    End e = run[0][lane];
+    fetch(0);
+    if (B == 2) fetch(1);
+    for (unsigned turn = 0; plans[turn % 3].live; ++turn) {
+        copy_wait<B - 1>();
+        __syncthreads();
+        const LruPlan& plan = plans[turn % 3];
+        F2 a[kLruRun], u[kLruRun];
+        {
+            const F2 k = RATE ? *reinterpret_cast<const F2*>(plan.rates + pair * 2) : 0;
+            const IO* from = in + (turn % B) * IN * N;
 #pragma unroll
-    for (int w = 1; w < kLruWarps; ++w) {
-        const End n = run[w][lane];
-        e.own = fma2(n.decay, e.own, n.own);
-        e.decay = mul2(n.decay, e.decay);
-    }
-    const float2 d = unpack2(e.decay), o = unpack2(e.own);
-    float2* out = ends + t.number * p.D + t.ch;
-    if (t.left > 0) out[0] = make_float2(d.x, o.x);
-    if (t.left > 1) out[1] = make_float2(d.y, o.y);
-}
-
-// The state in front of every tile, a thread a channel of a sequence.
-__global__ void __launch_bounds__(64) lru_join_kernel(Lru p, const float2* __restrict__ ends, float* __restrict__ kept) {
-    const int ch = blockIdx.x * 64 + threadIdx.x;
-    if (ch >= p.D) return;
-    for (int s = blockIdx.y; s < p.q.n; s += gridDim.y) {
-        int64_t start, len;
-        seq_range(p.q, s, &start, &len);
-        const int64_t first = first_tile(p.q, s, kLruTile), tiles = (len + kLruTile - 1) / kLruTile;
-        float h = p.h0 ? p.h0[(int64_t)s * p.D + ch] : 0.f;
-        kept[first * p.D + ch] = h;
-#pragma unroll 8
-        for (int64_t i = 0; i + 1 < tiles; ++i) {
-            const float2 e = ends[(first + i) * p.D + ch];
-            h = fmaf(e.x, h, e.y);
-            kept[(first + i + 1) * p.D + ch] = h;
+            for (int j = 0; j < kLruRun; ++j) {
+                F2 s, q;
+                decay_and_part<RATE>(lru_read(from, row + j, pair), k, a[j], s, q);
+                u[j] = mul2(s, lru_read(from + N, row + j, pair));
+                if (GATE) u[j] = mul2(u[j], sigmoid2(lru_read(from + 2 * N, row + j, pair)));
+            }
+        }
+        const int len = plan.t.len;
+        if (len < kLruTile)
+#pragma unroll
+            for (int j = 0; j < kLruRun; ++j)
+                if (row + j >= len) a[j] = both(1.f), u[j] = both(0.f);
+        Map m{a[0], u[0]};
+#pragma unroll
+        for (int j = 1; j < kLruRun; ++j) {
+            m.own = fma2(a[j], m.own, u[j]);
+            m.decay = mul2(a[j], m.decay);
+        }
+        runs[run][pair] = m;
+        __syncthreads();
+        fetch(turn + B);
+        m = Map{both(1.f), both(0.f)};                      // of the runs in front of the thread's
+        for (int w = 0; w < run; ++w) {
+            const Map n = runs[w][pair];
+            m.own = fma2(n.decay, m.own, n.own);
+            m.decay = mul2(n.decay, m.decay);
+        }
+        __syncthreads();
+        if (y && plan.t.seq >= 0) {
+            F2 h = fma2(m.decay, carry[pair], m.own);
+            const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch;
+            IO* yp = y + (plan.t.first + row) * p.D + ch;
+#pragma unroll
+            for (int j = 0; j < kLruRun; ++j) {
+                h = fma2(a[j], h, u[j]);
+                if (row + j < len) store2(yp, h, left, p.vec);
+                yp += p.D;
+            }
         }
     }
-}
-
-// kept: the states in front of the tiles (nullptr: every sequence is one tile, and starts from h0).
-template <typename IO, bool RATE, bool GATE>
-__global__ void __launch_bounds__(kLruWarps * 32)
-lru_forward_kernel(Lru p, const float* __restrict__ kept, IO* __restrict__ y, float* __restrict__ h_final) {
-    __shared__ End run[kLruWarps][32];
-    const LruTile t = lru_tile(p, blockIdx.x);
-    if (t.seq < 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t0 = warp * kLruTokens;
-    F2 h = kept ? state2(kept, t.number * p.D + t.ch, t.left) : state2(p.h0, (int64_t)t.seq * p.D + t.ch, t.left);
-    Rate k{0, 0};
-    if (RATE) k = load_rate(p, t.ch, false);
-    F2 a[kLruTokens], u[kLruTokens];
-    load_run<IO, RATE, GATE>(p, t, t0, k, a, u);
-    run[warp][lane] = end_of(a, u);
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) h = fma2(run[w][lane].decay, h, run[w][lane].own);
-    IO* yp = y + (t.first + t0) * p.D + t.ch;
-#pragma unroll
-    for (int j = 0; j < kLruTokens; ++j) {
-        h = fma2(a[j], h, u[j]);
-        if (t0 + j < t.len) store2(yp + (int64_t)j * p.D, h, t.left, p.vec);
-    }
-    if (h_final && t.tail && warp == kLruWarps - 1)      // past the end the state stays what it is
-        put_state2(h_final, (int64_t)t.seq * p.D + t.ch, h, t.left);
 }
 
 template <typename IO, bool RATE, bool GATE>
@@ -130,8 +138,9 @@ __global__ void __launch_bounds__(128)
 lru_step_kernel(Lru p, int64_t rows, int64_t pool, const int* __restrict__ slots, float* __restrict__ h, IO* __restrict__ y) {
     const int ch = (blockIdx.x * 128 + threadIdx.x) * 2, left = p.D - ch;
     if (left <= 0) return;
-    Rate k{0, 0};
-    if (RATE) k = load_rate(p, ch, false);
+    const auto in_pairs = [](const LruRows& v) { return v.unit >= (sizeof(IO) == 2 ? 4 : 16); };
+    F2 k = 0;
+    if (RATE) k = pack2(rate_of(p.lam[ch], p.c), left > 1 ? rate_of(p.lam[ch + 1], p.c) : 0.f);
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         const int64_t slot = slots ? slots[row] : row;
         IO* yp = y + row * p.D + ch;
@@ -139,55 +148,37 @@ lru_step_kernel(Lru p, int64_t rows, int64_t pool, const int* __restrict__ slots
             store2(yp, both(0.f), left, p.vec);
             continue;
         }
-        F2 a, s;
-        decay_and_part<RATE>(wide2(load2((const IO*)p.r.p + row * p.r.ld + ch, left, p.r.vec)), k, a, s);
-        F2 u = mul2(s, wide2(load2((const IO*)p.x.p + row * p.x.ld + ch, left, p.x.vec)));
-        if (GATE) u = mul2(u, sigmoid2(wide2(load2((const IO*)p.i.p + row * p.i.ld + ch, left, p.i.vec))));
+        F2 a, s, q;
+        decay_and_part<RATE>(wide2(load2((const IO*)p.r.p + row * p.r.ld + ch, left, in_pairs(p.r))), k, a, s, q);
+        F2 u = mul2(s, wide2(load2((const IO*)p.x.p + row * p.x.ld + ch, left, in_pairs(p.x))));
+        if (GATE) u = mul2(u, sigmoid2(wide2(load2((const IO*)p.i.p + row * p.i.ld + ch, left, in_pairs(p.i)))));
         const F2 n = fma2(a, state2(h, slot * p.D + ch, left), u);
         put_state2(h, slot * p.D + ch, n, left);
         store2(yp, n, left, p.vec);
     }
 }
 
-bool one_tile_each(const LruArgs& a) { return (a.cu ? a.total : a.T) <= kLruTile; }
-
 }  // namespace
 
 int64_t lru_tiles(const LruArgs& a) { return tile_count(Seqs{a.cu, a.total, a.T, (int)a.n}, kLruTile); }
 
-size_t lru_forward_workspace(const LruArgs& a, bool kept) {
-    if (one_tile_each(a)) return 0;
-    return (size_t)lru_tiles(a) * a.D * (kept ? 8 : 12);
+size_t lru_forward_workspace(const LruArgs& a) {
+    return lru_one_tile_each(a) ? 0 : lru_chain_bytes(lru_tiles(a), (a.D + kLruCols - 1) / kLruCols);
 }
 
-// The states in front of all tiles.
-cudaError_t lru_states(const LruArgs& args, const LruTensors& t, float2* ends, float* kept, cudaStream_t s) {
-    const Lru p = lru_of(args, t);
-    if (!one_tile_each(args)) {
-        const cudaError_t e = lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
-            lru_ends_kernel<decltype(io), decltype(rate)::value, decltype(gate)::value>
-                <<<(unsigned)(lru_tiles(args) * p.cols), kLruWarps * 32, 0, s>>>(p, ends);
-            return cudaGetLastError();
-        });
-        if (e != cudaSuccess) return e;
-    }
-    const dim3 grid((unsigned)((args.D + 63) / 64), (unsigned)std::min<int64_t>(args.n, 65535));
-    lru_join_kernel<<<grid, 64, 0, s>>>(p, ends, kept);
-    return cudaGetLastError();
-}
-
-cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float* h_final, float* kept, float* workspace,
+cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float* h_final, float* kept, void* workspace,
                         cudaStream_t s) {
     Lru p = lru_of(args, t);
     p.vec = lru_pairs(y, args.D, args.io == GDR_F32 ? 4 : 2);
-    float2* ends = (float2*)workspace;
-    if (!kept && !one_tile_each(args)) kept = workspace + lru_tiles(args) * args.D * 2;
-    if (kept)
-        if (cudaError_t e = lru_states(args, t, ends, kept, s)) return e;
+    LruChain chain;
+    if (cudaError_t e = lru_chain(args, workspace, &chain, s)) return e;
     return lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
-        lru_forward_kernel<IO, decltype(rate)::value, decltype(gate)::value>
-            <<<(unsigned)(lru_tiles(args) * p.cols), kLruWarps * 32, 0, s>>>(p, kept, (IO*)y, h_final);
+        constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
+        constexpr int bytes = lru_forward_smem<IO, G>();
+        const auto kernel = lru_forward_kernel<IO, R, G>;
+        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+        kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(p, chain, (IO*)y, kept, h_final);
         return cudaGetLastError();
     });
 }

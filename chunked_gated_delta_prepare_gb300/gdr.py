@@ -171,7 +171,7 @@ def load(path: str | None = None):
             "gdr_ssm_backward_workspace_bytes": [ctypes.POINTER(gdr_ssm_problem), ctypes.c_int32],
             "gdr_ssm_step": [ctypes.POINTER(gdr_ssm_problem)] + [vp] * 12,
             "gdr_lru_kept_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32],
-            "gdr_lru_forward_workspace_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32, ctypes.c_int32],
+            "gdr_lru_forward_workspace_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32],
             "gdr_lru_forward": [ctypes.POINTER(gdr_lru_problem)] + [vp] * 10 + [ctypes.c_size_t, vp],
             "gdr_lru_backward_workspace_bytes": [ctypes.POINTER(gdr_lru_problem), ctypes.c_int32, ctypes.c_int32],
             "gdr_lru_backward": [ctypes.POINTER(gdr_lru_problem)] + [vp] * 15 + [ctypes.c_size_t, vp],

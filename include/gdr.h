@@ -711,15 +711,14 @@ typedef struct gdr_lru_problem {
     float c;                 /* with lam: > 0, finite */
 } gdr_lru_problem;
 GDR_API size_t gdr_lru_kept_bytes(const gdr_lru_problem* p, int32_t packed);
-/* kept: whether the call will be given one. */
-GDR_API size_t gdr_lru_forward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept);
+GDR_API size_t gdr_lru_forward_workspace_bytes(const gdr_lru_problem* p, int32_t packed);
 GDR_API gdr_status gdr_lru_forward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r,
                                    const void* i, const float* lam, const float* h0, void* y, float* h_final,
                                    float* kept, void* workspace, size_t workspace_bytes, void* stream);
 /* The gradient of gdr_lru_forward's (y, h_final): dy like y; dh_final [n,D] fp32 or NULL; kept as the forward of the
  * same inputs wrote it, or NULL (the call then forms it again, reading x, r and i once more).  dx, dr and di (with i
  * only) are contiguous, io; dlam [D] (with lam only) and dh0 [n,D] (may be NULL: not written) fp32.  dlam sums over
- * all tokens in a fixed order. */
+ * all tokens in a fixed order.  kept (of the workspace's size): whether the call will be given kept states. */
 GDR_API size_t gdr_lru_backward_workspace_bytes(const gdr_lru_problem* p, int32_t packed, int32_t kept);
 GDR_API gdr_status gdr_lru_backward(const gdr_lru_problem* p, const int32_t* cu_seqlens, const void* x, const void* r,
                                     const void* i, const float* lam, const float* h0, const void* dy,

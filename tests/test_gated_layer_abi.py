@@ -75,7 +75,7 @@ def test_misaligned_pointer(lib, name, ptr):
 @pytest.mark.parametrize("name", [n for n, (_, p) in CALLS.items() if "ws" in p])
 def test_workspace(lib, name):
     make, ptrs = CALLS[name]
-    p, more = make(), [0, 1] if make is lru else []
+    p, more = make(), {"gdr_lru_forward": [0], "gdr_lru_backward": [0, 1]}.get(name, [])
     need = getattr(lib, name + "_workspace_bytes")(ctypes.byref(p), *more)
     assert need > 0
     assert call(name, p, (ptrs | dict(ws=None)).values()) == WORKSPACE
