@@ -13,6 +13,56 @@ struct alignas(16) Map {     // what a run of tokens makes of state h: h * decay
     F2 decay, own;
 };
 
+// The decays and terms of the thread's run, from shared memory; a = 1, u = 0 past the tile's end.
+template <typename IO, bool RATE, bool GATE>
+__device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k, F2 root, int len, int left,
+                                         F2 (&a)[kLruRun], F2 (&u)[kLruRun]) {
+    constexpr int N = kLruTile * kLruCols;
+    RawN<IO, 2> r[kLruRun], i[kLruRun];
+#pragma unroll
+    for (int j = 0; j < kLruRun; ++j) {
+        r[j] = lru_raw(from, row + j, pair);
+        if (GATE) i[j] = lru_raw(from + 2 * N, row + j, pair);
+    }
+    if (lru_short<RATE, GATE, !RATE>(r, i, k, len - row, left)) {
+        const F2 k2 = add2(k, k);
+#pragma unroll
+        for (int j = 0; j < kLruRun; ++j) {
+            const F2 x = lru_read(from + N, row + j, pair), iv = GATE ? wide2(i[j]) : 0;
+            if (RATE) {
+                F2 w, z;
+                lru_roots<GATE>(wide2(r[j]), iv, w, z);
+                const F2 v = mul2(k2, mul2(w, w));
+                a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
+                u[j] = mul2(mul2(z, lru_p(v)), mul2(root, x));
+            } else {
+                const F2 e = ex2_2(mul2(wide2(r[j]), both(-kLog2e))), t1 = add2(e, both(1.f));
+                if (GATE) {
+                    const F2 t2 = one_and_exp(iv), sg = mul2(e, rcp_2(mul2(t1, t2)));
+                    a[j] = fma2(mul2(sg, both(-1.f)), t2, both(1.f));
+                    u[j] = mul2(sg, x);
+                } else {
+                    const F2 s = mul2(e, rcp_2(t1));
+                    a[j] = fma2(s, both(-1.f), both(1.f));
+                    u[j] = mul2(s, x);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kLruRun; ++j) {
+            F2 s, q;
+            decay_and_part<RATE>(wide2(r[j]), k, a[j], s, q);
+            u[j] = mul2(s, lru_read(from + N, row + j, pair));
+            if (GATE) u[j] = mul2(u[j], sigmoid2(wide2(i[j])));
+        }
+    }
+    if (len < kLruTile)
+#pragma unroll
+        for (int j = 0; j < kLruRun; ++j)
+            if (row + j >= len) a[j] = both(1.f), u[j] = both(0.f);
+}
+
 constexpr int kBlocks = 3;   // an SM
 template <typename IO> constexpr int kBuffers = sizeof(IO) == 2 ? 2 : 1;      // of tiles
 
@@ -21,57 +71,94 @@ template <typename IO, bool GATE> constexpr int lru_forward_smem() {
 }
 
 // y, kept and h_final may each be nullptr.
-template <typename IO, bool RATE, bool GATE>
+template <typename IO, bool RATE, bool GATE, bool TMA>
 __global__ void __launch_bounds__(kLruThreads, kBlocks)
-lru_forward_kernel(Lru p, LruChain chain, IO* __restrict__ y, float* __restrict__ kept, float* __restrict__ h_final) {
+lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_maps, IO* __restrict__ y,
+                   float* __restrict__ kept, float* __restrict__ h_final) {
     constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 3 : 2;
-    extern __shared__ uint4 smem[];
-    __shared__ Map runs[kLruRuns][kLruPairs];
+    extern __shared__ __align__(128) uint4 smem[];
+    __shared__ Map maps[kLruWarps][kLruPairs], fronts[kLruWarps][kLruPairs];   // of a warp's tokens, of those in front of them
     __shared__ F2 carry[kLruPairs];
-    __shared__ LruPlan plans[3];
+    __shared__ LruPlan plans[kLruPlans];
+    __shared__ uint64_t ready, full[B];                     // the tile's maps are there; its inputs are
     IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, i
 
     if (threadIdx.x >= kLruWorkers) {                       // the guide
-        lru_plan<false, RATE>(p, chain, 0, plans);
-        lru_plan<false, RATE>(p, chain, 1, plans + 1);
+        const int lane = threadIdx.x - kLruWorkers, pair = lane % kLruPairs;
+        const bool first = lane < kLruPairs;                // the warp's other half only looks on
+        const auto issue = [&](unsigned turn) {
+            if (TMA && lane == 0 && plans[turn % kLruPlans].live) {
+                const LruTile& t = plans[turn % kLruPlans].t;
+                uint64_t* bar = full + turn % B;
+                IO* to = in + (turn % B) * IN * N;
+                if (t.len == 0) return bw::mbar_arrive(bar);
+                bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
+                lru_tma(to, &in_maps.r, bar, t);
+                lru_tma(to + N, &in_maps.x, bar, t);
+                if (GATE) lru_tma(to + 2 * N, &in_maps.i, bar, t);
+            }
+        };
+        if (lane == 0) {
+            bw::mbar_init(&ready, kLruWarps);
+            for (int i = 0; i < B; ++i) bw::mbar_init(full + i, 1);
+            bw::fence_mbar_init();
+        }
+        unsigned ticket = 0;
+        for (unsigned turn = 0; turn < 3; ++turn) {
+            if (lane == 0) ticket = take_ticket(chain, turn);
+            lru_plan<false, RATE>(p, ticket, plans + turn);
+        }
+        if (lane == 0) ticket = take_ticket(chain, 3);
+        for (unsigned turn = 0; turn < B; ++turn) issue(turn);
         __syncthreads();
-        const int pair = threadIdx.x % kLruPairs;
-        for (unsigned turn = 0; plans[turn % 3].live; ++turn) {
-            __syncthreads();                                // the tile is there
-            lru_plan<false, RATE>(p, chain, turn + 2, plans + (turn + 2) % 3);
-            const LruTile t = plans[turn % 3].t;
+        for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
+            const LruTile t = plans[turn % kLruPlans].t;
             const int ch = t.col * kLruCols + pair * 2, left = p.D - ch;
             const int64_t at = ((int64_t)t.number * p.cols + t.col) * kLruPairs + pair;
-            const bool first = threadIdx.x < kLruWorkers + kLruPairs;  // the warp's other half does the same again
-            F2 state = t.seq >= 0 ? state2(p.h0, (int64_t)t.seq * p.D + ch, left) : 0;
-            __syncthreads();                                // the runs' maps are there
-            Map all = runs[0][pair];
+            // the state may be there before the tile's maps are
+            F2 state = 0;
+            bool found = t.to_head == 0, there = false;
+            if (found && t.seq >= 0) state = state2(p.h0, (int64_t)t.seq * p.D + ch, left);
+            while (!found && !there) {
+                found = look_back<false>(chain, t, p.cols, pair, t.to_head, state);
+                there = __all_sync(0xffffffffu, bw::mbar_test_wait(&ready, turn & 1));
+            }
+            if (!there) bw::mbar_wait(&ready, turn & 1, chain.err, kDeviceErrTimeout);
+            Map m[kLruWarps], all{both(1.f), both(0.f)};
 #pragma unroll
-            for (int w = 1; w < kLruRuns; ++w) {
-                const Map n = runs[w][pair];
-                all.own = fma2(n.decay, all.own, n.own);
-                all.decay = mul2(n.decay, all.decay);
+            for (int w = 0; w < kLruWarps; ++w) m[w] = maps[w][pair];
+#pragma unroll
+            for (int w = 0; w < kLruWarps; ++w) {
+                if (first) fronts[w][pair] = all;
+                all.own = fma2(m[w].decay, all.own, m[w].own);
+                all.decay = mul2(m[w].decay, all.decay);
             }
-            if (t.seq >= 0) {
-                if (first && t.to_tail && t.to_head) publish_map(chain.maps + at, all.decay, all.own);
-                if (t.to_head) state = look_back<false>(chain, t, p.cols, pair, t.to_head);
-                const F2 end = fma2(all.decay, state, all.own);
-                if (first) {
-                    if (t.to_tail) publish_state(chain.states + at + (int64_t)p.cols * kLruPairs, end);
-                    carry[pair] = state;
-                    if (kept) put_state2(kept, (int64_t)t.number * p.D + ch, state, left);
-                    if (h_final && !t.to_tail) put_state2(h_final, (int64_t)t.seq * p.D + ch, end, left);
-                }
+            if (!found) {
+                if (first && t.to_tail) publish_map(chain.maps + at, all.decay, all.own);
+                issue(turn + B);                            // the workers have read the tile
+                state = wait_back<false>(chain, t, p.cols, pair, t.to_head);
             }
-            __syncthreads();                                // the state is there
+            const F2 end = fma2(all.decay, state, all.own);
+            if (first && t.to_tail) publish_state(chain.states + at + (int64_t)p.cols * kLruPairs, end);
+            if (first) carry[pair] = state;
+            lru_arrive<2, kLruThreads>();
+            if (found) issue(turn + B);
+            if (first && t.seq >= 0) {
+                if (kept) put_state2(kept, (int64_t)t.number * p.D + ch, state, left);
+                if (h_final && !t.to_tail) put_state2(h_final, (int64_t)t.seq * p.D + ch, end, left);
+            }
+            const unsigned after = lane == 0 ? take_ticket(chain, turn + 4) : 0;
+            lru_plan<false, RATE>(p, ticket, plans + (turn + 3) % kLruPlans);
+            ticket = after;
         }
         return;
     }
 
-    const int run = threadIdx.x / kLruPairs, pair = threadIdx.x % kLruPairs, row = run * kLruRun;
+    const int warp = threadIdx.x / 32, pair = threadIdx.x % kLruPairs, row = threadIdx.x / kLruPairs * kLruRun;
+    const bool second = threadIdx.x & 16;                   // run of the warp
     const auto fetch = [&](unsigned turn) {
-        if (plans[turn % 3].live) {
-            const LruTile t = plans[turn % 3].t;
+        if (plans[turn % kLruPlans].live) {
+            const LruTile t = plans[turn % kLruPlans].t;
             IO* to = in + (turn % B) * IN * N;
             lru_fetch(p.r, t, p.D, to);
             lru_fetch(p.x, t, p.D, to + N);
@@ -80,54 +167,56 @@ lru_forward_kernel(Lru p, LruChain chain, IO* __restrict__ y, float* __restrict_
         copy_group();
     };
     __syncthreads();
-    fetch(0);
-    if (B == 2) fetch(1);
-    for (unsigned turn = 0; plans[turn % 3].live; ++turn) {
-        copy_wait<B - 1>();
-        __syncthreads();
-        const LruPlan& plan = plans[turn % 3];
+    if (!TMA)
+        for (unsigned turn = 0; turn < B; ++turn) fetch(turn);
+    for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
+        if (TMA) {
+            bw::mbar_wait(full + turn % B, turn / B & 1, chain.err, kDeviceErrTimeout);
+        } else {
+            copy_wait<B - 1>();
+            lru_sync<1, kLruWorkers>();
+        }
+        const LruPlan& plan = plans[turn % kLruPlans];
+        const int len = plan.t.len, ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch;
         F2 a[kLruRun], u[kLruRun];
         {
-            const F2 k = RATE ? *reinterpret_cast<const F2*>(plan.rates + pair * 2) : 0;
-            const IO* from = in + (turn % B) * IN * N;
-#pragma unroll
-            for (int j = 0; j < kLruRun; ++j) {
-                F2 s, q;
-                decay_and_part<RATE>(lru_read(from, row + j, pair), k, a[j], s, q);
-                u[j] = mul2(s, lru_read(from + N, row + j, pair));
-                if (GATE) u[j] = mul2(u[j], sigmoid2(lru_read(from + 2 * N, row + j, pair)));
+            F2 k = 0, root = 0;
+            if (RATE) {
+                k = *reinterpret_cast<const F2*>(plan.rates + pair * 2);
+                root = *reinterpret_cast<const F2*>(plan.roots + pair * 2);
             }
+            read_run<IO, RATE, GATE>(in + (turn % B) * IN * N, row, pair, k, root, len, left, a, u);
         }
-        const int len = plan.t.len;
-        if (len < kLruTile)
-#pragma unroll
-            for (int j = 0; j < kLruRun; ++j)
-                if (row + j >= len) a[j] = both(1.f), u[j] = both(0.f);
         Map m{a[0], u[0]};
 #pragma unroll
         for (int j = 1; j < kLruRun; ++j) {
             m.own = fma2(a[j], m.own, u[j]);
             m.decay = mul2(a[j], m.decay);
         }
-        runs[run][pair] = m;
-        __syncthreads();
-        fetch(turn + B);
-        m = Map{both(1.f), both(0.f)};                      // of the runs in front of the thread's
-        for (int w = 0; w < run; ++w) {
-            const Map n = runs[w][pair];
-            m.own = fma2(n.decay, m.own, n.own);
-            m.decay = mul2(n.decay, m.decay);
-        }
-        __syncthreads();
+        Map o{swap_halves(m.decay), swap_halves(m.own)};    // of the warp's other run
+        if (!second) maps[warp][pair] = Map{mul2(o.decay, m.decay), fma2(o.decay, m.own, o.own)};
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&ready);
+        lru_sync<2, kLruThreads>();
+        if (!TMA) fetch(turn + B);
         if (y && plan.t.seq >= 0) {
-            F2 h = fma2(m.decay, carry[pair], m.own);
-            const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch;
+            F2 h = fma2(fronts[warp][pair].decay, carry[pair], fronts[warp][pair].own);
+            if (second) h = fma2(o.decay, h, o.own);
             IO* yp = y + (plan.t.first + row) * p.D + ch;
+            if (p.vec && len == kLruTile && left > 0) {
 #pragma unroll
-            for (int j = 0; j < kLruRun; ++j) {
-                h = fma2(a[j], h, u[j]);
-                if (row + j < len) store2(yp, h, left, p.vec);
-                yp += p.D;
+                for (int j = 0; j < kLruRun; ++j) {
+                    h = fma2(a[j], h, u[j]);
+                    store2(yp, h, 2, true);
+                    yp += p.D;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kLruRun; ++j) {
+                    h = fma2(a[j], h, u[j]);
+                    if (row + j < len) store2(yp, h, left, false);
+                    yp += p.D;
+                }
             }
         }
     }
@@ -172,14 +261,21 @@ cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float
     p.vec = lru_pairs(y, args.D, args.io == GDR_F32 ? 4 : 2);
     LruChain chain;
     if (cudaError_t e = lru_chain(args, workspace, &chain, s)) return e;
+    LruMaps m;
+    const bool tma = args.total > 0 && p.x.unit == 16 && p.r.unit == 16 && (!p.i.p || p.i.unit == 16);
+    if (tma && !(lru_map(&m.x, p.x, args) && lru_map(&m.r, p.r, args) && (!p.i.p || lru_map(&m.i, p.i, args))))
+        return cudaErrorInvalidValue;
     return lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
         constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
         constexpr int bytes = lru_forward_smem<IO, G>();
-        const auto kernel = lru_forward_kernel<IO, R, G>;
-        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-        kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(p, chain, (IO*)y, kept, h_final);
-        return cudaGetLastError();
+        const auto go = [&](auto kernel) {
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+            kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(p, chain, m, (IO*)y, kept,
+                                                                                                    h_final);
+            return cudaGetLastError();
+        };
+        return tma ? go(lru_forward_kernel<IO, R, G, true>) : go(lru_forward_kernel<IO, R, G, false>);
     });
 }
 

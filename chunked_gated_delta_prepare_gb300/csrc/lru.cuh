@@ -9,9 +9,11 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "blackwell.cuh"
 #include "gdr_internal.h"
 #include "layer_common.cuh"
 #include "layer_internal.h"
+#include "tma_host.h"
 
 namespace gdr {
 namespace layer {
@@ -19,10 +21,11 @@ namespace layer {
 // A tile: 128 tokens of a sequence by 32 channels, a block's work: 16 runs of 8 tokens, each on 16 lanes of two channels.
 // Narrow tiles leave few tiles of a strip of channels in flight at once, so a tile's state is never far away.
 constexpr int kLruRun = 8, kLruRuns = 16, kLruTile = kLruRun * kLruRuns, kLruCols = 32, kLruPairs = kLruCols / 2;
-constexpr int kLruWorkers = kLruRuns * kLruPairs, kLruThreads = kLruWorkers + 32;     // and a warp that guides them
+constexpr int kLruWorkers = kLruRuns * kLruPairs, kLruWarps = kLruWorkers / 32;
+constexpr int kLruThreads = kLruWorkers + 32;     // and a warp that guides the workers
 static_assert(kLruTile == kLruKept, "a kept state for each tile");
 
-// A tensor of tokens, copied in aligned units of 16 bytes, of 4, or (16-bit rows that start anywhere) by elements.
+// A tensor of tokens, copied in aligned units of 16 bytes (by TMA), of 4, or (16-bit rows that start anywhere) by elements.
 struct LruRows {
     const void* p;
     int64_t ld;
@@ -82,38 +85,21 @@ __device__ __forceinline__ void put_state2(float* p, int64_t at, F2 v, int left)
     if (left > 1) p[at + 1] = f.y;
 }
 
-// sigmoid(v) and 1 - sigmoid(v), both to relative accuracy: with e = e^-|v| <= 1 the smaller is e / (1 + e), the larger
-// one less that.
-__device__ __forceinline__ void sigmoid_both2(F2 v, F2& up, F2& down) {
-    const float2 f = unpack2(v);
-    const F2 e = pack2(ex2(-fabsf(f.x) * kLog2e), ex2(-fabsf(f.y) * kLog2e));
-    const F2 small = mul2(e, rcp_2(add2(both(1.f), e))), large = fma2(small, both(-1.f), both(1.f));
-    const float2 s = unpack2(small), l = unpack2(large);
-    up = pack2(f.x < 0.f ? s.x : l.x, f.y < 0.f ? s.y : l.y);
-    down = pack2(f.x < 0.f ? l.x : s.x, f.y < 0.f ? l.y : s.y);
-}
-
-// 1 - e^-v for v >= 0, given e^(-v/2) = a: 1 - a^2, and near 0, where that cancels, v (1 - v/2 + v^2/6 - ...), whose terms
-// after v^4/120 are below 2^-24 of the sum at v = 1/8.
-__device__ __forceinline__ F2 one_less(F2 v, F2 a) {
-    F2 p = fma2(v, both(1.f / 120), both(-1.f / 24));
-    p = fma2(v, p, both(1.f / 6));
-    p = fma2(v, p, both(-1.f / 2));
-    p = fma2(v, p, both(1.f));
-    const float2 near = unpack2(mul2(v, p)), far = unpack2(fma2(mul2(a, both(-1.f)), a, both(1.f))), at = unpack2(v);
-    return pack2(at.x < 0.125f ? near.x : far.x, at.y < 0.125f ? near.y : far.y);
-}
-
-__device__ __forceinline__ float rsqrt_fast(float x) {
+__device__ __forceinline__ float min_nan(float a, float b) {   // NaN where either is
     float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-// 1 / sqrt(v): finite for 0, and NaN is left to what it multiplies.
-__device__ __forceinline__ F2 rsqrt2(F2 v) {
-    const float2 f = unpack2(v);
-    return pack2(rsqrt_fast(fmaxf(f.x, 1e-37f)), rsqrt_fast(fmaxf(f.y, 1e-37f)));
+__device__ __forceinline__ float sqrt_fast(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+__device__ __forceinline__ F2 sqrt2(F2 v) {
+    const float2 f = unpack2(v);
+    return pack2(sqrt_fast(f.x), sqrt_fast(f.y));
+}
+// 1 / v for v >= 0: finite for 0, and NaN is left to what it multiplies.
 __device__ __forceinline__ F2 rcp2_finite(F2 v) {
     const float2 f = unpack2(v);
     return pack2(rcp(fmaxf(f.x, 3e-19f)), rcp(fmaxf(f.y, 3e-19f)));
@@ -126,19 +112,81 @@ __device__ __forceinline__ float rate_of(float lam, float c) {
 __device__ __forceinline__ float rate_slope(float lam, float c) { return c / (1.f + expf(-lam)); }
 
 // A token's decay a and input's part s; q = sigmoid(r).
+//
+// RATE: s^2 = 1 - e^-v with v = 2 k q: by a polynomial where 1 - a^2 cancels.  Else: with e = e^-r, q = 1 / (1 + e), s = e q
+// to relative accuracy, and a = 1 - s, which is exact where a state is kept.
 template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, F2& a, F2& s, F2& q) {
     if (RATE) {
         q = sigmoid2(r);
-        const F2 kq = mul2(k, q);
+        const F2 kq = mul2(k, q), v = add2(kq, kq);
         a = ex2_2(fma2(kq, both(-kLog2e), both(kLruLean)));
-        const F2 m = one_less(add2(kq, kq), a);
-        s = mul2(m, rsqrt2(m));
+        // (1 - e^-v) / v up to v = 1/2, the best polynomial of degree 4: off by 1.1e-7
+        F2 m = fma2(v, both(0x1.bb955ap-8f), both(-0x1.4fdc9cp-5f));
+        m = fma2(v, m, both(0x1.5516c6p-3f));
+        m = fma2(v, m, both(-0x1.fffe02p-2f));
+        m = mul2(v, fma2(v, m, both(0x1.fffffep-1f)));
+        const float2 near = unpack2(m), far = unpack2(fma2(mul2(a, both(-1.f)), a, both(1.f))), at = unpack2(v);
+        s = sqrt2(pack2(at.x < 0.5f ? near.x : far.x, at.y < 0.5f ? near.y : far.y));
     } else {
-        sigmoid_both2(r, a, s);
+        const float2 f = unpack2(mul2(r, both(-kLog2e)));
+        const F2 e = pack2(ex2(min_nan(f.x, 126.f)), ex2(min_nan(f.y, 126.f)));
+        s = mul2(e, rcp_2(add2(e, both(1.f))));
+        a = fma2(s, both(-1.f), both(1.f));
         q = a;
     }
 }
 
+// The same for a whole run at fewer reciprocals and roots, which take twice the time of 2^x and four times that of a product
+// (an SM does 16 of them a clock; formed one by one they bound the forward at 134 of 158 us for 32768 x 4096).
+//
+// RATE, where v = 2 k q stays below 1/2 (k <= 1/4: gates that keep more than 0.78 of a state when they are open): with
+// w = sqrt(q) = (1 + e^-r)^-1/2, s = sqrt(2 k) w P(v), P(v) = sqrt((1 - e^-v) / v), by a polynomial; one root of
+// (1 + e^-r)(1 + e^-i)^2 gives w g, times (1 + e^-i) it gives w.  Else: one reciprocal of (1 + e^-r)(1 + e^-i) gives q g.
+// The products must not overflow where q or g is large: i (and without rates r) is at least -27.
+constexpr float kLruSlow = 0.25f, kLruLeast = -27.f;
+__device__ __forceinline__ float rsqrt_fast(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ F2 rsqrt2(F2 v) {
+    const float2 f = unpack2(v);
+    return pack2(rsqrt_fast(f.x), rsqrt_fast(f.y));
+}
+__device__ __forceinline__ F2 one_and_exp(F2 v) { return add2(ex2_2(mul2(v, both(-kLog2e))), both(1.f)); }    // 1 + e^-v
+__device__ __forceinline__ F2 lru_p(F2 v) {      // off by 9e-9 up to 1/2
+    F2 p = fma2(v, both(0x1.9419eap-11f), both(-0x1.fd8e2ep-8f));
+    p = fma2(v, p, both(0x1.aa9cb4p-5f));
+    p = fma2(v, p, both(-0x1.ffffc8p-3f));
+    return fma2(v, p, both(1.f));
+}
+__device__ __forceinline__ F2 lru_p_inverse(F2 v) {      // 1 / P(v), off by 4e-8
+    F2 p = fma2(v, both(-0x1.5d5098p-9f), both(0x1.55d41ap-7f));
+    p = fma2(v, p, both(0x1.ffff5p-3f));
+    return fma2(v, p, both(1.f));
+}
+// w and z = w g.
+template <bool GATE> __device__ __forceinline__ void lru_roots(F2 r, F2 i, F2& w, F2& z) {
+    const F2 t1 = one_and_exp(r);
+    if (GATE) {
+        const F2 t2 = one_and_exp(i);
+        z = rsqrt2(mul2(t1, mul2(t2, t2)));
+        w = mul2(z, t2);
+    } else {
+        z = w = rsqrt2(t1);
+    }
+}
+
+// Minima of two channels, NaN where either is.
+__device__ __forceinline__ RawN<float, 2> min_pair(RawN<float, 2> a, RawN<float, 2> b) {
+    return {min_nan(a.e[0], b.e[0]), min_nan(a.e[1], b.e[1])};
+}
+template <typename IO> __device__ __forceinline__ RawN<IO, 2> min_pair(RawN<IO, 2> a, RawN<IO, 2> b) {
+    using Two = std::conditional_t<std::is_same_v<IO, __half>, __half2, __nv_bfloat162>;
+    RawN<IO, 2> r;
+    *reinterpret_cast<Two*>(&r) = __hmin2_nan(*reinterpret_cast<const Two*>(&a), *reinterpret_cast<const Two*>(&b));
+    return r;
+}
 // ---------------------------------------------------------------- tiles and their order
 
 struct LruTile {
@@ -175,8 +223,8 @@ template <bool BACK> __device__ __forceinline__ LruTile lru_tile(const Lru& a, u
     t.first += (int64_t)tile * kLruTile;
     len -= (int64_t)tile * kLruTile;
     t.len = t.seq < 0 ? 0 : (int)(len < kLruTile ? len : kLruTile);
-    t.to_head = tile;
-    t.to_tail = len <= kLruTile ? 0 : (unsigned)((len - 1) / kLruTile);
+    t.to_head = t.seq < 0 ? 0 : tile;
+    t.to_tail = t.seq < 0 || len <= kLruTile ? 0 : (unsigned)((len - 1) / kLruTile);
     return t;
 }
 
@@ -216,81 +264,107 @@ __device__ __forceinline__ F2 look_state(const F2* p) {
     return v;
 }
 
-constexpr int kLruLook = 4, kLruPolls = 1 << 20;       // about a second
+constexpr int kLruLook = 4;
 
-// The state that tile `t` goes on from, for the warp's channel pair at `pair`: the nearest one written among its own and
-// those of the kLruLook - 1 tiles before it (`near` of them in its sequence), taken through the maps of the tiles between.
-// These are applied one by one, from the state on, as the tiles themselves do: wherever the state comes from, the bits are
-// the same.  BACK: the tiles that come before are those behind.  A wait that runs out sets the error word and goes on with
-// zeros.
+// One look for the state that tile `t` goes on from, for the warp's channel pair at `pair`: the nearest one written among its
+// own and those of the kLruLook - 1 tiles before it (`near` of them in its sequence), taken through the maps of the tiles
+// between.  These are applied one by one, from the state on, as the tiles themselves do: wherever the state comes from, the
+// bits are the same.  BACK: the tiles that come before are those behind.
 template <bool BACK>
-__device__ __forceinline__ F2 look_back(const LruChain& c, const LruTile& t, unsigned cols, int pair, unsigned near) {
+__device__ __forceinline__ bool look_back(const LruChain& c, const LruTile& t, unsigned cols, int pair, unsigned near, F2& state) {
     const int64_t at = ((int64_t)t.number * cols + t.col) * kLruPairs + pair;
     const int64_t step = (BACK ? 1 : -1) * (int64_t)cols * kLruPairs;
+    F2 s[kLruLook];
+    ulonglong2 m[kLruLook];
+#pragma unroll
+    for (int j = 0; j < kLruLook; ++j) {           // s[j]: the state j tiles before; m[j]: the map of the tile after it
+        s[j] = ~0ull;
+        m[j] = make_ulonglong2(~0ull, ~0ull);
+        if ((unsigned)j < near) s[j] = look_state(c.states + at + j * step);
+        if ((unsigned)j + 1 < near && j + 1 < kLruLook) m[j] = look_map(c.maps + at + (j + 1) * step);
+    }
+    bool found = false, linked = true;
+    int from = 0;
+#pragma unroll
+    for (int j = 0; j < kLruLook; ++j) {
+        if (!found && linked && is_written(s[j])) found = true, state = s[j], from = j;
+        linked = linked && is_written(m[j].x) && is_written(m[j].y);
+    }
+    if (!__all_sync(0xffffffffu, found)) return false;
+#pragma unroll
+    for (int j = kLruLook - 2; j >= 0; --j)
+        if (j < from) state = fma2(m[j].x, state, m[j].y);
+    return true;
+}
+// The same until it is found.  A wait that runs out (about a second) sets the error word and goes on with zeros.
+constexpr int kLruPolls = 1 << 20;
+template <bool BACK>
+__device__ __forceinline__ F2 wait_back(const LruChain& c, const LruTile& t, unsigned cols, int pair, unsigned near) {
+    F2 state = 0;
     for (int poll = 0; poll < kLruPolls; ++poll) {
-        F2 s[kLruLook];
-        ulonglong2 m[kLruLook];
-#pragma unroll
-        for (int j = 0; j < kLruLook; ++j) {           // s[j]: the state j tiles before; m[j]: the map of the tile after it
-            s[j] = ~0ull;
-            m[j] = make_ulonglong2(~0ull, ~0ull);
-            if ((unsigned)j < near) s[j] = look_state(c.states + at + j * step);
-            if ((unsigned)j + 1 < near && j + 1 < kLruLook) m[j] = look_map(c.maps + at + (j + 1) * step);
-        }
-        bool found = false, linked = true;
-        F2 state = 0;
-        int from = 0;
-#pragma unroll
-        for (int j = 0; j < kLruLook; ++j) {
-            if (!found && linked && is_written(s[j])) found = true, state = s[j], from = j;
-            linked = linked && is_written(m[j].x) && is_written(m[j].y);
-        }
-        if (__all_sync(0xffffffffu, found)) {
-#pragma unroll
-            for (int j = kLruLook - 2; j >= 0; --j)
-                if (j < from) state = fma2(m[j].x, state, m[j].y);
-            return state;
-        }
+        if (look_back<BACK>(c, t, cols, pair, near, state)) return state;
         if ((poll & 4095) == 4095 && *reinterpret_cast<volatile unsigned*>(c.err)) break;
     }
     if ((threadIdx.x & 31) == 0) atomicCAS(c.err, 0u, kDeviceErrTimeout);
     return 0;
 }
 
-// What the guide tells the workers of a tile: three in turn, the next one's already known.
+// Named barriers: 1 and 3 of the workers, 2 of all, where the guide only arrives.
+template <int ID, int N> __device__ __forceinline__ void lru_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+template <int ID, int N> __device__ __forceinline__ void lru_arrive() {
+    asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+__device__ __forceinline__ F2 swap_halves(F2 v) { return __shfl_xor_sync(0xffffffffu, v, 16); }
+
+// What the guide tells the workers of a tile.  It plans three tiles ahead, after the present one's state is out, so that
+// neither the ticket's way nor the rates hold anyone up.
+constexpr int kLruPlans = 4;
 struct LruPlan {
     LruTile t;
     bool live;               // there is one
-    alignas(8) float rates[kLruCols];
+    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];      // k, sqrt(2 k), (BACK) k's slope
 };
 template <bool BACK, bool RATE>
-__device__ __forceinline__ void lru_plan(const Lru& p, const LruChain& c, unsigned turn, LruPlan* plan) {
+__device__ __forceinline__ void lru_plan(const Lru& p, unsigned ticket, LruPlan* plan) {
     const int lane = threadIdx.x & 31;
-    const unsigned ticket = __shfl_sync(0xffffffffu, lane == 0 ? take_ticket(c, turn) : 0, 0);
+    ticket = __shfl_sync(0xffffffffu, ticket, 0);
     const bool live = ticket < p.tiles * p.cols;
     if (lane == 0) plan->live = live;
-    if (!live) return;
-    const LruTile t = lru_tile<BACK>(p, ticket);
-    if (lane == 0) plan->t = t;
-    const int ch = t.col * kLruCols + lane;
-    if (RATE) plan->rates[lane] = ch < p.D ? rate_of(p.lam[ch], p.c) : 0.f;
+    if (live) {
+        const LruTile t = lru_tile<BACK>(p, ticket);
+        if (lane == 0) plan->t = t;
+        const int ch = t.col * kLruCols + lane;
+        if (RATE) {
+            const float lam = ch < p.D ? p.lam[ch] : 0.f, k = ch < p.D ? rate_of(lam, p.c) : 0.f;
+            plan->rates[lane] = k;
+            plan->roots[lane] = sqrtf(2.f * k);
+            if (BACK) plan->slopes[lane] = ch < p.D ? rate_slope(lam, p.c) : 0.f;
+        }
+    }
+    __syncwarp();
+}
+
+// Inputs on their way by TMA: a box of 128 rows and 32 channels, zeros outside the tensor.
+struct LruMaps {
+    CUtensorMap r, x, i, dy;
+};
+// One lane's request for a tile of a tensor.
+template <typename IO>
+__device__ __forceinline__ void lru_tma(IO* to, const CUtensorMap* map, uint64_t* bar, const LruTile& t) {
+    bw::tma_load_4d(to, map, bar, (int)t.col * kLruCols * (int)sizeof(IO) / 2, (int)t.first, 0, 0);
 }
 
 // ---------------------------------------------------------------- inputs
 
-// Where a row of a tile lies in shared memory.  Rows of 16-bit types, half a turn of the banks long, change places in every
-// second run, so that the two runs of a warp read different banks.
-template <typename IO> __device__ __forceinline__ int lru_place(int row) {
-    return (sizeof(IO) == 2 ? row ^ (row / kLruRun & 1) : row) * kLruCols;
-}
-template <int BYTES> __device__ __forceinline__ void lru_copy(void* to, const void* from, int bytes) {
+// Rows that TMA does not take, those that do not start on 16-byte boundaries, are copied by the workers in units of 4 bytes
+// or by elements.
+__device__ __forceinline__ void lru_copy(void* to, const void* from, int bytes) {
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
 }
-template <typename IO, int BYTES>
+template <typename IO>
 __device__ __forceinline__ void lru_fetch_units(const LruRows& v, const LruTile& t, int D, IO* to) {
-    constexpr int per = BYTES / (int)sizeof(IO), pieces = kLruCols / per, step = kLruWorkers / pieces;
+    constexpr int per = 4 / (int)sizeof(IO), pieces = kLruCols / per, step = kLruWorkers / pieces;
     const int piece = threadIdx.x % pieces, ch = t.col * kLruCols + piece * per;
     const int bytes = min(per, D - ch) * (int)sizeof(IO);
     if (bytes <= 0) return;
@@ -298,16 +372,14 @@ __device__ __forceinline__ void lru_fetch_units(const LruRows& v, const LruTile&
 #pragma unroll
     for (int k = 0; k < kLruTile / step; ++k) {
         const int row = threadIdx.x / pieces + k * step;
-        if (row < t.len) lru_copy<BYTES>(to + lru_place<IO>(row) + piece * per, from, bytes);
+        if (row < t.len) lru_copy(to + row * kLruCols + piece * per, from, bytes);
         from += step * v.ld;
     }
 }
 // A tile of a tensor on its way into shared memory, by the workers; rows past the tile's end stay what they were.
 template <typename IO> __device__ __forceinline__ void lru_fetch(const LruRows& v, const LruTile& t, int D, IO* to) {
-    if (v.unit == 16) {
-        lru_fetch_units<IO, 16>(v, t, D, to);
-    } else if (sizeof(IO) == 4 || v.unit == 4) {
-        lru_fetch_units<IO, 4>(v, t, D, to);
+    if (sizeof(IO) == 4 || v.unit >= 4) {
+        lru_fetch_units<IO>(v, t, D, to);
     } else {
         constexpr int step = kLruWorkers / kLruPairs, most = kLruTile / step;
         const int piece = threadIdx.x % kLruPairs, ch = t.col * kLruCols + piece * 2, row0 = threadIdx.x / kLruPairs;
@@ -322,13 +394,40 @@ template <typename IO> __device__ __forceinline__ void lru_fetch(const LruRows& 
         }
 #pragma unroll
         for (int k = 0; k < most; ++k)
-            *reinterpret_cast<RawN<IO, 2>*>(to + lru_place<IO>(row0 + k * step) + piece * 2) = e[k];
+            *reinterpret_cast<RawN<IO, 2>*>(to + (row0 + k * step) * kLruCols + piece * 2) = e[k];
     }
 }
 
 // A token of the thread's run, two channels; past the tile's end anything.
+template <typename IO> __device__ __forceinline__ RawN<IO, 2> lru_raw(const IO* from, int row, int pair) {
+    return *reinterpret_cast<const RawN<IO, 2>*>(from + row * kLruCols + pair * 2);
+}
 template <typename IO> __device__ __forceinline__ F2 lru_read(const IO* from, int row, int pair) {
-    return wide2(*reinterpret_cast<const RawN<IO, 2>*>(from + lru_place<IO>(row) + pair * 2));
+    return wide2(lru_raw(from, row, pair));
+}
+// Whether the thread's run may go by the shorter formulas; tokens past the tile's end and channels past the last, which hold
+// anything, are not asked.  BOUND: r too is to be at least kLruLeast.
+template <bool RATE, bool GATE, bool BOUND, typename IO>
+__device__ __forceinline__ bool lru_short(const RawN<IO, 2> (&r)[kLruRun], const RawN<IO, 2> (&i)[kLruRun], F2 k, int live,
+                                          int left) {
+    const float2 f = unpack2(k);
+    bool ok = !RATE || (f.x <= kLruSlow && f.y <= kLruSlow);
+    const auto ask = [&](const RawN<IO, 2> (&v)[kLruRun]) {
+        RawN<IO, 2> least = v[0];
+        if (live >= kLruRun) {
+#pragma unroll
+            for (int j = 1; j < kLruRun; ++j) least = min_pair(least, v[j]);
+        } else {
+#pragma unroll
+            for (int j = 1; j < kLruRun; ++j)
+                if (j < live) least = min_pair(least, v[j]);
+        }
+        const float2 g = to_f2(least.e);
+        return live <= 0 || ((left < 1 || g.x >= kLruLeast) && (left < 2 || g.y >= kLruLeast));
+    };
+    if (BOUND) ok = ok && ask(r);
+    if (GATE) ok = ok && ask(i);
+    return ok;
 }
 
 // Calls f with a value of the io type and whether there are rates and input gates.
@@ -365,16 +464,23 @@ inline Lru lru_of(const LruArgs& a, const LruTensors& t) {
     return k;
 }
 
+inline bool lru_map(CUtensorMap* m, const LruRows& v, const LruArgs& a) {
+    const uint64_t e = a.io == GDR_F32 ? 4 : 2, ld = (uint64_t)v.ld * e, rows = (uint64_t)a.total;
+    const uint64_t dims[4] = {(uint64_t)a.D * e / 2, rows, 1, 1}, strides[3] = {ld, ld, ld};
+    const uint32_t box[4] = {kLruCols * (uint32_t)e / 2, kLruTile, 1, 1};
+    return make_tmap_bf16_4d_mode(m, v.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);   // copies any type's bits
+}
+
 // The chain's words in the workspace, set to "not written"; with one tile a sequence there is none.
 inline bool lru_one_tile_each(const LruArgs& a) { return (a.cu ? a.total : a.T) <= kLruTile; }
 inline cudaError_t lru_chain(const LruArgs& a, void* workspace, LruChain* c, cudaStream_t s) {
     *c = LruChain{};
+    if (cudaError_t e = device_error_ptr(&c->err)) return e;
     if (lru_one_tile_each(a)) return cudaSuccess;
     const int64_t tiles = lru_tiles(a), cols = (a.D + kLruCols - 1) / kLruCols;
     c->ticket = (unsigned*)workspace;
     c->maps = (ulonglong2*)((char*)workspace + 256);
     c->states = (F2*)(c->maps + tiles * cols * kLruPairs);
-    if (cudaError_t e = device_error_ptr(&c->err)) return e;
     return cudaMemsetAsync(workspace, 0xff, lru_chain_bytes(tiles, cols), s);
 }
 

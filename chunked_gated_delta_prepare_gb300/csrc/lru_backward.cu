@@ -23,69 +23,200 @@ template <typename IO, bool GATE> constexpr int lru_backward_smem() {
 struct alignas(8) Run {      // of a run of tokens: its product of decays, its end from a zero state, and what it sends to the
     F2 decay, own, back;     // state before it with nothing behind it
 };
+struct alignas(16) Map {     // what tokens make of the gradient e from behind them: e * decay + back
+    F2 decay, back;
+};
+
+// The decays and terms of the thread's run, from shared memory, and what the gradients need beside them: the input's part s
+// (RATE and `shorter`: w = sqrt(q)), q, and the gate.  A token past the tile's end has a = 1, u = 0.
+template <typename IO, bool RATE, bool GATE>
+__device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k, F2 root, int len, int left,
+                                         F2 (&a)[kLruRun], F2 (&u)[kLruRun], F2 (&part)[kLruRun],
+                                         F2 (&gate)[kLruRun]) {
+    constexpr int N = kLruTile * kLruCols;
+    RawN<IO, 2> r[kLruRun], i[kLruRun];
+#pragma unroll
+    for (int j = 0; j < kLruRun; ++j) {
+        r[j] = lru_raw(from, row + j, pair);
+        if (GATE) i[j] = lru_raw(from + 3 * N, row + j, pair);
+    }
+    const bool shorter = lru_short<RATE, GATE, true>(r, i, k, len - row, left);
+    if (shorter) {
+        const F2 k2 = add2(k, k);
+#pragma unroll
+        for (int j = 0; j < kLruRun; ++j) {
+            const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
+            if (RATE) {
+                const F2 t1 = one_and_exp(rv);
+                F2 z;
+                if (GATE) {
+                    const F2 t2 = one_and_exp(iv);
+                    z = rsqrt2(mul2(t1, mul2(t2, t2)));      // w g
+                    part[j] = mul2(z, t2);                   // w
+                    gate[j] = mul2(mul2(z, z), mul2(t1, t2));   // g = z^2 t1 t2
+                } else {
+                    z = part[j] = rsqrt2(t1);
+                }
+                const F2 v = mul2(k2, mul2(part[j], part[j]));
+                a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
+                u[j] = mul2(mul2(z, lru_p(v)), mul2(root, x));
+            } else {
+                const F2 e = ex2_2(mul2(rv, both(-kLog2e))), t1 = add2(e, both(1.f));
+                if (GATE) {
+                    const F2 t2 = one_and_exp(iv), o = rcp_2(mul2(t1, t2)), sg = mul2(e, o);
+                    gate[j] = mul2(o, t1);
+                    part[j] = mul2(sg, t2);
+                    u[j] = mul2(sg, x);
+                } else {
+                    part[j] = mul2(e, rcp_2(t1));
+                    u[j] = mul2(part[j], x);
+                }
+                a[j] = fma2(part[j], both(-1.f), both(1.f));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kLruRun; ++j) {
+            F2 s, q;
+            decay_and_part<RATE>(wide2(r[j]), k, a[j], s, q);
+            u[j] = mul2(s, lru_read(from + N, row + j, pair));
+            if (GATE) gate[j] = sigmoid2(wide2(i[j])), u[j] = mul2(u[j], gate[j]);
+            part[j] = RATE ? q : s;
+        }
+    }
+    if (len < kLruTile)
+#pragma unroll
+        for (int j = 0; j < kLruRun; ++j)
+            if (row + j >= len) a[j] = both(1.f), u[j] = both(0.f);
+    return shorter;
+}
+
+// s, q and q / s of a token.
+struct Parts {
+    F2 s, q, ratio;
+};
+__device__ __forceinline__ Parts parts_of(F2 kept, F2 k, F2 root, F2 inverse, F2 a, bool shorter) {
+    Parts o;
+    if (shorter) {                           // w
+        o.q = mul2(kept, kept);
+        const F2 v = mul2(add2(k, k), o.q);
+        o.s = mul2(mul2(root, kept), lru_p(v));
+        o.ratio = mul2(mul2(inverse, kept), lru_p_inverse(v));
+    } else {                                 // q; 1 / s is finite where s = 0, and is multiplied by q or k = 0 there
+        o.q = kept;
+        const F2 kq = mul2(k, kept), v = add2(kq, kq);
+        F2 m = fma2(v, both(0x1.bb955ap-8f), both(-0x1.4fdc9cp-5f));
+        m = fma2(v, m, both(0x1.5516c6p-3f));
+        m = fma2(v, m, both(-0x1.fffe02p-2f));
+        m = mul2(v, fma2(v, m, both(0x1.fffffep-1f)));
+        const float2 near = unpack2(m), far = unpack2(fma2(mul2(a, both(-1.f)), a, both(1.f))), at = unpack2(v);
+        o.s = sqrt2(pack2(at.x < 0.5f ? near.x : far.x, at.y < 0.5f ? near.y : far.y));
+        o.ratio = mul2(kept, rcp2_finite(o.s));
+    }
+    return o;
+}
 
 // dlam: [tiles][D] partial sums, or nullptr.
-template <typename IO, bool RATE, bool GATE>
+template <typename IO, bool RATE, bool GATE, bool TMA>
 __global__ void __launch_bounds__(kLruThreads, kBlocks)
-lru_backward_kernel(Lru p, LruChain chain, LruRows dy, const float* __restrict__ kept, const float* __restrict__ dh_final,
+lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_maps, LruRows dy, const float* __restrict__ kept, const float* __restrict__ dh_final,
                     IO* __restrict__ dx, IO* __restrict__ dr, IO* __restrict__ di, float* __restrict__ dlam,
                     float* __restrict__ dh0) {
     constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 4 : 3;
-    extern __shared__ uint4 smem[];
-    __shared__ Run runs[kLruRuns][kLruPairs];
-    __shared__ F2 sums[kLruRuns][kLruPairs];
+    extern __shared__ __align__(128) uint4 smem[];
+    __shared__ Run runs[kLruWarps][kLruPairs];              // of a warp's tokens
+    __shared__ Map behind[kLruWarps][kLruPairs];            // of the tokens behind them
+    __shared__ F2 fronts[kLruWarps][kLruPairs], sums[kLruWarps][kLruPairs];    // states in front of them; sums for dlam
     __shared__ F2 carry[kLruPairs];
-    __shared__ LruPlan plans[3];
+    __shared__ LruPlan plans[kLruPlans];
+    __shared__ uint64_t ready, full[B], done;               // the tile's maps are there; its inputs are; they have been read
     IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, dy, i
 
     if (threadIdx.x >= kLruWorkers) {                       // the guide
-        lru_plan<true, RATE>(p, chain, 0, plans);
-        lru_plan<true, RATE>(p, chain, 1, plans + 1);
+        const int lane = threadIdx.x - kLruWorkers, pair = lane % kLruPairs;
+        const bool first = lane < kLruPairs;
+        const auto issue = [&](unsigned turn) {
+            if (TMA && lane == 0 && plans[turn % kLruPlans].live) {
+                const LruTile& t = plans[turn % kLruPlans].t;
+                uint64_t* bar = full + turn % B;
+                IO* to = in + (turn % B) * IN * N;
+                if (t.len == 0) return bw::mbar_arrive(bar);
+                bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
+                lru_tma(to, &in_maps.r, bar, t);
+                lru_tma(to + N, &in_maps.x, bar, t);
+                lru_tma(to + 2 * N, &in_maps.dy, bar, t);
+                if (GATE) lru_tma(to + 3 * N, &in_maps.i, bar, t);
+            }
+        };
+        if (lane == 0) {
+            bw::mbar_init(&ready, kLruWarps);
+            bw::mbar_init(&done, kLruWarps);
+            for (int i = 0; i < B; ++i) bw::mbar_init(full + i, 1);
+            bw::fence_mbar_init();
+        }
+        unsigned ticket = 0;
+        for (unsigned turn = 0; turn < 3; ++turn) {
+            if (lane == 0) ticket = take_ticket(chain, turn);
+            lru_plan<true, RATE>(p, ticket, plans + turn);
+        }
+        if (lane == 0) ticket = take_ticket(chain, 3);
+        for (unsigned turn = 0; turn < B; ++turn) issue(turn);
         __syncthreads();
-        const int pair = threadIdx.x % kLruPairs;
-        for (unsigned turn = 0; plans[turn % 3].live; ++turn) {
-            __syncthreads();                                // the tile is there
-            lru_plan<true, RATE>(p, chain, turn + 2, plans + (turn + 2) % 3);
-            const LruTile t = plans[turn % 3].t;
+        for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
+            const LruTile t = plans[turn % kLruPlans].t;
             const int ch = t.col * kLruCols + pair * 2, left = p.D - ch;
             const int64_t at = ((int64_t)t.number * p.cols + t.col) * kLruPairs + pair;
-            const bool first = threadIdx.x < kLruWorkers + kLruPairs;  // the warp's other half does the same again
-            F2 e = t.seq >= 0 ? state2(dh_final, (int64_t)t.seq * p.D + ch, left) : 0;
-            __syncthreads();                                // the runs are there
-            F2 d = both(1.f), b = both(0.f);
-#pragma unroll
-            for (int w = kLruRuns - 1; w >= 0; --w) {
-                b = fma2(runs[w][pair].decay, b, runs[w][pair].back);
-                d = mul2(runs[w][pair].decay, d);
+            F2 state = t.seq >= 0 ? state2(kept, (int64_t)t.number * p.D + ch, left) : 0;
+            if (TMA && turn > 0) {                          // the tile before has been read: its place is free
+                bw::mbar_wait(&done, turn - 1 & 1, chain.err, kDeviceErrTimeout);
+                issue(turn - 1 + B);
             }
-            if (t.seq >= 0) {
-                if (first && t.to_tail && t.to_head) publish_map(chain.maps + at, d, b);
-                if (t.to_tail) e = look_back<true>(chain, t, p.cols, pair, t.to_tail);
-                const F2 end = fma2(d, e, b);
-                if (first) {
-                    if (t.to_head) publish_state(chain.states + at - (int64_t)p.cols * kLruPairs, end);
-                    carry[pair] = e;
-                    if (dh0 && !t.to_head) put_state2(dh0, (int64_t)t.seq * p.D + ch, end, left);
+            F2 e = 0;
+            bool found = t.to_tail == 0, there = false;
+            if (found && t.seq >= 0) e = state2(dh_final, (int64_t)t.seq * p.D + ch, left);
+            while (!found && !there) {
+                found = look_back<true>(chain, t, p.cols, pair, t.to_tail, e);
+                there = __all_sync(0xffffffffu, bw::mbar_test_wait(&ready, turn & 1));
+            }
+            if (!there) bw::mbar_wait(&ready, turn & 1, chain.err, kDeviceErrTimeout);
+            F2 d = both(1.f), b = both(0.f);
+            if (first) {
+#pragma unroll
+                for (int w = kLruWarps - 1; w >= 0; --w) {
+                    behind[w][pair] = Map{d, b};
+                    b = fma2(runs[w][pair].decay, b, runs[w][pair].back);
+                    d = mul2(runs[w][pair].decay, d);
+                }
+            } else {                                        // meanwhile the states
+#pragma unroll
+                for (int w = 0; w < kLruWarps; ++w) {
+                    fronts[w][pair] = state;
+                    state = fma2(runs[w][pair].decay, state, runs[w][pair].own);
                 }
             }
-            __syncthreads();                                // the gradient from behind is there
-            F2 slope = 0;
-            if (RATE) slope = pack2(left > 0 ? rate_slope(p.lam[ch], p.c) : 0.f, left > 1 ? rate_slope(p.lam[ch + 1], p.c) : 0.f);
-            __syncthreads();                                // the tile is done
-            if (RATE) {                                     // the sums stay until the next tile's maps are there
-                F2 sum = sums[0][pair];
-#pragma unroll
-                for (int w = 1; w < kLruRuns; ++w) sum = add2(sum, sums[w][pair]);
-                if (first) put_state2(dlam, (int64_t)t.number * p.D + ch, mul2(sum, slope), left);
+            d = __shfl_sync(0xffffffffu, d, pair);
+            b = __shfl_sync(0xffffffffu, b, pair);
+            if (!found) {
+                if (first && t.to_head) publish_map(chain.maps + at, d, b);
+                e = wait_back<true>(chain, t, p.cols, pair, t.to_tail);
             }
+            const F2 end = fma2(d, e, b);
+            if (first && t.to_head) publish_state(chain.states + at - (int64_t)p.cols * kLruPairs, end);
+            if (first) carry[pair] = e;
+            lru_arrive<2, kLruThreads>();
+            if (first && dh0 && t.seq >= 0 && !t.to_head) put_state2(dh0, (int64_t)t.seq * p.D + ch, end, left);
+            const unsigned after = lane == 0 ? take_ticket(chain, turn + 4) : 0;
+            lru_plan<true, RATE>(p, ticket, plans + (turn + 3) % kLruPlans);
+            ticket = after;
         }
         return;
     }
 
-    const int run = threadIdx.x / kLruPairs, pair = threadIdx.x % kLruPairs, row = run * kLruRun;
+    const int warp = threadIdx.x / 32, pair = threadIdx.x % kLruPairs, row = threadIdx.x / kLruPairs * kLruRun;
+    const bool second = threadIdx.x & 16;                   // run of the warp
     const auto fetch = [&](unsigned turn) {
-        if (plans[turn % 3].live) {
-            const LruTile t = plans[turn % 3].t;
+        if (plans[turn % kLruPlans].live) {
+            const LruTile t = plans[turn % kLruPlans].t;
             IO* to = in + (turn % B) * IN * N;
             lru_fetch(p.r, t, p.D, to);
             lru_fetch(p.x, t, p.D, to + N);
@@ -95,25 +226,25 @@ lru_backward_kernel(Lru p, LruChain chain, LruRows dy, const float* __restrict__
         copy_group();
     };
     __syncthreads();
-    fetch(0);
-    if (B == 2) fetch(1);
-    for (unsigned turn = 0; plans[turn % 3].live; ++turn) {
-        const LruPlan& plan = plans[turn % 3];
-        const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch, len = plan.t.len;
-        const bool some = plan.t.seq >= 0;
-        F2 state = some ? state2(kept, (int64_t)plan.t.number * p.D + ch, left) : 0;
-        copy_wait<B - 1>();
-        __syncthreads();
-        const F2 k = RATE ? *reinterpret_cast<const F2*>(plan.rates + pair * 2) : 0;
-        const IO* from = in + (turn % B) * IN * N;
-        F2 a[kLruRun], h[kLruRun], part[kLruRun], q[kLruRun], gate[kLruRun];
-#pragma unroll
-        for (int j = 0; j < kLruRun; ++j) {
-            decay_and_part<RATE>(lru_read(from, row + j, pair), k, a[j], part[j], q[j]);
-            h[j] = mul2(part[j], lru_read(from + N, row + j, pair));
-            if (GATE) gate[j] = sigmoid2(lru_read(from + 3 * N, row + j, pair)), h[j] = mul2(h[j], gate[j]);
-            if (row + j >= len) a[j] = both(1.f), h[j] = both(0.f);
+    if (!TMA)
+        for (unsigned turn = 0; turn < B; ++turn) fetch(turn);
+    for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
+        if (TMA) {
+            bw::mbar_wait(full + turn % B, turn / B & 1, chain.err, kDeviceErrTimeout);
+        } else {
+            copy_wait<B - 1>();
+            lru_sync<1, kLruWorkers>();
         }
+        const LruPlan& plan = plans[turn % kLruPlans];
+        const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch, len = plan.t.len;
+        F2 k = 0, root = 0;
+        if (RATE) {
+            k = *reinterpret_cast<const F2*>(plan.rates + pair * 2);
+            root = *reinterpret_cast<const F2*>(plan.roots + pair * 2);
+        }
+        const IO* from = in + (turn % B) * IN * N;
+        F2 a[kLruRun], h[kLruRun], part[kLruRun], gate[kLruRun];
+        const bool shorter = read_run<IO, RATE, GATE>(from, row, pair, k, root, len, left, a, h, part, gate);
         Run m{both(1.f), both(0.f), both(0.f)};
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
@@ -123,51 +254,76 @@ lru_backward_kernel(Lru p, LruChain chain, LruRows dy, const float* __restrict__
 #pragma unroll
         for (int j = kLruRun - 1; j >= 0; --j)
             if (row + j < len) m.back = mul2(a[j], add2(m.back, lru_read(from + 2 * N, row + j, pair)));
-        runs[run][pair] = m;
-        __syncthreads();
-        for (int w = 0; w < run; ++w) state = fma2(runs[w][pair].decay, state, runs[w][pair].own);
-#pragma unroll
-        for (int j = 0; j < kLruRun; ++j) {
-            const F2 after = fma2(a[j], state, h[j]);
-            h[j] = state;                                   // the state in front of the token
-            state = after;
-        }
-        F2 over = both(1.f), more = both(0.f);              // the map of the runs behind
-        for (int w = kLruRuns - 1; w > run; --w) {
-            more = fma2(runs[w][pair].decay, more, runs[w][pair].back);
-            over = mul2(runs[w][pair].decay, over);
-        }
-        __syncthreads();
+        // the warp's other run; the first run passes its states on, the second what it sends back
+        const F2 decay = swap_halves(m.decay), other = swap_halves(second ? m.back : m.own);
+        const F2 more = swap_halves(second ? m.own : m.back);
+        if (!second) runs[warp][pair] = Run{mul2(m.decay, decay), fma2(decay, m.own, more), fma2(m.decay, other, m.back)};
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&ready);
+        lru_sync<2, kLruThreads>();
         F2 sum = both(0.f);
-        if (some) {
-            F2 e = fma2(over, carry[pair], more);
-            const int64_t at = (plan.t.first + row) * p.D + ch;
+        if (plan.t.seq >= 0) {
+            F2 state = fronts[warp][pair];
+            if (second) state = fma2(decay, state, other);
 #pragma unroll
-            for (int j = kLruRun - 1; j >= 0; --j) {
-                if (row + j >= len) continue;
+            for (int j = 0; j < kLruRun; ++j) {
+                const F2 after = fma2(a[j], state, h[j]);
+                h[j] = state;                               // the state in front of the token
+                state = after;
+            }
+            F2 e = fma2(behind[warp][pair].decay, carry[pair], behind[warp][pair].back);
+            if (!second) e = fma2(decay, e, other);
+            const int64_t at = (plan.t.first + row + kLruRun - 1) * p.D + ch;
+            IO *xp = dx + at, *rp = dr + at, *ip = di + at;
+            const F2 inverse = RATE ? rcp2_finite(root) : 0;
+            const auto token = [&](int j, bool by_w, bool all) {
                 e = add2(e, lru_read(from + 2 * N, row + j, pair));
                 const F2 x = lru_read(from + N, row + j, pair);
                 const F2 eg = GATE ? mul2(e, gate[j]) : e, egx = mul2(eg, x), ea = mul2(e, a[j]);
-                F2 dr_;
+                F2 dr_, s = part[j];
                 if (RATE) {
-                    // -dlog a q; 1 / s is finite where s = 0, and is multiplied by q or k = 0 there
-                    const F2 ratio = mul2(a[j], rcp2_finite(part[j]));
-                    const F2 base = mul2(q[j], fma2(mul2(egx, a[j]), ratio, neg2(mul2(ea, h[j]))));
+                    const Parts o = parts_of(part[j], k, root, inverse, a[j], by_w);
+                    s = o.s;
+                    const F2 base = fma2(mul2(mul2(egx, a[j]), a[j]), o.ratio, neg2(mul2(mul2(ea, h[j]), o.q)));   // -dlog a q
                     sum = add2(sum, base);
-                    dr_ = mul2(mul2(base, k), fma2(q[j], both(-1.f), both(1.f)));
+                    dr_ = mul2(mul2(base, k), fma2(o.q, both(-1.f), both(1.f)));
                 } else {
-                    dr_ = mul2(mul2(a[j], part[j]), fma2(e, h[j], neg2(egx)));
+                    dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(egx)));
                 }
-                const int64_t to = at + (int64_t)j * p.D;
-                store2(dx + to, mul2(eg, part[j]), left, p.vec);
-                store2(dr + to, dr_, left, p.vec);
-                if (GATE) store2(di + to, mul2(mul2(egx, part[j]), fma2(gate[j], both(-1.f), both(1.f))), left, p.vec);
+                store2(xp, mul2(eg, s), all ? 2 : left, all);
+                store2(rp, dr_, all ? 2 : left, all);
+                if (GATE) store2(ip, mul2(mul2(egx, s), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
                 e = ea;
+            };
+            if (p.vec && len == kLruTile && left > 0 && (shorter || !RATE)) {
+#pragma unroll
+                for (int j = kLruRun - 1; j >= 0; --j) {
+                    token(j, true, true);
+                    xp -= p.D, rp -= p.D, ip -= p.D;
+                }
+            } else {
+#pragma unroll
+                for (int j = kLruRun - 1; j >= 0; --j) {
+                    if (row + j < len) token(j, shorter, false);
+                    xp -= p.D, rp -= p.D, ip -= p.D;
+                }
             }
         }
-        if (RATE) sums[run][pair] = sum;
-        __syncthreads();
-        fetch(turn + B);
+        if (RATE) {
+            sum = add2(sum, swap_halves(sum));
+            if (!second) sums[warp][pair] = sum;
+        }
+        __syncwarp();
+        if (TMA && (threadIdx.x & 31) == 0) bw::mbar_arrive(&done);
+        if (RATE || !TMA) lru_sync<3, kLruWorkers>();
+        if (!TMA) fetch(turn + B);
+        if (RATE && warp == turn % kLruWarps && !second) {
+            sum = sums[0][pair];
+#pragma unroll
+            for (int w = 1; w < kLruWarps; ++w) sum = add2(sum, sums[w][pair]);
+            put_state2(dlam, (int64_t)plan.t.number * p.D + ch,
+                       mul2(sum, *reinterpret_cast<const F2*>(plan.slopes + pair * 2)), left);
+        }
     }
 }
 
@@ -195,15 +351,22 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
     const LruRows dy = lru_rows(RowTensor{g.dy, args.D, reinterpret_cast<uintptr_t>(g.dy) % 16 == 0 && args.D * es % 16 == 0}, es);
     LruChain chain;
     if (cudaError_t e = lru_chain(args, workspace, &chain, s)) return e;
+    LruMaps m;
+    const bool tma = args.total > 0 && p.x.unit == 16 && p.r.unit == 16 && dy.unit == 16 && (!p.i.p || p.i.unit == 16);
+    if (tma && !(lru_map(&m.x, p.x, args) && lru_map(&m.r, p.r, args) && lru_map(&m.dy, dy, args) &&
+                 (!p.i.p || lru_map(&m.i, p.i, args))))
+        return cudaErrorInvalidValue;
     const cudaError_t e = lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
         constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
         constexpr int bytes = lru_backward_smem<IO, G>();
-        const auto kernel = lru_backward_kernel<IO, R, G>;
-        if (cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return err;
-        kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(
-            p, chain, dy, kept, g.dh_final, (IO*)g.dx, (IO*)g.dr, (IO*)g.di, partial, g.dh0);
-        return cudaGetLastError();
+        const auto go = [&](auto kernel) {
+            if (cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return err;
+            kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(
+                p, chain, m, dy, kept, g.dh_final, (IO*)g.dx, (IO*)g.dr, (IO*)g.di, partial, g.dh0);
+            return cudaGetLastError();
+        };
+        return tma ? go(lru_backward_kernel<IO, R, G, true>) : go(lru_backward_kernel<IO, R, G, false>);
     });
     if (e != cudaSuccess || !t.lam) return e;
     return column_sum(partial, lru_tiles(args), args.D, args.D, g.dlam, 0, nullptr, s);
