@@ -83,33 +83,31 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
     __shared__ uint64_t ready, full[B];                     // the tile's maps are there; its inputs are
     IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, i
 
+    const auto issue = [&](unsigned turn) {                 // one lane asks for a tile
+        if (TMA && plans[turn % kLruPlans].live) {
+            const LruTile& t = plans[turn % kLruPlans].t;
+            uint64_t* bar = full + turn % B;
+            IO* to = in + (turn % B) * IN * N;
+            if (t.len == 0) return bw::mbar_arrive(bar);
+            bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
+            lru_tma(to, &in_maps.r, bar, t);
+            lru_tma(to + N, &in_maps.x, bar, t);
+            if (GATE) lru_tma(to + 2 * N, &in_maps.i, bar, t);
+        }
+    };
     if (threadIdx.x >= kLruWorkers) {                       // the guide
         const int lane = threadIdx.x - kLruWorkers, pair = lane % kLruPairs;
         const bool first = lane < kLruPairs;                // the warp's other half only looks on
-        const auto issue = [&](unsigned turn) {
-            if (TMA && lane == 0 && plans[turn % kLruPlans].live) {
-                const LruTile& t = plans[turn % kLruPlans].t;
-                uint64_t* bar = full + turn % B;
-                IO* to = in + (turn % B) * IN * N;
-                if (t.len == 0) return bw::mbar_arrive(bar);
-                bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
-                lru_tma(to, &in_maps.r, bar, t);
-                lru_tma(to + N, &in_maps.x, bar, t);
-                if (GATE) lru_tma(to + 2 * N, &in_maps.i, bar, t);
-            }
-        };
         if (lane == 0) {
             bw::mbar_init(&ready, kLruWarps);
             for (int i = 0; i < B; ++i) bw::mbar_init(full + i, 1);
             bw::fence_mbar_init();
         }
-        unsigned ticket = 0;
-        for (unsigned turn = 0; turn < 3; ++turn) {
-            if (lane == 0) ticket = take_ticket(chain, turn);
-            lru_plan<false, RATE>(p, ticket, plans + turn);
-        }
-        if (lane == 0) ticket = take_ticket(chain, 3);
-        for (unsigned turn = 0; turn < B; ++turn) issue(turn);
+        LruPlanner<false, RATE> planner;
+        planner.start(p, chain);
+        for (unsigned turn = 0; turn < 3; ++turn) planner.plan(p, chain, turn, plans + turn);
+        for (unsigned turn = 0; turn < B; ++turn)
+            if (lane == 0) issue(turn);
         __syncthreads();
         for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
             const LruTile t = plans[turn % kLruPlans].t;
@@ -133,23 +131,17 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
                 all.own = fma2(m[w].decay, all.own, m[w].own);
                 all.decay = mul2(m[w].decay, all.decay);
             }
-            if (!found) {
-                if (first && t.to_tail) publish_map(chain.maps + at, all.decay, all.own);
-                issue(turn + B);                            // the workers have read the tile
-                state = wait_back<false>(chain, t, p.cols, pair, t.to_head);
-            }
+            if (first && t.to_tail && t.to_head) publish_map(chain.maps + at, all.decay, all.own);
+            if (!found) state = wait_back<false>(chain, t, p.cols, pair, t.to_head);
             const F2 end = fma2(all.decay, state, all.own);
             if (first && t.to_tail) publish_state(chain.states + at + (int64_t)p.cols * kLruPairs, end);
             if (first) carry[pair] = state;
             lru_arrive<2, kLruThreads>();
-            if (found) issue(turn + B);
             if (first && t.seq >= 0) {
                 if (kept) put_state2(kept, (int64_t)t.number * p.D + ch, state, left);
                 if (h_final && !t.to_tail) put_state2(h_final, (int64_t)t.seq * p.D + ch, end, left);
             }
-            const unsigned after = lane == 0 ? take_ticket(chain, turn + 4) : 0;
-            lru_plan<false, RATE>(p, ticket, plans + (turn + 3) % kLruPlans);
-            ticket = after;
+            planner.plan(p, chain, turn + 3, plans + (turn + 3) % kLruPlans);
         }
         return;
     }
@@ -199,6 +191,7 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
         if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&ready);
         lru_sync<2, kLruThreads>();
         if (!TMA) fetch(turn + B);
+        else if (threadIdx.x == kLruWorkers - 32) issue(turn + B);
         if (y && plan.t.seq >= 0) {
             F2 h = fma2(fronts[warp][pair].decay, carry[pair], fronts[warp][pair].own);
             if (second) h = fma2(o.decay, h, o.own);
@@ -220,6 +213,15 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
             }
         }
     }
+}
+
+__global__ void __launch_bounds__(256)
+lru_chain_kernel(uint4* __restrict__ words, int64_t n, const float* __restrict__ lam, float c, int D, float4* __restrict__ rates,
+                 int channels) {
+    const int64_t step = (int64_t)gridDim.x * 256, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (int64_t i = at; i < n; i += step) words[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (lam)
+        for (int64_t ch = at; ch < channels; ch += step) rates[ch] = ch < D ? rates_of(lam[ch], c) : float4{};
 }
 
 template <typename IO, bool RATE, bool GATE>
@@ -255,12 +257,28 @@ size_t lru_forward_workspace(const LruArgs& a) {
     return lru_one_tile_each(a) ? 0 : lru_chain_bytes(lru_tiles(a), (a.D + kLruCols - 1) / kLruCols);
 }
 
+cudaError_t lru_chain(const LruArgs& a, const float* lam, void* workspace, LruChain* c, cudaStream_t s) {
+    *c = LruChain{};
+    if (cudaError_t e = device_error_ptr(&c->err)) return e;
+    if (lru_one_tile_each(a)) return cudaSuccess;
+    const int64_t cols = (a.D + kLruCols - 1) / kLruCols, cells = lru_tiles(a) * cols * kLruPairs;
+    c->ticket = (unsigned*)workspace;
+    c->maps = (ulonglong2*)((char*)workspace + 256);
+    c->states = (F2*)(c->maps + cells);
+    float4* rates = (float4*)(c->states + cells);
+    c->rates = lam ? rates : nullptr;
+    const int64_t n = 16 + cells * 24 / 16;                // 16 bytes each
+    lru_chain_kernel<<<(unsigned)std::min<int64_t>((n + 1023) / 1024, 8 * kSms), 256, 0, s>>>(
+        (uint4*)workspace, n, lam, a.c, a.D, rates, (int)(cols * kLruCols));
+    return cudaGetLastError();
+}
+
 cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float* h_final, float* kept, void* workspace,
                         cudaStream_t s) {
     Lru p = lru_of(args, t);
     p.vec = lru_pairs(y, args.D, args.io == GDR_F32 ? 4 : 2);
     LruChain chain;
-    if (cudaError_t e = lru_chain(args, workspace, &chain, s)) return e;
+    if (cudaError_t e = lru_chain(args, t.lam, workspace, &chain, s)) return e;
     LruMaps m;
     const bool tma = args.total > 0 && p.x.unit == 16 && p.r.unit == 16 && (!p.i.p || p.i.unit == 16);
     if (tma && !(lru_map(&m.x, p.x, args) && lru_map(&m.r, p.r, args) && (!p.i.p || lru_map(&m.i, p.i, args))))

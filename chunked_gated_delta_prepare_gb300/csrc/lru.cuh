@@ -32,11 +32,26 @@ struct LruRows {
     int unit;
 };
 
+// Division of numbers below 2^31 by one that the host knows: q = x m >> 31 + l, m = ceil(2^(31 + l) / d), 2^l >= d.
+struct Divisor {
+    unsigned d = 1, m = 0, l = 0;
+    __device__ __forceinline__ unsigned of(unsigned x) const { return d == 1 ? x : __umulhi(x, m) >> (l - 1); }
+};
+inline Divisor divisor(unsigned d) {
+    Divisor v;
+    v.d = d;
+    while ((uint64_t{1} << v.l) < d) ++v.l;
+    if (d > 1) v.m = (unsigned)(((uint64_t{1} << (31 + v.l)) + d - 1) / d);
+    return v;
+}
+
 // The operator as the kernels take it.
 struct Lru {
     Seqs q;
     int D;
     unsigned cols, tiles;    // blocks of channels, and tiles of the token axis
+    unsigned per;            // tiles of a sequence of a batch
+    Divisor by_cols, by_n;
     LruRows x, r, i;
     const float *lam, *h0;
     float c;
@@ -109,7 +124,10 @@ __device__ __forceinline__ F2 rcp2_finite(F2 v) {
 __device__ __forceinline__ float rate_of(float lam, float c) {
     return c * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam))));     // a NaN comes through the logarithm
 }
-__device__ __forceinline__ float rate_slope(float lam, float c) { return c / (1.f + expf(-lam)); }
+__device__ __forceinline__ float4 rates_of(float lam, float c) {
+    const float k = rate_of(lam, c);
+    return make_float4(k, sqrtf(2.f * k), c / (1.f + expf(-lam)), 0.f);
+}
 
 // A token's decay a and input's part s; q = sigmoid(r).
 //
@@ -201,7 +219,7 @@ struct LruTile {
 // tiles behind it).  The sequences of a batch take turns, so that a tile's neighbour in time is long done.
 template <bool BACK> __device__ __forceinline__ LruTile lru_tile(const Lru& a, unsigned ticket) {
     LruTile t;
-    unsigned k = ticket / a.cols;
+    unsigned k = a.by_cols.of(ticket);
     t.col = ticket - k * a.cols;
     if (BACK) k = a.tiles - 1 - k;
     int64_t len;
@@ -214,9 +232,9 @@ template <bool BACK> __device__ __forceinline__ LruTile lru_tile(const Lru& a, u
         len = at.len;
         tile = (unsigned)at.tile;
     } else {
-        tile = k / (unsigned)a.q.n;
+        tile = a.by_n.of(k);
         t.seq = (int)(k - tile * (unsigned)a.q.n);
-        t.number = (unsigned)t.seq * (a.tiles / (unsigned)a.q.n) + tile;
+        t.number = (unsigned)t.seq * a.per + tile;
         t.first = t.seq * a.q.T;
         len = a.q.T;
     }
@@ -234,9 +252,12 @@ struct LruChain {
     unsigned* ticket;        // tiles taken so far, less one; nullptr: no tile waits for another
     ulonglong2* maps;        // [tiles][cols][pairs]: a tile makes of state h  h * x + y
     F2* states;              // [tiles][cols][pairs]: the state that a tile goes on from
+    const float4* rates;     // [cols * 32]: rates_of each channel, or nullptr (the guides form them)
     unsigned* err;           // the device error word
 };
-inline size_t lru_chain_bytes(int64_t tiles, int64_t cols) { return 256 + (size_t)tiles * cols * kLruPairs * 24; }
+inline size_t lru_chain_bytes(int64_t tiles, int64_t cols) {       // the ticket, the maps, the states; the rates
+    return 256 + (size_t)tiles * cols * kLruPairs * 24 + (size_t)cols * kLruCols * 16;
+}
 
 // A block's k-th tile.  Tiles are handed out in order, so those that a tile waits for belong to blocks that run already.
 __device__ __forceinline__ unsigned take_ticket(const LruChain& c, unsigned k) {
@@ -316,33 +337,57 @@ template <int ID, int N> __device__ __forceinline__ void lru_arrive() {
 }
 __device__ __forceinline__ F2 swap_halves(F2 v) { return __shfl_xor_sync(0xffffffffu, v, 16); }
 
-// What the guide tells the workers of a tile.  It plans three tiles ahead, after the present one's state is out, so that
-// neither the ticket's way nor the rates hold anyone up.
+// What the guide tells the workers of a tile.
 constexpr int kLruPlans = 4;
 struct LruPlan {
     LruTile t;
     bool live;               // there is one
     alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];      // k, sqrt(2 k), (BACK) k's slope
 };
-template <bool BACK, bool RATE>
-__device__ __forceinline__ void lru_plan(const Lru& p, unsigned ticket, LruPlan* plan) {
-    const int lane = threadIdx.x & 31;
-    ticket = __shfl_sync(0xffffffffu, ticket, 0);
-    const bool live = ticket < p.tiles * p.cols;
-    if (lane == 0) plan->live = live;
-    if (live) {
-        const LruTile t = lru_tile<BACK>(p, ticket);
-        if (lane == 0) plan->t = t;
-        const int ch = t.col * kLruCols + lane;
-        if (RATE) {
-            const float lam = ch < p.D ? p.lam[ch] : 0.f, k = ch < p.D ? rate_of(lam, p.c) : 0.f;
-            plan->rates[lane] = k;
-            plan->roots[lane] = sqrtf(2.f * k);
-            if (BACK) plan->slopes[lane] = ch < p.D ? rate_slope(lam, p.c) : 0.f;
-        }
+// The guide's lane: tickets are taken five tiles ahead, a channel's lam is read four ahead and a tile planned three ahead,
+// after the present one's state is out, so that no way to memory holds anyone up.
+template <bool BACK, bool RATE> struct LruPlanner {
+    unsigned ticket, next;   // of the tile to be planned, and of the one after it
+    float4 rate;             // of the tile to be planned: k, sqrt(2 k), k's slope
+
+    __device__ __forceinline__ unsigned take(const LruChain& c, unsigned turn) const {
+        return (threadIdx.x & 31) == 0 ? take_ticket(c, turn) : 0;
     }
-    __syncwarp();
-}
+    __device__ __forceinline__ float4 read(const Lru& p, const LruChain& c, unsigned ticket) const {
+        if (!RATE || ticket >= p.tiles * p.cols) return float4{};
+        const unsigned col = ticket - p.by_cols.of(ticket) * p.cols;
+        const int ch = (int)col * kLruCols + (threadIdx.x & 31);
+        if (c.rates) return c.rates[ch];
+        return ch < p.D ? rates_of(p.lam[ch], p.c) : float4{};
+    }
+    __device__ __forceinline__ void start(const Lru& p, const LruChain& c) {
+        ticket = __shfl_sync(0xffffffffu, take(c, 0), 0);
+        rate = read(p, c, ticket);
+        next = take(c, 1);
+    }
+    // Plans the tile of turn `turn`.
+    __device__ __forceinline__ void plan(const Lru& p, const LruChain& c, unsigned turn, LruPlan* plan) {
+        const unsigned after = take(c, turn + 2);
+        next = __shfl_sync(0xffffffffu, next, 0);
+        const float4 rate_after = read(p, c, next);
+        const int lane = threadIdx.x & 31;
+        const bool live = ticket < p.tiles * p.cols;
+        if (lane == 0) plan->live = live;
+        if (live) {
+            const LruTile t = lru_tile<BACK>(p, ticket);
+            if (lane == 0) plan->t = t;
+            if (RATE) {
+                plan->rates[lane] = rate.x;
+                plan->roots[lane] = rate.y;
+                if (BACK) plan->slopes[lane] = rate.z;
+            }
+        }
+        ticket = next;
+        next = after;
+        rate = rate_after;
+        __syncwarp();
+    }
+};
 
 // Inputs on their way by TMA: a box of 128 rows and 32 channels, zeros outside the tensor.
 struct LruMaps {
@@ -455,6 +500,9 @@ inline Lru lru_of(const LruArgs& a, const LruTensors& t) {
     k.D = a.D;
     k.cols = (unsigned)((a.D + kLruCols - 1) / kLruCols);
     k.tiles = (unsigned)lru_tiles(a);
+    k.per = k.tiles / (unsigned)a.n;
+    k.by_cols = divisor(k.cols);
+    k.by_n = divisor((unsigned)a.n);
     k.x = lru_rows(t.x, e);
     k.r = lru_rows(t.r, e);
     k.i = lru_rows(t.i, e);
@@ -471,18 +519,9 @@ inline bool lru_map(CUtensorMap* m, const LruRows& v, const LruArgs& a) {
     return make_tmap_bf16_4d_mode(m, v.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);   // copies any type's bits
 }
 
-// The chain's words in the workspace, set to "not written"; with one tile a sequence there is none.
 inline bool lru_one_tile_each(const LruArgs& a) { return (a.cu ? a.total : a.T) <= kLruTile; }
-inline cudaError_t lru_chain(const LruArgs& a, void* workspace, LruChain* c, cudaStream_t s) {
-    *c = LruChain{};
-    if (cudaError_t e = device_error_ptr(&c->err)) return e;
-    if (lru_one_tile_each(a)) return cudaSuccess;
-    const int64_t tiles = lru_tiles(a), cols = (a.D + kLruCols - 1) / kLruCols;
-    c->ticket = (unsigned*)workspace;
-    c->maps = (ulonglong2*)((char*)workspace + 256);
-    c->states = (F2*)(c->maps + tiles * cols * kLruPairs);
-    return cudaMemsetAsync(workspace, 0xff, lru_chain_bytes(tiles, cols), s);
-}
+// The chain's words in the workspace, made "not written", and the rates; none of them with one tile a sequence.
+cudaError_t lru_chain(const LruArgs& a, const float* lam, void* workspace, LruChain* c, cudaStream_t s);
 
 }  // namespace layer
 }  // namespace gdr

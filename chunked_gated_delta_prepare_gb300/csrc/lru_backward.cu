@@ -129,48 +129,41 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
     __shared__ F2 fronts[kLruWarps][kLruPairs], sums[kLruWarps][kLruPairs];    // states in front of them; sums for dlam
     __shared__ F2 carry[kLruPairs];
     __shared__ LruPlan plans[kLruPlans];
-    __shared__ uint64_t ready, full[B], done;               // the tile's maps are there; its inputs are; they have been read
+    __shared__ uint64_t ready, full[B];                     // the tile's maps are there; its inputs are
     IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, dy, i
 
+    const auto issue = [&](unsigned turn) {                 // one lane asks for a tile
+        if (TMA && plans[turn % kLruPlans].live) {
+            const LruTile& t = plans[turn % kLruPlans].t;
+            uint64_t* bar = full + turn % B;
+            IO* to = in + (turn % B) * IN * N;
+            if (t.len == 0) return bw::mbar_arrive(bar);
+            bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
+            lru_tma(to, &in_maps.r, bar, t);
+            lru_tma(to + N, &in_maps.x, bar, t);
+            lru_tma(to + 2 * N, &in_maps.dy, bar, t);
+            if (GATE) lru_tma(to + 3 * N, &in_maps.i, bar, t);
+        }
+    };
     if (threadIdx.x >= kLruWorkers) {                       // the guide
         const int lane = threadIdx.x - kLruWorkers, pair = lane % kLruPairs;
         const bool first = lane < kLruPairs;
-        const auto issue = [&](unsigned turn) {
-            if (TMA && lane == 0 && plans[turn % kLruPlans].live) {
-                const LruTile& t = plans[turn % kLruPlans].t;
-                uint64_t* bar = full + turn % B;
-                IO* to = in + (turn % B) * IN * N;
-                if (t.len == 0) return bw::mbar_arrive(bar);
-                bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
-                lru_tma(to, &in_maps.r, bar, t);
-                lru_tma(to + N, &in_maps.x, bar, t);
-                lru_tma(to + 2 * N, &in_maps.dy, bar, t);
-                if (GATE) lru_tma(to + 3 * N, &in_maps.i, bar, t);
-            }
-        };
         if (lane == 0) {
             bw::mbar_init(&ready, kLruWarps);
-            bw::mbar_init(&done, kLruWarps);
             for (int i = 0; i < B; ++i) bw::mbar_init(full + i, 1);
             bw::fence_mbar_init();
         }
-        unsigned ticket = 0;
-        for (unsigned turn = 0; turn < 3; ++turn) {
-            if (lane == 0) ticket = take_ticket(chain, turn);
-            lru_plan<true, RATE>(p, ticket, plans + turn);
-        }
-        if (lane == 0) ticket = take_ticket(chain, 3);
-        for (unsigned turn = 0; turn < B; ++turn) issue(turn);
+        LruPlanner<true, RATE> planner;
+        planner.start(p, chain);
+        for (unsigned turn = 0; turn < 3; ++turn) planner.plan(p, chain, turn, plans + turn);
+        for (unsigned turn = 0; turn < B; ++turn)
+            if (lane == 0) issue(turn);
         __syncthreads();
         for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
             const LruTile t = plans[turn % kLruPlans].t;
             const int ch = t.col * kLruCols + pair * 2, left = p.D - ch;
             const int64_t at = ((int64_t)t.number * p.cols + t.col) * kLruPairs + pair;
             F2 state = t.seq >= 0 ? state2(kept, (int64_t)t.number * p.D + ch, left) : 0;
-            if (TMA && turn > 0) {                          // the tile before has been read: its place is free
-                bw::mbar_wait(&done, turn - 1 & 1, chain.err, kDeviceErrTimeout);
-                issue(turn - 1 + B);
-            }
             F2 e = 0;
             bool found = t.to_tail == 0, there = false;
             if (found && t.seq >= 0) e = state2(dh_final, (int64_t)t.seq * p.D + ch, left);
@@ -196,18 +189,14 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             }
             d = __shfl_sync(0xffffffffu, d, pair);
             b = __shfl_sync(0xffffffffu, b, pair);
-            if (!found) {
-                if (first && t.to_head) publish_map(chain.maps + at, d, b);
-                e = wait_back<true>(chain, t, p.cols, pair, t.to_tail);
-            }
+            if (first && t.to_head && t.to_tail) publish_map(chain.maps + at, d, b);
+            if (!found) e = wait_back<true>(chain, t, p.cols, pair, t.to_tail);
             const F2 end = fma2(d, e, b);
             if (first && t.to_head) publish_state(chain.states + at - (int64_t)p.cols * kLruPairs, end);
             if (first) carry[pair] = e;
             lru_arrive<2, kLruThreads>();
             if (first && dh0 && t.seq >= 0 && !t.to_head) put_state2(dh0, (int64_t)t.seq * p.D + ch, end, left);
-            const unsigned after = lane == 0 ? take_ticket(chain, turn + 4) : 0;
-            lru_plan<true, RATE>(p, ticket, plans + (turn + 3) % kLruPlans);
-            ticket = after;
+            planner.plan(p, chain, turn + 3, plans + (turn + 3) % kLruPlans);
         }
         return;
     }
@@ -313,10 +302,9 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             sum = add2(sum, swap_halves(sum));
             if (!second) sums[warp][pair] = sum;
         }
-        __syncwarp();
-        if (TMA && (threadIdx.x & 31) == 0) bw::mbar_arrive(&done);
-        if (RATE || !TMA) lru_sync<3, kLruWorkers>();
+        lru_sync<3, kLruWorkers>();                         // the tile has been read
         if (!TMA) fetch(turn + B);
+        else if (threadIdx.x == kLruWorkers - 32) issue(turn + B);
         if (RATE && warp == turn % kLruWarps && !second) {
             sum = sums[0][pair];
 #pragma unroll
@@ -350,7 +338,7 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
     for (const void* v : {(const void*)g.dx, (const void*)g.dr, (const void*)g.di}) p.vec = p.vec && lru_pairs(v, args.D, es);
     const LruRows dy = lru_rows(RowTensor{g.dy, args.D, reinterpret_cast<uintptr_t>(g.dy) % 16 == 0 && args.D * es % 16 == 0}, es);
     LruChain chain;
-    if (cudaError_t e = lru_chain(args, workspace, &chain, s)) return e;
+    if (cudaError_t e = lru_chain(args, t.lam, workspace, &chain, s)) return e;
     LruMaps m;
     const bool tma = args.total > 0 && p.x.unit == 16 && p.r.unit == 16 && dy.unit == 16 && (!p.i.p || p.i.unit == 16);
     if (tma && !(lru_map(&m.x, p.x, args) && lru_map(&m.r, p.r, args) && lru_map(&m.dy, dy, args) &&
