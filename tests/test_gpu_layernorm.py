@@ -123,6 +123,28 @@ def test_backward(rows, D, io, with_dr):
     backward_check(rows, D, io, with_dr)
 
 
+# many rows, which come through shared memory: each number of threads a row, whole and odd rows, more rows than places
+MANY = [(12000, 256), (11001, 128), (12345, 131), (8000, 512), (6000, 1000), (5001, 1027), (2800, 2048), (3001, 2050),
+        (2500, 4096), (2600, 4089), (1000, 8192), (1001, 8191), (700, 16384), (701, 16379), (4000, 2044)]
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("rows,D", MANY)
+def test_many_rows(rows, D, io):
+    test_forward(rows, D, io)
+    backward_check(rows, D, io, True)
+    backward_check(rows, D, io, False)
+
+
+@pytest.mark.parametrize("io", TYPES)
+def test_many_rows_of_a_slice(io):
+    x, res, w, b = make(3000, 2048, io, ld=2048 + 64)
+    y, r = layer.layernorm_forward(x, w, b, res, eps=EPS)
+    whole = layer.layernorm_forward(x.contiguous(), w, b, res, eps=EPS)
+    assert torch.equal(y, whole[0]) and torch.equal(r, whole[1])
+    check(y, x.double() + res.double(), w, b, io)
+
+
 @pytest.mark.parametrize("io", TYPES)
 @pytest.mark.parametrize("D", range(1, 20))
 def test_narrow_rows(D, io):
@@ -150,7 +172,8 @@ def test_backward_against_differences():
 
 
 @pytest.mark.parametrize("io", TYPES)
-@pytest.mark.parametrize("rows,D", [(7, 33), (700, 250), (1300, 887), (1300, 2133), (700, 4089), (700, 4096)])
+@pytest.mark.parametrize("rows,D", [(7, 33), (700, 250), (1300, 887), (1300, 2133), (700, 4089), (700, 4096), (6000, 1027),
+                                    (3001, 4089), (12000, 264)])
 def test_a_row_does_not_see_its_neighbours(rows, D, io):
     """Rows that share an aligned vector with their neighbours' ends, which hold NaN and infinity."""
     gen = torch.Generator().manual_seed(rows)
