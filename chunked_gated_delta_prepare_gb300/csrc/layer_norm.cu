@@ -16,12 +16,11 @@ namespace {
 
 // ---------------------------------------------------------------- rows through shared memory
 //
-// A block an SM: its threads make up places of TPR threads, each working on rows of its own with one ring of stages for
+// A block an SM: its threads make up places of `tpr` threads, each working on rows of its own with one ring of stages for
 // their inputs, so that the barriers of one row hold up no other.  The rows' copies are in flight whatever the threads wait
-// for.  768 threads where a row takes at most 256 of them: 80 registers a thread.
+// for.  Up to 384 threads a row a block has at most 768 (80 registers each), above that 1024.
 
 constexpr int kMaxStages = 4, kRingBytes = 200 * 1024;
-constexpr int ring_block(int tpr) { return tpr <= 256 ? 768 : tpr; }
 
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(bw::smem_u32(to)),
@@ -29,33 +28,33 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
                  : "memory");
 }
 
-// Sums over a place's TPR threads; red: [warps of the block][NV], not used again before another barrier of the place.
-template <int TPR, int NV> __device__ __forceinline__ void place_sum(float (&v)[NV], float (*red)[NV]) {
+constexpr int ring_most(int warps) { return warps <= 12 ? 24 : 32; }        // warps of a block
+constexpr int ring_places(int warps) { return ring_most(warps) / warps; }
+
+// Sums over a place's WARPS warps; red: [NV][places][WARPS, a multiple of 4], zero where there is no warp, not used again
+// before another barrier of the place.
+template <int WARPS> constexpr int kRedSlots = ring_places(WARPS) * ((WARPS + 3) / 4 * 4);
+template <int WARPS, int NV>
+__device__ __forceinline__ void place_sum(float (&v)[NV], float (*red)[kRedSlots<WARPS>]) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (TPR == 32) return;
-    constexpr int W = TPR / 32;
-    const int warp = threadIdx.x / 32, place = threadIdx.x / TPR, lane = threadIdx.x & 31;
-    if (lane == 0)
+    if (WARPS == 1) return;
+    constexpr int slots = (WARPS + 3) / 4 * 4;
+    const int warp = threadIdx.x / 32, place = warp / WARPS;
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) red[warp][i] = v[i];
-    bw::named_bar_sync(place + 1, TPR);        // 0 is the block's; at most 12 places
-    if (W <= 8) {
+        for (int i = 0; i < NV; ++i) red[i][place * slots + warp % WARPS] = v[i];
+    bw::named_bar_sync(place + 1, WARPS * 32);              // 0 is the block's; at most 12 places of two warps and more
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[i] = red[place * W][i];
+    for (int i = 0; i < NV; ++i) {
+        const float4* q = reinterpret_cast<const float4*>(red[i] + place * slots);
+        v[i] = 0.f;
 #pragma unroll
-            for (int w = 1; w < W; ++w) v[i] += red[place * W + w][i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float u = lane < W ? red[place * W + lane][i] : 0.f;
-#pragma unroll
-            for (int o = W / 2; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-            v[i] = __shfl_sync(0xffffffffu, u, 0);
+        for (int w = 0; w < slots / 4; ++w) {
+            const float4 f = q[w];
+            v[i] += (f.x + f.y) + (f.z + f.w);
         }
     }
 }
@@ -115,15 +114,41 @@ __device__ __forceinline__ Raw8<IO> ring_vector(const IO* row, int i, int c, int
     return r;
 }
 
-template <typename IO, int TPR, int VPT, bool CUT>
-__global__ void __launch_bounds__(ring_block(TPR), 1)
+// Zeroes the columns of a vector from column c on that lie outside the row.
+__device__ __forceinline__ void keep_columns(F2 (&v)[4], int c, int D) {
+    if (c < 0 || c + 8 > D)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack2(v[k]);
+            const int at = c + 2 * k;
+            v[k] = pack2(at >= 0 && at < D ? f.x : 0.f, at + 1 >= 0 && at + 1 < D ? f.y : 0.f);
+        }
+}
+__device__ __forceinline__ float both_halves(F2 v) {
+    const float2 f = unpack2(v);
+    return f.x + f.y;
+}
+template <typename IO> __device__ __forceinline__ void store_pairs(IO* row, const F2 (&v)[4], int c, int D) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2(v[k]);
+        x[2 * k] = f.x, x[2 * k + 1] = f.y;
+    }
+    store_cut(row, x, c, D, true);
+}
+
+template <typename IO, int WARPS, int VPT, bool CUT>
+__global__ void __launch_bounds__(ring_places(WARPS) * WARPS * 32, 1)
 layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict__ w, const IO* __restrict__ b,
-                      IO* __restrict__ y, IO* __restrict__ r, int stages, uint32_t pitch, bool vec_w, unsigned* err) {
-    constexpr int NT = ring_block(TPR), P = NT / TPR;
+                      IO* __restrict__ y, IO* __restrict__ r, int stages, uint32_t pitch, bool vec_w,
+                      unsigned* err) {
+    constexpr int P = ring_places(WARPS), tpr = WARPS * 32, NT = P * tpr;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float red[2][2][NT / 32][1];
+    __shared__ __align__(16) float red[2][2][1][kRedSlots<WARPS>];
     __shared__ uint64_t full[P][kMaxStages];
-    const int tid = threadIdx.x % TPR, place = threadIdx.x / TPR, D = a.D;
+    const int tid = threadIdx.x % tpr, place = threadIdx.x / tpr, D = a.D;
+    for (int i = threadIdx.x; i < 4 * kRedSlots<WARPS>; i += NT) (&red[0][0][0][0])[i] = 0.f;
     if (threadIdx.x == 0) {
         for (int i = 0; i < P * kMaxStages; ++i) bw::mbar_init(&full[0][0] + i, 1);
         bw::fence_mbar_init();
@@ -138,71 +163,71 @@ layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restri
     Raw8<IO> wr[VPT], br[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (tid + i * TPR) * 8 - shift;
+        const int c = (tid + i * tpr) * 8 - shift;
         wr[i] = load_cut(w, c, D, vec_w && shift == 0);
         br[i] = b ? load_cut(b, c, D, vec_w && shift == 0) : load8((const IO*)nullptr, 0, false);
     }
+    const float over = 1.f / (float)D;
     int stage = 0, phase = 0, turn = 0;
     for (int64_t row = first; row < a.rows; row += step, ++turn) {
         bw::mbar_wait(full[place] + stage, phase, err, kDeviceErrTimeout);
         const int copied = CUT ? ring.copied(row) : 0;
-        float v[VPT][8], sum[1] = {0.f}, var[1] = {0.f};
+        F2 v[VPT][4], part = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int n = tid + i * TPR, c = n * 8 - shift;
-            widen(ring_vector<IO, CUT>(ring.at(stage, 0), n, c, D, (const IO*)x.p + row * D, copied), v[i]);
+            const int n = tid + i * tpr, c = n * 8 - shift;
+            pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 0), n, c, D, (const IO*)x.p + row * D, copied), v[i]);
             if (res.p) {
-                float t[8];
-                widen(ring_vector<IO, CUT>(ring.at(stage, 1), n, c, D, (const IO*)res.p + row * D, copied), t);
+                F2 t[4];
+                pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 1), n, c, D, (const IO*)res.p + row * D, copied), t);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += t[j];
+                for (int k = 0; k < 4; ++k) v[i][k] = add2(v[i][k], t[k]);
             }
-            if (r) store_cut(r + row * D, v[i], c, D, true);
+            if (r) store_pairs(r + row * D, v[i], c, D);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[0] += v[i][j];
+            for (int k = 0; k < 4; ++k) part = add2(part, v[i][k]);
         }
-        place_sum<TPR, 1>(sum, red[turn & 1][0]);
+        float sum[1] = {both_halves(part)};
+        place_sum<WARPS, 1>(sum, red[turn & 1][0]);
         if (tid == 0) ring.issue(row + stages * step, stage, CUT);          // every thread has read the stage
         if (++stage == stages) stage = 0, phase ^= 1;
-        const float mean = sum[0] / (float)D;
+        const F2 less = both(-sum[0] * over);
+        part = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8 - shift;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] -= mean;
-            if (c < 0 || c + 8 > D)
+            for (int k = 0; k < 4; ++k) v[i][k] = add2(v[i][k], less);
+            keep_columns(v[i], (tid + i * tpr) * 8 - shift, D);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < 0 || c + j >= D) v[i][j] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) var[0] = fmaf(v[i][j], v[i][j], var[0]);
+            for (int k = 0; k < 4; ++k) part = fma2(v[i][k], v[i][k], part);
         }
-        place_sum<TPR, 1>(var, red[turn & 1][1]);
-        const float rstd = rsqrtf(var[0] / (float)D + a.eps);
+        float var[1] = {both_halves(part)};
+        place_sum<WARPS, 1>(var, red[turn & 1][1]);
+        const F2 rstd = both(rsqrtf(fmaf(var[0], over, a.eps)));
         if (!y) continue;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8 - shift;
-            float wf[8], bf[8];
-            widen(wr[i], wf), widen(br[i], bf);
+            F2 wf[4], bf[4];
+            pairs<IO, 8>(wr[i], wf), pairs<IO, 8>(br[i], bf);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, wf[j], bf[j]);
-            store_cut(y + row * D, v[i], c, D, true);
+            for (int k = 0; k < 4; ++k) v[i][k] = fma2(mul2(v[i][k], rstd), wf[k], bf[k]);
+            store_pairs(y + row * D, v[i], (tid + i * tpr) * 8 - shift, D);
         }
     }
 }
 
 // One vector a thread, whose sums of dw and db stay in registers; a block leaves one row of partial sums [2 D].
-template <typename IO, int TPR, bool CUT>
-__global__ void __launch_bounds__(ring_block(TPR), 1)
+template <typename IO, int WARPS, bool CUT>
+__global__ void __launch_bounds__(ring_places(WARPS) * WARPS * 32, 1)
 layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict__ r, const IO* __restrict__ w,
                                const IO* __restrict__ dr, IO* __restrict__ dx, float* __restrict__ partial, int stages,
                                uint32_t pitch, bool vec_w, unsigned* err) {
-    constexpr int NT = ring_block(TPR), P = NT / TPR;
+    constexpr int P = ring_places(WARPS), tpr = WARPS * 32, NT = P * tpr;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float red[2][2][NT / 32][2];
+    __shared__ __align__(16) float red[2][2][2][kRedSlots<WARPS>];
     __shared__ uint64_t full[P][kMaxStages];
-    const int tid = threadIdx.x % TPR, place = threadIdx.x / TPR, D = a.D;
+    const int tid = threadIdx.x % tpr, place = threadIdx.x / tpr, D = a.D;
+    for (int i = threadIdx.x; i < 8 * kRedSlots<WARPS>; i += NT) (&red[0][0][0][0])[i] = 0.f;
     if (threadIdx.x == 0) {
         for (int i = 0; i < P * kMaxStages; ++i) bw::mbar_init(&full[0][0] + i, 1);
         bw::fence_mbar_init();
@@ -215,49 +240,53 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
         for (int k = 0; k < stages; ++k) ring.issue(first + k * step, k, CUT);
     const int shift = CUT ? first_shift<IO>(first, D) : 0, c = tid * 8 - shift;
     const Raw8<IO> wr = load_cut(w, c, D, vec_w && shift == 0);
-    float dw[8], db[8];
+    F2 dw[4], db[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.f;
+    for (int k = 0; k < 4; ++k) dw[k] = db[k] = both(0.f);
+    const float over = 1.f / (float)D;
     int stage = 0, phase = 0, turn = 0;
     for (int64_t row = first; row < a.rows; row += step, ++turn) {
         bw::mbar_wait(full[place] + stage, phase, err, kDeviceErrTimeout);
         const int copied = CUT ? ring.copied(row) : 0;
-        float g[8], s[8], wf[8], o[8], one[2] = {0.f, 0.f}, two[2] = {0.f, 0.f};
-        widen(ring_vector<IO, CUT>(ring.at(stage, 0), tid, c, D, dy + row * D, copied), g);
-        widen(ring_vector<IO, CUT>(ring.at(stage, 1), tid, c, D, r + row * D, copied), s);
-        const Raw8<IO> er = dr ? ring_vector<IO, CUT>(ring.at(stage, 2), tid, c, D, dr + row * D, copied)
-                               : load8((const IO*)nullptr, 0, false);
-        widen(wr, wf);
+        F2 g[4], s[4], t[4], o[4];
+        pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 0), tid, c, D, dy + row * D, copied), g);
+        pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 1), tid, c, D, r + row * D, copied), s);
+        pairs<IO, 8>(wr, t);
+        F2 p0 = both(0.f), p1 = both(0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            one[0] += s[j];
-            one[1] = fmaf(wf[j], g[j], one[1]);
+        for (int k = 0; k < 4; ++k) {
+            t[k] = mul2(t[k], g[k]);                         // w dy
+            p0 = add2(p0, s[k]);
+            p1 = add2(p1, t[k]);
         }
-        place_sum<TPR, 2>(one, red[turn & 1][0]);
-        if (tid == 0) ring.issue(row + stages * step, stage, CUT);          // every thread has read the stage
+        float one[2] = {both_halves(p0), both_halves(p1)};
+        place_sum<WARPS, 2>(one, red[turn & 1][0]);
+        // every thread is done with the row before: its stage is free
+        if (tid == 0 && turn > 0) ring.issue(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1, CUT);
+        const F2 less = both(-one[0] * over), flat = both(-one[1] * over);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = add2(s[k], less);
+        keep_columns(s, c, D);
+        p0 = p1 = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            p0 = fma2(s[k], s[k], p0);
+            p1 = fma2(t[k], s[k], p1);
+        }
+        float two[2] = {both_halves(p0), both_halves(p1)};
+        place_sum<WARPS, 2>(two, red[turn & 1][1]);
+        const float rs = rsqrtf(fmaf(two[0], over, a.eps));
+        const F2 rstd = both(rs), back = both(-two[1] * over * rs * rs);
+        pairs<IO, 8>(dr ? ring_vector<IO, CUT>(ring.at(stage, 2), tid, c, D, dr + row * D, copied)
+                        : load8((const IO*)nullptr, 0, false), o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[k] = fma2(rstd, fma2(s[k], back, add2(t[k], flat)), o[k]);
+            dw[k] = fma2(g[k], mul2(s[k], rstd), dw[k]);
+            db[k] = add2(db[k], g[k]);
+        }
+        store_pairs(dx + row * D, o, c, D);
         if (++stage == stages) stage = 0, phase ^= 1;
-        const float mean = one[0] / (float)D, flat = one[1] / (float)D;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] -= mean;
-        if (c < 0 || c + 8 > D)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < 0 || c + j >= D) s[j] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            two[0] = fmaf(s[j], s[j], two[0]);
-            two[1] = fmaf(wf[j] * g[j], s[j], two[1]);
-        }
-        place_sum<TPR, 2>(two, red[turn & 1][1]);
-        const float rstd = rsqrtf(two[0] / (float)D + a.eps), back = two[1] / (float)D * rstd * rstd;
-        widen(er, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            o[j] = fmaf(rstd, fmaf(-s[j], back, fmaf(wf[j], g[j], -flat)), o[j]);
-            dw[j] = fmaf(g[j], s[j] * rstd, dw[j]);
-            db[j] += g[j];
-        }
-        store_cut(dx + row * D, o, c, D, true);
     }
     // the places' sums, one after another
     __syncthreads();
@@ -267,8 +296,12 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
     for (int p = 0; p < P; ++p) {
         if (place == p)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j >= 0 && c + j < D) sums[c + j] += dw[j], sums[D + c + j] += db[j];
+            for (int k = 0; k < 4; ++k) {
+                const float2 fw = unpack2(dw[k]), fb = unpack2(db[k]);
+                const int at = c + 2 * k;
+                if (at >= 0 && at < D) sums[at] += fw.x, sums[D + at] += fb.x;
+                if (at + 1 >= 0 && at + 1 < D) sums[at + 1] += fw.y, sums[D + at + 1] += fb.y;
+            }
         __syncthreads();
     }
     for (int i = threadIdx.x; i < 2 * D; i += NT) partial[(int64_t)blockIdx.x * 2 * D + i] = sums[i];
@@ -437,25 +470,32 @@ bool on_16(std::initializer_list<const void*> ps, int64_t row_bytes) {
     return vec;
 }
 
-// How rows go through the ring: threads of a row (0: they do not), stages, bytes of a row in shared memory.
+// How rows go through the ring: warps of a row (0: they do not), stages, bytes of a row in shared memory.
 struct RingPlan {
-    int tpr, stages;
-    uint32_t pitch;
-    int places() const { return ring_block(tpr) / tpr; }
-    int bytes(int tensors) const { return places() * stages * tensors * (int)pitch; }
+    int warps = 0, stages = 0;
+    uint32_t pitch = 0;
+    int bytes(int tensors) const { return ring_places(warps) * stages * tensors * (int)pitch; }
 };
 // At least three rows for each place of the GPU: below that nothing is ahead.  vpt: vectors a thread.
 RingPlan ring_plan(const NormArgs& a, int tensors, int vpt) {
-    RingPlan p{0, 0, 0};
-    const int e = a.io == GDR_F32 ? 4 : 2, v = vectors_of(a);
+    RingPlan p;
+    const int e = a.io == GDR_F32 ? 4 : 2, need = (vectors_of(a) + 32 * vpt - 1) / (32 * vpt);
     if (a.D * e < 256) return p;              // copies of a few lines each take longer than loads
-    p.tpr = 32;
-    while (p.tpr < 1024 && p.tpr * vpt < v) p.tpr *= 2;
-    if (p.tpr * vpt < v || a.rows < 3 * p.places() * kSms) return RingPlan{0, 0, 0};
+    for (int w : {1, 2, 3, 4, 6, 8, 12, 16, 32})
+        if (w >= need && !p.warps) p.warps = w;
+    if (!p.warps) return p;
+    const int places = ring_places(p.warps);
     p.pitch = (uint32_t)((a.D * e + 15 + 16 + 15) / 16 * 16);
-    p.stages = std::min<int>(kMaxStages, kRingBytes / (p.places() * tensors * (int)p.pitch));
-    if (p.stages < 2) p.tpr = 0;
+    p.stages = std::min<int>(kMaxStages, kRingBytes / (places * tensors * (int)p.pitch));
+    if (p.stages < 2 || a.rows < 3 * places * kSms) return RingPlan();
     return p;
+}
+template <typename F> cudaError_t ring_warps(int warps, F f) {
+#define GDR_WARPS(W) \
+    if (warps == W) return f(std::integral_constant<int, W>());
+    GDR_WARPS(1) GDR_WARPS(2) GDR_WARPS(3) GDR_WARPS(4) GDR_WARPS(6) GDR_WARPS(8) GDR_WARPS(12) GDR_WARPS(16) GDR_WARPS(32)
+#undef GDR_WARPS
+    return cudaErrorInvalidValue;
 }
 // Whether every row starts on a 16-byte boundary (1), or all tensors are contiguous from one on (2).
 int ring_rows(const NormArgs& a, std::initializer_list<RowTensor> in, std::initializer_list<const void*> contiguous) {
@@ -472,13 +512,6 @@ int ring_rows(const NormArgs& a, std::initializer_list<RowTensor> in, std::initi
     }
     return whole ? 1 : cut ? 2 : 0;
 }
-template <typename F> cudaError_t ring_threads(int tpr, F f) {
-#define GDR_TPR(T) \
-    if (tpr == T) return f(std::integral_constant<int, T>());
-    GDR_TPR(32) GDR_TPR(64) GDR_TPR(128) GDR_TPR(256) GDR_TPR(512) GDR_TPR(1024)
-#undef GDR_TPR
-    return cudaErrorInvalidValue;
-}
 template <typename F> cudaError_t io_type(int io, F f) {
     if (io == GDR_F32) return f(float());
     if (io == GDR_BF16) return f(__nv_bfloat16());
@@ -491,22 +524,22 @@ cudaError_t layernorm_forward(const NormArgs& a, RowTensor x, RowTensor res, con
                               void* r, cudaStream_t s) {
     const int vpt = a.io == GDR_F32 ? 1 : 2, rows = ring_rows(a, {x, res}, {y, r});
     const RingPlan plan = ring_plan(a, 2, vpt);
-    if (rows && plan.tpr) {
+    if (rows && plan.warps) {
         unsigned* err = nullptr;
         if (cudaError_t e = device_error_ptr(&err)) return e;
-        return ring_threads(plan.tpr, [&](auto tpr) {
+        return ring_warps(plan.warps, [&](auto warps) {
             return io_type(a.io, [&](auto io) {
                 using IO = decltype(io);
-                constexpr int T = decltype(tpr)::value, V = sizeof(IO) == 4 ? 1 : 2;
+                constexpr int W = decltype(warps)::value, V = sizeof(IO) == 4 ? 1 : 2;
                 const auto go = [&](auto kernel) {
                     const int bytes = plan.bytes(2);
                     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
                         return e;
-                    kernel<<<kSms, ring_block(T), bytes, s>>>(a, x, res, (const IO*)w, (const IO*)b, (IO*)y, (IO*)r,
-                                                             plan.stages, plan.pitch, on_16({w, b}, 16), err);
+                    kernel<<<kSms, ring_places(W) * W * 32, bytes, s>>>(a, x, res, (const IO*)w, (const IO*)b, (IO*)y, (IO*)r,
+                                                                        plan.stages, plan.pitch, on_16({w, b}, 16), err);
                     return cudaGetLastError();
                 };
-                return rows == 1 ? go(layernorm_ring_kernel<IO, T, V, false>) : go(layernorm_ring_kernel<IO, T, V, true>);
+                return rows == 1 ? go(layernorm_ring_kernel<IO, W, V, false>) : go(layernorm_ring_kernel<IO, W, V, true>);
             });
         });
     }
@@ -523,7 +556,7 @@ cudaError_t layernorm_forward(const NormArgs& a, RowTensor x, RowTensor res, con
 
 int64_t layernorm_partial_rows(const NormArgs& a) {      // of either way: which it is depends on the pointers
     const Shape h = shape_of(a.D);
-    return std::max<int64_t>(ring_plan(a, 3, 1).tpr ? kSms : 0, grid_of(a, h) * (h.tpr < 128 ? 128 / h.tpr : 1));
+    return std::max<int64_t>(ring_plan(a, 3, 1).warps ? kSms : 0, grid_of(a, h) * (h.tpr < 128 ? 128 / h.tpr : 1));
 }
 
 cudaError_t layernorm_backward(const NormArgs& a, const void* dy, const void* r, const void* w, const void* dr, void* dx,
@@ -531,23 +564,24 @@ cudaError_t layernorm_backward(const NormArgs& a, const void* dy, const void* r,
     const RowTensor none{nullptr, 0, false};
     const int rows = ring_rows(a, {none}, {dy, r, dr, dx});
     const RingPlan plan = ring_plan(a, 3, 1);
-    if (rows && plan.tpr) {
+    if (rows && plan.warps) {
         unsigned* err = nullptr;
         if (cudaError_t e = device_error_ptr(&err)) return e;
-        const cudaError_t e = ring_threads(plan.tpr, [&](auto tpr) {
+        const cudaError_t e = ring_warps(plan.warps, [&](auto warps) {
             return io_type(a.io, [&](auto io) {
                 using IO = decltype(io);
-                constexpr int T = decltype(tpr)::value;
+                constexpr int W = decltype(warps)::value;
                 const auto go = [&](auto kernel) {
                     const int bytes = std::max(plan.bytes(3), 8 * a.D);
                     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
                         return e;
-                    kernel<<<kSms, ring_block(T), bytes, s>>>(a, (const IO*)dy, (const IO*)r, (const IO*)w, (const IO*)dr,
-                                                             (IO*)dx, partial, plan.stages, plan.pitch, on_16({w}, 16), err);
+                    kernel<<<kSms, ring_places(W) * W * 32, bytes, s>>>(a, (const IO*)dy, (const IO*)r, (const IO*)w,
+                                                                        (const IO*)dr, (IO*)dx, partial, plan.stages,
+                                                                        plan.pitch, on_16({w}, 16), err);
                     return cudaGetLastError();
                 };
-                return rows == 1 ? go(layernorm_backward_ring_kernel<IO, T, false>)
-                                 : go(layernorm_backward_ring_kernel<IO, T, true>);
+                return rows == 1 ? go(layernorm_backward_ring_kernel<IO, W, false>)
+                                 : go(layernorm_backward_ring_kernel<IO, W, true>);
             });
         });
         if (e != cudaSuccess) return e;
