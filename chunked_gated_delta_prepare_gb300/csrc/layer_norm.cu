@@ -18,9 +18,11 @@ namespace {
 //
 // A block an SM: its threads make up places of `tpr` threads, each working on rows of its own with one ring of stages for
 // their inputs, so that the barriers of one row hold up no other.  The rows' copies are in flight whatever the threads wait
-// for.  Up to 384 threads a row a block has at most 768 (80 registers each), above that 1024.
+// for.
 
 constexpr int kMaxStages = 4, kRingBytes = 200 * 1024;
+constexpr int kForwardWarps = 24, kBackwardWarps = 16;       // of a block: 80 and 128 registers a thread
+constexpr int kBackwardVectors = 2;                          // a thread
 
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(bw::smem_u32(to)),
@@ -28,24 +30,30 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
                  : "memory");
 }
 
-constexpr int ring_most(int warps) { return warps <= 12 ? 24 : 32; }        // warps of a block
-constexpr int ring_places(int warps) { return ring_most(warps) / warps; }
+constexpr int ring_places(int warps, int most) { return (warps <= most ? most : 32) / warps; }
 
 // Sums over a place's WARPS warps; red: [NV][places][WARPS, a multiple of 4], zero where there is no warp, not used again
 // before another barrier of the place.
-template <int WARPS> constexpr int kRedSlots = ring_places(WARPS) * ((WARPS + 3) / 4 * 4);
-template <int WARPS, int NV>
-__device__ __forceinline__ void place_sum(float (&v)[NV], float (*red)[kRedSlots<WARPS>]) {
+template <int WARPS, int P> constexpr int kRedSlots = P * ((WARPS + 3) / 4 * 4);
+template <int WARPS, int NV, int SLOTS> __device__ __forceinline__ void place_sum(float (&v)[NV], float (*red)[SLOTS]) {
+    static_assert(NV == 1 || NV == 2, "one sum a lane, or one a half of the warp");
+    const int lane = threadIdx.x & 31;
+    float sum = v[0];
+    if (NV == 2) {                                          // the halves take a sum each
+        const bool second = lane & 16;
+        sum = second ? v[NV - 1] : v[0];
+        sum += __shfl_xor_sync(0xffffffffu, second ? v[0] : v[NV - 1], 16);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = NV == 2 ? 8 : 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (WARPS == 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (WARPS == 1) return;
+        for (int i = 0; i < NV; ++i) v[i] = NV == 1 ? sum : __shfl_sync(0xffffffffu, sum, 16 * i);
+        return;
+    }
     constexpr int slots = (WARPS + 3) / 4 * 4;
     const int warp = threadIdx.x / 32, place = warp / WARPS;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) red[i][place * slots + warp % WARPS] = v[i];
+    if (lane % (32 / NV) == 0) red[lane / (32 / NV)][place * slots + warp % WARPS] = sum;
     bw::named_bar_sync(place + 1, WARPS * 32);              // 0 is the block's; at most 12 places of two warps and more
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -139,16 +147,16 @@ template <typename IO> __device__ __forceinline__ void store_pairs(IO* row, cons
 }
 
 template <typename IO, int WARPS, int VPT, bool CUT>
-__global__ void __launch_bounds__(ring_places(WARPS) * WARPS * 32, 1)
+__global__ void __launch_bounds__(ring_places(WARPS, kForwardWarps) * WARPS * 32, 1)
 layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restrict__ w, const IO* __restrict__ b,
                       IO* __restrict__ y, IO* __restrict__ r, int stages, uint32_t pitch, bool vec_w,
                       unsigned* err) {
-    constexpr int P = ring_places(WARPS), tpr = WARPS * 32, NT = P * tpr;
+    constexpr int P = ring_places(WARPS, kForwardWarps), tpr = WARPS * 32, NT = P * tpr;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ __align__(16) float red[2][2][1][kRedSlots<WARPS>];
+    __shared__ __align__(16) float red[2][2][1][kRedSlots<WARPS, P>];
     __shared__ uint64_t full[P][kMaxStages];
     const int tid = threadIdx.x % tpr, place = threadIdx.x / tpr, D = a.D;
-    for (int i = threadIdx.x; i < 4 * kRedSlots<WARPS>; i += NT) (&red[0][0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < 4 * kRedSlots<WARPS, P>; i += NT) (&red[0][0][0][0])[i] = 0.f;
     if (threadIdx.x == 0) {
         for (int i = 0; i < P * kMaxStages; ++i) bw::mbar_init(&full[0][0] + i, 1);
         bw::fence_mbar_init();
@@ -216,18 +224,18 @@ layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restri
     }
 }
 
-// One vector a thread, whose sums of dw and db stay in registers; a block leaves one row of partial sums [2 D].
-template <typename IO, int WARPS, bool CUT>
-__global__ void __launch_bounds__(ring_places(WARPS) * WARPS * 32, 1)
+// The sums of dw and db stay in registers; a block leaves one row of partial sums [2 D].
+template <typename IO, int WARPS, int VPT, bool CUT>
+__global__ void __launch_bounds__(ring_places(WARPS, kBackwardWarps) * WARPS * 32, 1)
 layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* __restrict__ r, const IO* __restrict__ w,
                                const IO* __restrict__ dr, IO* __restrict__ dx, float* __restrict__ partial, int stages,
                                uint32_t pitch, bool vec_w, unsigned* err) {
-    constexpr int P = ring_places(WARPS), tpr = WARPS * 32, NT = P * tpr;
+    constexpr int P = ring_places(WARPS, kBackwardWarps), tpr = WARPS * 32, NT = P * tpr;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ __align__(16) float red[2][2][2][kRedSlots<WARPS>];
+    __shared__ __align__(16) float red[2][2][2][kRedSlots<WARPS, P>];
     __shared__ uint64_t full[P][kMaxStages];
     const int tid = threadIdx.x % tpr, place = threadIdx.x / tpr, D = a.D;
-    for (int i = threadIdx.x; i < 8 * kRedSlots<WARPS>; i += NT) (&red[0][0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < 8 * kRedSlots<WARPS, P>; i += NT) (&red[0][0][0][0])[i] = 0.f;
     if (threadIdx.x == 0) {
         for (int i = 0; i < P * kMaxStages; ++i) bw::mbar_init(&full[0][0] + i, 1);
         bw::fence_mbar_init();
@@ -238,54 +246,72 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
                            full[place]};
     if (tid == 0)
         for (int k = 0; k < stages; ++k) ring.issue(first + k * step, k, CUT);
-    const int shift = CUT ? first_shift<IO>(first, D) : 0, c = tid * 8 - shift;
-    const Raw8<IO> wr = load_cut(w, c, D, vec_w && shift == 0);
-    F2 dw[4], db[4];
+    const int shift = CUT ? first_shift<IO>(first, D) : 0;
+    Raw8<IO> wr[VPT];
+    F2 dw[VPT][4], db[VPT][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) dw[k] = db[k] = both(0.f);
+    for (int i = 0; i < VPT; ++i) {
+        wr[i] = load_cut(w, (tid + i * tpr) * 8 - shift, D, vec_w && shift == 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dw[i][k] = db[i][k] = both(0.f);
+    }
     const float over = 1.f / (float)D;
     int stage = 0, phase = 0, turn = 0;
     for (int64_t row = first; row < a.rows; row += step, ++turn) {
         bw::mbar_wait(full[place] + stage, phase, err, kDeviceErrTimeout);
         const int copied = CUT ? ring.copied(row) : 0;
-        F2 g[4], s[4], t[4], o[4];
-        pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 0), tid, c, D, dy + row * D, copied), g);
-        pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 1), tid, c, D, r + row * D, copied), s);
-        pairs<IO, 8>(wr, t);
-        F2 p0 = both(0.f), p1 = both(0.f);
+        F2 g[VPT][4], s[VPT][4], p0 = both(0.f), p1 = both(0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            t[k] = mul2(t[k], g[k]);                         // w dy
-            p0 = add2(p0, s[k]);
-            p1 = add2(p1, t[k]);
+        for (int i = 0; i < VPT; ++i) {
+            const int n = tid + i * tpr, c = n * 8 - shift;
+            F2 wf[4];
+            pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 0), n, c, D, dy + row * D, copied), g[i]);
+            pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 1), n, c, D, r + row * D, copied), s[i]);
+            pairs<IO, 8>(wr[i], wf);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                p0 = add2(p0, s[i][k]);
+                p1 = fma2(wf[k], g[i][k], p1);
+            }
         }
         float one[2] = {both_halves(p0), both_halves(p1)};
         place_sum<WARPS, 2>(one, red[turn & 1][0]);
         // every thread is done with the row before: its stage is free
         if (tid == 0 && turn > 0) ring.issue(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1, CUT);
         const F2 less = both(-one[0] * over), flat = both(-one[1] * over);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] = add2(s[k], less);
-        keep_columns(s, c, D);
         p0 = p1 = both(0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            p0 = fma2(s[k], s[k], p0);
-            p1 = fma2(t[k], s[k], p1);
+        for (int i = 0; i < VPT; ++i) {
+            F2 wf[4];
+            pairs<IO, 8>(wr[i], wf);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[i][k] = add2(s[i][k], less);
+            keep_columns(s[i], (tid + i * tpr) * 8 - shift, D);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                p0 = fma2(s[i][k], s[i][k], p0);
+                p1 = fma2(mul2(wf[k], g[i][k]), s[i][k], p1);
+            }
         }
         float two[2] = {both_halves(p0), both_halves(p1)};
         place_sum<WARPS, 2>(two, red[turn & 1][1]);
         const float rs = rsqrtf(fmaf(two[0], over, a.eps));
         const F2 rstd = both(rs), back = both(-two[1] * over * rs * rs);
-        pairs<IO, 8>(dr ? ring_vector<IO, CUT>(ring.at(stage, 2), tid, c, D, dr + row * D, copied)
-                        : load8((const IO*)nullptr, 0, false), o);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            o[k] = fma2(rstd, fma2(s[k], back, add2(t[k], flat)), o[k]);
-            dw[k] = fma2(g[k], mul2(s[k], rstd), dw[k]);
-            db[k] = add2(db[k], g[k]);
+        for (int i = 0; i < VPT; ++i) {
+            const int n = tid + i * tpr, c = n * 8 - shift;
+            F2 wf[4], o[4];
+            pairs<IO, 8>(wr[i], wf);
+            pairs<IO, 8>(dr ? ring_vector<IO, CUT>(ring.at(stage, 2), n, c, D, dr + row * D, copied)
+                            : load8((const IO*)nullptr, 0, false), o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o[k] = fma2(rstd, fma2(s[i][k], back, fma2(wf[k], g[i][k], flat)), o[k]);
+                dw[i][k] = fma2(g[i][k], mul2(s[i][k], rstd), dw[i][k]);
+                db[i][k] = add2(db[i][k], g[i][k]);
+            }
+            store_pairs(dx + row * D, o, c, D);
         }
-        store_pairs(dx + row * D, o, c, D);
         if (++stage == stages) stage = 0, phase ^= 1;
     }
     // the places' sums, one after another
@@ -296,12 +322,14 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
     for (int p = 0; p < P; ++p) {
         if (place == p)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 fw = unpack2(dw[k]), fb = unpack2(db[k]);
-                const int at = c + 2 * k;
-                if (at >= 0 && at < D) sums[at] += fw.x, sums[D + at] += fb.x;
-                if (at + 1 >= 0 && at + 1 < D) sums[at + 1] += fw.y, sums[D + at + 1] += fb.y;
-            }
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 fw = unpack2(dw[i][k]), fb = unpack2(db[i][k]);
+                    const int at = (tid + i * tpr) * 8 - shift + 2 * k;
+                    if (at >= 0 && at < D) sums[at] += fw.x, sums[D + at] += fb.x;
+                    if (at + 1 >= 0 && at + 1 < D) sums[at + 1] += fw.y, sums[D + at + 1] += fb.y;
+                }
         __syncthreads();
     }
     for (int i = threadIdx.x; i < 2 * D; i += NT) partial[(int64_t)blockIdx.x * 2 * D + i] = sums[i];
@@ -474,17 +502,17 @@ bool on_16(std::initializer_list<const void*> ps, int64_t row_bytes) {
 struct RingPlan {
     int warps = 0, stages = 0;
     uint32_t pitch = 0;
-    int bytes(int tensors) const { return ring_places(warps) * stages * tensors * (int)pitch; }
+    int bytes(int tensors, int most) const { return ring_places(warps, most) * stages * tensors * (int)pitch; }
 };
-// At least three rows for each place of the GPU: below that nothing is ahead.  vpt: vectors a thread.
-RingPlan ring_plan(const NormArgs& a, int tensors, int vpt) {
+// At least three rows for each place of the GPU: below that nothing is ahead.  vpt: vectors a thread; most: a block's warps.
+RingPlan ring_plan(const NormArgs& a, int tensors, int vpt, int most) {
     RingPlan p;
     const int e = a.io == GDR_F32 ? 4 : 2, need = (vectors_of(a) + 32 * vpt - 1) / (32 * vpt);
     if (a.D * e < 256) return p;              // copies of a few lines each take longer than loads
     for (int w : {1, 2, 3, 4, 6, 8, 12, 16, 32})
         if (w >= need && !p.warps) p.warps = w;
     if (!p.warps) return p;
-    const int places = ring_places(p.warps);
+    const int places = ring_places(p.warps, most);
     p.pitch = (uint32_t)((a.D * e + 15 + 16 + 15) / 16 * 16);
     p.stages = std::min<int>(kMaxStages, kRingBytes / (places * tensors * (int)p.pitch));
     if (p.stages < 2 || a.rows < 3 * places * kSms) return RingPlan();
@@ -523,7 +551,7 @@ template <typename F> cudaError_t io_type(int io, F f) {
 cudaError_t layernorm_forward(const NormArgs& a, RowTensor x, RowTensor res, const void* w, const void* b, void* y,
                               void* r, cudaStream_t s) {
     const int vpt = a.io == GDR_F32 ? 1 : 2, rows = ring_rows(a, {x, res}, {y, r});
-    const RingPlan plan = ring_plan(a, 2, vpt);
+    const RingPlan plan = ring_plan(a, 2, vpt, kForwardWarps);
     if (rows && plan.warps) {
         unsigned* err = nullptr;
         if (cudaError_t e = device_error_ptr(&err)) return e;
@@ -532,10 +560,10 @@ cudaError_t layernorm_forward(const NormArgs& a, RowTensor x, RowTensor res, con
                 using IO = decltype(io);
                 constexpr int W = decltype(warps)::value, V = sizeof(IO) == 4 ? 1 : 2;
                 const auto go = [&](auto kernel) {
-                    const int bytes = plan.bytes(2);
+                    const int bytes = plan.bytes(2, kForwardWarps);
                     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
                         return e;
-                    kernel<<<kSms, ring_places(W) * W * 32, bytes, s>>>(a, x, res, (const IO*)w, (const IO*)b, (IO*)y, (IO*)r,
+                    kernel<<<kSms, ring_places(W, kForwardWarps) * W * 32, bytes, s>>>(a, x, res, (const IO*)w, (const IO*)b, (IO*)y, (IO*)r,
                                                                         plan.stages, plan.pitch, on_16({w, b}, 16), err);
                     return cudaGetLastError();
                 };
@@ -556,14 +584,14 @@ cudaError_t layernorm_forward(const NormArgs& a, RowTensor x, RowTensor res, con
 
 int64_t layernorm_partial_rows(const NormArgs& a) {      // of either way: which it is depends on the pointers
     const Shape h = shape_of(a.D);
-    return std::max<int64_t>(ring_plan(a, 3, 1).warps ? kSms : 0, grid_of(a, h) * (h.tpr < 128 ? 128 / h.tpr : 1));
+    return std::max<int64_t>(ring_plan(a, 3, kBackwardVectors, kBackwardWarps).warps ? kSms : 0, grid_of(a, h) * (h.tpr < 128 ? 128 / h.tpr : 1));
 }
 
 cudaError_t layernorm_backward(const NormArgs& a, const void* dy, const void* r, const void* w, const void* dr, void* dx,
                                float* dw, float* db, float* partial, cudaStream_t s) {
     const RowTensor none{nullptr, 0, false};
     const int rows = ring_rows(a, {none}, {dy, r, dr, dx});
-    const RingPlan plan = ring_plan(a, 3, 1);
+    const RingPlan plan = ring_plan(a, 3, kBackwardVectors, kBackwardWarps);
     if (rows && plan.warps) {
         unsigned* err = nullptr;
         if (cudaError_t e = device_error_ptr(&err)) return e;
@@ -572,16 +600,16 @@ cudaError_t layernorm_backward(const NormArgs& a, const void* dy, const void* r,
                 using IO = decltype(io);
                 constexpr int W = decltype(warps)::value;
                 const auto go = [&](auto kernel) {
-                    const int bytes = std::max(plan.bytes(3), 8 * a.D);
+                    const int bytes = std::max(plan.bytes(3, kBackwardWarps), 8 * a.D);
                     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
                         return e;
-                    kernel<<<kSms, ring_places(W) * W * 32, bytes, s>>>(a, (const IO*)dy, (const IO*)r, (const IO*)w,
+                    kernel<<<kSms, ring_places(W, kBackwardWarps) * W * 32, bytes, s>>>(a, (const IO*)dy, (const IO*)r, (const IO*)w,
                                                                         (const IO*)dr, (IO*)dx, partial, plan.stages,
                                                                         plan.pitch, on_16({w}, 16), err);
                     return cudaGetLastError();
                 };
-                return rows == 1 ? go(layernorm_backward_ring_kernel<IO, W, false>)
-                                 : go(layernorm_backward_ring_kernel<IO, W, true>);
+                return rows == 1 ? go(layernorm_backward_ring_kernel<IO, W, kBackwardVectors, false>)
+                                 : go(layernorm_backward_ring_kernel<IO, W, kBackwardVectors, true>);
             });
         });
         if (e != cudaSuccess) return e;
