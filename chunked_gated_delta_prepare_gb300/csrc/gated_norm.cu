@@ -27,53 +27,91 @@ template <int TPR> __device__ __forceinline__ void sum_row(float (&v)[1], float*
     }
 }
 
-// f(z) and its slope.
-template <bool SILU> __device__ __forceinline__ float gate_of(float z) { return SILU ? z * sigmoid(z) : sigmoid(z); }
-template <bool SILU> __device__ __forceinline__ float2 gate_and_slope(float z) {
-    // with e = e^-|z| <= 1 both sigmoid(z) and 1 - sigmoid(z) keep their relative accuracy
-    const float e = ex2(-fabsf(z) * kLog2e), p = rcp(1.f + e), q = e * p;
-    const float s = z < 0.f ? q : p, rest = z < 0.f ? p : q;
-    return SILU ? make_float2(z * s, s * fmaf(z, rest, 1.f)) : make_float2(s, s * rest);
+// f(z) of two, and its slope: with e = e^-|z| <= 1 both sigmoid(z) and 1 - sigmoid(z) keep their relative accuracy.
+template <bool SILU> __device__ __forceinline__ F2 gate2(F2 z) { return SILU ? silu2(z) : sigmoid2(z); }
+template <bool SILU> __device__ __forceinline__ void gate_and_slope2(F2 z, F2& f, F2& slope) {
+    const float2 v = unpack2(z);
+    const F2 e = pack2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+    const F2 large = rcp_2(add2(both(1.f), e)), small = mul2(e, large);
+    const float2 l = unpack2(large), q = unpack2(small);
+    const F2 s = pack2(v.x < 0.f ? q.x : l.x, v.y < 0.f ? q.y : l.y);
+    const F2 rest = pack2(v.x < 0.f ? l.x : q.x, v.y < 0.f ? l.y : q.y);
+    f = SILU ? mul2(z, s) : s;
+    slope = SILU ? mul2(s, fma2(z, rest, both(1.f))) : mul2(s, rest);
 }
+__device__ __forceinline__ float both_halves(F2 v) {
+    const float2 f = unpack2(v);
+    return f.x + f.y;
+}
+template <typename IO> __device__ __forceinline__ void store_pairs(IO* p, const F2 (&v)[4], int left, bool vec) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2(v[k]);
+        x[2 * k] = f.x, x[2 * k + 1] = f.y;
+    }
+    store_n(p, x, left, vec);
+}
+
+// Rows of one place that are loaded together: what the threads have in flight is what counts.
+template <int TPR, int VPT> constexpr int kTogether = VPT == 1 && TPR <= 32 ? 2 : 1;
 
 template <typename IO, int TPR, int VPT, bool SILU>
 __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
 gated_norm_forward_kernel(GatedNormArgs a, Places pl, RowTensor x, RowTensor z, const IO* __restrict__ w,
                           IO* __restrict__ y, bool vec_w, bool vec_y) {
-    constexpr int NT = TPR > kThreads ? TPR : kThreads, RPB = NT / TPR;
+    constexpr int NT = TPR > kThreads ? TPR : kThreads, RPB = NT / TPR, U = kTogether<TPR, VPT>;
     __shared__ float red[2 * 32];
     const int tid = threadIdx.x % TPR, V = a.V;
     const int64_t place = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     const int head = (int)(place % a.H);
     const int64_t token0 = place / a.H;
     const IO* wp = w + (a.per_head ? (int64_t)head * V : 0);
-    for (int64_t turn = 0; turn < pl.turns; ++turn) {
-        const int64_t token = token0 + turn * pl.step;
-        const bool live = place < pl.count && token < a.tokens;
-        float v[VPT][8], sum[1] = {0.f};
+    Raw8<IO> wr[VPT];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8;
-            widen(load8((const IO*)x.p + token * x.ld + (int64_t)head * V + c, live ? V - c : 0, x.vec, c), v[i]);
+    for (int i = 0; i < VPT; ++i) wr[i] = load8(wp + (tid + i * TPR) * 8, V - (tid + i * TPR) * 8, vec_w, (tid + i * TPR) * 8);
+    const float over = 1.f / (float)V;
+    for (int64_t turn = 0; turn < pl.turns; turn += U) {
+        Raw8<IO> xr[U][VPT], zr[U][VPT];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t token = token0 + (turn + u) * pl.step;
+            const bool live = place < pl.count && token < a.tokens;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (tid + i * TPR) * 8, left = live ? V - c : 0;
+                xr[u][i] = load8((const IO*)x.p + token * x.ld + (int64_t)head * V + c, left, x.vec, c);
+                zr[u][i] = load8((const IO*)z.p + token * z.ld + (int64_t)head * V + c, left, z.vec, c);
+            }
         }
-        sum_row<TPR>(sum, red, (int)turn);
-        const float rstd = rsqrtf(sum[0] / (float)V + a.eps);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8;
-            float zf[8], wf[8];
-            widen(load8((const IO*)z.p + token * z.ld + (int64_t)head * V + c, live ? V - c : 0, z.vec, c), zf);
-            widen(load8(wp + c, V - c, vec_w, c), wf);
+        for (int u = 0; u < U; ++u) {
+            const int64_t token = token0 + (turn + u) * pl.step;
+            const bool live = place < pl.count && token < a.tokens;
+            F2 v[VPT][4], part = both(0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * wf[j] * gate_of<SILU>(zf[j]);
-            store_n(y + (token * a.H + head) * V + c, v[i], live ? V - c : 0, vec_y);
+            for (int i = 0; i < VPT; ++i) {
+                pairs<IO, 8>(xr[u][i], v[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) part = fma2(v[i][k], v[i][k], part);
+            }
+            float sum[1] = {both_halves(part)};
+            sum_row<TPR>(sum, red, (int)turn + u);
+            const F2 rstd = both(rsqrtf(fmaf(sum[0], over, a.eps)));
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (tid + i * TPR) * 8;
+                F2 zf[4], wf[4];
+                pairs<IO, 8>(zr[u][i], zf), pairs<IO, 8>(wr[i], wf);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[i][k] = mul2(mul2(mul2(v[i][k], rstd), wf[k]), gate2<SILU>(zf[k]));
+                store_pairs(y + (token * a.H + head) * V + c, v[i], live ? V - c : 0, vec_y);
+            }
         }
     }
 }
 
-// partial: a row of V sums for each place.
+// partial: a row of V sums for each place, or (one weight for all heads, rows of up to a warp) for each block.
 template <typename IO, int TPR, int VPT, bool SILU>
 __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
 gated_norm_backward_kernel(GatedNormArgs a, Places pl, const IO* __restrict__ dy, RowTensor x, RowTensor z,
@@ -86,57 +124,97 @@ gated_norm_backward_kernel(GatedNormArgs a, Places pl, const IO* __restrict__ dy
     const int head = (int)(place % a.H);
     const int64_t token0 = place / a.H;
     const IO* wp = w + (a.per_head ? (int64_t)head * V : 0);
-    float dw[VPT][8];
+    Raw8<IO> wr[VPT], xr[VPT], zr[VPT], gr[VPT];
+    F2 dw[VPT][4];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+        wr[i] = load8(wp + (tid + i * TPR) * 8, V - (tid + i * TPR) * 8, vec_w, (tid + i * TPR) * 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+        for (int k = 0; k < 4; ++k) dw[i][k] = both(0.f);
+    }
+    const float over = 1.f / (float)V;
+    const auto load = [&](int64_t turn) {
+        const int64_t token = token0 + turn * pl.step;
+        const bool live = place < pl.count && token < a.tokens;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (tid + i * TPR) * 8, left = live ? V - c : 0;
+            xr[i] = load8((const IO*)x.p + token * x.ld + (int64_t)head * V + c, left, x.vec, c);
+            zr[i] = load8((const IO*)z.p + token * z.ld + (int64_t)head * V + c, left, z.vec, c);
+            gr[i] = load8(dy + (token * a.H + head) * V + c, left, vec, c);
+        }
+    };
+    load(0);
     for (int64_t turn = 0; turn < pl.turns; ++turn) {
         const int64_t token = token0 + turn * pl.step;
         const bool live = place < pl.count && token < a.tokens;
-        Raw8<IO> xr[VPT], zr[VPT], gr[VPT], wr[VPT];
-        float sq[1] = {0.f}, dot[1] = {0.f};
+        F2 xf[VPT][4], gw[VPT][4], f[VPT][4], slope[VPT][4], p0 = both(0.f), p1 = both(0.f);
+        Raw8<IO> now[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (tid + i * TPR) * 8, left = live ? V - c : 0;
-            const int64_t at = (token * a.H + head) * V + c;
-            xr[i] = load8((const IO*)x.p + token * x.ld + (int64_t)head * V + c, left, x.vec, c);
-            zr[i] = load8((const IO*)z.p + token * z.ld + (int64_t)head * V + c, left, z.vec, c);
-            gr[i] = load8(dy + at, left, vec, c);
-            wr[i] = load8(wp + c, V - c, vec_w, c);
-            float xf[8], zf[8], gf[8], wf[8];
-            widen(xr[i], xf), widen(zr[i], zf), widen(gr[i], gf), widen(wr[i], wf);
+            F2 zf[4], wf[4];
+            now[i] = gr[i];
+            pairs<IO, 8>(xr[i], xf[i]), pairs<IO, 8>(zr[i], zf), pairs<IO, 8>(gr[i], gw[i]), pairs<IO, 8>(wr[i], wf);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sq[0] = fmaf(xf[j], xf[j], sq[0]);
-                dot[0] = fmaf(gf[j] * wf[j] * gate_of<SILU>(zf[j]), xf[j], dot[0]);
+            for (int k = 0; k < 4; ++k) {
+                gate_and_slope2<SILU>(zf[k], f[i][k], slope[i][k]);
+                gw[i][k] = mul2(gw[i][k], wf[k]);
+                p0 = fma2(xf[i][k], xf[i][k], p0);
+                p1 = fma2(mul2(gw[i][k], f[i][k]), xf[i][k], p1);
             }
         }
+        if (turn + 1 < pl.turns) load(turn + 1);             // on their way while this row is worked on
+        float sq[1] = {both_halves(p0)}, dot[1] = {both_halves(p1)};
         sum_row<TPR>(sq, red[0], (int)turn);
         sum_row<TPR>(dot, red[1], (int)turn);
-        const float rstd = rsqrtf(sq[0] / (float)V + a.eps), back = dot[0] / (float)V * rstd * rstd;
+        const float rs = rsqrtf(fmaf(sq[0], over, a.eps));
+        const F2 rstd = both(rs), back = both(-dot[0] * over * rs * rs);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (tid + i * TPR) * 8, left = live ? V - c : 0;
             const int64_t at = (token * a.H + head) * V + c;
-            float xf[8], zf[8], gf[8], wf[8], o[8], oz[8];
-            widen(xr[i], xf), widen(zr[i], zf), widen(gr[i], gf), widen(wr[i], wf);
+            F2 g[4], o[4], oz[4];
+            pairs<IO, 8>(now[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = gate_and_slope<SILU>(zf[j]);
-                const float n = xf[j] * rstd, gw = gf[j] * wf[j];
-                o[j] = rstd * fmaf(-xf[j], back, gw * f.x);
-                oz[j] = gw * n * f.y;
-                if (live) dw[i][j] = fmaf(gf[j] * n, f.x, dw[i][j]);
+            for (int k = 0; k < 4; ++k) {
+                const F2 n = mul2(xf[i][k], rstd);
+                o[k] = mul2(rstd, fma2(xf[i][k], back, mul2(gw[i][k], f[i][k])));
+                oz[k] = mul2(mul2(gw[i][k], n), slope[i][k]);
+                dw[i][k] = fma2(mul2(g[k], n), f[i][k], dw[i][k]);          // a row that is not there adds zero
             }
-            store_n(dx + at, o, left, vec);
-            store_n(dz + at, oz, left, vec);
+            store_pairs(dx + at, o, left, vec);
+            store_pairs(dz + at, oz, left, vec);
         }
     }
-    if (place < pl.count)
+    if (TPR <= 32 && !a.per_head) {                          // the block's places, one after another
+        __shared__ float sums[TPR <= 32 ? RPB : 1][TPR <= 32 ? TPR * VPT * 8 : 1];
+        float* mine = sums[threadIdx.x / TPR];
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            store_cut(partial + place * V, dw[i], (tid + i * TPR) * 8, V, (V & 3) == 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 v = unpack2(dw[i][k]);
+                mine[(tid + i * TPR) * 8 + 2 * k] = v.x, mine[(tid + i * TPR) * 8 + 2 * k + 1] = v.y;
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < V; c += NT) {
+            float sum = 0.f;
+#pragma unroll
+            for (int p = 0; p < RPB; ++p) sum += sums[p][c];
+            partial[(int64_t)blockIdx.x * V + c] = sum;
+        }
+    } else if (place < pl.count) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 q = unpack2(dw[i][k]);
+                v[2 * k] = q.x, v[2 * k + 1] = q.y;
+            }
+            store_cut(partial + place * V, v, (tid + i * TPR) * 8, V, (V & 3) == 0);
+        }
+    }
 }
 
 Shape shape_of(int V) {
@@ -174,6 +252,9 @@ template <typename F> cudaError_t with_types(const GatedNormArgs& a, Shape h, F 
     return cudaErrorInvalidValue;
 }
 
+// Rows of a warp at most, one weight for all heads: one for each block.
+bool rows_by_block(const GatedNormArgs& a, Shape h) { return h.tpr <= 32 && !a.per_head; }
+
 // Whether the heads' rows of all these tensors start on 16-byte boundaries.
 bool on_16(std::initializer_list<const void*> ps, int64_t head_bytes) {
     bool vec = head_bytes % 16 == 0;
@@ -198,7 +279,11 @@ cudaError_t gated_norm_forward(const GatedNormArgs& a, RowTensor x, RowTensor z,
     });
 }
 
-int64_t gated_norm_partial_rows(const GatedNormArgs& a) { return places_of(a, shape_of(a.V)).count; }
+int64_t gated_norm_partial_rows(const GatedNormArgs& a) {
+    const Shape h = shape_of(a.V);
+    const int64_t places = places_of(a, h).count, rpb = std::max(h.tpr, kThreads) / h.tpr;
+    return rows_by_block(a, h) ? (places + rpb - 1) / rpb : places;
+}
 
 cudaError_t gated_norm_backward(const GatedNormArgs& a, const void* dy, RowTensor x, RowTensor z, const void* w, void* dx,
                                 void* dz, float* dw, float* partial, cudaStream_t s) {
@@ -217,7 +302,8 @@ cudaError_t gated_norm_backward(const GatedNormArgs& a, const void* dy, RowTenso
     });
     if (e != cudaSuccess) return e;
     const int64_t cols = (int64_t)a.V * (a.per_head ? a.H : 1);
-    return column_sum(partial, p.count * a.V / cols, cols, cols, dw, 0, nullptr, s);
+    const int64_t rows = rows_by_block(a, h) ? gated_norm_partial_rows(a) : p.count * a.V / cols;
+    return column_sum(partial, rows, cols, cols, dw, 0, nullptr, s);
 }
 
 }  // namespace layer
