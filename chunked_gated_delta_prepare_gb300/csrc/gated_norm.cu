@@ -53,11 +53,15 @@ template <typename IO> __device__ __forceinline__ void store_pairs(IO* p, const 
     store_n(p, x, left, vec);
 }
 
+// Blocks an SM that the registers leave room for; the grid is one wave of them.
+constexpr int forward_blocks(int tpr, int vpt) { return tpr > kThreads ? 1 : vpt == 1 ? 4 : 2; }
+constexpr int backward_blocks(int tpr, int vpt) { return tpr > kThreads || vpt > 1 ? 1 : 2; }
+
 // Rows of one place that are loaded together: what the threads have in flight is what counts.
 template <int TPR, int VPT> constexpr int kTogether = VPT == 1 && TPR <= 32 ? 2 : 1;
 
 template <typename IO, int TPR, int VPT, bool SILU>
-__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
+__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, forward_blocks(TPR, VPT))
 gated_norm_forward_kernel(GatedNormArgs a, Places pl, RowTensor x, RowTensor z, const IO* __restrict__ w,
                           IO* __restrict__ y, bool vec_w, bool vec_y) {
     constexpr int NT = TPR > kThreads ? TPR : kThreads, RPB = NT / TPR, U = kTogether<TPR, VPT>;
@@ -113,7 +117,7 @@ gated_norm_forward_kernel(GatedNormArgs a, Places pl, RowTensor x, RowTensor z, 
 
 // partial: a row of V sums for each place, or (one weight for all heads, rows of up to a warp) for each block.
 template <typename IO, int TPR, int VPT, bool SILU>
-__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
+__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, backward_blocks(TPR, VPT))
 gated_norm_backward_kernel(GatedNormArgs a, Places pl, const IO* __restrict__ dy, RowTensor x, RowTensor z,
                            const IO* __restrict__ w, IO* __restrict__ dx, IO* __restrict__ dz,
                            float* __restrict__ partial, bool vec_w, bool vec) {
@@ -224,9 +228,8 @@ Shape shape_of(int V) {
     return {v <= 512 ? 256 : 512, 2};
 }
 
-// Blocks an SM: 4 of 256 threads.
-Places places_of(const GatedNormArgs& a, Shape h) {
-    const int64_t rpb = std::max(h.tpr, kThreads) / h.tpr, most = (int64_t)kSms * 4 * rpb;
+Places places_of(const GatedNormArgs& a, Shape h, int blocks) {
+    const int64_t rpb = std::max(h.tpr, kThreads) / h.tpr, most = (int64_t)kSms * blocks * rpb;
     Places p;
     p.step = std::min<int64_t>(a.tokens, std::max<int64_t>(1, most / a.H));
     p.count = p.step * a.H;
@@ -266,7 +269,7 @@ bool on_16(std::initializer_list<const void*> ps, int64_t head_bytes) {
 
 cudaError_t gated_norm_forward(const GatedNormArgs& a, RowTensor x, RowTensor z, const void* w, void* y, cudaStream_t s) {
     const Shape h = shape_of(a.V);
-    const Places p = places_of(a, h);
+    const Places p = places_of(a, h, forward_blocks(h.tpr, h.vpt));
     return with_types(a, h, [&](auto io, auto tpr, auto vpt, auto silu) {
         using IO = decltype(io);
         constexpr int T = decltype(tpr)::value, NT = T > kThreads ? T : kThreads;
@@ -281,14 +284,14 @@ cudaError_t gated_norm_forward(const GatedNormArgs& a, RowTensor x, RowTensor z,
 
 int64_t gated_norm_partial_rows(const GatedNormArgs& a) {
     const Shape h = shape_of(a.V);
-    const int64_t places = places_of(a, h).count, rpb = std::max(h.tpr, kThreads) / h.tpr;
+    const int64_t places = places_of(a, h, backward_blocks(h.tpr, h.vpt)).count, rpb = std::max(h.tpr, kThreads) / h.tpr;
     return rows_by_block(a, h) ? (places + rpb - 1) / rpb : places;
 }
 
 cudaError_t gated_norm_backward(const GatedNormArgs& a, const void* dy, RowTensor x, RowTensor z, const void* w, void* dx,
                                 void* dz, float* dw, float* partial, cudaStream_t s) {
     const Shape h = shape_of(a.V);
-    const Places p = places_of(a, h);
+    const Places p = places_of(a, h, backward_blocks(h.tpr, h.vpt));
     const cudaError_t e = with_types(a, h, [&](auto io, auto tpr, auto vpt, auto silu) {
         using IO = decltype(io);
         constexpr int T = decltype(tpr)::value, NT = T > kThreads ? T : kThreads;
