@@ -3,7 +3,7 @@
 //   n = x rstd, rstd = 1 / sqrt(mean x^2 + eps),  y = n w f(z),  f = silu or sigmoid
 //   dn = dy w f(z),  dx = rstd (dn - n mean(dn n)),  dz = dy n w f'(z),  dw = sum dy n f(z)
 //
-// Bound: memory.  A row lies on TPR threads (4 to 32 up to 1024 columns, sums by shuffles; a block above), and a row's place
+// Bound: memory.  A row lies on TPR threads (4 to 32 up to 256 columns, sums by shuffles; a block above), and a row's place
 // in the grid keeps its head: the number of places is a multiple of H, so w and the sums of dw stay in registers.
 #include "norm.cuh"
 
@@ -11,7 +11,7 @@ namespace gdr {
 namespace layer {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int block_of(int tpr) { return tpr <= 32 ? 256 : tpr; }      // a row of more than a warp is a block's
 
 struct Places {              // of rows in the grid: place p has head p % H of the tokens p / H + k * step
     int64_t count, step, turns;
@@ -53,18 +53,18 @@ template <typename IO> __device__ __forceinline__ void store_pairs(IO* p, const 
     store_n(p, x, left, vec);
 }
 
-// Blocks an SM that the registers leave room for; the grid is one wave of them.
-constexpr int forward_blocks(int tpr, int vpt) { return tpr > kThreads ? 1 : vpt == 1 ? 4 : 2; }
-constexpr int backward_blocks(int tpr, int vpt) { return tpr > kThreads || vpt > 1 ? 1 : 2; }
+// Blocks an SM that the registers leave room for (64, 128 a thread at one vector); the grid is one wave of them.
+constexpr int forward_blocks(int tpr, int vpt) { return (vpt == 1 ? 1024 : 512) / block_of(tpr); }
+constexpr int backward_blocks(int tpr, int vpt) { return vpt == 1 ? 512 / block_of(tpr) : 1; }
 
 // Rows of one place that are loaded together: what the threads have in flight is what counts.
-template <int TPR, int VPT> constexpr int kTogether = VPT == 1 && TPR <= 32 ? 2 : 1;
+template <int VPT> constexpr int kTogether = VPT == 1 ? 2 : 1;
 
 template <typename IO, int TPR, int VPT, bool SILU>
-__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, forward_blocks(TPR, VPT))
+__global__ void __launch_bounds__(block_of(TPR), forward_blocks(TPR, VPT))
 gated_norm_forward_kernel(GatedNormArgs a, Places pl, RowTensor x, RowTensor z, const IO* __restrict__ w,
                           IO* __restrict__ y, bool vec_w, bool vec_y) {
-    constexpr int NT = TPR > kThreads ? TPR : kThreads, RPB = NT / TPR, U = kTogether<TPR, VPT>;
+    constexpr int NT = block_of(TPR), RPB = NT / TPR, U = kTogether<VPT>;
     __shared__ float red[2 * 32];
     const int tid = threadIdx.x % TPR, V = a.V;
     const int64_t place = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -117,11 +117,11 @@ gated_norm_forward_kernel(GatedNormArgs a, Places pl, RowTensor x, RowTensor z, 
 
 // partial: a row of V sums for each place, or (one weight for all heads, rows of up to a warp) for each block.
 template <typename IO, int TPR, int VPT, bool SILU>
-__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, backward_blocks(TPR, VPT))
+__global__ void __launch_bounds__(block_of(TPR), backward_blocks(TPR, VPT))
 gated_norm_backward_kernel(GatedNormArgs a, Places pl, const IO* __restrict__ dy, RowTensor x, RowTensor z,
                            const IO* __restrict__ w, IO* __restrict__ dx, IO* __restrict__ dz,
                            float* __restrict__ partial, bool vec_w, bool vec) {
-    constexpr int NT = TPR > kThreads ? TPR : kThreads, RPB = NT / TPR;
+    constexpr int NT = block_of(TPR), RPB = NT / TPR;
     __shared__ float red[2][2 * 32];
     const int tid = threadIdx.x % TPR, V = a.V;
     const int64_t place = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -223,13 +223,13 @@ gated_norm_backward_kernel(GatedNormArgs a, Places pl, const IO* __restrict__ dy
 
 Shape shape_of(int V) {
     const int v = (V + 7) / 8;
-    if (v <= 32) return {v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : 32, 1};
-    if (v <= 128) return {32, v <= 64 ? 2 : 4};
+    for (int tpr = 4; tpr <= 256; tpr *= 2)
+        if (v <= tpr) return {tpr, 1};
     return {v <= 512 ? 256 : 512, 2};
 }
 
 Places places_of(const GatedNormArgs& a, Shape h, int blocks) {
-    const int64_t rpb = std::max(h.tpr, kThreads) / h.tpr, most = (int64_t)kSms * blocks * rpb;
+    const int64_t rpb = block_of(h.tpr) / h.tpr, most = (int64_t)kSms * blocks * rpb;
     Places p;
     p.step = std::min<int64_t>(a.tokens, std::max<int64_t>(1, most / a.H));
     p.count = p.step * a.H;
@@ -249,7 +249,7 @@ template <typename F> cudaError_t with_types(const GatedNormArgs& a, Shape h, F 
     };
 #define GDR_SHAPE(T, V) \
     if (h.tpr == T && h.vpt == V) return types(std::integral_constant<int, T>(), std::integral_constant<int, V>());
-    GDR_SHAPE(4, 1) GDR_SHAPE(8, 1) GDR_SHAPE(16, 1) GDR_SHAPE(32, 1) GDR_SHAPE(32, 2) GDR_SHAPE(32, 4)
+    GDR_SHAPE(4, 1) GDR_SHAPE(8, 1) GDR_SHAPE(16, 1) GDR_SHAPE(32, 1) GDR_SHAPE(64, 1) GDR_SHAPE(128, 1) GDR_SHAPE(256, 1)
     GDR_SHAPE(256, 2) GDR_SHAPE(512, 2)
 #undef GDR_SHAPE
     return cudaErrorInvalidValue;
@@ -272,7 +272,7 @@ cudaError_t gated_norm_forward(const GatedNormArgs& a, RowTensor x, RowTensor z,
     const Places p = places_of(a, h, forward_blocks(h.tpr, h.vpt));
     return with_types(a, h, [&](auto io, auto tpr, auto vpt, auto silu) {
         using IO = decltype(io);
-        constexpr int T = decltype(tpr)::value, NT = T > kThreads ? T : kThreads;
+        constexpr int T = decltype(tpr)::value, NT = block_of(T);
         const int64_t bytes = (int64_t)a.V * sizeof(IO);
         x.vec = x.vec && bytes % 16 == 0, z.vec = z.vec && bytes % 16 == 0;
         gated_norm_forward_kernel<IO, T, decltype(vpt)::value, decltype(silu)::value>
@@ -284,7 +284,7 @@ cudaError_t gated_norm_forward(const GatedNormArgs& a, RowTensor x, RowTensor z,
 
 int64_t gated_norm_partial_rows(const GatedNormArgs& a) {
     const Shape h = shape_of(a.V);
-    const int64_t places = places_of(a, h, backward_blocks(h.tpr, h.vpt)).count, rpb = std::max(h.tpr, kThreads) / h.tpr;
+    const int64_t places = places_of(a, h, backward_blocks(h.tpr, h.vpt)).count, rpb = block_of(h.tpr) / h.tpr;
     return rows_by_block(a, h) ? (places + rpb - 1) / rpb : places;
 }
 
@@ -294,7 +294,7 @@ cudaError_t gated_norm_backward(const GatedNormArgs& a, const void* dy, RowTenso
     const Places p = places_of(a, h, backward_blocks(h.tpr, h.vpt));
     const cudaError_t e = with_types(a, h, [&](auto io, auto tpr, auto vpt, auto silu) {
         using IO = decltype(io);
-        constexpr int T = decltype(tpr)::value, NT = T > kThreads ? T : kThreads;
+        constexpr int T = decltype(tpr)::value, NT = block_of(T);
         const int64_t bytes = (int64_t)a.V * sizeof(IO);
         x.vec = x.vec && bytes % 16 == 0, z.vec = z.vec && bytes % 16 == 0;
         gated_norm_backward_kernel<IO, T, decltype(vpt)::value, decltype(silu)::value>
