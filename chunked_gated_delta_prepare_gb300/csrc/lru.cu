@@ -63,30 +63,37 @@ __device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k
             if (row + j >= len) a[j] = both(1.f), u[j] = both(0.f);
 }
 
-constexpr int kBlocks = 3;   // an SM
+constexpr int kGroups = 3;   // 72 registers a thread
 template <typename IO> constexpr int kBuffers = sizeof(IO) == 2 ? 2 : 1;      // of tiles
 
-template <typename IO, bool GATE> constexpr int lru_forward_smem() {
+template <typename IO, bool GATE> constexpr int lru_forward_smem() {      // of a group
     return kBuffers<IO> * (GATE ? 3 : 2) * kLruTile * kLruCols * (int)sizeof(IO);
 }
 
 // y, kept and h_final may each be nullptr.
 template <typename IO, bool RATE, bool GATE, bool TMA>
-__global__ void __launch_bounds__(kLruThreads, kBlocks)
+__global__ void __launch_bounds__(kGroups * kLruThreads, 1)
 lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_maps, IO* __restrict__ y,
                    float* __restrict__ kept, float* __restrict__ h_final) {
     constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 3 : 2;
+    struct Group {
+        Map maps[kLruWarps][kLruPairs], fronts[kLruWarps][kLruPairs];      // of a warp's tokens, of those in front of them
+        F2 carry[kLruPairs];
+        LruPlan plans[kLruPlans];
+        LruHand hand;                                       // to the next group
+        uint64_t ready, full[B];                            // the tile's maps are there; its inputs are
+    };
     extern __shared__ __align__(128) uint4 smem[];
-    __shared__ Map maps[kLruWarps][kLruPairs], fronts[kLruWarps][kLruPairs];   // of a warp's tokens, of those in front of them
-    __shared__ F2 carry[kLruPairs];
-    __shared__ LruPlan plans[kLruPlans];
-    __shared__ uint64_t ready, full[B];                     // the tile's maps are there; its inputs are
-    IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, i
+    __shared__ Group all_groups[kGroups];
+    const int group = threadIdx.x / kLruThreads, thread = threadIdx.x - group * kLruThreads;
+    Group& me = all_groups[group];
+    LruPlan* plans = me.plans;
+    IO* in = reinterpret_cast<IO*>(smem) + group * (B * IN * N);           // [B][IN][N]: r, x, i
 
     const auto issue = [&](unsigned turn) {                 // one lane asks for a tile
         if (TMA && plans[turn % kLruPlans].live) {
             const LruTile& t = plans[turn % kLruPlans].t;
-            uint64_t* bar = full + turn % B;
+            uint64_t* bar = me.full + turn % B;
             IO* to = in + (turn % B) * IN * N;
             if (t.len == 0) return bw::mbar_arrive(bar);
             bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
@@ -95,17 +102,19 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
             if (GATE) lru_tma(to + 2 * N, &in_maps.i, bar, t);
         }
     };
-    if (threadIdx.x >= kLruWorkers) {                       // the guide
-        const int lane = threadIdx.x - kLruWorkers, pair = lane % kLruPairs;
+    if (thread >= kLruWorkers) {                            // the guide
+        const int lane = thread - kLruWorkers, pair = lane % kLruPairs;
         const bool first = lane < kLruPairs;                // the warp's other half only looks on
         if (lane == 0) {
-            bw::mbar_init(&ready, kLruWarps);
-            for (int i = 0; i < B; ++i) bw::mbar_init(full + i, 1);
+            bw::mbar_init(&me.ready, kLruWarps);
+            bw::mbar_init(&me.hand.given, 1);
+            bw::mbar_init(&me.hand.taken, 1);
+            for (int i = 0; i < B; ++i) bw::mbar_init(me.full + i, 1);
             bw::fence_mbar_init();
         }
-        LruPlanner<false, RATE> planner;
-        planner.start(p, chain);
-        for (unsigned turn = 0; turn < 3; ++turn) planner.plan(p, chain, turn, plans + turn);
+        LruPlanner<false, RATE, kGroups> planner;
+        planner.read(p, chain, 0);
+        for (unsigned turn = 0; turn < 3; ++turn) planner.plan(p, chain, turn, group, plans + turn);
         for (unsigned turn = 0; turn < B; ++turn)
             if (lane == 0) issue(turn);
         __syncthreads();
@@ -113,48 +122,54 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
             const LruTile t = plans[turn % kLruPlans].t;
             const int ch = t.col * kLruCols + pair * 2, left = p.D - ch;
             const int64_t at = ((int64_t)t.number * p.cols + t.col) * kLruPairs + pair;
-            // the state may be there before the tile's maps are
             F2 state = 0;
             bool found = t.to_head == 0, there = false;
             if (found && t.seq >= 0) state = state2(p.h0, (int64_t)t.seq * p.D + ch, left);
-            while (!found && !there) {
-                found = look_back<false>(chain, t, p.cols, pair, t.to_head, state);
-                there = __all_sync(0xffffffffu, bw::mbar_test_wait(&ready, turn & 1));
-            }
-            if (!there) bw::mbar_wait(&ready, turn & 1, chain.err, kDeviceErrTimeout);
+            if (group == 0)                                 // another block's state may be there before the tile's maps are
+                while (!found && !there) {
+                    found = look_back<false>(chain, t, p.cols, pair, t.to_head, state);
+                    there = __all_sync(0xffffffffu, bw::mbar_test_wait(&me.ready, turn & 1));
+                }
+            if (!there) bw::mbar_wait(&me.ready, turn & 1, chain.err, kDeviceErrTimeout);
             Map m[kLruWarps], all{both(1.f), both(0.f)};
 #pragma unroll
-            for (int w = 0; w < kLruWarps; ++w) m[w] = maps[w][pair];
+            for (int w = 0; w < kLruWarps; ++w) m[w] = me.maps[w][pair];
 #pragma unroll
             for (int w = 0; w < kLruWarps; ++w) {
-                if (first) fronts[w][pair] = all;
+                if (first) me.fronts[w][pair] = all;
                 all.own = fma2(m[w].decay, all.own, m[w].own);
                 all.decay = mul2(m[w].decay, all.decay);
             }
             if (first && t.to_tail && t.to_head) publish_map(chain.maps + at, all.decay, all.own);
-            if (!found) state = wait_back<false>(chain, t, p.cols, pair, t.to_head);
+            if (group == 0) {
+                if (!found) state = wait_back<false>(chain, t, p.cols, pair, t.to_head);
+            } else if (chain.maps) {
+                const F2 given = lru_take(all_groups[group - 1].hand, turn, chain.err);
+                if (!found) state = given;
+            }
             const F2 end = fma2(all.decay, state, all.own);
+            if (first) me.carry[pair] = state;
+            lru_arrive<2, kLruThreads>(group);
+            if (group + 1 < kGroups && chain.maps) lru_give(me.hand, end, turn, chain.err);
             if (first && t.to_tail) publish_state(chain.states + at + (int64_t)p.cols * kLruPairs, end);
-            if (first) carry[pair] = state;
-            lru_arrive<2, kLruThreads>();
             if (first && t.seq >= 0) {
                 if (kept) put_state2(kept, (int64_t)t.number * p.D + ch, state, left);
                 if (h_final && !t.to_tail) put_state2(h_final, (int64_t)t.seq * p.D + ch, end, left);
             }
-            planner.plan(p, chain, turn + 3, plans + (turn + 3) % kLruPlans);
+            planner.plan(p, chain, turn + 3, group, plans + (turn + 3) % kLruPlans);
         }
         return;
     }
 
-    const int warp = threadIdx.x / 32, pair = threadIdx.x % kLruPairs, row = threadIdx.x / kLruPairs * kLruRun;
-    const bool second = threadIdx.x & 16;                   // run of the warp
+    const int warp = thread / 32, pair = thread % kLruPairs, row = thread / kLruPairs * kLruRun;
+    const bool second = thread & 16;                        // run of the warp
     const auto fetch = [&](unsigned turn) {
         if (plans[turn % kLruPlans].live) {
             const LruTile t = plans[turn % kLruPlans].t;
             IO* to = in + (turn % B) * IN * N;
-            lru_fetch(p.r, t, p.D, to);
-            lru_fetch(p.x, t, p.D, to + N);
-            if (GATE) lru_fetch(p.i, t, p.D, to + 2 * N);
+            lru_fetch(p.r, t, p.D, thread, to);
+            lru_fetch(p.x, t, p.D, thread, to + N);
+            if (GATE) lru_fetch(p.i, t, p.D, thread, to + 2 * N);
         }
         copy_group();
     };
@@ -163,10 +178,10 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
         for (unsigned turn = 0; turn < B; ++turn) fetch(turn);
     for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
         if (TMA) {
-            bw::mbar_wait(full + turn % B, turn / B & 1, chain.err, kDeviceErrTimeout);
+            bw::mbar_wait(me.full + turn % B, turn / B & 1, chain.err, kDeviceErrTimeout);
         } else {
             copy_wait<B - 1>();
-            lru_sync<1, kLruWorkers>();
+            lru_sync<1, kLruWorkers>(group);
         }
         const LruPlan& plan = plans[turn % kLruPlans];
         const int len = plan.t.len, ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch;
@@ -186,14 +201,14 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
             m.decay = mul2(a[j], m.decay);
         }
         Map o{swap_halves(m.decay), swap_halves(m.own)};    // of the warp's other run
-        if (!second) maps[warp][pair] = Map{mul2(o.decay, m.decay), fma2(o.decay, m.own, o.own)};
+        if (!second) me.maps[warp][pair] = Map{mul2(o.decay, m.decay), fma2(o.decay, m.own, o.own)};
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&ready);
-        lru_sync<2, kLruThreads>();
+        if ((thread & 31) == 0) bw::mbar_arrive(&me.ready);
+        lru_sync<2, kLruThreads>(group);
         if (!TMA) fetch(turn + B);
-        else if (threadIdx.x == kLruWorkers - 32) issue(turn + B);
+        else if (thread == kLruWorkers - 32) issue(turn + B);
         if (y && plan.t.seq >= 0) {
-            F2 h = fma2(fronts[warp][pair].decay, carry[pair], fronts[warp][pair].own);
+            F2 h = fma2(me.fronts[warp][pair].decay, me.carry[pair], me.fronts[warp][pair].own);
             if (second) h = fma2(o.decay, h, o.own);
             IO* yp = y + (plan.t.first + row) * p.D + ch;
             if (p.vec && len == kLruTile && left > 0) {
@@ -262,12 +277,11 @@ cudaError_t lru_chain(const LruArgs& a, const float* lam, void* workspace, LruCh
     if (cudaError_t e = device_error_ptr(&c->err)) return e;
     if (lru_one_tile_each(a)) return cudaSuccess;
     const int64_t cols = (a.D + kLruCols - 1) / kLruCols, cells = lru_tiles(a) * cols * kLruPairs;
-    c->ticket = (unsigned*)workspace;
-    c->maps = (ulonglong2*)((char*)workspace + 256);
+    c->maps = (ulonglong2*)workspace;
     c->states = (F2*)(c->maps + cells);
     float4* rates = (float4*)(c->states + cells);
     c->rates = lam ? rates : nullptr;
-    const int64_t n = 16 + cells * 24 / 16;                // 16 bytes each
+    const int64_t n = cells * 24 / 16;                     // 16 bytes each
     lru_chain_kernel<<<(unsigned)std::min<int64_t>((n + 1023) / 1024, 8 * kSms), 256, 0, s>>>(
         (uint4*)workspace, n, lam, a.c, a.D, rates, (int)(cols * kLruCols));
     return cudaGetLastError();
@@ -275,7 +289,7 @@ cudaError_t lru_chain(const LruArgs& a, const float* lam, void* workspace, LruCh
 
 cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float* h_final, float* kept, void* workspace,
                         cudaStream_t s) {
-    Lru p = lru_of(args, t);
+    Lru p = lru_of(args, t, kGroups);
     p.vec = lru_pairs(y, args.D, args.io == GDR_F32 ? 4 : 2);
     LruChain chain;
     if (cudaError_t e = lru_chain(args, t.lam, workspace, &chain, s)) return e;
@@ -286,12 +300,9 @@ cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float
     return lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
         constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
-        constexpr int bytes = lru_forward_smem<IO, G>();
         const auto go = [&](auto kernel) {
-            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-            kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(p, chain, m, (IO*)y, kept,
-                                                                                                    h_final);
-            return cudaGetLastError();
+            return lru_launch(kernel, p, chain, kGroups * kLruThreads, kGroups * lru_forward_smem<IO, G>(), s, m, (IO*)y, kept,
+                              h_final);
         };
         return tma ? go(lru_forward_kernel<IO, R, G, true>) : go(lru_forward_kernel<IO, R, G, false>);
     });
@@ -299,7 +310,7 @@ cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float
 
 cudaError_t lru_step(const LruArgs& args, const LruTensors& t, int64_t pool, const int* slots, float* h, void* y,
                      cudaStream_t s) {
-    Lru p = lru_of(args, t);
+    Lru p = lru_of(args, t, kGroups);
     p.vec = lru_pairs(y, args.D, args.io == GDR_F32 ? 4 : 2);
     const dim3 grid((unsigned)((args.D + 255) / 256), (unsigned)std::min<int64_t>(args.n, 65535));
     return lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {

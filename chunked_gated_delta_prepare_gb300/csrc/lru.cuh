@@ -18,11 +18,12 @@
 namespace gdr {
 namespace layer {
 
-// A tile: 128 tokens of a sequence by 32 channels, a block's work: 16 runs of 8 tokens, each on 16 lanes of two channels.
-// Narrow tiles leave few tiles of a strip of channels in flight at once, so a tile's state is never far away.
+// A tile: 128 tokens of a sequence by 32 channels, a group's work: 16 runs of 8 tokens, each on 16 lanes of two channels.
+// A block, one an SM, has as many groups as the registers hold, on neighbouring tiles of a strip of channels: a state goes
+// from one group to the next through shared memory, and only the first group's comes from another block.
 constexpr int kLruRun = 8, kLruRuns = 16, kLruTile = kLruRun * kLruRuns, kLruCols = 32, kLruPairs = kLruCols / 2;
 constexpr int kLruWorkers = kLruRuns * kLruPairs, kLruWarps = kLruWorkers / 32;
-constexpr int kLruThreads = kLruWorkers + 32;     // and a warp that guides the workers
+constexpr int kLruThreads = kLruWorkers + 32;     // of a group: the workers and a warp that guides them
 static_assert(kLruTile == kLruKept, "a kept state for each tile");
 
 // A tensor of tokens, copied in aligned units of 16 bytes (by TMA), of 4, or (16-bit rows that start anywhere) by elements.
@@ -49,9 +50,11 @@ inline Divisor divisor(unsigned d) {
 struct Lru {
     Seqs q;
     int D;
-    unsigned cols, tiles;    // blocks of channels, and tiles of the token axis
+    unsigned cols, tiles;    // strips of channels, and tiles of the token axis
     unsigned per;            // tiles of a sequence of a batch
-    Divisor by_cols, by_n;
+    unsigned jobs;           // of the blocks: as many tiles of a strip as there are groups
+    bool in_turns;           // the jobs of a batch's sequences take turns
+    Divisor by_cols, by_n, by_per;
     LruRows x, r, i;
     const float *lam, *h0;
     float c;
@@ -215,29 +218,44 @@ struct LruTile {
     unsigned to_head, to_tail;  // tiles before it and behind it in its sequence
 };
 
-// Tiles in the order they are worked on: all channels of one after all of another, each after those it waits for (BACK: the
-// tiles behind it).  The sequences of a batch take turns, so that a tile's neighbour in time is long done.
-template <bool BACK> __device__ __forceinline__ LruTile lru_tile(const Lru& a, unsigned ticket) {
+// Group `group`'s tile of a job.  Jobs go through all strips before they go on in time, each after those it waits for (BACK:
+// from behind); where there are few strips the sequences of a batch take turns, so that a job's neighbour in time is long
+// done.  A job's last tiles may not exist (`number` is ~0 then).
+template <bool BACK, int GROUPS> __device__ __forceinline__ LruTile lru_tile(const Lru& a, unsigned job, unsigned group) {
     LruTile t;
-    unsigned k = a.by_cols.of(ticket);
-    t.col = ticket - k * a.cols;
-    if (BACK) k = a.tiles - 1 - k;
-    int64_t len;
-    unsigned tile;
-    if (a.q.cu) {
-        const TileAt at = find_tile(a.q, k, kLruTile);
+    const unsigned row = a.by_cols.of(job);
+    t.col = job - row * a.cols;
+    int64_t len = 0;
+    unsigned tile = 0;
+    bool some;
+    if (a.in_turns) {
+        const unsigned k = a.by_n.of(row);
+        t.seq = (int)(row - k * (unsigned)a.q.n);
+        tile = k * GROUPS + group;
+        some = tile < a.per;
+        if (BACK) tile = a.per - 1 - tile;
+        t.number = (unsigned)t.seq * a.per + tile;
+    } else {
+        t.number = row * GROUPS + group;
+        some = t.number < a.tiles;
+        if (BACK) t.number = a.tiles - 1 - t.number;
+        if (!a.q.cu) {
+            t.seq = (int)a.by_per.of(some ? t.number : 0);
+            tile = t.number - (unsigned)t.seq * a.per;
+        }
+    }
+    t.first = 0;
+    if (some && a.q.cu) {
+        const TileAt at = find_tile(a.q, t.number, kLruTile);
         t.seq = at.seq;
-        t.number = k;
         t.first = at.start;
         len = at.len;
         tile = (unsigned)at.tile;
-    } else {
-        tile = a.by_n.of(k);
-        t.seq = (int)(k - tile * (unsigned)a.q.n);
-        t.number = (unsigned)t.seq * a.per + tile;
+    } else if (some) {
         t.first = t.seq * a.q.T;
         len = a.q.T;
     }
+    if (!some) t.seq = -1, t.number = ~0u;
     t.first += (int64_t)tile * kLruTile;
     len -= (int64_t)tile * kLruTile;
     t.len = t.seq < 0 ? 0 : (int)(len < kLruTile ? len : kLruTile);
@@ -249,19 +267,13 @@ template <bool BACK> __device__ __forceinline__ LruTile lru_tile(const Lru& a, u
 // What the blocks of a launch tell one another.  Everything starts as 0xff bytes: a NaN that no arithmetic makes says that a
 // word is not written yet.  Each word is written once, whole, so it needs no flag and no fence.
 struct LruChain {
-    unsigned* ticket;        // tiles taken so far, less one; nullptr: no tile waits for another
-    ulonglong2* maps;        // [tiles][cols][pairs]: a tile makes of state h  h * x + y
+    ulonglong2* maps;        // [tiles][cols][pairs]: a tile makes of state h  h * x + y; nullptr: no tile waits for another
     F2* states;              // [tiles][cols][pairs]: the state that a tile goes on from
     const float4* rates;     // [cols * 32]: rates_of each channel, or nullptr (the guides form them)
     unsigned* err;           // the device error word
 };
-inline size_t lru_chain_bytes(int64_t tiles, int64_t cols) {       // the ticket, the maps, the states; the rates
-    return 256 + (size_t)tiles * cols * kLruPairs * 24 + (size_t)cols * kLruCols * 16;
-}
-
-// A block's k-th tile.  Tiles are handed out in order, so those that a tile waits for belong to blocks that run already.
-__device__ __forceinline__ unsigned take_ticket(const LruChain& c, unsigned k) {
-    return c.ticket ? atomicAdd(c.ticket, 1u) + 1u : blockIdx.x + k * gridDim.x;
+inline size_t lru_chain_bytes(int64_t tiles, int64_t cols) {       // the maps, the states, the rates
+    return (size_t)tiles * cols * kLruPairs * 24 + (size_t)cols * kLruCols * 16;
 }
 
 __device__ __forceinline__ F2 written(F2 v) {         // a payload that says "not written" becomes the usual NaN
@@ -330,10 +342,17 @@ __device__ __forceinline__ F2 wait_back(const LruChain& c, const LruTile& t, uns
     return 0;
 }
 
-// Named barriers: 1 and 3 of the workers, 2 of all, where the guide only arrives.
-template <int ID, int N> __device__ __forceinline__ void lru_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
-template <int ID, int N> __device__ __forceinline__ void lru_arrive() {
-    asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory");
+// Named barriers of a group: 1 and 3 of the workers, 2 of all, where the guide only arrives.  Their names are known to the
+// compiler: from registers they take several times as long.
+template <int ID, int N> __device__ __forceinline__ void lru_sync(int group) {
+    if (group == 0) asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+    else if (group == 1) asm volatile("bar.sync %0, %1;" ::"n"(ID + 3), "n"(N) : "memory");
+    else asm volatile("bar.sync %0, %1;" ::"n"(ID + 6), "n"(N) : "memory");
+}
+template <int ID, int N> __device__ __forceinline__ void lru_arrive(int group) {
+    if (group == 0) asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory");
+    else if (group == 1) asm volatile("bar.arrive %0, %1;" ::"n"(ID + 3), "n"(N) : "memory");
+    else asm volatile("bar.arrive %0, %1;" ::"n"(ID + 6), "n"(N) : "memory");
 }
 __device__ __forceinline__ F2 swap_halves(F2 v) { return __shfl_xor_sync(0xffffffffu, v, 16); }
 
@@ -344,37 +363,26 @@ struct LruPlan {
     bool live;               // there is one
     alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];      // k, sqrt(2 k), (BACK) k's slope
 };
-// The guide's lane: tickets are taken five tiles ahead, a channel's lam is read four ahead and a tile planned three ahead,
-// after the present one's state is out, so that no way to memory holds anyone up.
-template <bool BACK, bool RATE> struct LruPlanner {
-    unsigned ticket, next;   // of the tile to be planned, and of the one after it
+// The guide's: a channel's rates are read four tiles ahead and a tile planned three ahead, after the present one's state is
+// out, so that no way to memory holds anyone up.
+template <bool BACK, bool RATE, int GROUPS> struct LruPlanner {
     float4 rate;             // of the tile to be planned: k, sqrt(2 k), k's slope
 
-    __device__ __forceinline__ unsigned take(const LruChain& c, unsigned turn) const {
-        return (threadIdx.x & 31) == 0 ? take_ticket(c, turn) : 0;
-    }
-    __device__ __forceinline__ float4 read(const Lru& p, const LruChain& c, unsigned ticket) const {
-        if (!RATE || ticket >= p.tiles * p.cols) return float4{};
-        const unsigned col = ticket - p.by_cols.of(ticket) * p.cols;
+    __device__ __forceinline__ unsigned job(unsigned turn) const { return blockIdx.x + turn * gridDim.x; }
+    __device__ __forceinline__ void read(const Lru& p, const LruChain& c, unsigned turn) {
+        if (!RATE || job(turn) >= p.jobs) return;
+        const unsigned col = job(turn) - p.by_cols.of(job(turn)) * p.cols;
         const int ch = (int)col * kLruCols + (threadIdx.x & 31);
-        if (c.rates) return c.rates[ch];
-        return ch < p.D ? rates_of(p.lam[ch], p.c) : float4{};
+        if (c.rates) rate = c.rates[ch];
+        else rate = ch < p.D ? rates_of(p.lam[ch], p.c) : float4{};
     }
-    __device__ __forceinline__ void start(const Lru& p, const LruChain& c) {
-        ticket = __shfl_sync(0xffffffffu, take(c, 0), 0);
-        rate = read(p, c, ticket);
-        next = take(c, 1);
-    }
-    // Plans the tile of turn `turn`.
-    __device__ __forceinline__ void plan(const Lru& p, const LruChain& c, unsigned turn, LruPlan* plan) {
-        const unsigned after = take(c, turn + 2);
-        next = __shfl_sync(0xffffffffu, next, 0);
-        const float4 rate_after = read(p, c, next);
+    // Plans the tile of turn `turn`, in order.
+    __device__ __forceinline__ void plan(const Lru& p, const LruChain& c, unsigned turn, unsigned group, LruPlan* plan) {
         const int lane = threadIdx.x & 31;
-        const bool live = ticket < p.tiles * p.cols;
+        const bool live = job(turn) < p.jobs;
         if (lane == 0) plan->live = live;
         if (live) {
-            const LruTile t = lru_tile<BACK>(p, ticket);
+            const LruTile t = lru_tile<BACK, GROUPS>(p, job(turn), group);
             if (lane == 0) plan->t = t;
             if (RATE) {
                 plan->rates[lane] = rate.x;
@@ -382,12 +390,29 @@ template <bool BACK, bool RATE> struct LruPlanner {
                 if (BACK) plan->slopes[lane] = rate.z;
             }
         }
-        ticket = next;
-        next = after;
-        rate = rate_after;
+        read(p, c, turn + 1);
         __syncwarp();
     }
 };
+
+// The way of a state from a group to the next one: given once a turn, and taken before it is given again.
+struct LruHand {
+    F2 state[kLruPairs];
+    uint64_t given, taken;
+};
+__device__ __forceinline__ void lru_give(LruHand& h, F2 state, unsigned turn, unsigned* err) {      // by a warp
+    if (turn > 0) bw::mbar_wait(&h.taken, turn - 1 & 1, err, kDeviceErrTimeout);
+    if ((threadIdx.x & 31) < kLruPairs) h.state[threadIdx.x & 31] = state;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&h.given);
+}
+__device__ __forceinline__ F2 lru_take(LruHand& h, unsigned turn, unsigned* err) {
+    bw::mbar_wait(&h.given, turn & 1, err, kDeviceErrTimeout);
+    const F2 state = h.state[threadIdx.x % kLruPairs];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&h.taken);
+    return state;
+}
 
 // Inputs on their way by TMA: a box of 128 rows and 32 channels, zeros outside the tensor.
 struct LruMaps {
@@ -408,26 +433,27 @@ __device__ __forceinline__ void lru_copy(void* to, const void* from, int bytes) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
 }
 template <typename IO>
-__device__ __forceinline__ void lru_fetch_units(const LruRows& v, const LruTile& t, int D, IO* to) {
+__device__ __forceinline__ void lru_fetch_units(const LruRows& v, const LruTile& t, int D, int thread, IO* to) {
     constexpr int per = 4 / (int)sizeof(IO), pieces = kLruCols / per, step = kLruWorkers / pieces;
-    const int piece = threadIdx.x % pieces, ch = t.col * kLruCols + piece * per;
+    const int piece = thread % pieces, ch = t.col * kLruCols + piece * per;
     const int bytes = min(per, D - ch) * (int)sizeof(IO);
     if (bytes <= 0) return;
-    const IO* from = (const IO*)v.p + (t.first + threadIdx.x / pieces) * v.ld + ch;
+    const IO* from = (const IO*)v.p + (t.first + thread / pieces) * v.ld + ch;
 #pragma unroll
     for (int k = 0; k < kLruTile / step; ++k) {
-        const int row = threadIdx.x / pieces + k * step;
+        const int row = thread / pieces + k * step;
         if (row < t.len) lru_copy(to + row * kLruCols + piece * per, from, bytes);
         from += step * v.ld;
     }
 }
 // A tile of a tensor on its way into shared memory, by the workers; rows past the tile's end stay what they were.
-template <typename IO> __device__ __forceinline__ void lru_fetch(const LruRows& v, const LruTile& t, int D, IO* to) {
+template <typename IO>
+__device__ __forceinline__ void lru_fetch(const LruRows& v, const LruTile& t, int D, int thread, IO* to) {
     if (sizeof(IO) == 4 || v.unit >= 4) {
-        lru_fetch_units<IO>(v, t, D, to);
+        lru_fetch_units<IO>(v, t, D, thread, to);
     } else {
         constexpr int step = kLruWorkers / kLruPairs, most = kLruTile / step;
-        const int piece = threadIdx.x % kLruPairs, ch = t.col * kLruCols + piece * 2, row0 = threadIdx.x / kLruPairs;
+        const int piece = thread % kLruPairs, ch = t.col * kLruCols + piece * 2, row0 = thread / kLruPairs;
         const IO* from = (const IO*)v.p + (t.first + row0) * v.ld + ch;
         RawN<IO, 2> e[most];
 #pragma unroll
@@ -493,7 +519,7 @@ inline LruRows lru_rows(const RowTensor& t, int64_t e) {
     const bool four = reinterpret_cast<uintptr_t>(t.p) % 4 == 0 && t.ld * e % 4 == 0;
     return LruRows{t.p, t.ld, t.vec ? 16 : four ? 4 : 2};
 }
-inline Lru lru_of(const LruArgs& a, const LruTensors& t) {
+inline Lru lru_of(const LruArgs& a, const LruTensors& t, int groups) {
     const int64_t e = a.io == GDR_F32 ? 4 : 2;
     Lru k{};
     k.q = Seqs{a.cu, a.total, a.T, (int)a.n};
@@ -503,6 +529,10 @@ inline Lru lru_of(const LruArgs& a, const LruTensors& t) {
     k.per = k.tiles / (unsigned)a.n;
     k.by_cols = divisor(k.cols);
     k.by_n = divisor((unsigned)a.n);
+    k.by_per = divisor(k.per ? k.per : 1);
+    // in turns at the price of the last job's idle groups; a strip has about 152 / cols jobs in flight
+    k.in_turns = !a.cu && a.n > 1 && k.cols < 64 && k.per >= 4 * (unsigned)groups;
+    k.jobs = k.cols * (k.in_turns ? (k.per + groups - 1) / groups * (unsigned)a.n : (k.tiles + groups - 1) / groups);
     k.x = lru_rows(t.x, e);
     k.r = lru_rows(t.r, e);
     k.i = lru_rows(t.i, e);
@@ -520,6 +550,23 @@ inline bool lru_map(CUtensorMap* m, const LruRows& v, const LruArgs& a) {
 }
 
 inline bool lru_one_tile_each(const LruArgs& a) { return (a.cu ? a.total : a.T) <= kLruTile; }
+// One block an SM at most; blocks that wait for one another run together or not at all.
+template <typename... A, typename... B>
+cudaError_t lru_launch(void (*kernel)(A...), const Lru& p, const LruChain& c, int threads, int bytes, cudaStream_t s, B... args) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    cudaLaunchAttribute together{};
+    together.id = cudaLaunchAttributeCooperative;
+    together.val.cooperative = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(std::min(p.jobs, (unsigned)kSms));
+    config.blockDim = dim3((unsigned)threads);
+    config.dynamicSmemBytes = (size_t)bytes;
+    config.stream = s;
+    config.attrs = &together;
+    config.numAttrs = c.maps ? 1 : 0;
+    return cudaLaunchKernelEx(&config, kernel, p, c, args...);
+}
+
 // The chain's words in the workspace, made "not written", and the rates; none of them with one tile a sequence.
 cudaError_t lru_chain(const LruArgs& a, const float* lam, void* workspace, LruChain* c, cudaStream_t s);
 

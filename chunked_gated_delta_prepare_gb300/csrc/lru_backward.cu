@@ -13,10 +13,10 @@ namespace gdr {
 namespace layer {
 namespace {
 
-constexpr int kBlocks = 2;   // an SM
+constexpr int kGroups = 2;   // 96 registers a thread
 template <typename IO> constexpr int kBuffers = sizeof(IO) == 2 ? 2 : 1;      // of tiles
 
-template <typename IO, bool GATE> constexpr int lru_backward_smem() {
+template <typename IO, bool GATE> constexpr int lru_backward_smem() {     // of a group
     return kBuffers<IO> * (GATE ? 4 : 3) * kLruTile * kLruCols * (int)sizeof(IO);
 }
 
@@ -118,24 +118,31 @@ __device__ __forceinline__ Parts parts_of(F2 kept, F2 k, F2 root, F2 inverse, F2
 
 // dlam: [tiles][D] partial sums, or nullptr.
 template <typename IO, bool RATE, bool GATE, bool TMA>
-__global__ void __launch_bounds__(kLruThreads, kBlocks)
+__global__ void __launch_bounds__(kGroups * kLruThreads, 1)
 lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_maps, LruRows dy, const float* __restrict__ kept, const float* __restrict__ dh_final,
                     IO* __restrict__ dx, IO* __restrict__ dr, IO* __restrict__ di, float* __restrict__ dlam,
                     float* __restrict__ dh0) {
     constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 4 : 3;
+    struct Group {
+        Run runs[kLruWarps][kLruPairs];                     // of a warp's tokens
+        Map behind[kLruWarps][kLruPairs];                   // of the tokens behind them
+        F2 fronts[kLruWarps][kLruPairs], sums[kLruWarps][kLruPairs];       // states in front of them; sums for dlam
+        F2 carry[kLruPairs];
+        LruPlan plans[kLruPlans];
+        LruHand hand;                                       // to the next group, which has the tile before
+        uint64_t ready, full[B];                            // the tile's maps are there; its inputs are
+    };
     extern __shared__ __align__(128) uint4 smem[];
-    __shared__ Run runs[kLruWarps][kLruPairs];              // of a warp's tokens
-    __shared__ Map behind[kLruWarps][kLruPairs];            // of the tokens behind them
-    __shared__ F2 fronts[kLruWarps][kLruPairs], sums[kLruWarps][kLruPairs];    // states in front of them; sums for dlam
-    __shared__ F2 carry[kLruPairs];
-    __shared__ LruPlan plans[kLruPlans];
-    __shared__ uint64_t ready, full[B];                     // the tile's maps are there; its inputs are
-    IO* in = reinterpret_cast<IO*>(smem);                   // [B][IN][N]: r, x, dy, i
+    __shared__ Group all_groups[kGroups];
+    const int group = threadIdx.x / kLruThreads, thread = threadIdx.x - group * kLruThreads;
+    Group& me = all_groups[group];
+    LruPlan* plans = me.plans;
+    IO* in = reinterpret_cast<IO*>(smem) + group * (B * IN * N);           // [B][IN][N]: r, x, dy, i
 
     const auto issue = [&](unsigned turn) {                 // one lane asks for a tile
         if (TMA && plans[turn % kLruPlans].live) {
             const LruTile& t = plans[turn % kLruPlans].t;
-            uint64_t* bar = full + turn % B;
+            uint64_t* bar = me.full + turn % B;
             IO* to = in + (turn % B) * IN * N;
             if (t.len == 0) return bw::mbar_arrive(bar);
             bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
@@ -145,17 +152,19 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             if (GATE) lru_tma(to + 3 * N, &in_maps.i, bar, t);
         }
     };
-    if (threadIdx.x >= kLruWorkers) {                       // the guide
-        const int lane = threadIdx.x - kLruWorkers, pair = lane % kLruPairs;
+    if (thread >= kLruWorkers) {                            // the guide
+        const int lane = thread - kLruWorkers, pair = lane % kLruPairs;
         const bool first = lane < kLruPairs;
         if (lane == 0) {
-            bw::mbar_init(&ready, kLruWarps);
-            for (int i = 0; i < B; ++i) bw::mbar_init(full + i, 1);
+            bw::mbar_init(&me.ready, kLruWarps);
+            bw::mbar_init(&me.hand.given, 1);
+            bw::mbar_init(&me.hand.taken, 1);
+            for (int i = 0; i < B; ++i) bw::mbar_init(me.full + i, 1);
             bw::fence_mbar_init();
         }
-        LruPlanner<true, RATE> planner;
-        planner.start(p, chain);
-        for (unsigned turn = 0; turn < 3; ++turn) planner.plan(p, chain, turn, plans + turn);
+        LruPlanner<true, RATE, kGroups> planner;
+        planner.read(p, chain, 0);
+        for (unsigned turn = 0; turn < 3; ++turn) planner.plan(p, chain, turn, group, plans + turn);
         for (unsigned turn = 0; turn < B; ++turn)
             if (lane == 0) issue(turn);
         __syncthreads();
@@ -167,50 +176,57 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             F2 e = 0;
             bool found = t.to_tail == 0, there = false;
             if (found && t.seq >= 0) e = state2(dh_final, (int64_t)t.seq * p.D + ch, left);
-            while (!found && !there) {
-                found = look_back<true>(chain, t, p.cols, pair, t.to_tail, e);
-                there = __all_sync(0xffffffffu, bw::mbar_test_wait(&ready, turn & 1));
-            }
-            if (!there) bw::mbar_wait(&ready, turn & 1, chain.err, kDeviceErrTimeout);
+            if (group == 0)
+                while (!found && !there) {
+                    found = look_back<true>(chain, t, p.cols, pair, t.to_tail, e);
+                    there = __all_sync(0xffffffffu, bw::mbar_test_wait(&me.ready, turn & 1));
+                }
+            if (!there) bw::mbar_wait(&me.ready, turn & 1, chain.err, kDeviceErrTimeout);
             F2 d = both(1.f), b = both(0.f);
             if (first) {
 #pragma unroll
                 for (int w = kLruWarps - 1; w >= 0; --w) {
-                    behind[w][pair] = Map{d, b};
-                    b = fma2(runs[w][pair].decay, b, runs[w][pair].back);
-                    d = mul2(runs[w][pair].decay, d);
+                    me.behind[w][pair] = Map{d, b};
+                    b = fma2(me.runs[w][pair].decay, b, me.runs[w][pair].back);
+                    d = mul2(me.runs[w][pair].decay, d);
                 }
             } else {                                        // meanwhile the states
 #pragma unroll
                 for (int w = 0; w < kLruWarps; ++w) {
-                    fronts[w][pair] = state;
-                    state = fma2(runs[w][pair].decay, state, runs[w][pair].own);
+                    me.fronts[w][pair] = state;
+                    state = fma2(me.runs[w][pair].decay, state, me.runs[w][pair].own);
                 }
             }
             d = __shfl_sync(0xffffffffu, d, pair);
             b = __shfl_sync(0xffffffffu, b, pair);
             if (first && t.to_head && t.to_tail) publish_map(chain.maps + at, d, b);
-            if (!found) e = wait_back<true>(chain, t, p.cols, pair, t.to_tail);
+            if (group == 0) {
+                if (!found) e = wait_back<true>(chain, t, p.cols, pair, t.to_tail);
+            } else if (chain.maps) {
+                const F2 given = lru_take(all_groups[group - 1].hand, turn, chain.err);
+                if (!found) e = given;
+            }
             const F2 end = fma2(d, e, b);
+            if (first) me.carry[pair] = e;
+            lru_arrive<2, kLruThreads>(group);
+            if (group + 1 < kGroups && chain.maps) lru_give(me.hand, end, turn, chain.err);
             if (first && t.to_head) publish_state(chain.states + at - (int64_t)p.cols * kLruPairs, end);
-            if (first) carry[pair] = e;
-            lru_arrive<2, kLruThreads>();
             if (first && dh0 && t.seq >= 0 && !t.to_head) put_state2(dh0, (int64_t)t.seq * p.D + ch, end, left);
-            planner.plan(p, chain, turn + 3, plans + (turn + 3) % kLruPlans);
+            planner.plan(p, chain, turn + 3, group, plans + (turn + 3) % kLruPlans);
         }
         return;
     }
 
-    const int warp = threadIdx.x / 32, pair = threadIdx.x % kLruPairs, row = threadIdx.x / kLruPairs * kLruRun;
-    const bool second = threadIdx.x & 16;                   // run of the warp
+    const int warp = thread / 32, pair = thread % kLruPairs, row = thread / kLruPairs * kLruRun;
+    const bool second = thread & 16;                        // run of the warp
     const auto fetch = [&](unsigned turn) {
         if (plans[turn % kLruPlans].live) {
             const LruTile t = plans[turn % kLruPlans].t;
             IO* to = in + (turn % B) * IN * N;
-            lru_fetch(p.r, t, p.D, to);
-            lru_fetch(p.x, t, p.D, to + N);
-            lru_fetch(dy, t, p.D, to + 2 * N);
-            if (GATE) lru_fetch(p.i, t, p.D, to + 3 * N);
+            lru_fetch(p.r, t, p.D, thread, to);
+            lru_fetch(p.x, t, p.D, thread, to + N);
+            lru_fetch(dy, t, p.D, thread, to + 2 * N);
+            if (GATE) lru_fetch(p.i, t, p.D, thread, to + 3 * N);
         }
         copy_group();
     };
@@ -219,10 +235,10 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         for (unsigned turn = 0; turn < B; ++turn) fetch(turn);
     for (unsigned turn = 0; plans[turn % kLruPlans].live; ++turn) {
         if (TMA) {
-            bw::mbar_wait(full + turn % B, turn / B & 1, chain.err, kDeviceErrTimeout);
+            bw::mbar_wait(me.full + turn % B, turn / B & 1, chain.err, kDeviceErrTimeout);
         } else {
             copy_wait<B - 1>();
-            lru_sync<1, kLruWorkers>();
+            lru_sync<1, kLruWorkers>(group);
         }
         const LruPlan& plan = plans[turn % kLruPlans];
         const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch, len = plan.t.len;
@@ -246,13 +262,13 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         // the warp's other run; the first run passes its states on, the second what it sends back
         const F2 decay = swap_halves(m.decay), other = swap_halves(second ? m.back : m.own);
         const F2 more = swap_halves(second ? m.own : m.back);
-        if (!second) runs[warp][pair] = Run{mul2(m.decay, decay), fma2(decay, m.own, more), fma2(m.decay, other, m.back)};
+        if (!second) me.runs[warp][pair] = Run{mul2(m.decay, decay), fma2(decay, m.own, more), fma2(m.decay, other, m.back)};
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) bw::mbar_arrive(&ready);
-        lru_sync<2, kLruThreads>();
+        if ((thread & 31) == 0) bw::mbar_arrive(&me.ready);
+        lru_sync<2, kLruThreads>(group);
         F2 sum = both(0.f);
         if (plan.t.seq >= 0) {
-            F2 state = fronts[warp][pair];
+            F2 state = me.fronts[warp][pair];
             if (second) state = fma2(decay, state, other);
 #pragma unroll
             for (int j = 0; j < kLruRun; ++j) {
@@ -260,7 +276,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                 h[j] = state;                               // the state in front of the token
                 state = after;
             }
-            F2 e = fma2(behind[warp][pair].decay, carry[pair], behind[warp][pair].back);
+            F2 e = fma2(me.behind[warp][pair].decay, me.carry[pair], me.behind[warp][pair].back);
             if (!second) e = fma2(decay, e, other);
             const int64_t at = (plan.t.first + row + kLruRun - 1) * p.D + ch;
             IO *xp = dx + at, *rp = dr + at, *ip = di + at;
@@ -300,15 +316,15 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         }
         if (RATE) {
             sum = add2(sum, swap_halves(sum));
-            if (!second) sums[warp][pair] = sum;
+            if (!second) me.sums[warp][pair] = sum;
         }
-        lru_sync<3, kLruWorkers>();                         // the tile has been read
+        lru_sync<3, kLruWorkers>(group);                         // the tile has been read
         if (!TMA) fetch(turn + B);
-        else if (threadIdx.x == kLruWorkers - 32) issue(turn + B);
-        if (RATE && warp == turn % kLruWarps && !second) {
-            sum = sums[0][pair];
+        else if (thread == kLruWorkers - 32) issue(turn + B);
+        if (RATE && warp == turn % kLruWarps && !second && plan.t.number != ~0u) {
+            sum = me.sums[0][pair];
 #pragma unroll
-            for (int w = 1; w < kLruWarps; ++w) sum = add2(sum, sums[w][pair]);
+            for (int w = 1; w < kLruWarps; ++w) sum = add2(sum, me.sums[w][pair]);
             put_state2(dlam, (int64_t)plan.t.number * p.D + ch,
                        mul2(sum, *reinterpret_cast<const F2*>(plan.slopes + pair * 2)), left);
         }
@@ -333,7 +349,7 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
         kept = states;
     }
     const int64_t es = args.io == GDR_F32 ? 4 : 2;
-    Lru p = lru_of(args, t);
+    Lru p = lru_of(args, t, kGroups);
     p.vec = true;
     for (const void* v : {(const void*)g.dx, (const void*)g.dr, (const void*)g.di}) p.vec = p.vec && lru_pairs(v, args.D, es);
     const LruRows dy = lru_rows(RowTensor{g.dy, args.D, reinterpret_cast<uintptr_t>(g.dy) % 16 == 0 && args.D * es % 16 == 0}, es);
@@ -347,12 +363,9 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
     const cudaError_t e = lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
         constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
-        constexpr int bytes = lru_backward_smem<IO, G>();
         const auto go = [&](auto kernel) {
-            if (cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return err;
-            kernel<<<std::min(p.tiles * p.cols, (unsigned)(kBlocks * kSms)), kLruThreads, bytes, s>>>(
-                p, chain, m, dy, kept, g.dh_final, (IO*)g.dx, (IO*)g.dr, (IO*)g.di, partial, g.dh0);
-            return cudaGetLastError();
+            return lru_launch(kernel, p, chain, kGroups * kLruThreads, kGroups * lru_backward_smem<IO, G>(), s, m, dy, kept,
+                              g.dh_final, (IO*)g.dx, (IO*)g.dr, (IO*)g.di, partial, g.dh0);
         };
         return tma ? go(lru_backward_kernel<IO, R, G, true>) : go(lru_backward_kernel<IO, R, G, false>);
     });
