@@ -117,19 +117,15 @@ __device__ __forceinline__ F2 sqrt2(F2 v) {
     const float2 f = unpack2(v);
     return pack2(sqrt_fast(f.x), sqrt_fast(f.y));
 }
-// 1 / v for v >= 0: finite for 0, and NaN is left to what it multiplies.
-__device__ __forceinline__ F2 rcp2_finite(F2 v) {
-    const float2 f = unpack2(v);
-    return pack2(rcp(fmaxf(f.x, 3e-19f)), rcp(fmaxf(f.y, 3e-19f)));
-}
-
 // A channel's k = c softplus(lam), and its slope c sigmoid(lam).
 __device__ __forceinline__ float rate_of(float lam, float c) {
     return c * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam))));     // a NaN comes through the logarithm
 }
+// k, sqrt(2 k), and k's slope by lam over sqrt(2 k).
 __device__ __forceinline__ float4 rates_of(float lam, float c) {
     const float k = rate_of(lam, c);
-    return make_float4(k, sqrtf(2.f * k), c / (1.f + expf(-lam)), 0.f);
+    const float root = sqrtf(2.f * k);
+    return make_float4(k, root, c / (1.f + expf(-lam)) / fmaxf(root, 1e-30f), 0.f);
 }
 
 // A token's decay a and input's part s; q = sigmoid(r).
@@ -361,12 +357,12 @@ constexpr int kLruPlans = 4;
 struct LruPlan {
     LruTile t;
     bool live;               // there is one
-    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];      // k, sqrt(2 k), (BACK) k's slope
+    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];      // rates_of; BACK: the last
 };
 // The guide's: a channel's rates are read four tiles ahead and a tile planned three ahead, after the present one's state is
 // out, so that no way to memory holds anyone up.
 template <bool BACK, bool RATE, int GROUPS> struct LruPlanner {
-    float4 rate;             // of the tile to be planned: k, sqrt(2 k), k's slope
+    float4 rate;             // of the tile to be planned: rates_of
 
     __device__ __forceinline__ unsigned job(unsigned turn) const { return blockIdx.x + turn * gridDim.x; }
     __device__ __forceinline__ void read(const Lru& p, const LruChain& c, unsigned turn) {

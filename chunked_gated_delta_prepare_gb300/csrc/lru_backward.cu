@@ -28,7 +28,8 @@ struct alignas(16) Map {     // what tokens make of the gradient e from behind t
 };
 
 // The decays and terms of the thread's run, from shared memory, and what the gradients need beside them: the input's part s
-// (RATE and `shorter`: w = sqrt(q)), q, and the gate.  A token past the tile's end has a = 1, u = 0.
+// (RATE: q, or by the shorter formulas w = sqrt(q)), and the gate.  RATE: the terms, and so all states here, have the other
+// sign, which saves the gradients a negation.  A token past the tile's end has a = 1, u = 0.
 template <typename IO, bool RATE, bool GATE>
 __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k, F2 root, int len, int left,
                                          F2 (&a)[kLruRun], F2 (&u)[kLruRun], F2 (&part)[kLruRun],
@@ -42,7 +43,7 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
     }
     const bool shorter = lru_short<RATE, GATE, true>(r, i, k, len - row, left);
     if (shorter) {
-        const F2 k2 = add2(k, k);
+        const F2 minus = neg2(root);
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
             const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
@@ -57,9 +58,9 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
                 } else {
                     z = part[j] = rsqrt2(t1);
                 }
-                const F2 v = mul2(k2, mul2(part[j], part[j]));
+                const F2 rw = mul2(root, part[j]), v = mul2(rw, rw);
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
-                u[j] = mul2(mul2(z, lru_p(v)), mul2(root, x));
+                u[j] = mul2(mul2(z, lru_p(v)), mul2(minus, x));
             } else {
                 const F2 e = ex2_2(mul2(rv, both(-kLog2e))), t1 = add2(e, both(1.f));
                 if (GATE) {
@@ -79,7 +80,7 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
         for (int j = 0; j < kLruRun; ++j) {
             F2 s, q;
             decay_and_part<RATE>(wide2(r[j]), k, a[j], s, q);
-            u[j] = mul2(s, lru_read(from + N, row + j, pair));
+            u[j] = mul2(RATE ? neg2(s) : s, lru_read(from + N, row + j, pair));
             if (GATE) gate[j] = sigmoid2(wide2(i[j])), u[j] = mul2(u[j], gate[j]);
             part[j] = RATE ? q : s;
         }
@@ -91,27 +92,18 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
     return shorter;
 }
 
-// s, q and q / s of a token.
+// RATE: s, q and sqrt(2 k) q / s of a token, the last by w / P(v) where 1 - a^2 cancels: finite where s is zero.
 struct Parts {
     F2 s, q, ratio;
 };
-__device__ __forceinline__ Parts parts_of(F2 kept, F2 k, F2 root, F2 inverse, F2 a, bool shorter) {
-    Parts o;
-    if (shorter) {                           // w
-        o.q = mul2(kept, kept);
-        const F2 v = mul2(add2(k, k), o.q);
-        o.s = mul2(mul2(root, kept), lru_p(v));
-        o.ratio = mul2(mul2(inverse, kept), lru_p_inverse(v));
-    } else {                                 // q; 1 / s is finite where s = 0, and is multiplied by q or k = 0 there
-        o.q = kept;
-        const F2 kq = mul2(k, kept), v = add2(kq, kq);
-        F2 m = fma2(v, both(0x1.bb955ap-8f), both(-0x1.4fdc9cp-5f));
-        m = fma2(v, m, both(0x1.5516c6p-3f));
-        m = fma2(v, m, both(-0x1.fffe02p-2f));
-        m = mul2(v, fma2(v, m, both(0x1.fffffep-1f)));
-        const float2 near = unpack2(m), far = unpack2(fma2(mul2(a, both(-1.f)), a, both(1.f))), at = unpack2(v);
-        o.s = sqrt2(pack2(at.x < 0.5f ? near.x : far.x, at.y < 0.5f ? near.y : far.y));
-        o.ratio = mul2(kept, rcp2_finite(o.s));
+__device__ __forceinline__ Parts parts_of(F2 kept, F2 root, F2 a, bool shorter) {
+    const F2 w = shorter ? kept : sqrt2(kept), rw = mul2(root, w), v = mul2(rw, rw);
+    Parts o{mul2(rw, lru_p(v)), shorter ? mul2(w, w) : kept, mul2(w, lru_p_inverse(v))};
+    if (!shorter) {
+        const F2 s = sqrt2(fma2(mul2(a, both(-1.f)), a, both(1.f))), far = mul2(mul2(root, kept), rcp_2(s));
+        const float2 at = unpack2(v), s0 = unpack2(o.s), s1 = unpack2(s), r0 = unpack2(o.ratio), r1 = unpack2(far);
+        o.s = pack2(at.x < 0.5f ? s0.x : s1.x, at.y < 0.5f ? s0.y : s1.y);
+        o.ratio = pack2(at.x < 0.5f ? r0.x : r1.x, at.y < 0.5f ? r0.y : r1.y);
     }
     return o;
 }
@@ -173,6 +165,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             const int ch = t.col * kLruCols + pair * 2, left = p.D - ch;
             const int64_t at = ((int64_t)t.number * p.cols + t.col) * kLruPairs + pair;
             F2 state = t.seq >= 0 ? state2(kept, (int64_t)t.number * p.D + ch, left) : 0;
+            if (RATE) state = neg2(state);
             F2 e = 0;
             bool found = t.to_tail == 0, there = false;
             if (found && t.seq >= 0) e = state2(dh_final, (int64_t)t.seq * p.D + ch, left);
@@ -182,19 +175,25 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                     there = __all_sync(0xffffffffu, bw::mbar_test_wait(&me.ready, turn & 1));
                 }
             if (!there) bw::mbar_wait(&me.ready, turn & 1, chain.err, kDeviceErrTimeout);
-            F2 d = both(1.f), b = both(0.f);
+            // one half joins the gradients' maps from behind, the other the states
+            F2 d = both(1.f), b = both(0.f), decay[kLruWarps], part[kLruWarps];
+#pragma unroll
+            for (int w = 0; w < kLruWarps; ++w) {
+                decay[w] = me.runs[w][pair].decay;
+                part[w] = first ? me.runs[w][pair].back : me.runs[w][pair].own;
+            }
             if (first) {
 #pragma unroll
                 for (int w = kLruWarps - 1; w >= 0; --w) {
                     me.behind[w][pair] = Map{d, b};
-                    b = fma2(me.runs[w][pair].decay, b, me.runs[w][pair].back);
-                    d = mul2(me.runs[w][pair].decay, d);
+                    b = fma2(decay[w], b, part[w]);
+                    d = mul2(decay[w], d);
                 }
-            } else {                                        // meanwhile the states
+            } else {
 #pragma unroll
                 for (int w = 0; w < kLruWarps; ++w) {
                     me.fronts[w][pair] = state;
-                    state = fma2(me.runs[w][pair].decay, state, me.runs[w][pair].own);
+                    state = fma2(decay[w], state, part[w]);
                 }
             }
             d = __shfl_sync(0xffffffffu, d, pair);
@@ -278,39 +277,38 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             }
             F2 e = fma2(me.behind[warp][pair].decay, me.carry[pair], me.behind[warp][pair].back);
             if (!second) e = fma2(decay, e, other);
-            const int64_t at = (plan.t.first + row + kLruRun - 1) * p.D + ch;
-            IO *xp = dx + at, *rp = dr + at, *ip = di + at;
-            const F2 inverse = RATE ? rcp2_finite(root) : 0;
+            int64_t at = (plan.t.first + row + kLruRun - 1) * p.D + ch;
             const auto token = [&](int j, bool by_w, bool all) {
                 e = add2(e, lru_read(from + 2 * N, row + j, pair));
                 const F2 x = lru_read(from + N, row + j, pair);
                 const F2 eg = GATE ? mul2(e, gate[j]) : e, egx = mul2(eg, x), ea = mul2(e, a[j]);
                 F2 dr_, s = part[j];
                 if (RATE) {
-                    const Parts o = parts_of(part[j], k, root, inverse, a[j], by_w);
+                    const Parts o = parts_of(part[j], root, a[j], by_w);
                     s = o.s;
-                    const F2 base = fma2(mul2(mul2(egx, a[j]), a[j]), o.ratio, neg2(mul2(mul2(ea, h[j]), o.q)));   // -dlog a q
+                    // -dlog a q sqrt(2 k); k = sqrt(2 k)^2 / 2
+                    const F2 base = fma2(mul2(mul2(egx, a[j]), a[j]), o.ratio, mul2(mul2(ea, h[j]), mul2(o.q, root)));
                     sum = add2(sum, base);
-                    dr_ = mul2(mul2(base, k), fma2(o.q, both(-1.f), both(1.f)));
+                    dr_ = mul2(mul2(base, root), fma2(o.q, both(-0.5f), both(0.5f)));
                 } else {
                     dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(egx)));
                 }
-                store2(xp, mul2(eg, s), all ? 2 : left, all);
-                store2(rp, dr_, all ? 2 : left, all);
-                if (GATE) store2(ip, mul2(mul2(egx, s), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
+                store2(dx + at, mul2(eg, s), all ? 2 : left, all);
+                store2(dr + at, dr_, all ? 2 : left, all);
+                if (GATE) store2(di + at, mul2(mul2(egx, s), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
                 e = ea;
             };
             if (p.vec && len == kLruTile && left > 0 && (shorter || !RATE)) {
 #pragma unroll
                 for (int j = kLruRun - 1; j >= 0; --j) {
                     token(j, true, true);
-                    xp -= p.D, rp -= p.D, ip -= p.D;
+                    at -= p.D;
                 }
             } else {
 #pragma unroll
                 for (int j = kLruRun - 1; j >= 0; --j) {
                     if (row + j < len) token(j, shorter, false);
-                    xp -= p.D, rp -= p.D, ip -= p.D;
+                    at -= p.D;
                 }
             }
         }
