@@ -41,7 +41,7 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
         r[j] = lru_raw(from, row + j, pair);
         if (GATE) i[j] = lru_raw(from + 3 * N, row + j, pair);
     }
-    const bool shorter = lru_short<RATE, GATE, true>(r, i, k, len - row, left);
+    const bool shorter = lru_short<RATE, GATE, !RATE>(r, i, k, len - row, left);
     if (shorter) {
         const F2 minus = neg2(root);
 #pragma unroll
@@ -54,7 +54,7 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
                     const F2 t2 = one_and_exp(iv);
                     z = rsqrt2(mul2(t1, mul2(t2, t2)));      // w g
                     part[j] = mul2(z, t2);                   // w
-                    gate[j] = mul2(mul2(z, z), mul2(t1, t2));   // g = z^2 t1 t2
+                    gate[j] = rcp_2(t2);
                 } else {
                     z = part[j] = rsqrt2(t1);
                 }
@@ -255,9 +255,14 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             m.own = fma2(a[j], m.own, h[j]);
             m.decay = mul2(m.decay, a[j]);
         }
+        if (len == kLruTile) {
 #pragma unroll
-        for (int j = kLruRun - 1; j >= 0; --j)
-            if (row + j < len) m.back = mul2(a[j], add2(m.back, lru_read(from + 2 * N, row + j, pair)));
+            for (int j = kLruRun - 1; j >= 0; --j) m.back = mul2(a[j], add2(m.back, lru_read(from + 2 * N, row + j, pair)));
+        } else {
+#pragma unroll
+            for (int j = kLruRun - 1; j >= 0; --j)
+                if (row + j < len) m.back = mul2(a[j], add2(m.back, lru_read(from + 2 * N, row + j, pair)));
+        }
         // the warp's other run; the first run passes its states on, the second what it sends back
         const F2 decay = swap_halves(m.decay), other = swap_halves(second ? m.back : m.own);
         const F2 more = swap_halves(second ? m.own : m.back);
@@ -277,38 +282,41 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             }
             F2 e = fma2(me.behind[warp][pair].decay, me.carry[pair], me.behind[warp][pair].back);
             if (!second) e = fma2(decay, e, other);
-            int64_t at = (plan.t.first + row + kLruRun - 1) * p.D + ch;
+            const int64_t tile = plan.t.first * p.D + plan.t.col * kLruCols;      // offsets within a tile have 32 bits
+            IO *const xp = dx + tile, *const rp = dr + tile, *const ip = di + tile;
+            unsigned at = (unsigned)(row + kLruRun - 1) * (unsigned)p.D + pair * 2;
             const auto token = [&](int j, bool by_w, bool all) {
                 e = add2(e, lru_read(from + 2 * N, row + j, pair));
-                const F2 x = lru_read(from + N, row + j, pair);
-                const F2 eg = GATE ? mul2(e, gate[j]) : e, egx = mul2(eg, x), ea = mul2(e, a[j]);
+                const F2 x = lru_read(from + N, row + j, pair), eg = GATE ? mul2(e, gate[j]) : e, ea = mul2(e, a[j]);
                 F2 dr_, s = part[j];
                 if (RATE) {
                     const Parts o = parts_of(part[j], root, a[j], by_w);
                     s = o.s;
-                    // -dlog a q sqrt(2 k); k = sqrt(2 k)^2 / 2
-                    const F2 base = fma2(mul2(mul2(egx, a[j]), a[j]), o.ratio, mul2(mul2(ea, h[j]), mul2(o.q, root)));
+                    // -dlog a q sqrt(2 k) = e a (a g x q / s - h q) sqrt(2 k); k = sqrt(2 k)^2 / 2
+                    const F2 gxa = mul2(GATE ? mul2(gate[j], x) : x, a[j]);
+                    const F2 base = mul2(ea, fma2(gxa, o.ratio, mul2(h[j], mul2(o.q, root))));
                     sum = add2(sum, base);
                     dr_ = mul2(mul2(base, root), fma2(o.q, both(-0.5f), both(0.5f)));
                 } else {
-                    dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(egx)));
+                    dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(mul2(eg, x))));
                 }
-                store2(dx + at, mul2(eg, s), all ? 2 : left, all);
-                store2(dr + at, dr_, all ? 2 : left, all);
-                if (GATE) store2(di + at, mul2(mul2(egx, s), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
+                const F2 dx_ = mul2(eg, s);
+                store2(xp + at, dx_, all ? 2 : left, all);
+                store2(rp + at, dr_, all ? 2 : left, all);
+                if (GATE) store2(ip + at, mul2(mul2(dx_, x), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
                 e = ea;
             };
             if (p.vec && len == kLruTile && left > 0 && (shorter || !RATE)) {
 #pragma unroll
                 for (int j = kLruRun - 1; j >= 0; --j) {
                     token(j, true, true);
-                    at -= p.D;
+                    at -= (unsigned)p.D;
                 }
             } else {
 #pragma unroll
                 for (int j = kLruRun - 1; j >= 0; --j) {
                     if (row + j < len) token(j, shorter, false);
-                    at -= p.D;
+                    at -= (unsigned)p.D;
                 }
             }
         }
