@@ -239,28 +239,41 @@ lru_chain_kernel(uint4* __restrict__ words, int64_t n, const float* __restrict__
         for (int64_t ch = at; ch < channels; ch += step) rates[ch] = ch < D ? rates_of(lam[ch], c) : float4{};
 }
 
+// A thread takes four neighbouring channels of a row; quads: whole vectors of them are aligned in every tensor.
 template <typename IO, bool RATE, bool GATE>
 __global__ void __launch_bounds__(128)
-lru_step_kernel(Lru p, int64_t rows, int64_t pool, const int* __restrict__ slots, float* __restrict__ h, IO* __restrict__ y) {
-    const int ch = (blockIdx.x * 128 + threadIdx.x) * 2, left = p.D - ch;
+lru_step_kernel(Lru p, int64_t rows, int64_t pool, const int* __restrict__ slots, float* __restrict__ h, IO* __restrict__ y,
+                bool quads) {
+    const int ch = (blockIdx.x * 128 + threadIdx.x) * 4, left = p.D - ch;
     if (left <= 0) return;
-    const auto in_pairs = [](const LruRows& v) { return v.unit >= (sizeof(IO) == 2 ? 4 : 16); };
-    F2 k = 0;
-    if (RATE) k = pack2(rate_of(p.lam[ch], p.c), left > 1 ? rate_of(p.lam[ch + 1], p.c) : 0.f);
+    F2 k[2] = {0, 0};
+    if (RATE)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            k[c] = pack2(left > 2 * c ? rate_of(p.lam[ch + 2 * c], p.c) : 0.f, left > 2 * c + 1 ? rate_of(p.lam[ch + 2 * c + 1], p.c) : 0.f);
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         const int64_t slot = slots ? slots[row] : row;
-        IO* yp = y + row * p.D + ch;
-        if (slot < 0 || slot >= pool) {
-            store2(yp, both(0.f), left, p.vec);
-            continue;
+        const bool some = slot >= 0 && slot < pool;
+        float* hp = h + slot * p.D + ch;
+        float out[4] = {0.f, 0.f, 0.f, 0.f};
+        if (some) {
+            const auto in = [&](const LruRows& v) { return load_n<4>((const IO*)v.p + row * v.ld + ch, left, quads); };
+            const RawN<IO, 4> r = in(p.r), x = in(p.x), i = GATE ? in(p.i) : r;
+            const RawN<float, 4> old = load_own<4>(hp, left, quads);
+            F2 rv[2], xv[2], iv[2];
+            pairs<IO, 4>(r, rv), pairs<IO, 4>(x, xv), pairs<IO, 4>(i, iv);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                F2 a, s, q;
+                decay_and_part<RATE>(rv[c], k[c], a, s, q);
+                F2 u = mul2(s, xv[c]);
+                if (GATE) u = mul2(u, sigmoid2(iv[c]));
+                const float2 n = unpack2(fma2(a, pack2(old.e[2 * c], old.e[2 * c + 1]), u));
+                out[2 * c] = n.x, out[2 * c + 1] = n.y;
+            }
+            store_n(hp, out, left, quads);
         }
-        F2 a, s, q;
-        decay_and_part<RATE>(wide2(load2((const IO*)p.r.p + row * p.r.ld + ch, left, in_pairs(p.r))), k, a, s, q);
-        F2 u = mul2(s, wide2(load2((const IO*)p.x.p + row * p.x.ld + ch, left, in_pairs(p.x))));
-        if (GATE) u = mul2(u, sigmoid2(wide2(load2((const IO*)p.i.p + row * p.i.ld + ch, left, in_pairs(p.i)))));
-        const F2 n = fma2(a, state2(h, slot * p.D + ch, left), u);
-        put_state2(h, slot * p.D + ch, n, left);
-        store2(yp, n, left, p.vec);
+        store_n(y + row * p.D + ch, out, left, quads);
     }
 }
 
@@ -310,13 +323,16 @@ cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float
 
 cudaError_t lru_step(const LruArgs& args, const LruTensors& t, int64_t pool, const int* slots, float* h, void* y,
                      cudaStream_t s) {
-    Lru p = lru_of(args, t, kGroups);
-    p.vec = lru_pairs(y, args.D, args.io == GDR_F32 ? 4 : 2);
-    const dim3 grid((unsigned)((args.D + 255) / 256), (unsigned)std::min<int64_t>(args.n, 65535));
+    const Lru p = lru_of(args, t, kGroups);
+    const int64_t e = args.io == GDR_F32 ? 4 : 2;
+    bool quads = args.D % 4 == 0 && reinterpret_cast<uintptr_t>(h) % 16 == 0 && reinterpret_cast<uintptr_t>(y) % (4 * e) == 0;
+    for (const LruRows* v : {&p.x, &p.r, &p.i})
+        quads = quads && reinterpret_cast<uintptr_t>(v->p) % (4 * e) == 0 && (!v->p || v->ld % 4 == 0);
+    const dim3 grid((unsigned)((args.D + 511) / 512), (unsigned)std::min<int64_t>(args.n, 65535));
     return lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
         lru_step_kernel<IO, decltype(rate)::value, decltype(gate)::value>
-            <<<grid, 128, 0, s>>>(p, args.n, pool, slots, h, (IO*)y);
+            <<<grid, 128, 0, s>>>(p, args.n, pool, slots, h, (IO*)y, quads);
         return cudaGetLastError();
     });
 }

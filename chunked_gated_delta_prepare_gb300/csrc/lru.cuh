@@ -66,17 +66,6 @@ constexpr float kLruLean = 8e-9f;
 
 __device__ __forceinline__ F2 neg2(F2 v) { return v ^ 0x8000000080000000ull; }
 
-template <typename IO> __device__ __forceinline__ RawN<IO, 2> load2(const IO* p, int left, bool vec) {
-    RawN<IO, 2> r;
-    if (vec && left >= 2) {
-        if constexpr (sizeof(IO) == 4) *reinterpret_cast<uint2*>(&r) = __ldg(reinterpret_cast<const uint2*>(p));
-        else *reinterpret_cast<uint32_t*>(&r) = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-        r.e[0] = left > 0 ? p[0] : from_f<IO>(0.f);
-        r.e[1] = left > 1 ? p[1] : from_f<IO>(0.f);
-    }
-    return r;
-}
 template <typename IO> __device__ __forceinline__ void store2(IO* p, F2 v, int left, bool vec) {
     const float2 f = unpack2(v);
     RawN<IO, 2> r;
@@ -121,11 +110,10 @@ __device__ __forceinline__ F2 sqrt2(F2 v) {
 __device__ __forceinline__ float rate_of(float lam, float c) {
     return c * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam))));     // a NaN comes through the logarithm
 }
-// k, sqrt(2 k), and k's slope by lam over sqrt(2 k).
+// k, sqrt(2 k), k's slope by lam over 2 k, and -1 / (4 k); the last two zero for a channel that neither forgets nor takes.
 __device__ __forceinline__ float4 rates_of(float lam, float c) {
-    const float k = rate_of(lam, c);
-    const float root = sqrtf(2.f * k);
-    return make_float4(k, root, c / (1.f + expf(-lam)) / fmaxf(root, 1e-30f), 0.f);
+    const float k = rate_of(lam, c), slope = c / (1.f + expf(-lam));
+    return make_float4(k, sqrtf(2.f * k), k > 1e-37f ? slope / (2.f * k) : 0.f, k > 1e-37f ? -0.25f / k : 0.f);
 }
 
 // A token's decay a and input's part s; q = sigmoid(r).
@@ -357,7 +345,7 @@ constexpr int kLruPlans = 4;
 struct LruPlan {
     LruTile t;
     bool live;               // there is one
-    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];      // rates_of; BACK: the last
+    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols], inverses[kLruCols];       // rates_of
 };
 // The guide's: a channel's rates are read four tiles ahead and a tile planned three ahead, after the present one's state is
 // out, so that no way to memory holds anyone up.
@@ -383,7 +371,7 @@ template <bool BACK, bool RATE, int GROUPS> struct LruPlanner {
             if (RATE) {
                 plan->rates[lane] = rate.x;
                 plan->roots[lane] = rate.y;
-                if (BACK) plan->slopes[lane] = rate.z;
+                if (BACK) plan->slopes[lane] = rate.z, plan->inverses[lane] = rate.w;
             }
         }
         read(p, c, turn + 1);
@@ -422,15 +410,15 @@ __device__ __forceinline__ void lru_tma(IO* to, const CUtensorMap* map, uint64_t
 
 // ---------------------------------------------------------------- inputs
 
-// Rows that TMA does not take, those that do not start on 16-byte boundaries, are copied by the workers in units of 4 bytes
-// or by elements.
-__device__ __forceinline__ void lru_copy(void* to, const void* from, int bytes) {
+// Without TMA the workers copy: rows on 16-byte boundaries in such units, others in units of 4 bytes or by elements.
+template <int UNIT> __device__ __forceinline__ void lru_copy(void* to, const void* from, int bytes) {
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+    if (UNIT == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
 }
-template <typename IO>
+template <typename IO, int UNIT>
 __device__ __forceinline__ void lru_fetch_units(const LruRows& v, const LruTile& t, int D, int thread, IO* to) {
-    constexpr int per = 4 / (int)sizeof(IO), pieces = kLruCols / per, step = kLruWorkers / pieces;
+    constexpr int per = UNIT / (int)sizeof(IO), pieces = kLruCols / per, step = kLruWorkers / pieces;
     const int piece = thread % pieces, ch = t.col * kLruCols + piece * per;
     const int bytes = min(per, D - ch) * (int)sizeof(IO);
     if (bytes <= 0) return;
@@ -438,15 +426,17 @@ __device__ __forceinline__ void lru_fetch_units(const LruRows& v, const LruTile&
 #pragma unroll
     for (int k = 0; k < kLruTile / step; ++k) {
         const int row = thread / pieces + k * step;
-        if (row < t.len) lru_copy(to + row * kLruCols + piece * per, from, bytes);
+        if (row < t.len) lru_copy<UNIT>(to + row * kLruCols + piece * per, from, bytes);
         from += step * v.ld;
     }
 }
 // A tile of a tensor on its way into shared memory, by the workers; rows past the tile's end stay what they were.
 template <typename IO>
 __device__ __forceinline__ void lru_fetch(const LruRows& v, const LruTile& t, int D, int thread, IO* to) {
-    if (sizeof(IO) == 4 || v.unit >= 4) {
-        lru_fetch_units<IO>(v, t, D, thread, to);
+    if (v.unit == 16) {
+        lru_fetch_units<IO, 16>(v, t, D, thread, to);
+    } else if (sizeof(IO) == 4 || v.unit >= 4) {
+        lru_fetch_units<IO, 4>(v, t, D, thread, to);
     } else {
         constexpr int step = kLruWorkers / kLruPairs, most = kLruTile / step;
         const int piece = thread % kLruPairs, ch = t.col * kLruCols + piece * 2, row0 = thread / kLruPairs;

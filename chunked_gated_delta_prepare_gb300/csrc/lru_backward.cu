@@ -28,7 +28,7 @@ struct alignas(16) Map {     // what tokens make of the gradient e from behind t
 };
 
 // The decays and terms of the thread's run, from shared memory, and what the gradients need beside them: the input's part s
-// (RATE: q, or by the shorter formulas w = sqrt(q)), and the gate.  RATE: the terms, and so all states here, have the other
+// (RATE: sqrt(v), v = 2 k q), and the gate.  RATE: the terms, and so all states here, have the other
 // sign, which saves the gradients a negation.  A token past the tile's end has a = 1, u = 0.
 template <typename IO, bool RATE, bool GATE>
 __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k, F2 root, int len, int left,
@@ -52,13 +52,14 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
                 F2 z;
                 if (GATE) {
                     const F2 t2 = one_and_exp(iv);
-                    z = rsqrt2(mul2(t1, mul2(t2, t2)));      // w g
-                    part[j] = mul2(z, t2);                   // w
+                    z = rsqrt2(mul2(t1, mul2(t2, t2)));      // sqrt(q) g
+                    part[j] = mul2(mul2(z, root), t2);
                     gate[j] = rcp_2(t2);
                 } else {
-                    z = part[j] = rsqrt2(t1);
+                    z = rsqrt2(t1);
+                    part[j] = mul2(root, z);
                 }
-                const F2 rw = mul2(root, part[j]), v = mul2(rw, rw);
+                const F2 v = mul2(part[j], part[j]);
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(minus, x));
             } else {
@@ -82,7 +83,7 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
             decay_and_part<RATE>(wide2(r[j]), k, a[j], s, q);
             u[j] = mul2(RATE ? neg2(s) : s, lru_read(from + N, row + j, pair));
             if (GATE) gate[j] = sigmoid2(wide2(i[j])), u[j] = mul2(u[j], gate[j]);
-            part[j] = RATE ? q : s;
+            part[j] = RATE ? mul2(root, sqrt2(q)) : s;
         }
     }
     if (len < kLruTile)
@@ -92,15 +93,15 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
     return shorter;
 }
 
-// RATE: s, q and sqrt(2 k) q / s of a token, the last by w / P(v) where 1 - a^2 cancels: finite where s is zero.
+// RATE: v = 2 k q of a token, s and v / s, the last two by P(v) where 1 - a^2 cancels: finite where s is zero.
 struct Parts {
-    F2 s, q, ratio;
+    F2 v, s, ratio;
 };
-__device__ __forceinline__ Parts parts_of(F2 kept, F2 root, F2 a, bool shorter) {
-    const F2 w = shorter ? kept : sqrt2(kept), rw = mul2(root, w), v = mul2(rw, rw);
-    Parts o{mul2(rw, lru_p(v)), shorter ? mul2(w, w) : kept, mul2(w, lru_p_inverse(v))};
+__device__ __forceinline__ Parts parts_of(F2 rw, F2 a, bool shorter) {
+    const F2 v = mul2(rw, rw);
+    Parts o{v, mul2(rw, lru_p(v)), mul2(rw, lru_p_inverse(v))};
     if (!shorter) {
-        const F2 s = sqrt2(fma2(mul2(a, both(-1.f)), a, both(1.f))), far = mul2(mul2(root, kept), rcp_2(s));
+        const F2 s = sqrt2(fma2(mul2(a, both(-1.f)), a, both(1.f))), far = mul2(v, rcp_2(s));
         const float2 at = unpack2(v), s0 = unpack2(o.s), s1 = unpack2(s), r0 = unpack2(o.ratio), r1 = unpack2(far);
         o.s = pack2(at.x < 0.5f ? s0.x : s1.x, at.y < 0.5f ? s0.y : s1.y);
         o.ratio = pack2(at.x < 0.5f ? r0.x : r1.x, at.y < 0.5f ? r0.y : r1.y);
@@ -280,6 +281,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                 h[j] = state;                               // the state in front of the token
                 state = after;
             }
+            const F2 half_inverse = RATE ? *reinterpret_cast<const F2*>(plan.inverses + pair * 2) : 0;     // -1 / (4 k)
             F2 e = fma2(me.behind[warp][pair].decay, me.carry[pair], me.behind[warp][pair].back);
             if (!second) e = fma2(decay, e, other);
             const int64_t tile = plan.t.first * p.D + plan.t.col * kLruCols;      // offsets within a tile have 32 bits
@@ -290,13 +292,13 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                 const F2 x = lru_read(from + N, row + j, pair), eg = GATE ? mul2(e, gate[j]) : e, ea = mul2(e, a[j]);
                 F2 dr_, s = part[j];
                 if (RATE) {
-                    const Parts o = parts_of(part[j], root, a[j], by_w);
+                    const Parts o = parts_of(part[j], a[j], by_w);
                     s = o.s;
-                    // -dlog a q sqrt(2 k) = e a (a g x q / s - h q) sqrt(2 k); k = sqrt(2 k)^2 / 2
+                    // -dlog a v = e a (a g x v / s - h v); dr is that times (1 - q) / 2
                     const F2 gxa = mul2(GATE ? mul2(gate[j], x) : x, a[j]);
-                    const F2 base = mul2(ea, fma2(gxa, o.ratio, mul2(h[j], mul2(o.q, root))));
+                    const F2 base = mul2(ea, fma2(gxa, o.ratio, mul2(h[j], o.v)));
                     sum = add2(sum, base);
-                    dr_ = mul2(mul2(base, root), fma2(o.q, both(-0.5f), both(0.5f)));
+                    dr_ = mul2(base, fma2(o.v, half_inverse, both(0.5f)));
                 } else {
                     dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(mul2(eg, x))));
                 }
