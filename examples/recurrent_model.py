@@ -4,10 +4,11 @@ and training steps.
     python examples/recurrent_model.py
 
 Each layer is  residual + norm -> input projection -> short convolution -> recurrence -> output projection, the
-recurrence being the gated delta rule or the selective state space scan.  Serving takes the norm's 8-bit output: a
-row's scale commutes with the projection, so it is applied to the product (in bf16 here: torch's product widens the
-values first, so the 8 bits save no time in this example).  Decoding continues from the states the
-prompt left, and its logits are those of the whole sequence run as a prompt.
+recurrence being the gated delta rule, the selective state space scan or the gated linear recurrence.  Serving takes
+the norm's 8-bit output: a row's scale commutes with the projection, so it is applied to the product (in bf16 here:
+torch's product widens the values first, so the 8 bits save no time in this example).  A layer of the gated linear
+recurrence has a layer norm in front, and a gated norm of each head behind the recurrence.  Decoding continues from the
+states the prompt left, and its logits are those of the whole sequence run as a prompt.
 """
 import os
 import sys
@@ -76,10 +77,52 @@ class Scan(torch.autograd.Function):
         return d.dx, d.ddt, d.dA, d.dB, d.dC, d.dD, d.dz, d.ddt_bias
 
 
+class LayerNorm(torch.autograd.Function):
+    """(y, r) of the layer norm with the residual's addition."""
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual):
+        y, r = layer.layernorm_forward(x, weight, bias, residual)
+        ctx.save_for_backward(r, weight)
+        return y, r
+
+    @staticmethod
+    def backward(ctx, dy, dr):
+        r, weight = ctx.saved_tensors
+        dx, dw, db = layer.layernorm_backward(dy, r, weight, dr)
+        return dx, dw.to(weight.dtype), db.to(weight.dtype), dx
+
+
+class Recurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, i, lam):
+        y, _, kept = layer.lru_forward(x, r, i, lam, want_h_final=False, want_kept=True)
+        ctx.save_for_backward(x, r, i, lam, kept)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, r, i, lam, kept = ctx.saved_tensors
+        d = layer.lru_backward(x, r, i, lam, dy, kept=kept)
+        return d.dx, d.dr, d.di, d.dlam
+
+
+class GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, z, weight):
+        ctx.save_for_backward(x, z, weight)
+        return layer.gated_norm_forward(x, z, weight)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, z, weight = ctx.saved_tensors
+        dx, dz, dw = layer.gated_norm_backward(dy, x, z, weight)
+        return dx, dz, dw.to(weight.dtype)
+
+
 # ---------------------------------------------------------------- layers
 
 class Layer:
-    """One recurrent layer's weights; `kind` is "delta" or "ssm"."""
+    """One recurrent layer's weights; `kind` is "delta", "ssm" or "lru"."""
 
     def __init__(self, kind, gen):
         def weight(*shape, scale=None):
@@ -92,6 +135,13 @@ class Layer:
             self.channels = 3 * HEADS * HEAD
             self.inp = weight(self.channels + 2 * HEADS, DIM)          # q, k, v, then the gate's and beta's logits
             self.out = weight(DIM, HEADS * HEAD)
+        elif kind == "lru":
+            self.channels = INNER
+            self.inp = weight(4 * INNER, DIM)                          # x, the two gates' logits, z
+            self.norm_bias = torch.zeros(DIM, dtype=IO, device="cuda")
+            self.lam = torch.linspace(-9.0, -4.3, INNER, device="cuda")   # decays of 0.999 to 0.9 at an open gate
+            self.gain = torch.ones(HEAD, dtype=IO, device="cuda")
+            self.out = weight(DIM, INNER)
         else:
             self.channels = INNER
             self.inp = weight(2 * INNER, DIM)                          # x, z
@@ -108,7 +158,7 @@ class Layer:
 
     def new_states(self, slots):
         conv = torch.zeros(slots, TAPS - 1, self.channels, dtype=IO, device="cuda")
-        shape = (HEADS, HEAD, HEAD) if self.kind == "delta" else (INNER, STATES)
+        shape = {"delta": (HEADS, HEAD, HEAD), "ssm": (INNER, STATES), "lru": (INNER,)}[self.kind]
         return conv, torch.zeros(slots, *shape, device="cuda")
 
     def delta_inputs(self, conv, logits):
@@ -124,8 +174,12 @@ class Layer:
 
     def serve(self, x, residual, states, cu=None, slots=None):
         """Packed prompts [total, DIM] (cu), whose final states go to the pool's slots, or one token of each row."""
-        _, r, x8, scale = layer.norm_forward(x, self.norm, residual, quant="row", want_y=False)
-        p = ((x8.to(IO) @ self.inp.t()).float() * scale).to(IO)
+        if self.kind == "lru":
+            y, r = layer.layernorm_forward(x, self.norm, self.norm_bias, residual)
+            p = y @ self.inp.t()
+        else:
+            _, r, x8, scale = layer.norm_forward(x, self.norm, residual, quant="row", want_y=False)
+            p = ((x8.to(IO) @ self.inp.t()).float() * scale).to(IO)
         conv_states, pool = states
         c = p[:, :self.channels]
         if cu is not None:
@@ -141,6 +195,14 @@ class Layer:
                 pool[slots.long()] = h
             else:
                 o = layer.delta_step(q, k, v, g, beta, pool, slots=slots)
+        elif self.kind == "lru":
+            gate, inlet, z = rest.split(INNER, -1)
+            if cu is not None:
+                o, h, _ = layer.lru_forward(c, gate, inlet, self.lam, cu_seqlens=cu)
+                pool[slots.long()] = h
+            else:
+                o = layer.lru_step(c, gate, inlet, self.lam, pool, slots=slots)
+            o = layer.gated_norm_forward(o.unflatten(-1, (-1, HEAD)), z.unflatten(-1, (-1, HEAD)), self.gain)
         else:
             first, more = self.scan_inputs(c, rest)
             if cu is not None:
@@ -152,12 +214,17 @@ class Layer:
 
     def train(self, x, residual):
         """x, residual [B, T, DIM] -> the layer's output and the new residual."""
-        y, r = Norm.apply(x, self.norm, residual)
+        y, r = (LayerNorm.apply(x, self.norm, self.norm_bias, residual) if self.kind == "lru"
+                else Norm.apply(x, self.norm, residual))
         p = y @ self.inp.t()
         c = Conv.apply(p[..., :self.channels], self.taps, self.bias)
         rest = p[..., self.channels:]
         if self.kind == "delta":
             o = Delta.apply(*self.delta_inputs(c, rest))
+        elif self.kind == "lru":
+            gate, inlet, z = rest.split(INNER, -1)
+            o = Recurrence.apply(c, gate, inlet, self.lam)
+            o = GatedNorm.apply(o.unflatten(-1, (-1, HEAD)), z.unflatten(-1, (-1, HEAD)), self.gain)
         else:
             (x, dt, A, B, C), (D, z, dt_bias) = self.scan_inputs(c, rest)
             o = Scan.apply(x, dt, A, B, C, D, z, dt_bias)
@@ -246,7 +313,7 @@ def train(model, steps=20, lr=0.05, seed=2):
 
 
 def main():
-    model = Model()
+    model = Model(("delta", "ssm", "lru"))
     gap, top = decode_gap(model)
     print(f"decoding against the whole prompt: logits differ by at most {gap:.3f} of {top:.1f}")
     losses = train(model)
