@@ -102,29 +102,32 @@ template <typename IO, int T> struct Ring {
     }
 };
 
-// The thread's vector of 8 columns from column c = 8 i - shift on; zeros outside the row.
+// The thread's vector of 8 columns from column c = 8 i - shift on; zeros outside the row.  Rows that are not cut have zeros
+// behind them (clear_ends), so that no thread asks where they end.
 template <typename IO, bool CUT>
 __device__ __forceinline__ Raw8<IO> ring_vector(const IO* row, int i, int c, int D, const IO* global, int copied) {
     Raw8<IO> r;
-    if (CUT ? c >= D : c + 8 > D) {
-        if (!CUT && c < D) {                   // fp32 rows of 4 columns more than a multiple of 8
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r.e[j] = c + j < D ? row[8 * i + j] : from_f<IO>(0.f);
-            return r;
-        }
-        return load8((const IO*)nullptr, 0, false);
-    }
+    if (CUT && c >= D) return load8((const IO*)nullptr, 0, false);
     if (CUT && 8 * i + 8 > copied) return load_cut(global, c, D, false);
+    const IO* from = row + (CUT ? 8 * i : min(c, D));
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(r) / 16; ++k)
-        reinterpret_cast<uint4*>(&r)[k] = reinterpret_cast<const uint4*>(row + 8 * i)[k];
+    for (int k = 0; k < (int)sizeof(r) / 16; ++k) reinterpret_cast<uint4*>(&r)[k] = reinterpret_cast<const uint4*>(from)[k];
     if (CUT) mask_cut(r, c, D);
     return r;
 }
+// The 32 bytes behind each of n rows that are not cut.
+__device__ __forceinline__ void clear_ends(unsigned char* smem, int n, uint32_t pitch, uint32_t bytes, int threads) {
+    for (int i = threadIdx.x; i < 2 * n; i += threads)
+        *reinterpret_cast<uint4*>(smem + (i >> 1) * pitch + bytes + (i & 1) * 16) = make_uint4(0, 0, 0, 0);
+}
 
-// Zeroes the columns of a vector from column c on that lie outside the row.
-__device__ __forceinline__ void keep_columns(F2 (&v)[4], int c, int D) {
-    if (c < 0 || c + 8 > D)
+// v + less in the columns of the row, zero outside.
+template <typename IO, bool CUT> __device__ __forceinline__ void shift_columns(F2 (&v)[4], float less, int c, int D) {
+    // not cut: whole halves of a vector, or (16 bits) whole vectors, are there or not
+    const float lo = CUT || c < D ? less : 0.f, hi = CUT ? less : sizeof(IO) == 2 ? lo : c + 4 < D ? less : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = add2(v[k], both(k < 2 ? lo : hi));
+    if (CUT && (c < 0 || c + 8 > D))
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 f = unpack2(v[k]);
@@ -136,14 +139,20 @@ __device__ __forceinline__ float both_halves(F2 v) {
     const float2 f = unpack2(v);
     return f.x + f.y;
 }
-template <typename IO> __device__ __forceinline__ void store_pairs(IO* row, const F2 (&v)[4], int c, int D) {
+template <typename IO, bool CUT> __device__ __forceinline__ void store_pairs(IO* row, const F2 (&v)[4], int c, int D) {
     float x[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float2 f = unpack2(v[k]);
         x[2 * k] = f.x, x[2 * k + 1] = f.y;
     }
-    store_cut(row, x, c, D, true);
+    if (CUT) return store_cut(row, x, c, D, true);
+    Raw8<IO> r;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) from_f2(r.e + i, x[i], x[i + 1]);
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(r) / 16; ++k)
+        if (c + 4 * k < D) reinterpret_cast<uint4*>(row + c)[k] = reinterpret_cast<const uint4*>(&r)[k];
 }
 
 template <typename IO, int WARPS, int VPT, bool CUT>
@@ -157,6 +166,7 @@ layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restri
     __shared__ uint64_t full[P][kMaxStages];
     const int tid = threadIdx.x % tpr, place = threadIdx.x / tpr, D = a.D;
     for (int i = threadIdx.x; i < 4 * kRedSlots<WARPS, P>; i += NT) (&red[0][0][0][0])[i] = 0.f;
+    if (!CUT) clear_ends(smem, P * stages * 2, pitch, D * (uint32_t)sizeof(IO), NT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < P * kMaxStages; ++i) bw::mbar_init(&full[0][0] + i, 1);
         bw::fence_mbar_init();
@@ -191,7 +201,7 @@ layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restri
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i][k] = add2(v[i][k], t[k]);
             }
-            if (r) store_pairs(r + row * D, v[i], c, D);
+            if (r) store_pairs<IO, CUT>(r + row * D, v[i], c, D);
 #pragma unroll
             for (int k = 0; k < 4; ++k) part = add2(part, v[i][k]);
         }
@@ -199,13 +209,10 @@ layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restri
         place_sum<WARPS, 1>(sum, red[turn & 1][0]);
         if (tid == 0) ring.issue(row + stages * step, stage, CUT);          // every thread has read the stage
         if (++stage == stages) stage = 0, phase ^= 1;
-        const F2 less = both(-sum[0] * over);
         part = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] = add2(v[i][k], less);
-            keep_columns(v[i], (tid + i * tpr) * 8 - shift, D);
+            shift_columns<IO, CUT>(v[i], -sum[0] * over, (tid + i * tpr) * 8 - shift, D);
 #pragma unroll
             for (int k = 0; k < 4; ++k) part = fma2(v[i][k], v[i][k], part);
         }
@@ -219,7 +226,7 @@ layernorm_ring_kernel(NormArgs a, RowTensor x, RowTensor res, const IO* __restri
             pairs<IO, 8>(wr[i], wf), pairs<IO, 8>(br[i], bf);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = fma2(mul2(v[i][k], rstd), wf[k], bf[k]);
-            store_pairs(y + row * D, v[i], (tid + i * tpr) * 8 - shift, D);
+            store_pairs<IO, CUT>(y + row * D, v[i], (tid + i * tpr) * 8 - shift, D);
         }
     }
 }
@@ -236,6 +243,7 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
     __shared__ uint64_t full[P][kMaxStages];
     const int tid = threadIdx.x % tpr, place = threadIdx.x / tpr, D = a.D;
     for (int i = threadIdx.x; i < 8 * kRedSlots<WARPS, P>; i += NT) (&red[0][0][0][0])[i] = 0.f;
+    if (!CUT) clear_ends(smem, P * stages * 3, pitch, D * (uint32_t)sizeof(IO), NT);
     if (threadIdx.x == 0) {
         for (int i = 0; i < P * kMaxStages; ++i) bw::mbar_init(&full[0][0] + i, 1);
         bw::fence_mbar_init();
@@ -278,15 +286,13 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
         place_sum<WARPS, 2>(one, red[turn & 1][0]);
         // every thread is done with the row before: its stage is free
         if (tid == 0 && turn > 0) ring.issue(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1, CUT);
-        const F2 less = both(-one[0] * over), flat = both(-one[1] * over);
+        const F2 flat = both(-one[1] * over);
         p0 = p1 = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             F2 wf[4];
             pairs<IO, 8>(wr[i], wf);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[i][k] = add2(s[i][k], less);
-            keep_columns(s[i], (tid + i * tpr) * 8 - shift, D);
+            shift_columns<IO, CUT>(s[i], -one[0] * over, (tid + i * tpr) * 8 - shift, D);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 p0 = fma2(s[i][k], s[i][k], p0);
@@ -310,7 +316,7 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
                 dw[i][k] = fma2(g[i][k], mul2(s[i][k], rstd), dw[i][k]);
                 db[i][k] = add2(db[i][k], g[i][k]);
             }
-            store_pairs(dx + row * D, o, c, D);
+            store_pairs<IO, CUT>(dx + row * D, o, c, D);
         }
         if (++stage == stages) stage = 0, phase ^= 1;
     }
