@@ -255,11 +255,10 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
     if (tid == 0)
         for (int k = 0; k < stages; ++k) ring.issue(first + k * step, k, CUT);
     const int shift = CUT ? first_shift<IO>(first, D) : 0;
-    Raw8<IO> wr[VPT];
-    F2 dw[VPT][4], db[VPT][4];
+    F2 wf[VPT][4], dw[VPT][4], db[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        wr[i] = load_cut(w, (tid + i * tpr) * 8 - shift, D, vec_w && shift == 0);
+        pairs<IO, 8>(load_cut(w, (tid + i * tpr) * 8 - shift, D, vec_w && shift == 0), wf[i]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) dw[i][k] = db[i][k] = both(0.f);
     }
@@ -272,14 +271,12 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int n = tid + i * tpr, c = n * 8 - shift;
-            F2 wf[4];
             pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 0), n, c, D, dy + row * D, copied), g[i]);
             pairs<IO, 8>(ring_vector<IO, CUT>(ring.at(stage, 1), n, c, D, r + row * D, copied), s[i]);
-            pairs<IO, 8>(wr[i], wf);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 p0 = add2(p0, s[i][k]);
-                p1 = fma2(wf[k], g[i][k], p1);
+                p1 = fma2(wf[i][k], g[i][k], p1);
             }
         }
         float one[2] = {both_halves(p0), both_halves(p1)};
@@ -290,13 +287,11 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
         p0 = p1 = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            F2 wf[4];
-            pairs<IO, 8>(wr[i], wf);
             shift_columns<IO, CUT>(s[i], -one[0] * over, (tid + i * tpr) * 8 - shift, D);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 p0 = fma2(s[i][k], s[i][k], p0);
-                p1 = fma2(mul2(wf[k], g[i][k]), s[i][k], p1);
+                p1 = fma2(mul2(wf[i][k], g[i][k]), s[i][k], p1);
             }
         }
         float two[2] = {both_halves(p0), both_halves(p1)};
@@ -306,13 +301,12 @@ layernorm_backward_ring_kernel(NormArgs a, const IO* __restrict__ dy, const IO* 
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int n = tid + i * tpr, c = n * 8 - shift;
-            F2 wf[4], o[4];
-            pairs<IO, 8>(wr[i], wf);
+            F2 o[4];
             pairs<IO, 8>(dr ? ring_vector<IO, CUT>(ring.at(stage, 2), n, c, D, dr + row * D, copied)
                             : load8((const IO*)nullptr, 0, false), o);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                o[k] = fma2(rstd, fma2(s[i][k], back, fma2(wf[k], g[i][k], flat)), o[k]);
+                o[k] = fma2(rstd, fma2(s[i][k], back, fma2(wf[i][k], g[i][k], flat)), o[k]);
                 dw[i][k] = fma2(g[i][k], mul2(s[i][k], rstd), dw[i][k]);
                 db[i][k] = add2(db[i][k], g[i][k]);
             }
