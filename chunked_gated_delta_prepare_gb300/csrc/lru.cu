@@ -96,7 +96,7 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
             uint64_t* bar = me.full + turn % B;
             IO* to = in + (turn % B) * IN * N;
             if (t.len == 0) return bw::mbar_arrive(bar);
-            bw::mbar_arrive_expect_tx(bar, IN * N * sizeof(IO));
+            bw::mbar_arrive_expect_tx(bar, in_maps.rows * IN * kLruCols * (unsigned)sizeof(IO));
             lru_tma(to, &in_maps.r, bar, t);
             lru_tma(to + N, &in_maps.x, bar, t);
             if (GATE) lru_tma(to + 2 * N, &in_maps.i, bar, t);
@@ -185,20 +185,23 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
         }
         const LruPlan& plan = plans[turn % kLruPlans];
         const int len = plan.t.len, ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch;
+        const bool some = warp * 2 * kLruRun < len;         // short sequences leave warps without a token: 2000 of 16 x 4096
+                                                            // take half the time of going through them all
         F2 a[kLruRun], u[kLruRun];
-        {
+        Map m{both(1.f), both(0.f)};
+        if (some) {
             F2 k = 0, root = 0;
             if (RATE) {
                 k = *reinterpret_cast<const F2*>(plan.rates + pair * 2);
                 root = *reinterpret_cast<const F2*>(plan.roots + pair * 2);
             }
             read_run<IO, RATE, GATE>(in + (turn % B) * IN * N, row, pair, k, root, len, left, a, u);
-        }
-        Map m{a[0], u[0]};
+            m = Map{a[0], u[0]};
 #pragma unroll
-        for (int j = 1; j < kLruRun; ++j) {
-            m.own = fma2(a[j], m.own, u[j]);
-            m.decay = mul2(a[j], m.decay);
+            for (int j = 1; j < kLruRun; ++j) {
+                m.own = fma2(a[j], m.own, u[j]);
+                m.decay = mul2(a[j], m.decay);
+            }
         }
         Map o{swap_halves(m.decay), swap_halves(m.own)};    // of the warp's other run
         if (!second) me.maps[warp][pair] = Map{mul2(o.decay, m.decay), fma2(o.decay, m.own, o.own)};
@@ -207,7 +210,7 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
         lru_sync<2, kLruThreads>(group);
         if (!TMA) fetch(turn + B);
         else if (thread == kLruWorkers - 32) issue(turn + B);
-        if (y && plan.t.seq >= 0) {
+        if (y && some) {
             F2 h = fma2(me.fronts[warp][pair].decay, me.carry[pair], me.fronts[warp][pair].own);
             if (second) h = fma2(o.decay, h, o.own);
             IO* yp = y + (plan.t.first + row) * p.D + ch;
@@ -307,6 +310,7 @@ cudaError_t lru_forward(const LruArgs& args, const LruTensors& t, void* y, float
     LruChain chain;
     if (cudaError_t e = lru_chain(args, t.lam, workspace, &chain, s)) return e;
     LruMaps m;
+    m.rows = lru_box(args);
     const bool tma = args.total > 0 && p.x.unit == 16 && p.r.unit == 16 && (!p.i.p || p.i.unit == 16);
     if (tma && !(lru_map(&m.x, p.x, args) && lru_map(&m.r, p.r, args) && (!p.i.p || lru_map(&m.i, p.i, args))))
         return cudaErrorInvalidValue;
