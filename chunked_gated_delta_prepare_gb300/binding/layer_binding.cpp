@@ -485,7 +485,8 @@ struct Lru {
     const float* lam;
     gdr_lru_problem p;
 
-    Lru(const Call& c, const Tensor& xt, PyObject* const* a, PyObject* rate, int64_t n, int64_t T, int64_t total, int64_t pool) {
+    Lru(const Call& c, const Tensor& xt, PyObject* const* a, PyObject* rate, int64_t n, int64_t T, int64_t total,
+        int64_t pool) {
         const IntArrayRef shape = xt.sizes();
         const int64_t D = shape.back();
         x = rows(c, a[0], shape, "x");
@@ -652,7 +653,8 @@ PyObject* gated_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const Call& c = v.c;
     const Tensor dy = gradient(c, a[0], c.io, v.shape, "dy");
     TORCH_CHECK_VALUE(dy.defined(), "dy: a tensor is needed");
-    const std::array<Tensor, 3> out{c.empty(v.shape, c.io), c.empty(v.shape, c.io), c.empty(tensor(a[3], "weight").sizes(), F32)};
+    const std::array<Tensor, 3> out{c.empty(v.shape, c.io), c.empty(v.shape, c.io),
+                                    c.empty(tensor(a[3], "weight").sizes(), F32)};
     const Workspace ws(c, a[6], gdr_gated_norm_backward_workspace_bytes(&v.p));
     const int st = gdr_gated_norm_backward(&v.p, dy.data_ptr(), v.xr.p, v.zr.p, v.w, out[0].data_ptr(), out[1].data_ptr(),
                                            (float*)out[2].data_ptr(), ws.p, ws.bytes, c.stream());

@@ -288,7 +288,8 @@ constexpr int kLruLook = 4;
 // between.  These are applied one by one, from the state on, as the tiles themselves do: wherever the state comes from, the
 // bits are the same.  BACK: the tiles that come before are those behind.
 template <bool BACK>
-__device__ __forceinline__ bool look_back(const LruChain& c, const LruTile& t, unsigned cols, int pair, unsigned near, F2& state) {
+__device__ __forceinline__ bool look_back(const LruChain& c, const LruTile& t, unsigned cols, int pair, unsigned near,
+                                          F2& state) {
     const int64_t at = ((int64_t)t.number * cols + t.col) * kLruPairs + pair;
     const int64_t step = (BACK ? 1 : -1) * (int64_t)cols * kLruPairs;
     F2 s[kLruLook];
@@ -543,7 +544,8 @@ inline bool lru_map(CUtensorMap* m, const LruRows& v, const LruArgs& a) {
 inline bool lru_one_tile_each(const LruArgs& a) { return (a.cu ? a.total : a.T) <= kLruTile; }
 // One block an SM at most; blocks that wait for one another run together or not at all.
 template <typename... A, typename... B>
-cudaError_t lru_launch(void (*kernel)(A...), const Lru& p, const LruChain& c, int threads, int bytes, cudaStream_t s, B... args) {
+cudaError_t lru_launch(void (*kernel)(A...), const Lru& p, const LruChain& c, int threads, int bytes, cudaStream_t s,
+                       B... args) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
     cudaLaunchAttribute together{};
     together.id = cudaLaunchAttributeCooperative;
