@@ -223,3 +223,58 @@ def test_autograd_beside_captured_gradients():
     torch.cuda.synchronize()
     want = torch.autograd.grad(eager, (x, r), dy)
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+FAR, WIDE = 1_060_000, 2048                                 # more than 2^31 values
+
+
+def test_recurrence_past_2_31_values():
+    """A short sequence behind a very long one: the bits of the short one alone."""
+    io, tail = torch.bfloat16, 300
+    x, r, i, dy = (torch.randn(FAR, WIDE, device="cuda", dtype=io) for _ in range(4))
+    lam = torch.rand(WIDE, device="cuda") * 2 - 5
+    cu = torch.tensor([0, FAR - tail, FAR], dtype=torch.int32, device="cuda")
+    y, h, kept = layer.lru_forward(x, r, i, lam, cu_seqlens=cu, want_kept=True)
+    d = layer.lru_backward(x, r, i, lam, dy, kept=kept, cu_seqlens=cu)
+    part = [t[-tail:].unsqueeze(0).clone() for t in (x, r, i)]
+    want, want_h, _ = layer.lru_forward(*part, lam)
+    grads = layer.lru_backward(*part, lam, dy[-tail:].unsqueeze(0).clone())
+    assert torch.equal(y[-tail:], want[0]) and torch.equal(h[1], want_h[0])
+    for a, b in zip(d[:3], grads[:3]):
+        assert torch.equal(a[-tail:], b[0])
+    assert gdr.gdr_get_device_status() == 0
+
+
+def test_norms_past_2_31_values():
+    """Their last rows against the definitions; the gradients of the weights with nothing but the last rows in them."""
+    io, tail = torch.bfloat16, 8
+    x = torch.randn(FAR, WIDE, device="cuda", dtype=io)
+    z = torch.randn(FAR, WIDE, device="cuda", dtype=io)
+    w = (1 + 0.1 * torch.randn(WIDE, device="cuda")).to(io)
+    dy = torch.zeros(FAR, WIDE, device="cuda", dtype=io)
+    dy[-tail:] = torch.randn(tail, WIDE, device="cuda").to(io)
+    tol = 2.0 ** -8 + 3e-5
+
+    def near(got, want, tol=tol):
+        assert float((got.double() - want).abs().max()) <= tol * float(want.abs().max())
+
+    y, s = layer.layernorm_forward(x, w, None, z)
+    dx, dw, db = layer.layernorm_backward(dy, s, w)
+    s64, w64 = s[-tail:].double().requires_grad_(), w.double().requires_grad_()
+    want = torch.nn.functional.layer_norm(s64, (WIDE,), w64, None, 1e-5)
+    near(s[-tail:], x[-tail:].double() + z[-tail:].double())
+    near(y[-tail:], want.detach(), 2 * tol)                 # of s itself, here of its rounding
+    ds, dw64 = torch.autograd.grad(want, (s64, w64), dy[-tail:].double())
+    near(dx[-tail:], ds)
+    near(dw, dw64, 1e-4)
+    near(db, dy[-tail:].double().sum(0), 1e-4)
+    del y, s, dx
+    heads = lambda t: t.unflatten(-1, (16, WIDE // 16))  # noqa: E731
+    g = w[:WIDE // 16].contiguous()
+    y = layer.gated_norm_forward(heads(x), heads(z), g)
+    dx, dz, dg = layer.gated_norm_backward(heads(dy), heads(x), heads(z), g)
+    x64, z64, g64 = (t.double().requires_grad_() for t in (heads(x[-tail:]), heads(z[-tail:]), g))
+    want = x64 / torch.sqrt((x64 * x64).mean(-1, keepdim=True) + 1e-6) * g64 * z64 * torch.sigmoid(z64)
+    near(y[-tail:], want.detach())
+    for got, grad in zip((dx[-tail:], dz[-tail:], dg), torch.autograd.grad(want, (x64, z64, g64), heads(dy[-tail:]).double())):
+        near(got, grad)
