@@ -147,7 +147,8 @@ template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, 
 // RATE, where v = 2 k q stays below 1/2 (k <= 1/4: gates that keep more than 0.78 of a state when they are open): with
 // w = sqrt(q) = (1 + e^-r)^-1/2, s = sqrt(2 k) w P(v), P(v) = sqrt((1 - e^-v) / v), by a polynomial; one root of
 // (1 + e^-r)(1 + e^-i)^2 gives w g, times (1 + e^-i) it gives w.  Else: one reciprocal of (1 + e^-r)(1 + e^-i) gives q g.
-// The products must not overflow where q or g is large: i (and without rates r) is at least -27.
+// The products must not overflow where q or g is large: i (and without rates r) is at least -27.  With rates a gate r so far
+// shut that the product still does (an inflow below 2^-64 of x) lets nothing in.
 constexpr float kLruSlow = 0.25f, kLruLeast = -27.f;
 __device__ __forceinline__ float rsqrt_fast(float x) {
     float y;
