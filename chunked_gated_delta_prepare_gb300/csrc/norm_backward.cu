@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
     __shared__ float part[32][33];
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the kernel before is done
     if (c < cols + cols2) {
 #pragma unroll 8
         for (int64_t i = threadIdx.y; i < rows; i += 32) s += in[i * ld + c];
@@ -255,9 +256,16 @@ cudaError_t norm_backward(const NormArgs& a, const void* dy, const void* r, cons
 cudaError_t column_sum(const float* in, int64_t rows, int64_t ld, int64_t cols, float* out, int64_t cols2, float* out2,
                        cudaStream_t s) {
     if (cols + cols2 <= 0) return cudaSuccess;
-    column_sum_kernel<<<(unsigned)((cols + cols2 + 31) / 32), dim3(32, 32), 0, s>>>(in, rows, ld, cols, out, cols2,
-                                                                                    out2);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((unsigned)((cols + cols2 + 31) / 32));
+    config.blockDim = dim3(32, 32);
+    config.stream = s;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, column_sum_kernel, in, rows, ld, cols, out, cols2, out2);
 }
 
 }  // namespace layer
