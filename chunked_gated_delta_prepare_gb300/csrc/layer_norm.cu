@@ -8,7 +8,7 @@
 // by bulk copies, several rows ahead of the threads that work on them.
 //
 // Measured (bf16): 32768 x 4096 with residual in 185 us, 5.8 TB/s, 0.86 of a copy's rate (277 by loads into registers);
-// 8192 x 2048 forward 22, gradient 28 and 4 for column_sum; 4451 x 2278 fp32, rows that start between boundaries, 75 in all.
+// 8192 x 2048 forward 22, gradient 28 and 3 for column_sum; 4451 x 2278 fp32, rows that start between boundaries, 72 in all.
 // The gradient has 16 warps an SM (dw and db take 32 registers of a thread's 120) and issues in 0.47 of its slots: each
 // instruction less shows.  One barrier a row instead of two, by joining the warps' own means and squares, takes more of them
 // and measured slower (16384 x 2048: 62 us against 57).
