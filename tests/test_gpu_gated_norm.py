@@ -192,3 +192,17 @@ def test_refusals():
     with pytest.raises(GdrError) as e:
         layer.gated_norm_backward(x, x, z, w, workspace=torch.empty(1, device="cuda", dtype=torch.uint8))
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("tokens,H,V", [(2600, 3, 33), (1, 1, 9), (9000, 1, 100), (701, 7, 251), (400, 5, 1001), (50, 1, 8180)])
+def test_rows_between_boundaries(tokens, H, V, per_head, io):
+    """All tensors' rows lie alike between 16-byte boundaries, the gate's in a wider row; what lies beside it is not seen."""
+    x, _, w = make(tokens, H, V, io, per_head, seed=5)
+    gen = torch.Generator().manual_seed(6)
+    z = torch.full((tokens, H * V + 24), float("nan")).to(io)
+    z[:, :H * V] = 2 * torch.randn(tokens, H * V, generator=gen)
+    z = z.cuda()[:, :H * V].unflatten(1, (H, V))
+    check(layer.gated_norm_forward(x, z, w), x, z, w, "silu", io)
+    backward_check(x, z, w, "silu", io)
