@@ -176,7 +176,7 @@ gated_norm_backward_kernel(GatedNormArgs a, Places pl, const IO* __restrict__ dy
         float sq[1] = {both_halves(p0)}, dot[1] = {both_halves(p1)};
         sum_row<TPR>(sq, red[0], (int)turn);
         sum_row<TPR>(dot, red[1], (int)turn);
-        const float rs = rsqrtf(fmaf(sq[0], over, a.eps));
+        const float rs = live ? rsqrtf(fmaf(sq[0], over, a.eps)) : 0.f;     // with eps = 0 a row that is not there has none
         const F2 rstd = both(rs), back = both(-dot[0] * over * rs * rs);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
