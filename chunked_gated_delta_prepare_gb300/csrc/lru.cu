@@ -21,7 +21,7 @@ struct alignas(16) Map {     // what a run of tokens makes of state h: h * decay
 
 // The decays and terms of the thread's run, from shared memory; a = 1, u = 0 past the tile's end.
 template <typename IO, bool RATE, bool GATE>
-__device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k, F2 root, int len, int left,
+__device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k, F2 root, bool far, int len, int left,
                                          F2 (&a)[kLruRun], F2 (&u)[kLruRun]) {
     constexpr int N = kLruTile * kLruCols;
     RawN<IO, 2> r[kLruRun], i[kLruRun];
@@ -30,39 +30,33 @@ __device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k
         r[j] = lru_raw(from, row + j, pair);
         if (GATE) i[j] = lru_raw(from + 2 * N, row + j, pair);
     }
-    if (lru_short<RATE, GATE, !RATE>(r, i, k, len - row, left)) {
-        const F2 k2 = add2(k, k);
+    const F2 k2 = add2(k, k);
+    const auto run = [&](auto far_, auto wild_) {
+        constexpr bool FAR = decltype(far_)::value, WILD = decltype(wild_)::value;
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
-            const F2 x = lru_read(from + N, row + j, pair), iv = GATE ? wide2(i[j]) : 0;
+            const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
             if (RATE) {
-                F2 w, z;
-                lru_roots<GATE>(wide2(r[j]), iv, w, z);
+                F2 w, z, t2 = 0;
+                lru_roots<GATE, WILD>(rv, iv, w, z, t2);
                 const F2 v = mul2(k2, mul2(w, w));
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(root, x));
-            } else {
-                const F2 e = ex2_2(mul2(wide2(r[j]), both(-kLog2e))), t1 = add2(e, both(1.f));
-                if (GATE) {
-                    const F2 t2 = one_and_exp(iv), sg = mul2(e, rcp_2(mul2(t1, t2)));
-                    a[j] = fma2(mul2(sg, both(-1.f)), t2, both(1.f));
-                    u[j] = mul2(sg, x);
-                } else {
-                    const F2 s = mul2(e, rcp_2(t1));
-                    a[j] = fma2(s, both(-1.f), both(1.f));
-                    u[j] = mul2(s, x);
+                if (FAR) {
+                    const F2 s = sqrt2(fma2(mul2(a[j], both(-1.f)), a[j], both(1.f)));
+                    u[j] = below(v, kLruNear, u[j], mul2(s, GATE ? mul2(rcp_2(t2), x) : x));
                 }
+            } else {
+                F2 s, g, sg;
+                lru_parts<GATE, WILD>(rv, iv, a[j], s, g, sg);
+                u[j] = mul2(sg, x);
             }
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kLruRun; ++j) {
-            F2 s, q;
-            decay_and_part<RATE>(wide2(r[j]), k, a[j], s, q);
-            u[j] = mul2(s, lru_read(from + N, row + j, pair));
-            if (GATE) u[j] = mul2(u[j], sigmoid2(wide2(i[j])));
-        }
-    }
+    };
+    const bool tame = lru_tame<RATE, GATE>(r, i, len - row, left);
+    if (tame && !(RATE && far)) run(std::false_type(), std::false_type());
+    else if (RATE && tame) run(std::true_type(), std::false_type());
+    else run(std::bool_constant<RATE>(), std::true_type());
     if (len < kLruTile)
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j)
@@ -201,7 +195,7 @@ lru_forward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_map
                 k = *reinterpret_cast<const F2*>(plan.rates + pair * 2);
                 root = *reinterpret_cast<const F2*>(plan.roots + pair * 2);
             }
-            read_run<IO, RATE, GATE>(in + (turn % B) * IN * N, row, pair, k, root, len, left, a, u);
+            read_run<IO, RATE, GATE>(in + (turn % B) * IN * N, row, pair, k, root, plan.far, len, left, a, u);
             m = Map{a[0], u[0]};
 #pragma unroll
             for (int j = 1; j < kLruRun; ++j) {

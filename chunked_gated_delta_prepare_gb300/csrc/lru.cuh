@@ -97,6 +97,10 @@ __device__ __forceinline__ float min_nan(float a, float b) {   // NaN where eith
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
+__device__ __forceinline__ F2 max_nan2(F2 a, F2 b) {
+    const float2 x = unpack2(a), y = unpack2(b);
+    return pack2(max_nan(x.x, y.x), max_nan(x.y, y.y));
+}
 __device__ __forceinline__ float sqrt_fast(float x) {
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -147,9 +151,13 @@ template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, 
 // RATE, where v = 2 k q stays below 1/2 (k <= 1/4: gates that keep more than 0.78 of a state when they are open): with
 // w = sqrt(q) = (1 + e^-r)^-1/2, s = sqrt(2 k) w P(v), P(v) = sqrt((1 - e^-v) / v), by a polynomial; one root of
 // (1 + e^-r)(1 + e^-i)^2 gives w g, times (1 + e^-i) it gives w.  Else: one reciprocal of (1 + e^-r)(1 + e^-i) gives q g.
-// The products must not overflow where q or g is large: i (and without rates r) is at least -27.  With rates a gate r so far
+// The products must not overflow where q or g is small: i (and without rates r) is at least -27.  With rates a gate r so far
 // shut that the product still does (an inflow below 2^-64 of x) lets nothing in.
-constexpr float kLruSlow = 0.25f, kLruLeast = -27.f;
+//
+// A warp goes by them alone (EASY) where every token and channel of its runs may; elsewhere it forms the others' terms too and
+// selects, so that a token's bits follow from its own channel's numbers, whatever its neighbours hold.
+constexpr float kLruSlow = 0.25f, kLruNear = 0.50001f;      // the largest k, and what v stays below when q is rounded up
+constexpr float kLruLeast = -27.f, kLruJoint = 0x1p39f;     // the least logit, and what 1 + e^27 stays below
 __device__ __forceinline__ float rsqrt_fast(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,15 +179,43 @@ __device__ __forceinline__ F2 lru_p_inverse(F2 v) {      // 1 / P(v), off by 4e-
     p = fma2(v, p, both(0x1.ffff5p-3f));
     return fma2(v, p, both(1.f));
 }
-// w and z = w g.
-template <bool GATE> __device__ __forceinline__ void lru_roots(F2 r, F2 i, F2& w, F2& z) {
+// Of each channel `yes` where x is below the bound, else (or NaN) `no`.
+__device__ __forceinline__ F2 below(F2 x, float bound, F2 yes, F2 no) {
+    const float2 at = unpack2(x), y = unpack2(yes), n = unpack2(no);
+    return pack2(at.x < bound ? y.x : n.x, at.y < bound ? y.y : n.y);
+}
+// RATE: w, z = w g, and 1 / g.  WILD: i may be anything.
+template <bool GATE, bool WILD> __device__ __forceinline__ void lru_roots(F2 r, F2 i, F2& w, F2& z, F2& t2) {
     const F2 t1 = one_and_exp(r);
     if (GATE) {
-        const F2 t2 = one_and_exp(i);
+        t2 = one_and_exp(i);
         z = rsqrt2(mul2(t1, mul2(t2, t2)));
         w = mul2(z, t2);
+        if (WILD) {
+            const F2 alone = rsqrt2(t1);
+            z = below(t2, kLruJoint, z, mul2(alone, rcp_2(t2)));
+            w = below(t2, kLruJoint, w, alone);
+        }
     } else {
         z = w = rsqrt2(t1);
+    }
+}
+// Else: a, its complement s, g and s g.  WILD: r and i may be anything.
+template <bool GATE, bool WILD> __device__ __forceinline__ void lru_parts(F2 r, F2 i, F2& a, F2& s, F2& g, F2& sg) {
+    const F2 e = ex2_2(mul2(r, both(-kLog2e))), t1 = add2(e, both(1.f)), t2 = GATE ? one_and_exp(i) : both(1.f);
+    const F2 o = rcp_2(GATE ? mul2(t1, t2) : t1);
+    sg = mul2(e, o);
+    s = GATE ? mul2(sg, t2) : sg;
+    g = GATE ? mul2(o, t1) : both(1.f);
+    a = fma2(s, both(-1.f), both(1.f));
+    if (WILD) {
+        F2 a_, s_, q_;
+        decay_and_part<false>(r, 0, a_, s_, q_);
+        const F2 g_ = GATE ? sigmoid2(i) : both(1.f), worst = GATE ? max_nan2(e, t2) : e;
+        a = below(worst, kLruJoint, a, a_);
+        s = below(worst, kLruJoint, s, s_);
+        g = below(worst, kLruJoint, g, g_);
+        sg = below(worst, kLruJoint, sg, mul2(s_, g_));
     }
 }
 
@@ -342,11 +378,12 @@ template <int ID, int N> __device__ __forceinline__ void lru_arrive(int group) {
 }
 __device__ __forceinline__ F2 swap_halves(F2 v) { return __shfl_xor_sync(0xffffffffu, v, 16); }
 
-// What the guide tells the workers of a tile.
+// What the guide tells the workers of a tile; rates alone have a `far`.
 constexpr int kLruPlans = 4;
 struct LruPlan {
     LruTile t;
     bool live;               // there is one
+    bool far;                // some channel's rate is above kLruSlow
     alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols], inverses[kLruCols];       // rates_of
 };
 // The guide's: a channel's rates are read four tiles ahead and a tile planned three ahead, after the present one's state is
@@ -371,6 +408,8 @@ template <bool BACK, bool RATE, int GROUPS> struct LruPlanner {
             const LruTile t = lru_tile<BACK, GROUPS>(p, job(turn), group);
             if (lane == 0) plan->t = t;
             if (RATE) {
+                const bool far = __any_sync(0xffffffffu, rate.x > kLruSlow);
+                if (lane == 0) plan->far = far;
                 plan->rates[lane] = rate.x;
                 plan->roots[lane] = rate.y;
                 if (BACK) plan->slopes[lane] = rate.z, plan->inverses[lane] = rate.w;
@@ -469,29 +508,28 @@ template <typename IO> __device__ __forceinline__ RawN<IO, 2> lru_raw(const IO* 
 template <typename IO> __device__ __forceinline__ F2 lru_read(const IO* from, int row, int pair) {
     return wide2(lru_raw(from, row, pair));
 }
-// Whether the thread's run may go by the shorter formulas; tokens past the tile's end and channels past the last, which hold
-// anything, are not asked.  BOUND: r too is to be at least kLruLeast.
-template <bool RATE, bool GATE, bool BOUND, typename IO>
-__device__ __forceinline__ bool lru_short(const RawN<IO, 2> (&r)[kLruRun], const RawN<IO, 2> (&i)[kLruRun], F2 k, int live,
-                                          int left) {
-    const float2 f = unpack2(k);
-    bool ok = !RATE || (f.x <= kLruSlow && f.y <= kLruSlow);
-    const auto ask = [&](const RawN<IO, 2> (&v)[kLruRun]) {
-        RawN<IO, 2> least = v[0];
-        if (live >= kLruRun) {
+// Whether the gates of all the warp's runs are at least kLruLeast, and none is NaN; tokens past the tile's end and channels past
+// the last, which hold anything, are not asked.
+template <typename IO>
+__device__ __forceinline__ bool lru_least(const RawN<IO, 2> (&v)[kLruRun], int live, int left) {
+    RawN<IO, 2> least = v[0];
+    if (live >= kLruRun) {
 #pragma unroll
-            for (int j = 1; j < kLruRun; ++j) least = min_pair(least, v[j]);
-        } else {
+        for (int j = 1; j < kLruRun; ++j) least = min_pair(least, v[j]);
+    } else {
 #pragma unroll
-            for (int j = 1; j < kLruRun; ++j)
-                if (j < live) least = min_pair(least, v[j]);
-        }
-        const float2 g = to_f2(least.e);
-        return live <= 0 || ((left < 1 || g.x >= kLruLeast) && (left < 2 || g.y >= kLruLeast));
-    };
-    if (BOUND) ok = ok && ask(r);
-    if (GATE) ok = ok && ask(i);
-    return ok;
+        for (int j = 1; j < kLruRun; ++j)
+            if (j < live) least = min_pair(least, v[j]);
+    }
+    const float2 g = to_f2(least.e);
+    return live <= 0 || ((left < 1 || g.x >= kLruLeast) && (left < 2 || g.y >= kLruLeast));
+}
+template <bool RATE, bool GATE, typename IO>
+__device__ __forceinline__ bool lru_tame(const RawN<IO, 2> (&r)[kLruRun], const RawN<IO, 2> (&i)[kLruRun], int live, int left) {
+    bool ok = true;
+    if (!RATE) ok = lru_least(r, live, left);
+    if (GATE) ok = ok && lru_least(i, live, left);
+    return (RATE && !GATE) || __all_sync(0xffffffffu, ok);
 }
 
 // Calls f with a value of the io type and whether there are rates and input gates.

@@ -36,7 +36,7 @@ struct alignas(16) Map {     // what tokens make of the gradient e from behind t
 // (RATE: sqrt(v), v = 2 k q), and the gate.  RATE: the terms, and so all states here, have the other
 // sign, which saves the gradients a negation.  A token past the tile's end has a = 1, u = 0.
 template <typename IO, bool RATE, bool GATE>
-__device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k, F2 root, int len, int left,
+__device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 root, bool far, int len, int left,
                                          F2 (&a)[kLruRun], F2 (&u)[kLruRun], F2 (&part)[kLruRun],
                                          F2 (&gate)[kLruRun]) {
     constexpr int N = kLruTile * kLruCols;
@@ -46,70 +46,52 @@ __device__ __forceinline__ bool read_run(const IO* from, int row, int pair, F2 k
         r[j] = lru_raw(from, row + j, pair);
         if (GATE) i[j] = lru_raw(from + 3 * N, row + j, pair);
     }
-    const bool shorter = lru_short<RATE, GATE, !RATE>(r, i, k, len - row, left);
-    if (shorter) {
-        const F2 minus = neg2(root);
+    const F2 minus = neg2(root);
+    const auto run = [&](auto far_, auto wild_) {
+        constexpr bool FAR = decltype(far_)::value, WILD = decltype(wild_)::value;
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
             const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
             if (RATE) {
-                const F2 t1 = one_and_exp(rv);
-                F2 z;
-                if (GATE) {
-                    const F2 t2 = one_and_exp(iv);
-                    z = rsqrt2(mul2(t1, mul2(t2, t2)));      // sqrt(q) g
-                    part[j] = mul2(mul2(z, root), t2);
-                    gate[j] = rcp_2(t2);
-                } else {
-                    z = rsqrt2(t1);
-                    part[j] = mul2(root, z);
-                }
+                F2 w, z, t2 = 0;
+                lru_roots<GATE, WILD>(rv, iv, w, z, t2);
+                if (GATE) gate[j] = rcp_2(t2);
+                part[j] = mul2(root, w);
                 const F2 v = mul2(part[j], part[j]);
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(minus, x));
-            } else {
-                const F2 e = ex2_2(mul2(rv, both(-kLog2e))), t1 = add2(e, both(1.f));
-                if (GATE) {
-                    const F2 t2 = one_and_exp(iv), o = rcp_2(mul2(t1, t2)), sg = mul2(e, o);
-                    gate[j] = mul2(o, t1);
-                    part[j] = mul2(sg, t2);
-                    u[j] = mul2(sg, x);
-                } else {
-                    part[j] = mul2(e, rcp_2(t1));
-                    u[j] = mul2(part[j], x);
+                if (FAR) {
+                    const F2 s = sqrt2(fma2(mul2(a[j], both(-1.f)), a[j], both(1.f)));
+                    u[j] = below(v, kLruNear, u[j], mul2(neg2(s), GATE ? mul2(gate[j], x) : x));
                 }
-                a[j] = fma2(part[j], both(-1.f), both(1.f));
+            } else {
+                F2 sg;
+                lru_parts<GATE, WILD>(rv, iv, a[j], part[j], gate[j], sg);
+                u[j] = mul2(sg, x);
             }
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kLruRun; ++j) {
-            F2 s, q;
-            decay_and_part<RATE>(wide2(r[j]), k, a[j], s, q);
-            u[j] = mul2(RATE ? neg2(s) : s, lru_read(from + N, row + j, pair));
-            if (GATE) gate[j] = sigmoid2(wide2(i[j])), u[j] = mul2(u[j], gate[j]);
-            part[j] = RATE ? mul2(root, sqrt2(q)) : s;
-        }
-    }
+    };
+    const bool tame = lru_tame<RATE, GATE>(r, i, len - row, left);
+    if (tame && !(RATE && far)) run(std::false_type(), std::false_type());
+    else if (RATE && tame) run(std::true_type(), std::false_type());
+    else run(std::bool_constant<RATE>(), std::true_type());
     if (len < kLruTile)
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j)
             if (row + j >= len) a[j] = both(1.f), u[j] = both(0.f);
-    return shorter;
 }
 
 // RATE: v = 2 k q of a token, s and v / s, the last two by P(v) where 1 - a^2 cancels: finite where s is zero.
 struct Parts {
     F2 v, s, ratio;
 };
-__device__ __forceinline__ Parts parts_of(F2 rw, F2 a, bool shorter) {
+__device__ __forceinline__ Parts parts_of(F2 rw, F2 a, bool far) {
     const F2 v = mul2(rw, rw);
     Parts o{v, mul2(rw, lru_p(v)), mul2(rw, lru_p_inverse(v))};
-    if (!shorter) {
-        const F2 s = sqrt2(fma2(mul2(a, both(-1.f)), a, both(1.f))), far = mul2(v, rcp_2(s));
-        const float2 at = unpack2(v), s0 = unpack2(o.s), s1 = unpack2(s), r0 = unpack2(o.ratio), r1 = unpack2(far);
-        o.s = pack2(at.x < 0.5f ? s0.x : s1.x, at.y < 0.5f ? s0.y : s1.y);
-        o.ratio = pack2(at.x < 0.5f ? r0.x : r1.x, at.y < 0.5f ? r0.y : r1.y);
+    if (far) {
+        const F2 s = sqrt2(fma2(mul2(a, both(-1.f)), a, both(1.f)));
+        o.s = below(v, kLruNear, o.s, s);
+        o.ratio = below(v, kLruNear, o.ratio, mul2(v, rcp_2(s)));
     }
     return o;
 }
@@ -247,14 +229,10 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         }
         const LruPlan& plan = plans[turn % kLruPlans];
         const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch, len = plan.t.len;
-        F2 k = 0, root = 0;
-        if (RATE) {
-            k = *reinterpret_cast<const F2*>(plan.rates + pair * 2);
-            root = *reinterpret_cast<const F2*>(plan.roots + pair * 2);
-        }
+        const F2 root = RATE ? *reinterpret_cast<const F2*>(plan.roots + pair * 2) : 0;
         const IO* from = in + (turn % B) * IN * N;
         F2 a[kLruRun], h[kLruRun], part[kLruRun], gate[kLruRun];
-        const bool shorter = read_run<IO, RATE, GATE>(from, row, pair, k, root, len, left, a, h, part, gate);
+        read_run<IO, RATE, GATE>(from, row, pair, root, plan.far, len, left, a, h, part, gate);
         Run m{both(1.f), both(0.f), both(0.f)};
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
@@ -291,18 +269,21 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             if (!second) e = fma2(decay, e, other);
             const int64_t tile = plan.t.first * p.D + plan.t.col * kLruCols;      // offsets within a tile have 32 bits
             IO *const xp = dx + tile, *const rp = dr + tile, *const ip = di + tile;
+            F2 behind = both(1.f);                               // the decay of the token behind; sums that follow a product are
+                                                                // written as one operation, or the loops below differ in it
             unsigned at = (unsigned)(row + kLruRun - 1) * (unsigned)p.D + pair * 2;
-            const auto token = [&](int j, bool by_w, bool all) {
-                e = add2(e, lru_read(from + 2 * N, row + j, pair));
+            const auto token = [&](int j, bool far, bool all) {
+                e = fma2(e, behind, lru_read(from + 2 * N, row + j, pair));
+                behind = a[j];
                 const F2 x = lru_read(from + N, row + j, pair), eg = GATE ? mul2(e, gate[j]) : e, ea = mul2(e, a[j]);
                 F2 dr_, s = part[j];
                 if (RATE) {
-                    const Parts o = parts_of(part[j], a[j], by_w);
+                    const Parts o = parts_of(part[j], a[j], far);
                     s = o.s;
                     // -dlog a v = e a (a g x v / s - h v); dr is that times (1 - q) / 2
                     const F2 gxa = mul2(GATE ? mul2(gate[j], x) : x, a[j]);
-                    const F2 base = mul2(ea, fma2(gxa, o.ratio, mul2(h[j], o.v)));
-                    sum = add2(sum, base);
+                    const F2 term = fma2(gxa, o.ratio, mul2(h[j], o.v)), base = mul2(ea, term);
+                    sum = fma2(ea, term, sum);
                     dr_ = mul2(base, fma2(o.v, half_inverse, both(0.5f)));
                 } else {
                     dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(mul2(eg, x))));
@@ -311,18 +292,17 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                 store2(xp + at, dx_, all ? 2 : left, all);
                 store2(rp + at, dr_, all ? 2 : left, all);
                 if (GATE) store2(ip + at, mul2(mul2(dx_, x), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
-                e = ea;
             };
-            if (p.vec && len == kLruTile && left > 0 && (shorter || !RATE)) {
+            if (p.vec && len == kLruTile && left > 0 && !(RATE && plan.far)) {
 #pragma unroll
                 for (int j = kLruRun - 1; j >= 0; --j) {
-                    token(j, true, true);
+                    token(j, false, true);
                     at -= (unsigned)p.D;
                 }
             } else {
 #pragma unroll
                 for (int j = kLruRun - 1; j >= 0; --j) {
-                    if (row + j < len) token(j, shorter, false);
+                    if (row + j < len) token(j, RATE && plan.far, false);
                     at -= (unsigned)p.D;
                 }
             }

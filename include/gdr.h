@@ -699,6 +699,7 @@ GDR_API gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const int32_t* slots, 
  *     lam NULL:   a_t = q,                       u_t = (1 - a_t) g x_t           (c is not used)
  * x, r, i, y: tokens of D channels, io; lam [D] fp32; h_0 from h0 [n,D] fp32 (NULL: zero); h_final [n,D] fp32 or NULL:
  * the state after each sequence's last token.  fp32 arithmetic for every io type.
+ * A channel's results follow from that channel's inputs alone, bit for bit.
  * kept [rows,D] fp32 or NULL: the state before every 128th token of each sequence, for the gradient; its bytes come
  * from gdr_lru_kept_bytes.  A long sequence is scanned in tiles of that many tokens at once; a tile's state follows
  * from its predecessor's in a fixed order, so the result of a call does not change from run to run. */
