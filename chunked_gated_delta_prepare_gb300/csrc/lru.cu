@@ -37,8 +37,9 @@ __device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k
         for (int j = 0; j < kLruRun; ++j) {
             const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
             if (RATE) {
-                F2 w, z, t2 = 0;
-                lru_roots<GATE, WILD>(rv, iv, w, z, t2);
+                const F2 t2 = GATE ? one_and_exp(iv) : 0;
+                F2 w, z;
+                lru_roots<GATE, WILD>(one_and_exp(rv), t2, w, z);
                 const F2 v = mul2(k2, mul2(w, w));
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(root, x));
@@ -47,8 +48,8 @@ __device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k
                     u[j] = below(v, kLruNear, u[j], mul2(s, GATE ? mul2(rcp_2(t2), x) : x));
                 }
             } else {
-                F2 s, g, sg;
-                lru_parts<GATE, WILD>(rv, iv, a[j], s, g, sg);
+                F2 s, sg;
+                lru_parts<GATE, WILD>(rv, iv, a[j], s, sg);
                 u[j] = mul2(sg, x);
             }
         }

@@ -158,6 +158,7 @@ template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, 
 // selects, so that a token's bits follow from its own channel's numbers, whatever its neighbours hold.
 constexpr float kLruSlow = 0.25f, kLruNear = 0.50001f;      // the largest k, and what v stays below when q is rounded up
 constexpr float kLruLeast = -27.f, kLruJoint = 0x1p39f;     // the least logit, and what 1 + e^27 stays below
+constexpr float kLruHuge = 0x1.8p126f;      // what an e^-i is cut to that would be infinite: 1 / (1 + it) is still flushed to zero
 __device__ __forceinline__ float rsqrt_fast(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -184,11 +185,9 @@ __device__ __forceinline__ F2 below(F2 x, float bound, F2 yes, F2 no) {
     const float2 at = unpack2(x), y = unpack2(yes), n = unpack2(no);
     return pack2(at.x < bound ? y.x : n.x, at.y < bound ? y.y : n.y);
 }
-// RATE: w, z = w g, and 1 / g.  WILD: i may be anything.
-template <bool GATE, bool WILD> __device__ __forceinline__ void lru_roots(F2 r, F2 i, F2& w, F2& z, F2& t2) {
-    const F2 t1 = one_and_exp(r);
+// RATE: w and z = w g from t1 = 1 + e^-r and t2 = 1 + e^-i.  WILD: i may be anything.
+template <bool GATE, bool WILD> __device__ __forceinline__ void lru_roots(F2 t1, F2 t2, F2& w, F2& z) {
     if (GATE) {
-        t2 = one_and_exp(i);
         z = rsqrt2(mul2(t1, mul2(t2, t2)));
         w = mul2(z, t2);
         if (WILD) {
@@ -200,13 +199,12 @@ template <bool GATE, bool WILD> __device__ __forceinline__ void lru_roots(F2 r, 
         z = w = rsqrt2(t1);
     }
 }
-// Else: a, its complement s, g and s g.  WILD: r and i may be anything.
-template <bool GATE, bool WILD> __device__ __forceinline__ void lru_parts(F2 r, F2 i, F2& a, F2& s, F2& g, F2& sg) {
+// Else: a, its complement s, and s g.  WILD: r and i may be anything.
+template <bool GATE, bool WILD> __device__ __forceinline__ void lru_parts(F2 r, F2 i, F2& a, F2& s, F2& sg) {
     const F2 e = ex2_2(mul2(r, both(-kLog2e))), t1 = add2(e, both(1.f)), t2 = GATE ? one_and_exp(i) : both(1.f);
     const F2 o = rcp_2(GATE ? mul2(t1, t2) : t1);
     sg = mul2(e, o);
     s = GATE ? mul2(sg, t2) : sg;
-    g = GATE ? mul2(o, t1) : both(1.f);
     a = fma2(s, both(-1.f), both(1.f));
     if (WILD) {
         F2 a_, s_, q_;
@@ -214,7 +212,6 @@ template <bool GATE, bool WILD> __device__ __forceinline__ void lru_parts(F2 r, 
         const F2 g_ = GATE ? sigmoid2(i) : both(1.f), worst = GATE ? max_nan2(e, t2) : e;
         a = below(worst, kLruJoint, a, a_);
         s = below(worst, kLruJoint, s, s_);
-        g = below(worst, kLruJoint, g, g_);
         sg = below(worst, kLruJoint, sg, mul2(s_, g_));
     }
 }

@@ -21,8 +21,10 @@ namespace {
 constexpr int kGroups = 2;   // 96 registers a thread
 template <typename IO> constexpr int kBuffers = sizeof(IO) == 2 ? 2 : 1;      // of tiles
 
-template <typename IO, bool GATE> constexpr int lru_backward_smem() {     // of a group
-    return kBuffers<IO> * (GATE ? 4 : 3) * kLruTile * kLruCols * (int)sizeof(IO);
+// Places of a tile: r, x, dy, and i or what 16-bit types set aside there.
+template <typename IO, bool RATE, bool GATE> constexpr int kPlaces = GATE || (RATE && sizeof(IO) == 2) ? 4 : 3;
+template <typename IO, bool RATE, bool GATE> constexpr int lru_backward_smem() {     // of a group
+    return kBuffers<IO> * kPlaces<IO, RATE, GATE> * kLruTile * kLruCols * (int)sizeof(IO);
 }
 
 struct alignas(8) Run {      // of a run of tokens: its product of decays, its end from a zero state, and what it sends to the
@@ -32,13 +34,35 @@ struct alignas(16) Map {     // what tokens make of the gradient e from behind t
     F2 decay, back;
 };
 
+// A number for each of a token's two channels, in the place of its r (16-bit types: of its r and its i), which no other thread
+// reads.  Registers do not hold them beside the run's other 64 (146 us for 4 x 2048 x 4096 bf16, by spills); formed again
+// where they are used they take 138, and this 132.
+template <typename IO> __device__ __forceinline__ void put_aside(IO* from, int row, int pair, F2 v) {
+    if constexpr (sizeof(IO) == 4) {
+        *reinterpret_cast<F2*>(from + row * kLruCols + pair * 2) = v;
+    } else {
+        const float2 f = unpack2(v);
+        *reinterpret_cast<float*>(from + row * kLruCols + pair * 2) = f.x;
+        *reinterpret_cast<float*>(from + (row + 3 * kLruTile) * kLruCols + pair * 2) = f.y;
+    }
+}
+template <typename IO> __device__ __forceinline__ F2 set_aside(const IO* from, int row, int pair) {
+    if constexpr (sizeof(IO) == 4) return *reinterpret_cast<const F2*>(from + row * kLruCols + pair * 2);
+    return pack2(*reinterpret_cast<const float*>(from + row * kLruCols + pair * 2),
+                 *reinterpret_cast<const float*>(from + (row + 3 * kLruTile) * kLruCols + pair * 2));
+}
+__device__ __forceinline__ F2 at_most(F2 v, float bound) {
+    const float2 f = unpack2(v);
+    return pack2(min_nan(f.x, bound), min_nan(f.y, bound));
+}
+
 // The decays and terms of the thread's run, from shared memory, and what the gradients need beside them: the input's part s
-// (RATE: sqrt(v), v = 2 k q), and the gate.  RATE: the terms, and so all states here, have the other
-// sign, which saves the gradients a negation.  A token past the tile's end has a = 1, u = 0.
+// (RATE: sqrt(v), v = 2 k q), e^-i, and (RATE, set aside in shared memory) (1 - q) / 2.  1 - q and 1 - g = e^-i g come from the
+// exponentials: from q and g, which are rounded, an open gate's would be noise.  RATE: the terms, and so all states here, have
+// the other sign, which saves the gradients a negation.  A token past the tile's end has a = 1, u = 0.
 template <typename IO, bool RATE, bool GATE>
-__device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 root, bool far, int len, int left,
-                                         F2 (&a)[kLruRun], F2 (&u)[kLruRun], F2 (&part)[kLruRun],
-                                         F2 (&gate)[kLruRun]) {
+__device__ __forceinline__ void read_run(IO* from, int row, int pair, F2 root, bool far, int len, int left, F2 (&a)[kLruRun],
+                                         F2 (&u)[kLruRun], F2 (&part)[kLruRun], F2 (&shut)[kLruRun]) {
     constexpr int N = kLruTile * kLruCols;
     RawN<IO, 2> r[kLruRun], i[kLruRun];
 #pragma unroll
@@ -52,23 +76,26 @@ __device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 r
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
             const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
+            F2 e = GATE ? ex2_2(mul2(iv, both(-kLog2e))) : 0;
             if (RATE) {
-                F2 w, z, t2 = 0;
-                lru_roots<GATE, WILD>(rv, iv, w, z, t2);
-                if (GATE) gate[j] = rcp_2(t2);
+                F2 w, z;
+                const F2 half = ex2_2(fma2(rv, both(-kLog2e), both(-1.f)));         // e^-r / 2
+                lru_roots<GATE, WILD>(fma2(half, both(2.f), both(1.f)), add2(e, both(1.f)), w, z);
                 part[j] = mul2(root, w);
                 const F2 v = mul2(part[j], part[j]);
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(minus, x));
                 if (FAR) {
                     const F2 s = sqrt2(fma2(mul2(a[j], both(-1.f)), a[j], both(1.f)));
-                    u[j] = below(v, kLruNear, u[j], mul2(neg2(s), GATE ? mul2(gate[j], x) : x));
+                    u[j] = below(v, kLruNear, u[j], mul2(neg2(s), GATE ? mul2(rcp_2(add2(e, both(1.f))), x) : x));
                 }
+                put_aside(from, row + j, pair, mul2(at_most(half, kLruHuge), mul2(w, w)));
             } else {
                 F2 sg;
-                lru_parts<GATE, WILD>(rv, iv, a[j], part[j], gate[j], sg);
+                lru_parts<GATE, WILD>(rv, iv, a[j], part[j], sg);
                 u[j] = mul2(sg, x);
             }
+            if (GATE) shut[j] = WILD ? at_most(e, kLruHuge) : e;
         }
     };
     const bool tame = lru_tame<RATE, GATE>(r, i, len - row, left);
@@ -102,7 +129,7 @@ __global__ void __launch_bounds__(kGroups * kLruThreads, 1)
 lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_maps, LruRows dy, const float* __restrict__ kept,
                     const float* __restrict__ dh_final, IO* __restrict__ dx, IO* __restrict__ dr, IO* __restrict__ di,
                     float* __restrict__ dlam, float* __restrict__ dh0) {
-    constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 4 : 3;
+    constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, TENSORS = GATE ? 4 : 3, IN = kPlaces<IO, RATE, GATE>;
     struct Group {
         Run runs[kLruWarps][kLruPairs];                     // of a warp's tokens
         Map behind[kLruWarps][kLruPairs];                   // of the tokens behind them
@@ -125,7 +152,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             uint64_t* bar = me.full + turn % B;
             IO* to = in + (turn % B) * IN * N;
             if (t.len == 0) return bw::mbar_arrive(bar);
-            bw::mbar_arrive_expect_tx(bar, in_maps.rows * IN * kLruCols * (unsigned)sizeof(IO));
+            bw::mbar_arrive_expect_tx(bar, in_maps.rows * TENSORS * kLruCols * (unsigned)sizeof(IO));
             lru_tma(to, &in_maps.r, bar, t);
             lru_tma(to + N, &in_maps.x, bar, t);
             lru_tma(to + 2 * N, &in_maps.dy, bar, t);
@@ -230,9 +257,9 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         const LruPlan& plan = plans[turn % kLruPlans];
         const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch, len = plan.t.len;
         const F2 root = RATE ? *reinterpret_cast<const F2*>(plan.roots + pair * 2) : 0;
-        const IO* from = in + (turn % B) * IN * N;
-        F2 a[kLruRun], h[kLruRun], part[kLruRun], gate[kLruRun];
-        read_run<IO, RATE, GATE>(from, row, pair, root, plan.far, len, left, a, h, part, gate);
+        IO* from = in + (turn % B) * IN * N;
+        F2 a[kLruRun], h[kLruRun], part[kLruRun], shut[kLruRun];
+        read_run<IO, RATE, GATE>(from, row, pair, root, plan.far, len, left, a, h, part, shut);
         Run m{both(1.f), both(0.f), both(0.f)};
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
@@ -264,7 +291,6 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                 h[j] = state;                               // the state in front of the token
                 state = after;
             }
-            const F2 half_inverse = RATE ? *reinterpret_cast<const F2*>(plan.inverses + pair * 2) : 0;     // -1 / (4 k)
             F2 e = fma2(me.behind[warp][pair].decay, me.carry[pair], me.behind[warp][pair].back);
             if (!second) e = fma2(decay, e, other);
             const int64_t tile = plan.t.first * p.D + plan.t.col * kLruCols;      // offsets within a tile have 32 bits
@@ -275,23 +301,24 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             const auto token = [&](int j, bool far, bool all) {
                 e = fma2(e, behind, lru_read(from + 2 * N, row + j, pair));
                 behind = a[j];
-                const F2 x = lru_read(from + N, row + j, pair), eg = GATE ? mul2(e, gate[j]) : e, ea = mul2(e, a[j]);
+                const F2 g = GATE ? rcp_2(add2(shut[j], both(1.f))) : 0;
+                const F2 x = lru_read(from + N, row + j, pair), eg = GATE ? mul2(e, g) : e, ea = mul2(e, a[j]);
                 F2 dr_, s = part[j];
                 if (RATE) {
                     const Parts o = parts_of(part[j], a[j], far);
                     s = o.s;
                     // -dlog a v = e a (a g x v / s - h v); dr is that times (1 - q) / 2
-                    const F2 gxa = mul2(GATE ? mul2(gate[j], x) : x, a[j]);
+                    const F2 gxa = mul2(GATE ? mul2(g, x) : x, a[j]);
                     const F2 term = fma2(gxa, o.ratio, mul2(h[j], o.v)), base = mul2(ea, term);
                     sum = fma2(ea, term, sum);
-                    dr_ = mul2(base, fma2(o.v, half_inverse, both(0.5f)));
+                    dr_ = mul2(base, set_aside(from, row + j, pair));
                 } else {
                     dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(mul2(eg, x))));
                 }
                 const F2 dx_ = mul2(eg, s);
                 store2(xp + at, dx_, all ? 2 : left, all);
                 store2(rp + at, dr_, all ? 2 : left, all);
-                if (GATE) store2(ip + at, mul2(mul2(dx_, x), fma2(gate[j], both(-1.f), both(1.f))), all ? 2 : left, all);
+                if (GATE) store2(ip + at, mul2(mul2(dx_, x), mul2(shut[j], g)), all ? 2 : left, all);
             };
             if (p.vec && len == kLruTile && left > 0 && !(RATE && plan.far)) {
 #pragma unroll
@@ -311,6 +338,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             sum = add2(sum, swap_halves(sum));
             if (!second) me.sums[warp][pair] = sum;
         }
+        if (TMA && RATE) bw::fence_async_shared();         // what was set aside, before the next tile arrives there
         lru_sync<3, kLruWorkers>(group);                         // the tile has been read
         if (!TMA) fetch(turn + B);
         else if (thread == kLruWorkers - 32) issue(turn + B);
@@ -359,7 +387,7 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
         using IO = decltype(io);
         constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
         const auto go = [&](auto kernel) {
-            return lru_launch(kernel, p, chain, kGroups * kLruThreads, kGroups * lru_backward_smem<IO, G>(), s, m, dy, kept,
+            return lru_launch(kernel, p, chain, kGroups * kLruThreads, kGroups * lru_backward_smem<IO, R, G>(), s, m, dy, kept,
                               g.dh_final, (IO*)g.dx, (IO*)g.dr, (IO*)g.di, partial, g.dh0);
         };
         return tma ? go(lru_backward_kernel<IO, R, G, true>) : go(lru_backward_kernel<IO, R, G, false>);
