@@ -31,33 +31,32 @@ __device__ __forceinline__ void read_run(const IO* from, int row, int pair, F2 k
         if (GATE) i[j] = lru_raw(from + 2 * N, row + j, pair);
     }
     const F2 k2 = add2(k, k);
-    const auto run = [&](auto far_, auto wild_) {
-        constexpr bool FAR = decltype(far_)::value, WILD = decltype(wild_)::value;
+    const auto run = [&](auto more, auto wild) {
+        constexpr bool MORE = decltype(more)::value, WILD = decltype(wild)::value;
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
-            const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
+            const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), t2 = GATE ? one_and_exp(wide2(i[j])) : 0;
             if (RATE) {
-                const F2 t2 = GATE ? one_and_exp(iv) : 0;
                 F2 w, z;
                 lru_roots<GATE, WILD>(one_and_exp(rv), t2, w, z);
                 const F2 v = mul2(k2, mul2(w, w));
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(root, x));
-                if (FAR) {
+                if (MORE) {
                     const F2 s = sqrt2(fma2(mul2(a[j], both(-1.f)), a[j], both(1.f)));
                     u[j] = below(v, kLruNear, u[j], mul2(s, GATE ? mul2(rcp_2(t2), x) : x));
                 }
             } else {
                 F2 s, sg;
-                lru_parts<GATE, WILD>(rv, iv, a[j], s, sg);
+                lru_parts<GATE, MORE>(rv, t2, a[j], s, sg);
                 u[j] = mul2(sg, x);
             }
         }
     };
-    const bool tame = lru_tame<RATE, GATE>(r, i, len - row, left);
+    const bool tame = lru_tame<RATE, RATE && GATE>(r, i, len - row, left);
     if (tame && !(RATE && far)) run(std::false_type(), std::false_type());
     else if (RATE && tame) run(std::true_type(), std::false_type());
-    else run(std::bool_constant<RATE>(), std::true_type());
+    else run(std::true_type(), std::bool_constant<RATE>());
     if (len < kLruTile)
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j)

@@ -97,10 +97,6 @@ __device__ __forceinline__ float min_nan(float a, float b) {   // NaN where eith
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-__device__ __forceinline__ F2 max_nan2(F2 a, F2 b) {
-    const float2 x = unpack2(a), y = unpack2(b);
-    return pack2(max_nan(x.x, y.x), max_nan(x.y, y.y));
-}
 __device__ __forceinline__ float sqrt_fast(float x) {
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -114,16 +110,25 @@ __device__ __forceinline__ F2 sqrt2(F2 v) {
 __device__ __forceinline__ float rate_of(float lam, float c) {
     return c * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam))));     // a NaN comes through the logarithm
 }
-// k, sqrt(2 k), k's slope by lam over 2 k, and -1 / (4 k); the last two zero for a channel that neither forgets nor takes.
+// k, sqrt(2 k), and k's slope by lam over 2 k, which is zero for a channel that neither forgets nor takes.
 __device__ __forceinline__ float4 rates_of(float lam, float c) {
     const float k = rate_of(lam, c), slope = c / (1.f + expf(-lam));
-    return make_float4(k, sqrtf(2.f * k), k > 1e-37f ? slope / (2.f * k) : 0.f, k > 1e-37f ? -0.25f / k : 0.f);
+    return make_float4(k, sqrtf(2.f * k), k > 1e-37f ? slope / (2.f * k) : 0.f, 0.f);
 }
 
+// Of each channel `yes` where x is below, above the bound, else (or NaN) `no`.
+__device__ __forceinline__ F2 below(F2 x, float bound, F2 yes, F2 no) {
+    const float2 at = unpack2(x), y = unpack2(yes), n = unpack2(no);
+    return pack2(at.x < bound ? y.x : n.x, at.y < bound ? y.y : n.y);
+}
+__device__ __forceinline__ F2 above(F2 x, float bound, F2 yes, F2 no) {
+    const float2 at = unpack2(x), y = unpack2(yes), n = unpack2(no);
+    return pack2(at.x > bound ? y.x : n.x, at.y > bound ? y.y : n.y);
+}
 // A token's decay a and input's part s; q = sigmoid(r).
 //
-// RATE: s^2 = 1 - e^-v with v = 2 k q: by a polynomial where 1 - a^2 cancels.  Else: with e = e^-r, q = 1 / (1 + e), s = e q
-// to relative accuracy, and a = 1 - s, which is exact where a state is kept.
+// RATE: s^2 = 1 - e^-v with v = 2 k q: by a polynomial where 1 - a^2 cancels.  Else the smaller of a and s comes from e^-|r| to
+// relative accuracy, and the other is 1 less it, which is exact where a state is kept.
 template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, F2& a, F2& s, F2& q) {
     if (RATE) {
         q = sigmoid2(r);
@@ -137,27 +142,30 @@ template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, 
         const float2 near = unpack2(m), far = unpack2(fma2(mul2(a, both(-1.f)), a, both(1.f))), at = unpack2(v);
         s = sqrt2(pack2(at.x < 0.5f ? near.x : far.x, at.y < 0.5f ? near.y : far.y));
     } else {
-        const float2 f = unpack2(mul2(r, both(-kLog2e)));
-        const F2 e = pack2(ex2(min_nan(f.x, 126.f)), ex2(min_nan(f.y, 126.f)));
-        s = mul2(e, rcp_2(add2(e, both(1.f))));
-        a = fma2(s, both(-1.f), both(1.f));
+        const float2 f = unpack2(r);
+        const F2 e = pack2(ex2(-fabsf(f.x) * kLog2e), ex2(-fabsf(f.y) * kLog2e));
+        const F2 small = mul2(e, rcp_2(add2(e, both(1.f)))), rest = fma2(small, both(-1.f), both(1.f));
+        a = below(r, 0.f, small, rest);
+        s = below(r, 0.f, rest, small);
         q = a;
     }
 }
 
 // The same for a whole run at fewer reciprocals and roots, which take twice the time of 2^x and four times that of a product
-// (an SM does 16 of them a clock; formed one by one they bound the forward at 134 of 158 us for 32768 x 4096).
+// (an SM does 16 of them a clock; formed one by one they bound the forward with rates at 134 of 158 us for 32768 x 4096).
 //
 // RATE, where v = 2 k q stays below 1/2 (k <= 1/4: gates that keep more than 0.78 of a state when they are open): with
 // w = sqrt(q) = (1 + e^-r)^-1/2, s = sqrt(2 k) w P(v), P(v) = sqrt((1 - e^-v) / v), by a polynomial; one root of
-// (1 + e^-r)(1 + e^-i)^2 gives w g, times (1 + e^-i) it gives w.  Else: one reciprocal of (1 + e^-r)(1 + e^-i) gives q g.
-// The products must not overflow where q or g is small: i (and without rates r) is at least -27.  With rates a gate r so far
-// shut that the product still does (an inflow below 2^-64 of x) lets nothing in.
+// (1 + e^-r)(1 + e^-i)^2 gives w g, times (1 + e^-i) it gives w.  The product must not overflow where g is small: i is at least
+// -27.  A gate r so far shut that it still does (an inflow below 2^-64 of x) lets nothing in.
+// Else: q = 1 / (1 + e^-r), s = e^-r q, and a = 1 - s, exact where a state is kept but off by up to 4e-7: below r = -3 a is q.
+// (q near 1 is rounded once a token, which a long life adds up; from -3 on the 4e-7 are below 1e-5 of a.)
 //
-// A warp goes by them alone (EASY) where every token and channel of its runs may; elsewhere it forms the others' terms too and
+// A warp goes by these alone where every token and channel of its runs may; elsewhere it forms the others' terms too and
 // selects, so that a token's bits follow from its own channel's numbers, whatever its neighbours hold.
 constexpr float kLruSlow = 0.25f, kLruNear = 0.50001f;      // the largest k, and what v stays below when q is rounded up
-constexpr float kLruLeast = -27.f, kLruJoint = 0x1p39f;     // the least logit, and what 1 + e^27 stays below
+constexpr float kLruLeast = -27.f, kLruJoint = 0x1p39f;     // the least i, and what 1 + e^27 stays below
+constexpr float kLruShut = -3.f, kLruShutE = 20.086f;       // the least r that has a = 1 - s, and what e^3 stays below
 constexpr float kLruHuge = 0x1.8p126f;      // what an e^-i is cut to that would be infinite: 1 / (1 + it) is still flushed to zero
 __device__ __forceinline__ float rsqrt_fast(float x) {
     float y;
@@ -180,11 +188,6 @@ __device__ __forceinline__ F2 lru_p_inverse(F2 v) {      // 1 / P(v), off by 4e-
     p = fma2(v, p, both(0x1.ffff5p-3f));
     return fma2(v, p, both(1.f));
 }
-// Of each channel `yes` where x is below the bound, else (or NaN) `no`.
-__device__ __forceinline__ F2 below(F2 x, float bound, F2 yes, F2 no) {
-    const float2 at = unpack2(x), y = unpack2(yes), n = unpack2(no);
-    return pack2(at.x < bound ? y.x : n.x, at.y < bound ? y.y : n.y);
-}
 // RATE: w and z = w g from t1 = 1 + e^-r and t2 = 1 + e^-i.  WILD: i may be anything.
 template <bool GATE, bool WILD> __device__ __forceinline__ void lru_roots(F2 t1, F2 t2, F2& w, F2& z) {
     if (GATE) {
@@ -199,21 +202,16 @@ template <bool GATE, bool WILD> __device__ __forceinline__ void lru_roots(F2 t1,
         z = w = rsqrt2(t1);
     }
 }
-// Else: a, its complement s, and s g.  WILD: r and i may be anything.
-template <bool GATE, bool WILD> __device__ __forceinline__ void lru_parts(F2 r, F2 i, F2& a, F2& s, F2& sg) {
-    const F2 e = ex2_2(mul2(r, both(-kLog2e))), t1 = add2(e, both(1.f)), t2 = GATE ? one_and_exp(i) : both(1.f);
-    const F2 o = rcp_2(GATE ? mul2(t1, t2) : t1);
-    sg = mul2(e, o);
-    s = GATE ? mul2(sg, t2) : sg;
+// Else: a, its complement s, and s g; t2 = 1 + e^-i.  SHUT: r may be below kLruShut.
+template <bool GATE, bool SHUT> __device__ __forceinline__ void lru_parts(F2 r, F2 t2, F2& a, F2& s, F2& sg) {
+    const F2 e = ex2_2(mul2(r, both(-kLog2e))), q = rcp_2(add2(e, both(1.f)));
+    s = mul2(e, q);
     a = fma2(s, both(-1.f), both(1.f));
-    if (WILD) {
-        F2 a_, s_, q_;
-        decay_and_part<false>(r, 0, a_, s_, q_);
-        const F2 g_ = GATE ? sigmoid2(i) : both(1.f), worst = GATE ? max_nan2(e, t2) : e;
-        a = below(worst, kLruJoint, a, a_);
-        s = below(worst, kLruJoint, s, s_);
-        sg = below(worst, kLruJoint, sg, mul2(s_, g_));
+    if (SHUT) {
+        a = below(e, kLruShutE, a, q);
+        s = above(e, 0x1p100f, both(1.f), s);           // q is flushed to zero from 2^126 on
     }
+    sg = GATE ? mul2(s, rcp_2(t2)) : s;
 }
 
 // Minima of two channels, NaN where either is.
@@ -381,7 +379,7 @@ struct LruPlan {
     LruTile t;
     bool live;               // there is one
     bool far;                // some channel's rate is above kLruSlow
-    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols], inverses[kLruCols];       // rates_of
+    alignas(8) float rates[kLruCols], roots[kLruCols], slopes[kLruCols];       // rates_of
 };
 // The guide's: a channel's rates are read four tiles ahead and a tile planned three ahead, after the present one's state is
 // out, so that no way to memory holds anyone up.
@@ -409,7 +407,7 @@ template <bool BACK, bool RATE, int GROUPS> struct LruPlanner {
                 if (lane == 0) plan->far = far;
                 plan->rates[lane] = rate.x;
                 plan->roots[lane] = rate.y;
-                if (BACK) plan->slopes[lane] = rate.z, plan->inverses[lane] = rate.w;
+                if (BACK) plan->slopes[lane] = rate.z;
             }
         }
         read(p, c, turn + 1);
@@ -505,10 +503,9 @@ template <typename IO> __device__ __forceinline__ RawN<IO, 2> lru_raw(const IO* 
 template <typename IO> __device__ __forceinline__ F2 lru_read(const IO* from, int row, int pair) {
     return wide2(lru_raw(from, row, pair));
 }
-// Whether the gates of all the warp's runs are at least kLruLeast, and none is NaN; tokens past the tile's end and channels past
-// the last, which hold anything, are not asked.
-template <typename IO>
-__device__ __forceinline__ bool lru_least(const RawN<IO, 2> (&v)[kLruRun], int live, int left) {
+// Whether a run's gates are all at least `bound`, and none NaN; tokens past the tile's end and channels past the last, which
+// hold anything, are not asked.
+template <typename IO> __device__ __forceinline__ bool lru_above(const RawN<IO, 2> (&v)[kLruRun], float bound, int live, int left) {
     RawN<IO, 2> least = v[0];
     if (live >= kLruRun) {
 #pragma unroll
@@ -519,13 +516,14 @@ __device__ __forceinline__ bool lru_least(const RawN<IO, 2> (&v)[kLruRun], int l
             if (j < live) least = min_pair(least, v[j]);
     }
     const float2 g = to_f2(least.e);
-    return live <= 0 || ((left < 1 || g.x >= kLruLeast) && (left < 2 || g.y >= kLruLeast));
+    return live <= 0 || ((left < 1 || g.x >= bound) && (left < 2 || g.y >= bound));
 }
+// Whether no gate of the warp's runs is so far shut that the short formulas are not enough.  GATE: whether i is asked.
 template <bool RATE, bool GATE, typename IO>
 __device__ __forceinline__ bool lru_tame(const RawN<IO, 2> (&r)[kLruRun], const RawN<IO, 2> (&i)[kLruRun], int live, int left) {
     bool ok = true;
-    if (!RATE) ok = lru_least(r, live, left);
-    if (GATE) ok = ok && lru_least(i, live, left);
+    if (!RATE) ok = lru_above(r, kLruShut, live, left);
+    if (GATE) ok = ok && lru_above(i, kLruLeast, live, left);
     return (RATE && !GATE) || __all_sync(0xffffffffu, ok);
 }
 

@@ -71,12 +71,12 @@ __device__ __forceinline__ void read_run(IO* from, int row, int pair, F2 root, b
         if (GATE) i[j] = lru_raw(from + 3 * N, row + j, pair);
     }
     const F2 minus = neg2(root);
-    const auto run = [&](auto far_, auto wild_) {
-        constexpr bool FAR = decltype(far_)::value, WILD = decltype(wild_)::value;
+    const auto run = [&](auto more, auto wild) {
+        constexpr bool MORE = decltype(more)::value, WILD = decltype(wild)::value;
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
-            const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]), iv = GATE ? wide2(i[j]) : 0;
-            F2 e = GATE ? ex2_2(mul2(iv, both(-kLog2e))) : 0;
+            const F2 x = lru_read(from + N, row + j, pair), rv = wide2(r[j]);
+            const F2 e = GATE ? ex2_2(mul2(wide2(i[j]), both(-kLog2e))) : 0;
             if (RATE) {
                 F2 w, z;
                 const F2 half = ex2_2(fma2(rv, both(-kLog2e), both(-1.f)));         // e^-r / 2
@@ -85,23 +85,23 @@ __device__ __forceinline__ void read_run(IO* from, int row, int pair, F2 root, b
                 const F2 v = mul2(part[j], part[j]);
                 a[j] = ex2_2(fma2(v, both(-0.5f * kLog2e), both(kLruLean)));
                 u[j] = mul2(mul2(z, lru_p(v)), mul2(minus, x));
-                if (FAR) {
+                if (MORE) {
                     const F2 s = sqrt2(fma2(mul2(a[j], both(-1.f)), a[j], both(1.f)));
                     u[j] = below(v, kLruNear, u[j], mul2(neg2(s), GATE ? mul2(rcp_2(add2(e, both(1.f))), x) : x));
                 }
                 put_aside(from, row + j, pair, mul2(at_most(half, kLruHuge), mul2(w, w)));
             } else {
                 F2 sg;
-                lru_parts<GATE, WILD>(rv, iv, a[j], part[j], sg);
+                lru_parts<GATE, MORE>(rv, add2(e, both(1.f)), a[j], part[j], sg);
                 u[j] = mul2(sg, x);
             }
-            if (GATE) shut[j] = WILD ? at_most(e, kLruHuge) : e;
+            if (GATE) shut[j] = WILD || (MORE && !RATE) ? at_most(e, kLruHuge) : e;
         }
     };
     const bool tame = lru_tame<RATE, GATE>(r, i, len - row, left);
     if (tame && !(RATE && far)) run(std::false_type(), std::false_type());
     else if (RATE && tame) run(std::true_type(), std::false_type());
-    else run(std::bool_constant<RATE>(), std::true_type());
+    else run(std::true_type(), std::bool_constant<RATE>());
     if (len < kLruTile)
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j)
