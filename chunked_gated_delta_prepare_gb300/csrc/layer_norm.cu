@@ -37,6 +37,9 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
 }
 
 constexpr int ring_places(int warps, int most) { return (warps <= most ? most : 32) / warps; }
+// A place's rows are kSms places apart times a block's: where rows are cut at the boundaries, their shift, and with it the
+// columns of the weights and sums in a thread's registers, repeats after at most 8 rows.
+static_assert(kSms % 8 == 0, "every row of a place has the shift of its first");
 
 // Sums over a place's WARPS warps; red: [NV][places][WARPS, a multiple of 4], zero where there is no warp, not used again
 // before another barrier of the place.
