@@ -152,7 +152,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             uint64_t* bar = me.full + turn % B;
             IO* to = in + (turn % B) * IN * N;
             if (t.len == 0) return bw::mbar_arrive(bar);
-            bw::mbar_arrive_expect_tx(bar, in_maps.rows * TENSORS * kLruCols * (unsigned)sizeof(IO));
+            bw::mbar_arrive_expect_tx(bar, (unsigned)(TENSORS * N * sizeof(IO)));
             lru_tma(to, &in_maps.r, bar, t);
             lru_tma(to + N, &in_maps.x, bar, t);
             lru_tma(to + 2 * N, &in_maps.dy, bar, t);
@@ -378,7 +378,6 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
     LruChain chain;
     if (cudaError_t e = lru_chain(args, t.lam, workspace, &chain, s)) return e;
     LruMaps m;
-    m.rows = lru_box(args);
     const bool tma = args.total > 0 && p.x.unit == 16 && p.r.unit == 16 && dy.unit == 16 && (!p.i.p || p.i.unit == 16);
     if (tma && !(lru_map(&m.x, p.x, args) && lru_map(&m.r, p.r, args) && lru_map(&m.dy, dy, args) &&
                  (!p.i.p || lru_map(&m.i, p.i, args))))

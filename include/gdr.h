@@ -702,7 +702,9 @@ GDR_API gdr_status gdr_ssm_step(const gdr_ssm_problem* p, const int32_t* slots, 
  * A channel's results follow from that channel's inputs alone, bit for bit.
  * kept [rows,D] fp32 or NULL: the state before every 128th token of each sequence, for the gradient; its bytes come
  * from gdr_lru_kept_bytes.  A long sequence is scanned in tiles of that many tokens at once; a tile's state follows
- * from its predecessor's in a fixed order, so the result of a call does not change from run to run. */
+ * from its predecessor's in a fixed order, so the result of a call does not change from run to run.
+ * Sequences of more than one tile are scanned by blocks that wait for one another, one on each SM of the device, and so
+ * start together once all of these are free.  A stream that is confined to some of them (a green context) gets GDR_ERR_CUDA. */
 typedef struct gdr_lru_problem {
     int64_t n, T, total;     /* n >= 1 sequences (rows of gdr_lru_step); of T >= 1 tokens, or packed on total >= 0 */
     int64_t D;
