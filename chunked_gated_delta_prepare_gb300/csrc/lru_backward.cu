@@ -21,10 +21,41 @@ namespace {
 constexpr int kGroups = 2;   // 96 registers a thread
 template <typename IO> constexpr int kBuffers = sizeof(IO) == 2 ? 2 : 1;      // of tiles
 
-// Places of a tile: r, x, dy, and i or what 16-bit types set aside there.
-template <typename IO, bool RATE, bool GATE> constexpr int kPlaces = GATE || (RATE && sizeof(IO) == 2) ? 4 : 3;
-template <typename IO, bool RATE, bool GATE> constexpr int lru_backward_smem() {     // of a group
-    return kBuffers<IO> * kPlaces<IO, RATE, GATE> * kLruTile * kLruCols * (int)sizeof(IO);
+// A token's e^-i, and (RATE) (1 - q) / 2, wait in shared memory while the tile's maps are joined: in registers, beside the run's
+// a, h and s, they spill (4 x 2048 x 4096 bf16 133 us, so 120).  They lie in room of their own behind the tiles, a number of a
+// thread's token j at [j][thread]; but without TMA, where rows come through the L1 that this room is taken from, the second
+// lies in the place of its r (16-bit types: of its r and its i), which no other thread reads (8192 x 4094 226 us otherwise, so
+// 191).
+template <bool RATE, bool GATE, bool TMA> constexpr bool kHalfBehind = RATE && (TMA || !GATE);
+constexpr int kAside = kLruRun * kLruWorkers;
+template <typename IO, bool RATE, bool GATE, bool TMA> struct Aside {
+    static constexpr int numbers = kHalfBehind<RATE, GATE, TMA> + GATE;
+    F2* room;                // the thread's
+    IO* place;               // the tile
+
+    __device__ __forceinline__ F2& shut(int j) const { return room[kHalfBehind<RATE, GATE, TMA> * kAside + j * kLruWorkers]; }
+    __device__ __forceinline__ void put_half(int j, int row, int pair, F2 v) const {
+        IO* const at = place + (row + j) * kLruCols + pair * 2;
+        if constexpr (kHalfBehind<RATE, GATE, TMA>) {
+            room[j * kLruWorkers] = v;
+        } else if constexpr (sizeof(IO) == 4) {
+            *reinterpret_cast<F2*>(at) = v;
+        } else {
+            const float2 f = unpack2(v);
+            *reinterpret_cast<float*>(at) = f.x;
+            *reinterpret_cast<float*>(at + 3 * kLruTile * kLruCols) = f.y;
+        }
+    }
+    __device__ __forceinline__ F2 half(int j, int row, int pair) const {
+        const IO* const at = place + (row + j) * kLruCols + pair * 2;
+        if constexpr (kHalfBehind<RATE, GATE, TMA>) return room[j * kLruWorkers];
+        else if constexpr (sizeof(IO) == 4) return *reinterpret_cast<const F2*>(at);
+        else return pack2(*reinterpret_cast<const float*>(at), *reinterpret_cast<const float*>(at + 3 * kLruTile * kLruCols));
+    }
+};
+template <typename IO, bool RATE, bool GATE, bool TMA> constexpr int lru_backward_smem() {     // of a group
+    return kBuffers<IO> * (GATE ? 4 : 3) * kLruTile * kLruCols * (int)sizeof(IO) +
+           Aside<IO, RATE, GATE, TMA>::numbers * kAside * (int)sizeof(F2);
 }
 
 struct alignas(8) Run {      // of a run of tokens: its product of decays, its end from a zero state, and what it sends to the
@@ -34,35 +65,19 @@ struct alignas(16) Map {     // what tokens make of the gradient e from behind t
     F2 decay, back;
 };
 
-// A number for each of a token's two channels, in the place of its r (16-bit types: of its r and its i), which no other thread
-// reads.  Registers do not hold them beside the run's other 64 (146 us for 4 x 2048 x 4096 bf16, by spills); formed again
-// where they are used they take 138, and this 132.
-template <typename IO> __device__ __forceinline__ void put_aside(IO* from, int row, int pair, F2 v) {
-    if constexpr (sizeof(IO) == 4) {
-        *reinterpret_cast<F2*>(from + row * kLruCols + pair * 2) = v;
-    } else {
-        const float2 f = unpack2(v);
-        *reinterpret_cast<float*>(from + row * kLruCols + pair * 2) = f.x;
-        *reinterpret_cast<float*>(from + (row + 3 * kLruTile) * kLruCols + pair * 2) = f.y;
-    }
-}
-template <typename IO> __device__ __forceinline__ F2 set_aside(const IO* from, int row, int pair) {
-    if constexpr (sizeof(IO) == 4) return *reinterpret_cast<const F2*>(from + row * kLruCols + pair * 2);
-    return pack2(*reinterpret_cast<const float*>(from + row * kLruCols + pair * 2),
-                 *reinterpret_cast<const float*>(from + (row + 3 * kLruTile) * kLruCols + pair * 2));
-}
 __device__ __forceinline__ F2 at_most(F2 v, float bound) {
     const float2 f = unpack2(v);
     return pack2(min_nan(f.x, bound), min_nan(f.y, bound));
 }
 
 // The decays and terms of the thread's run, from shared memory, and what the gradients need beside them: the input's part s
-// (RATE: sqrt(v), v = 2 k q), e^-i, and (RATE, set aside in shared memory) (1 - q) / 2.  1 - q and 1 - g = e^-i g come from the
-// exponentials: from q and g, which are rounded, an open gate's would be noise.  RATE: the terms, and so all states here, have
-// the other sign, which saves the gradients a negation.  A token past the tile's end has a = 1, u = 0.
-template <typename IO, bool RATE, bool GATE>
-__device__ __forceinline__ void read_run(IO* from, int row, int pair, F2 root, bool far, int len, int left, F2 (&a)[kLruRun],
-                                         F2 (&u)[kLruRun], F2 (&part)[kLruRun], F2 (&shut)[kLruRun]) {
+// (RATE: sqrt(v), v = 2 k q), and what is set aside.  1 - q and 1 - g = e^-i g come from the exponentials: from q and g, which
+// are rounded, an open gate's would be noise.  RATE: the terms, and so all states here, have the other sign, which saves the
+// gradients a negation.  A token past the tile's end has a = 1, u = 0.
+template <typename IO, bool RATE, bool GATE, bool TMA>
+__device__ __forceinline__ void read_run(const Aside<IO, RATE, GATE, TMA>& aside, int row, int pair, F2 root, bool far, int len,
+                                         int left, F2 (&a)[kLruRun], F2 (&u)[kLruRun], F2 (&part)[kLruRun]) {
+    const IO* const from = aside.place;
     constexpr int N = kLruTile * kLruCols;
     RawN<IO, 2> r[kLruRun], i[kLruRun];
 #pragma unroll
@@ -89,13 +104,13 @@ __device__ __forceinline__ void read_run(IO* from, int row, int pair, F2 root, b
                     const F2 s = sqrt2(fma2(mul2(a[j], both(-1.f)), a[j], both(1.f)));
                     u[j] = below(v, kLruNear, u[j], mul2(neg2(s), GATE ? mul2(rcp_2(add2(e, both(1.f))), x) : x));
                 }
-                put_aside(from, row + j, pair, mul2(at_most(half, kLruHuge), mul2(w, w)));
+                aside.put_half(j, row, pair, mul2(at_most(half, kLruHuge), mul2(w, w)));
             } else {
                 F2 sg;
                 lru_parts<GATE, MORE>(rv, add2(e, both(1.f)), a[j], part[j], sg);
                 u[j] = mul2(sg, x);
             }
-            if (GATE) shut[j] = WILD || (MORE && !RATE) ? at_most(e, kLruHuge) : e;
+            if (GATE) aside.shut(j) = WILD || (MORE && !RATE) ? at_most(e, kLruHuge) : e;
         }
     };
     const bool tame = lru_tame<RATE, GATE>(r, i, len - row, left);
@@ -129,7 +144,7 @@ __global__ void __launch_bounds__(kGroups * kLruThreads, 1)
 lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_maps, LruRows dy, const float* __restrict__ kept,
                     const float* __restrict__ dh_final, IO* __restrict__ dx, IO* __restrict__ dr, IO* __restrict__ di,
                     float* __restrict__ dlam, float* __restrict__ dh0) {
-    constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, TENSORS = GATE ? 4 : 3, IN = kPlaces<IO, RATE, GATE>;
+    constexpr int B = kBuffers<IO>, N = kLruTile * kLruCols, IN = GATE ? 4 : 3;
     struct Group {
         Run runs[kLruWarps][kLruPairs];                     // of a warp's tokens
         Map behind[kLruWarps][kLruPairs];                   // of the tokens behind them
@@ -152,7 +167,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             uint64_t* bar = me.full + turn % B;
             IO* to = in + (turn % B) * IN * N;
             if (t.len == 0) return bw::mbar_arrive(bar);
-            bw::mbar_arrive_expect_tx(bar, (unsigned)(TENSORS * N * sizeof(IO)));
+            bw::mbar_arrive_expect_tx(bar, (unsigned)(IN * N * sizeof(IO)));
             lru_tma(to, &in_maps.r, bar, t);
             lru_tma(to + N, &in_maps.x, bar, t);
             lru_tma(to + 2 * N, &in_maps.dy, bar, t);
@@ -231,6 +246,9 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         return;
     }
 
+    using Aside = Aside<IO, RATE, GATE, TMA>;
+    F2* const room = reinterpret_cast<F2*>(reinterpret_cast<IO*>(smem) + kGroups * B * IN * N) + group * Aside::numbers * kAside +
+                     thread;
     const int warp = thread / 32, pair = thread % kLruPairs, row = thread / kLruPairs * kLruRun;
     const bool second = thread & 16;                        // run of the warp
     const auto fetch = [&](unsigned turn) {
@@ -257,9 +275,10 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
         const LruPlan& plan = plans[turn % kLruPlans];
         const int ch = plan.t.col * kLruCols + pair * 2, left = p.D - ch, len = plan.t.len;
         const F2 root = RATE ? *reinterpret_cast<const F2*>(plan.roots + pair * 2) : 0;
-        IO* from = in + (turn % B) * IN * N;
-        F2 a[kLruRun], h[kLruRun], part[kLruRun], shut[kLruRun];
-        read_run<IO, RATE, GATE>(from, row, pair, root, plan.far, len, left, a, h, part, shut);
+        const Aside aside{room, in + (turn % B) * IN * N};
+        const IO* const from = aside.place;
+        F2 a[kLruRun], h[kLruRun], part[kLruRun];
+        read_run(aside, row, pair, root, RATE && plan.far, len, left, a, h, part);
         Run m{both(1.f), both(0.f), both(0.f)};
 #pragma unroll
         for (int j = 0; j < kLruRun; ++j) {
@@ -301,7 +320,7 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             const auto token = [&](int j, bool far, bool all) {
                 e = fma2(e, behind, lru_read(from + 2 * N, row + j, pair));
                 behind = a[j];
-                const F2 g = GATE ? rcp_2(add2(shut[j], both(1.f))) : 0;
+                const F2 shut = GATE ? aside.shut(j) : 0, g = GATE ? rcp_2(add2(shut, both(1.f))) : 0;
                 const F2 x = lru_read(from + N, row + j, pair), eg = GATE ? mul2(e, g) : e, ea = mul2(e, a[j]);
                 F2 dr_, s = part[j];
                 if (RATE) {
@@ -311,14 +330,14 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
                     const F2 gxa = mul2(GATE ? mul2(g, x) : x, a[j]);
                     const F2 term = fma2(gxa, o.ratio, mul2(h[j], o.v)), base = mul2(ea, term);
                     sum = fma2(ea, term, sum);
-                    dr_ = mul2(base, set_aside(from, row + j, pair));
+                    dr_ = mul2(base, aside.half(j, row, pair));
                 } else {
                     dr_ = mul2(mul2(a[j], s), fma2(e, h[j], neg2(mul2(eg, x))));
                 }
                 const F2 dx_ = mul2(eg, s);
                 store2(xp + at, dx_, all ? 2 : left, all);
                 store2(rp + at, dr_, all ? 2 : left, all);
-                if (GATE) store2(ip + at, mul2(mul2(dx_, x), mul2(shut[j], g)), all ? 2 : left, all);
+                if (GATE) store2(ip + at, mul2(mul2(dx_, x), mul2(shut, g)), all ? 2 : left, all);
             };
             if (p.vec && len == kLruTile && left > 0 && !(RATE && plan.far)) {
 #pragma unroll
@@ -338,7 +357,6 @@ lru_backward_kernel(Lru p, LruChain chain, const __grid_constant__ LruMaps in_ma
             sum = add2(sum, swap_halves(sum));
             if (!second) me.sums[warp][pair] = sum;
         }
-        if (TMA && RATE) bw::fence_async_shared();         // what was set aside, before the next tile arrives there
         lru_sync<3, kLruWorkers>(group);                         // the tile has been read
         if (!TMA) fetch(turn + B);
         else if (thread == kLruWorkers - 32) issue(turn + B);
@@ -385,11 +403,12 @@ cudaError_t lru_backward(const LruArgs& args, const LruTensors& t, const LruGrad
     const cudaError_t e = lru_types(args.io, t.lam, t.i.p, [&](auto io, auto rate, auto gate) {
         using IO = decltype(io);
         constexpr bool R = decltype(rate)::value, G = decltype(gate)::value;
-        const auto go = [&](auto kernel) {
-            return lru_launch(kernel, p, chain, kGroups * kLruThreads, kGroups * lru_backward_smem<IO, R, G>(), s, m, dy, kept,
+        const auto go = [&](auto kernel, int bytes) {
+            return lru_launch(kernel, p, chain, kGroups * kLruThreads, kGroups * bytes, s, m, dy, kept,
                               g.dh_final, (IO*)g.dx, (IO*)g.dr, (IO*)g.di, partial, g.dh0);
         };
-        return tma ? go(lru_backward_kernel<IO, R, G, true>) : go(lru_backward_kernel<IO, R, G, false>);
+        return tma ? go(lru_backward_kernel<IO, R, G, true>, lru_backward_smem<IO, R, G, true>())
+                   : go(lru_backward_kernel<IO, R, G, false>, lru_backward_smem<IO, R, G, false>());
     });
     if (e != cudaSuccess || !t.lam) return e;
     return column_sum(partial, lru_tiles(args), args.D, args.D, g.dlam, 0, nullptr, s);
