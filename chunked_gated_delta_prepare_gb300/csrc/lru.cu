@@ -4,10 +4,11 @@
 // the decays a and terms u of its run of 8 tokens in registers, the runs' maps h -> h * decay + own are joined through
 // shared memory, the tile's state comes from the tiles before it (look_back), and the run is gone over again from its state.
 //
-// Measured (bf16, both gates): 32768 x 4096 in 205 us, 5.2 TB/s, 0.77 of a copy's rate.  What is left is the wait for a
-// tile's state: 4.2 of 10 warps an issue stand at the group's barrier, and the issue slots are 0.56 full.  Blocks of one group
-// that all look back through the L2 took 239, tiles fetched by the workers' own loads 286, gates by a reciprocal and a root
-// each (see lru.cuh) 254.  Rows that TMA cannot take: 8192 x 4094 94 us, 4095 (by elements) 131, 4096 63.
+// Measured (bf16, both gates): 32768 x 4096 in 205 us, 5.2 TB/s, 0.77 of a copy's rate; with rates above 1/4 236, without
+// rates 195.  What is left is the wait for a tile's state: 3.9 of 10 warps an issue stand at the group's barrier, and the issue
+// slots are 0.56 full.  Blocks of one group that all look back through the L2 took 239, tiles fetched by the workers' own loads
+// 286, gates by a reciprocal and a root each (see lru.cuh) 254.  Rows that TMA cannot take: 8192 x 4094 94 us, 4095 (by
+// elements) 132, 4096 62.
 // A step of 256 x 8192 fp16: 6.2 us, 4.8 TB/s; of 16 rows, the host's call.
 #include "lru.cuh"
 

@@ -162,7 +162,8 @@ template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, 
 // (q near 1 is rounded once a token, which a long life adds up; from -3 on the 4e-7 are below 1e-5 of a.)
 //
 // A warp goes by these alone where every token and channel of its runs may; elsewhere it forms the others' terms too and
-// selects, so that a token's bits follow from its own channel's numbers, whatever its neighbours hold.
+// selects, so that a token's bits follow from its own channel's numbers, whatever its neighbours hold.  What that costs (8192 x
+// 4096 bf16, forward and gradient): all k <= 1/4 62 and 120 us, k up to 0.84 or to 5 71 and 156.
 constexpr float kLruSlow = 0.25f, kLruNear = 0.50001f;      // the largest k, and what v stays below when q is rounded up
 constexpr float kLruLeast = -27.f, kLruJoint = 0x1p39f;     // the least i, and what 1 + e^27 stays below
 constexpr float kLruShut = -3.f, kLruShutE = 20.086f;       // the least r that has a = 1 - s, and what e^3 stays below

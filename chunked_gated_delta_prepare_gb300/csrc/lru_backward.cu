@@ -7,11 +7,12 @@
 //
 // Bound: memory, and (at 18 warps an SM) the latency of what a tile waits for in turn: its inputs, the gradient from behind,
 // its outputs.  One pass over the tiles from behind: as in the forward, with the gradient that reaches a tile from behind in
-// the place of its state, which is the forward's kept one.  Two groups a block: a run's a, h, s and gates take 64 registers,
-// and three groups' 72 a thread do not hold them.
+// the place of its state, which is the forward's kept one.  Two groups a block: of three neither the registers (72 a thread, of
+// which a run's a, h and s take 48) nor, with gates, the shared memory would hold the work.
 //
-// Measured (bf16, both gates, kept states): 4 x 2048 x 4096 in 115 us, 4.1 TB/s, 0.60 of a copy's rate; issue slots 0.49 full.
-// With the gates' products formed token by token, with 64-bit offsets and reciprocals of their own it took 130.
+// Measured (bf16, both gates, kept states): 4 x 2048 x 4096 in 110 us, 4.3 TB/s, 0.63 of a copy's rate; issue slots 0.52 full
+// with 4.5 warps in each to choose from.  With the gates' products formed token by token, with 64-bit offsets and reciprocals
+// of their own it took 130.  With rates above 1/4, 8192 x 4096: 156 us (120 below); without rates 98.
 #include "lru.cuh"
 
 namespace gdr {
