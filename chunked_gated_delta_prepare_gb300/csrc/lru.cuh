@@ -167,7 +167,7 @@ template <bool RATE> __device__ __forceinline__ void decay_and_part(F2 r, F2 k, 
 constexpr float kLruSlow = 0.25f, kLruNear = 0.50001f;      // the largest k, and what v stays below when q is rounded up
 constexpr float kLruLeast = -27.f, kLruJoint = 0x1p39f;     // the least i, and what 1 + e^27 stays below
 constexpr float kLruShut = -3.f, kLruShutE = 20.086f;       // the least r that has a = 1 - s, and what e^3 stays below
-constexpr float kLruHuge = 0x1.8p126f;      // what an e^-i is cut to that would be infinite: 1 / (1 + it) is still flushed to zero
+constexpr float kLruHuge = 0x1.8p126f;      // what an infinite e^-r or e^-i is cut to: 1 / (1 + it) is still flushed to zero
 __device__ __forceinline__ float rsqrt_fast(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -502,7 +502,8 @@ template <typename IO> __device__ __forceinline__ F2 lru_read(const IO* from, in
 }
 // Whether a run's gates are all at least `bound`, and none NaN; tokens past the tile's end and channels past the last, which
 // hold anything, are not asked.
-template <typename IO> __device__ __forceinline__ bool lru_above(const RawN<IO, 2> (&v)[kLruRun], float bound, int live, int left) {
+template <typename IO>
+__device__ __forceinline__ bool lru_above(const RawN<IO, 2> (&v)[kLruRun], float bound, int live, int left) {
     RawN<IO, 2> least = v[0];
     if (live >= kLruRun) {
 #pragma unroll

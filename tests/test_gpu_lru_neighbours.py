@@ -70,6 +70,24 @@ def test_channels_cut_anywhere():
         assert torch.equal(getattr(a, name)[..., 1:], getattr(b, name)), name
 
 
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("form,gate", FORMS)
+def test_channels_by_either_way_into_shared_memory(form, gate, io):
+    """Rows on 16-byte boundaries and rows that start anywhere take other kernels: the same bits."""
+    s = make((3, 300), 72, io, form, gate)
+    if form == "rate":
+        s["lam"][::5] = 0.0
+    dy = randn(3, 300, 72, io=io, seed=1)
+    cut = {k: (None if v is None else v[..., :67].contiguous()) for k, v in s.items()}
+    (y, h, kept), (y1, h1, kept1) = (layer.lru_forward(**v, want_kept=True) for v in (s, cut))
+    assert torch.equal(y[..., :67], y1) and torch.equal(h[:, :67], h1) and torch.equal(kept[:, :67], kept1)
+    a = layer.lru_backward(s["x"], s["r"], s["i"], s["lam"], dy, s["h0"], kept=kept)
+    b = layer.lru_backward(cut["x"], cut["r"], cut["i"], cut["lam"], dy[..., :67].contiguous(), cut["h0"], kept=kept1)
+    for name in ("dx", "dr", "di", "dh0", "dlam"):
+        u, v = getattr(a, name), getattr(b, name)
+        assert u is None or torch.equal(u[..., :67], v), name
+
+
 # ---------------------------------------------------------------- rates on both sides of 1/4
 
 @pytest.mark.parametrize("io", TYPES)
